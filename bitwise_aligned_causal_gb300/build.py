@@ -1,6 +1,6 @@
 """Build libkb_attn.so in-tree with nvcc for sm_103a.
 
-The three CUDA translation units compile in parallel, then link into one
+The CUDA translation units compile in parallel, then link into one
 shared library next to this file.  No CMake, no PyTorch extension machinery:
 the library exports a plain C ABI (include/kb_attn.h).
 """
@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkb_attn.so")
-SOURCES = ["kb_host.cu", "kb_prefill2.cu", "kb_decode.cu", "kb_backward.cu", "kb_segment.cu"]
+SOURCES = ["kb_host.cu", "kb_prefill2.cu", "kb_decode.cu", "kb_backward.cu", "kb_segment.cu",
+           "kb_host_sparse.cu", "kb_append.cu", "kb_select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -13,12 +13,13 @@
 
 #include "../../include/kb_attn.h"
 #include "kb_contract.cuh"
+#include "kb_host.h"
 #include "kb_launch.h"
 
 namespace {
 
-constexpr int kMaxRows = 1 << 22;     // positions per sequence (4M)
-constexpr int kMaxDevices = 64;
+using kb::kMaxDevices;
+using kb::kMaxRows;
 
 // Device error word (0 = fine).  Kernels get its address as an argument.
 __device__ uint32_t g_kb_error_word;
@@ -376,6 +377,52 @@ constexpr int kDefaultQTilesPerCta = kb::kShapeOneTilePerSm;
 int chunk_cta_shape(int L) { return L <= kb::kMaxPackedRows ? 0 : kDefaultQTilesPerCta; }
 
 }  // namespace
+
+// What kb_host_sparse.cu shares (kb_host.h).
+namespace kb {
+
+kb_status host_device(HostDevice* out) {
+  DeviceState* st = nullptr;
+  const kb_status s = get_device_state(&st);
+  if (s != KB_OK) return s;
+  out->index = static_cast<int>(st - g_dev);
+  out->err = st->err;
+  out->sm_count = st->sm_count;
+  return KB_OK;
+}
+
+kb_status host_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+kb_status host_device_pointer(const void* p) { return check_device_pointer(p); }
+
+kb_status host_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {
+  return encode_rows_map(m, base, rows, planes, plane_stride);
+}
+
+kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t groups) {
+  const cuuint64_t head_stride = rows * kHeadDim * 2u;
+  cuuint64_t dims[5] = {64u, rows, static_cast<cuuint64_t>(kGroup), 2u, groups};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(kHeadDim) * 2u, head_stride, 128u, kGroup * head_stride};
+  cuuint32_t box[5] = {64u, 32u, static_cast<cuuint32_t>(kGroup), 2u, 1u};
+  cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KB_OK : KB_ERR_CUDA;
+}
+
+kb_status host_check_heads(int B, int Hq, int Hkv) { return check_heads(B, Hq, Hkv); }
+
+kb_status host_check_paging(const int* block_table, int pages_per_seq, int page_size, int num_pages, int Hkv) {
+  Paging pg;
+  pg.block_table = block_table;
+  pg.pages_per_seq = pages_per_seq;
+  pg.page_size = page_size;
+  pg.num_pages = num_pages;
+  return check_paging(pg, Hkv);
+}
+
+}  // namespace kb
 
 extern "C" {
 

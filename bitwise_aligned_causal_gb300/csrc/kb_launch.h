@@ -103,6 +103,66 @@ cudaError_t launch_backward(const CUtensorMap& tq, const CUtensorMap& tk, const 
 // (rows = B*Hq*L, row r of a (b, h) at position start + r), then C4 into o.
 cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
                             cudaStream_t s);
+
+// Rotation of rows x[b, h, i] (strides in elements, last dimension contiguous)
+// at positions start + i into contiguous out [B, H, L, 128] (kb_append.cu).
+struct RopeArgs {
+  const void* x;
+  long long sb, sh, sl;
+  void* out;
+  const float* table;      // [positions, rot_dim / 2, 2] (cos, sin)
+  int rot_dim;
+  bool interleaved, inverse;
+  int B, H, L;
+  int start;
+  uint32_t* err;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+// (cos, sin) of position * inv_freq[plane], positions 0..n_pos-1.
+cudaError_t launch_rope_table(float* table, int n_pos, int rot_dim, const double* inv_freq, cudaStream_t s);
+
+// Append L new rows per sequence to a K/V cache, turned by their positions.
+struct AppendArgs {
+  const void *q, *k, *v;       // [B, Hq or Hkv, L, 128], last dimension contiguous; q may be null
+  long long qs[3], ks[3], vs[3];   // their batch, head and row strides in elements
+  void* q_out;                 // [B, Hq, L, 128] contiguous
+  void *k_cache, *v_cache;     // [B, Hkv, kv_cap, 128], or pools [num_pages, Hkv, page_size, 128]
+  void* boxes;                 // optional: [planes, blocks per plane, 2, 128] bf16
+  const float* table;          // as RopeArgs; null: no rotation
+  int n_pos, rot_dim;
+  bool interleaved;
+  int B, Hkv, L;
+  int start;
+  const int* starts;           // optional device [B]: per-sequence start ...
+  const int* lens;             // ... and row count (else L)
+  int kv_cap;                  // positions per sequence the cache can hold
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  uint32_t* err;
+};
+// only_boxes: read the cache's keys at the rows' positions and make their
+// blocks' boxes anew (q, k, v unused).
+cudaError_t launch_append(const AppendArgs& a, bool only_boxes, cudaStream_t s);
+
+// Choice of key blocks per query row (kb_select.cu).
+struct SelectArgs {
+  const void* q;               // [B, Hq, L, 128] bf16
+  const void* boxes;           // [planes, blocks_per_plane, 2, 128] bf16
+  int* blocks;                 // [B, Hkv, L, n]
+  int B, Hkv, L, n;
+  int keep_first, keep_last;
+  int start;
+  const int* starts;           // optional device [B] ...
+  const int* lens;             // ... and row counts (else L)
+  int kv_cap;
+  int blocks_per_plane;        // boxes per (batch, KV head), or per (page, KV head)
+  int max_blocks;              // blocks of the longest row the call can hold
+  const int* block_table;
+  int pages_per_seq, num_pages;
+  uint32_t* err;
+};
+cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s);
+
 cudaError_t launch_wait_probe(uint32_t* err, unsigned long long limit_ns, cudaStream_t s);
 
 }  // namespace kb

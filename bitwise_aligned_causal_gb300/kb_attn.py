@@ -31,6 +31,7 @@ KB_ERR_TIMEOUT = 4
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_N = ctypes.POINTER(ctypes.c_longlong)
 _SIGS = {
     "kb_attn_prefill": [_P, _P, _P, _P, _I, _I, _I, _I, _P],
     "kb_attn_chunk": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P],
@@ -48,6 +49,12 @@ _SIGS = {
     "kb_attn_seg_workspace_bytes": [_I, _I, _I, _I, _I],
     "kb_attn_decode_seg_static": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P],
     "kb_attn_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P],
+    "kb_attn_rope_table": [_P, _I, _I, _P, _P],
+    "kb_attn_rope": [_P, _N, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P],
+    "kb_attn_append": [_P, _P, _P, _N, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I,
+                       _P],
+    "kb_attn_block_boxes": [_P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_select_blocks": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
     "kb_status_string": [_I],
     "kb_contract_version": [],
     "kb_attn_last_cuda_error": [],
@@ -153,6 +160,33 @@ def kb_attn_decode_seg_static(q, k, v, o, B, Hq, Hkv, ctx_len, kv_cap, seg_tiles
 
 def kb_attn_seg_workspace_bytes(B, Hq, L, start, seg_tiles) -> int:
     return int(_lib.kb_attn_seg_workspace_bytes(B, Hq, L, start, seg_tiles))
+
+
+def kb_attn_rope_table(table, n_pos, rot_dim, inv_freq, stream=None) -> int:
+    return _lib.kb_attn_rope_table(table, n_pos, rot_dim, inv_freq, stream)
+
+
+def kb_attn_rope(x, strides, out, table, n_pos, rot_dim, interleaved, inverse, B, H, L, start, stream=None) -> int:
+    return _lib.kb_attn_rope(x, strides, out, table, n_pos, rot_dim, interleaved, inverse, B, H, L, start, stream)
+
+
+def kb_attn_append(q, k, v, strides, q_out, k_cache, v_cache, boxes, table, n_pos, rot_dim, interleaved, B, Hq, Hkv, L,
+                   start, starts, lens, kv_cap, block_table, pages_per_seq, page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_append(q, k, v, strides, q_out, k_cache, v_cache, boxes, table, n_pos, rot_dim, interleaved, B,
+                               Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq, page_size,
+                               num_pages, stream)
+
+
+def kb_attn_block_boxes(k_cache, boxes, B, Hkv, kv_len, kv_lens, kv_cap, block_table, pages_per_seq, page_size,
+                        num_pages, stream=None) -> int:
+    return _lib.kb_attn_block_boxes(k_cache, boxes, B, Hkv, kv_len, kv_lens, kv_cap, block_table, pages_per_seq,
+                                    page_size, num_pages, stream)
+
+
+def kb_attn_select_blocks(q, boxes, blocks, B, Hq, Hkv, L, n_select, keep_first, keep_last, start, starts, lens,
+                          n_blocks, block_table, pages_per_seq, page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_select_blocks(q, boxes, blocks, B, Hq, Hkv, L, n_select, keep_first, keep_last, start, starts,
+                                      lens, n_blocks, block_table, pages_per_seq, page_size, num_pages, stream)
 
 
 def kb_attn_check_device_status(stream=None) -> int:
@@ -459,3 +493,172 @@ def decode_seg_static(q, k, v, ctx_len, seg_tiles, out=None, stream=None, check=
                                       int(ctx_len), cap, int(seg_tiles), _stream(stream)),
             "kb_attn_decode_seg_static", check, stream)
     return o
+
+
+# ------------------------------------------------ rotation, cache append, block selection
+
+def _check_view(t, name):
+    """A [*, *, *, 128] view whose last dimension is contiguous: slices of a fused projection need no copy."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions [batch, heads, seq, head_dim]")
+    if t.stride(3) != 1 or t.stride(0) % 8 or t.stride(1) % 8 or t.stride(2) % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have a contiguous last dimension, strides that are multiples of 8 and 16-byte "
+                         f"alignment, got strides {t.stride()}")
+    _on_current_device(t, name)
+
+
+def _strides(*tensors):
+    return (ctypes.c_longlong * (3 * len(tensors)))(*(x for t in tensors for x in
+                                                      ((0, 0, 0) if t is None else t.stride()[:3])))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _optional(check, *pairs):
+    for t, name in pairs:
+        if t is not None:
+            check(t, name)
+
+
+def _check_boxes(t, name):
+    _check(t, name, ndim=5)
+
+
+def rope_table(n_pos, rot_dim=128, theta=10000.0, inv_freq=None, device=None, stream=None):
+    """Cosines and sines of position * inv_freq for positions 0..n_pos-1: float32 [n_pos, rot_dim/2, 2].  inv_freq
+    (float64 [rot_dim/2]) defaults to theta ** (-2 i / rot_dim); angles are formed in 64 bits."""
+    torch = _torch()
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if inv_freq is None:
+        inv_freq = float(theta) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    if inv_freq.dim() != 1 or 2 * inv_freq.numel() != rot_dim:
+        raise ValueError(f"inv_freq must have shape ({rot_dim // 2},), got {tuple(inv_freq.shape)}")
+    inv_freq = inv_freq.to(device=device, dtype=torch.float64).contiguous()
+    table = torch.empty((int(n_pos), rot_dim // 2, 2), dtype=torch.float32, device=device)
+    shapes.rope_table(table.shape)
+    _on_current_device(table, "table")
+    _raise(kb_attn_rope_table(table.data_ptr(), int(n_pos), int(rot_dim), inv_freq.data_ptr(), _stream(stream)),
+           "kb_attn_rope_table")
+    return table
+
+
+def rope(x, table, start=0, inverse=False, interleaved=False, out=None, stream=None, check=False):
+    """Rotate x [B,H,L,128] (any strides, last dimension contiguous) by its positions start..start+L-1; inverse=True
+    rotates by the negative angle, which turns the gradient of the result into the gradient of x."""
+    _check_view(x, "x")
+    _check_f32(table, "table")
+    _optional(_check, (out, "out"))
+    B, H, L, n_pos, rot_dim = shapes.rope(x.shape, table.shape, start, None if out is None else out.shape)
+    o = _torch().empty((B, H, L, 128), dtype=x.dtype, device=x.device) if out is None else out
+    _finish(kb_attn_rope(x.data_ptr(), _strides(x), o.data_ptr(), table.data_ptr(), n_pos, rot_dim, int(interleaved),
+                         int(inverse), B, H, L, int(start), _stream(stream)), "kb_attn_rope", check, stream)
+    return o
+
+
+def _append(q, k, v, k_cache, v_cache, table, start, starts, lens, block_table, boxes, interleaved, out, stream, check):
+    for t, n in ((k, "k"), (v, "v")):
+        _check_view(t, n)
+    _optional(_check_view, (q, "q"))
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, n)
+    _optional(_check_f32, (table, "table"))
+    _optional(_check_i32, (starts, "starts"), (lens, "lens"), (block_table, "block_table"))
+    _optional(_check_boxes, (boxes, "boxes"))
+    _optional(_check, (out, "out"))
+    shape = [None if t is None else t.shape for t in (q, k, v, k_cache, v_cache, table, boxes, block_table, out)]
+    B, Hq, Hkv, L, cap, num_pages, page, pps, n_pos, rot_dim = shapes.append(*shape)
+    shapes.per_sequence(B, starts=starts if starts is None else starts.shape, lens=lens if lens is None else lens.shape)
+    if starts is None and not 0 <= start <= cap - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
+    if starts is None and table is not None and start > n_pos - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the table's 0..{n_pos - 1}")
+    if q is not None and out is None:
+        out = _torch().empty((B, Hq, L, 128), dtype=q.dtype, device=q.device)
+    _finish(kb_attn_append(_ptr(q), k.data_ptr(), v.data_ptr(), _strides(q, k, v), _ptr(out), k_cache.data_ptr(),
+                           v_cache.data_ptr(), _ptr(boxes), _ptr(table), n_pos, rot_dim, int(interleaved), B, Hq, Hkv,
+                           L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
+                           _stream(stream)), "kb_attn_append", check, stream)
+    return out
+
+
+def append(q, k, v, k_cache, v_cache, table, start, boxes=None, interleaved=False, out=None, stream=None, check=False):
+    """Append k, v [B,Hkv,L,128] to caches [B,Hkv,cap,128] at positions start..start+L-1, k and q [B,Hq,L,128]
+    rotated by them (table from rope_table, None: not rotated), and widen the boxes of the touched key blocks.
+    Returns the rotated q, contiguous (None without q).  q, k, v may be slices of one fused projection."""
+    return _append(q, k, v, k_cache, v_cache, table, int(start), None, None, None, boxes, interleaved, out, stream,
+                   check)
+
+
+def append_varlen(q, k, v, k_cache, v_cache, table, starts, lens=None, block_table=None, boxes=None, interleaved=False,
+                  out=None, stream=None, check=False):
+    """append with a start (and row count, default all rows) per sequence, int32 [B] on the device; with block_table
+    [B,pages_per_seq] the caches are pools [num_pages,Hkv,page_size,128].  Rows of the result from lens[b] on are left
+    as they were."""
+    if starts is None:
+        raise TypeError("starts must be a contiguous int32 CUDA tensor")
+    return _append(q, k, v, k_cache, v_cache, table, 0, starts, lens, block_table, boxes, interleaved, out, stream,
+                   check)
+
+
+def block_boxes(k, kv_len=None, kv_lens=None, block_table=None, boxes=None, stream=None, check=False):
+    """Boxes (upper and lower bound per channel) of the blocks of 128 keys of a cache [B,Hkv,cap,128], or of pools with
+    block_table: of its first kv_len keys (default: all), or kv_lens[b] of sequence b.  Returns bf16
+    [B or num_pages, Hkv, blocks, 2, 128]; blocks beyond are zero in a new tensor and left as they were in `boxes`."""
+    torch = _torch()
+    _check(k, "k")
+    _optional(_check_i32, (kv_lens, "kv_lens"), (block_table, "block_table"))
+    _optional(_check_boxes, (boxes, "boxes"))
+    B, Hkv, cap, num_pages, page, pps, box = shapes.block_boxes(
+        k.shape, None if block_table is None else block_table.shape, None if boxes is None else boxes.shape)
+    shapes.per_sequence(B, kv_lens=None if kv_lens is None else kv_lens.shape)
+    kv_len = cap if kv_len is None else int(kv_len)
+    if not 1 <= kv_len <= cap:
+        raise ValueError(f"kv_len must lie in 1..{cap} (the cache capacity), got {kv_len}")
+    if boxes is None:
+        boxes = torch.zeros(box, dtype=torch.bfloat16, device=k.device)
+    _finish(kb_attn_block_boxes(k.data_ptr(), boxes.data_ptr(), B, Hkv, kv_len, _ptr(kv_lens), cap, _ptr(block_table),
+                                pps, page, num_pages, _stream(stream)), "kb_attn_block_boxes", check, stream)
+    return boxes
+
+
+def _select(q, boxes, start, starts, lens, n, keep_first, keep_last, block_table, out, stream, check):
+    torch = _torch()
+    _check(q, "q")
+    _check_boxes(boxes, "boxes")
+    _optional(_check_i32, (starts, "starts"), (lens, "lens"), (block_table, "block_table"), (out, "out"))
+    B, Hq, Hkv, L, per_plane, num_pages, page, pps = shapes.select(
+        q.shape, boxes.shape, n, keep_first, keep_last, None if block_table is None else block_table.shape,
+        None if out is None else out.shape)
+    shapes.per_sequence(B, starts=starts if starts is None else starts.shape, lens=lens if lens is None else lens.shape)
+    if starts is None and not 0 <= start <= per_plane * shapes.BLOCK - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the boxes' 0..{per_plane * shapes.BLOCK - 1}")
+    if out is None:
+        out = torch.empty((B, Hkv, L, n), dtype=torch.int32, device=q.device)
+    _finish(kb_attn_select_blocks(q.data_ptr(), boxes.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, n, keep_first,
+                                  keep_last, start, _ptr(starts), _ptr(lens), per_plane, _ptr(block_table), pps, page,
+                                  num_pages, _stream(stream)), "kb_attn_select_blocks", check, stream)
+    return out
+
+
+def select_blocks(q, boxes, start, n, keep_first=1, keep_last=1, out=None, stream=None, check=False):
+    """The n key blocks each row of q [B,Hq,L,128] (positions start..) attends to, by the boxes [B,Hkv,blocks,2,128]
+    of the keys: int32 [B,Hkv,L,n], ascending, -1 behind the last.  The first keep_first and last keep_last of a row's
+    blocks are always taken."""
+    return _select(q, boxes, int(start), None, None, int(n), int(keep_first), int(keep_last), None, out, stream, check)
+
+
+def select_blocks_varlen(q, boxes, starts, n, lens=None, block_table=None, keep_first=1, keep_last=1, out=None,
+                         stream=None, check=False):
+    """select_blocks with a start (and row count) per sequence, int32 [B] on the device, and optionally the boxes of
+    paged pools [num_pages,Hkv,page_size/128,2,128] with block_table [B,pages_per_seq].  Rows from lens[b] on are left
+    as they were."""
+    if starts is None:
+        raise TypeError("starts must be a contiguous int32 CUDA tensor")
+    return _select(q, boxes, 0, starts, lens, int(n), int(keep_first), int(keep_last), block_table, out, stream, check)

@@ -272,6 +272,110 @@ kb_status kb_attn_backward(const void* q, const void* k, const void* v, const vo
                            int B, int Hq, int Hkv, int S, void* stream);
 
 /*
+ * Position rotation (rotary embedding).  A row of 128 values at position p is
+ * turned in rot_dim/2 planes; plane i holds values i and i + rot_dim/2 (or,
+ * with interleaved != 0, values 2i and 2i+1) and turns by p * inv_freq[i]:
+ *   a' = a cos - b sin,  b' = b cos + a sin   (fp32, rounded to bf16 once);
+ * values from rot_dim on pass unchanged.  Without a paper counterpart: the
+ * pages' attention takes queries and keys that are already turned.
+ *
+ * kb_attn_rope_table fills table [n_pos, rot_dim/2, 2] fp32 (16-byte aligned)
+ * with (cos, sin) of p * inv_freq[i], angles formed in 64 bits; inv_freq is a
+ * device array of rot_dim/2 doubles.  rot_dim: a multiple of 16 up to 128.
+ *
+ * kb_attn_rope turns x [B, H, L, 128] at positions start..start+L-1 (all
+ * below n_pos) into contiguous out [B, H, L, 128].  strides: host array of
+ * x's batch, head and row strides in elements (multiples of 8; the last
+ * dimension is contiguous).  out may be x itself when x is contiguous, and
+ * must not overlap it otherwise.  inverse != 0 turns by the negative angle,
+ * which is the gradient of the rotation (dx from dout).
+ */
+kb_status kb_attn_rope_table(float* table, int n_pos, int rot_dim, const double* inv_freq, void* stream);
+kb_status kb_attn_rope(const void* x, const long long* strides, void* out, const float* table, int n_pos,
+                       int rot_dim, int interleaved, int inverse, int B, int H, int L, int start,
+                       void* stream);
+
+/*
+ * Append L new positions per sequence to a KV cache: turns q and k by their
+ * positions, writes k and v into the cache, q into q_out, and widens the
+ * boxes of the key blocks that the new keys fall into.
+ *   q       : [B, Hq, L, 128], k, v: [B, Hkv, L, 128] bf16 views; strides is a
+ *             host array of nine: q's batch, head and row strides in elements,
+ *             then k's, then v's (multiples of 8, last dimension contiguous),
+ *             so slices of one fused projection need no copy.  q and q_out may
+ *             be NULL together.
+ *   q_out   : [B, Hq, L, 128] contiguous
+ *   k_cache,
+ *   v_cache : block_table == NULL: [B, Hkv, kv_cap, 128], else pools
+ *             [num_pages, Hkv, page_size, 128] as in kb_attn_chunk_paged
+ *   boxes   : NULL, or bf16 [B, Hkv, ceil(kv_cap/128), 2, 128], or with a page
+ *             table [num_pages, Hkv, page_size/128, 2, 128]: per block of 128
+ *             keys the upper and lower bound of every channel (see
+ *             kb_attn_block_boxes)
+ *   table   : from kb_attn_rope_table, or NULL (no rotation)
+ *   start   : position of row 0 of every sequence when starts is NULL
+ *   starts,
+ *   lens    : NULL, or device int32 [B]: row i < lens[b] (L rows when lens is
+ *             NULL) of sequence b goes to position starts[b] + i; rows from
+ *             lens[b] on are neither read nor written
+ * A block whose first key is among the new ones gets a new box; any other
+ * touched block's box is widened, so keys overwritten inside a block leave
+ * their old bounds in its box until kb_attn_block_boxes makes it anew.
+ * Keys, queries and boxes have the same bits for any split of a sequence into
+ * appends.  No two sequences may append to the same page.  Out-of-range
+ * starts, lens or page indices are found on the device: that sequence (or
+ * block) is not written and the next kb_attn_check_device_status returns
+ * KB_ERR_INVALID_ARG.
+ */
+kb_status kb_attn_append(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
+                         void* k_cache, void* v_cache, void* boxes, const float* table, int n_pos,
+                         int rot_dim, int interleaved, int B, int Hq, int Hkv, int L, int start,
+                         const int* starts, const int* lens, int kv_cap, const int* block_table,
+                         int pages_per_seq, int page_size, int num_pages, void* stream);
+
+/*
+ * Boxes of the blocks of a cache's first kv_len keys (kv_lens[b] of sequence
+ * b when kv_lens is not NULL, each in 0..kv_len).  With E the smallest
+ * integer in -100..100 for which the block's largest |key| is at most
+ * 127 * 2^(E-7), the upper bound of a channel is ceil(max 2^(7-E)) 2^(E-7)
+ * and the lower one floor(min 2^(7-E)) 2^(E-7).  Layouts as in kb_attn_append;
+ * boxes of blocks beyond are left as they were.  Keys are finite (infinities
+ * saturate, a NaN does not count).
+ */
+kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, int kv_len,
+                              const int* kv_lens, int kv_cap, const int* block_table, int pages_per_seq,
+                              int page_size, int num_pages, void* stream);
+
+/* Most blocks a row can choose. */
+#define KB_MAX_SELECT 128
+
+/*
+ * Choose the key blocks that each query row attends to (one list per row and
+ * KV head, shared by its four query heads).
+ *   q      : [B, Hq, L, 128] bf16 contiguous, turned; row i at position start
+ *            + i, or starts[b] + i for i < lens[b] (as in kb_attn_append)
+ *   boxes  : block_table == NULL: [B, Hkv, n_blocks, 2, 128], else
+ *            [num_pages, Hkv, page_size/128, 2, 128]
+ *   blocks : int32 [B, Hkv, L, n_select] (output): ascending block indices,
+ *            -1 behind the last; rows from lens[b] on are left as they were
+ * A row at position p has the blocks 0 .. p/128.  The first keep_first and the
+ * last keep_last >= 1 of them (the last holds the row's own key) are always
+ * taken, the others by score until n_select are taken, ties to the lowest
+ * block.  Score: t_h = rint(q_h 2^(15-E)) of the group's four heads with their
+ * common E (as for a box), u = sum_h t_h, n = rint(u 2^(7-E')) with E' that of
+ * u, score = sum_d max(n_d upper_d, n_d lower_d).  Every step is exact, so the
+ * choice does not depend on the batch, the split or the kernel.
+ * keep_first + keep_last <= n_select <= KB_MAX_SELECT.  Out-of-range starts or
+ * lens are found on the device (that sequence's rows are not written), as are
+ * page indices (the row's list is then any list within its blocks); the next
+ * kb_attn_check_device_status returns KB_ERR_INVALID_ARG.
+ */
+kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, int B, int Hq, int Hkv, int L,
+                                int n_select, int keep_first, int keep_last, int start, const int* starts,
+                                const int* lens, int n_blocks, const int* block_table, int pages_per_seq,
+                                int page_size, int num_pages, void* stream);
+
+/*
  * Prefill/chunk with an explicit kernel shape, for tests of the contract:
  * q_tiles_per_cta = 3 runs the tile kernel (one 128-row query tile per CTA,
  * one CTA per SM, three score buffers, so Q K^T of later key tiles overlaps
