@@ -199,7 +199,12 @@ __device__ __forceinline__ float row_softmax_tile(const uint32_t (&s)[128], int 
 // same order as the single-thread tree, so the bits are the same; p[r] is the
 // bf16 pair of keys 8r+2u, 8r+2u+1 (TMEM column 4r+u of P).  All 32 lanes of
 // the warp must call it together.
-template <bool kMasked>
+//
+// kMaybeNone: the row may see none of the tile's keys (n_valid <= 0, masked
+// tiles of block-sparse attention).  Such a tile leaves the state as it was
+// and gives p = 0: -inf scores never move m, and while m is still -inf the
+// exponent takes 0 in its place, since -inf + inf has no value.
+template <bool kMasked, bool kMaybeNone = false>
 __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, int n_valid, RowState& st,
                                                        uint32_t (&p)[16]) {
   const float c = score_scale_log2();
@@ -231,7 +236,8 @@ __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, in
     st.mc = mc_new;
   }
   const float2 c2 = make_float2(c, c);
-  const float2 nmc2 = make_float2(-st.mc, -st.mc);
+  const float nmc = (kMaybeNone && st.m == -INFINITY) ? 0.0f : -st.mc;
+  const float2 nmc2 = make_float2(nmc, nmc);
   float2 acc;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {

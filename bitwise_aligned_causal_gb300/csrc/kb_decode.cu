@@ -53,7 +53,7 @@
 
 namespace kb {
 
-template <bool kWide, int kNumSBufs>
+template <bool kWide, int kNumSBufs, bool kSparse = false>
 struct PackedCfg {
   static constexpr int kSoftmaxWarps = kWide ? 4 : 1;
   static constexpr int kKProdWarp = kWide ? 4 : 1;
@@ -98,7 +98,11 @@ struct PackedCfg {
   static constexpr uint32_t kStatsOff = kMiscOff + 16u;      // narrow: float2 (m, l) of rows 0..7
   // narrow: the rest of shared memory holds the segment partials a
   // non-first CTA of a cluster leaves for the first one
-  static constexpr uint32_t kPartOff = (kStatsOff + 64u + 15u) & ~15u;
+  // sparse: before them the row's walk (listed key blocks, ascending) and the
+  // walk's first entry of each segment
+  static constexpr uint32_t kWalkOff = (kStatsOff + 64u + 15u) & ~15u;
+  static constexpr uint32_t kSegFirstOff = kWalkOff + (kSparse ? KB_MAX_SELECT * 4u : 0u);
+  static constexpr uint32_t kPartOff = (kSegFirstOff + (kSparse ? (KB_MAX_SELECT + 1u) * 4u : 0u) + 15u) & ~15u;
   static constexpr uint32_t kSmemCap = 227u * 1024u - 1024u;   // usable once the base is 1 KB aligned
   static constexpr uint32_t kPartBytes = kWide ? 0u : ((kSmemCap - kPartOff) & ~15u);
   static constexpr uint32_t kSmemUsed = kPartOff + kPartBytes;
@@ -106,8 +110,9 @@ struct PackedCfg {
 };
 
 // Partials a narrow CTA can hold in shared memory, for n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows) {
-  return PackedCfg<false, 3>::kPartBytes / (static_cast<uint32_t>(n_rows) * kPartFloats * 4u);
+uint32_t packed_partial_slots(int n_rows, bool sparse) {
+  return (sparse ? PackedCfg<false, 3, true>::kPartBytes : PackedCfg<false, 3>::kPartBytes) /
+         (static_cast<uint32_t>(n_rows) * kPartFloats * 4u);
 }
 
 __device__ __forceinline__ void packed_drain_wait(uint32_t bar, uint32_t parity) {
@@ -142,11 +147,60 @@ __device__ __forceinline__ bool kv_tile_coords(const PackedArgs& a, int b, int g
 // blocks (ceil(c ns / C)): rank 0 always gets at least one segment.
 __device__ __forceinline__ int seg_block_start(int c, int ns, int C) { return (c * ns + C - 1) / C; }
 
-template <bool kWide, int kNumSBufs>
-__global__ void __launch_bounds__(PackedCfg<kWide, kNumSBufs>::kThreads, 1)
+// The walk of a block-sparse token: its listed blocks up to `own`, ascending,
+// each once, and where each C5 segment of the walk starts.  Every thread of
+// the CTA calls it; returns {entries, segments}.  An index out of range is
+// recorded.
+__device__ __forceinline__ int2 build_walk(const int* list, int n_select, int own, int n_cap, int* walk, int* seg_first,
+                                           uint32_t* err) {
+  const int t = static_cast<int>(threadIdx.x);       // the CTA has more threads than KB_MAX_SELECT
+  constexpr int kDropped = 0x7FFFFFFF;
+  int mine = kDropped;
+  if (t < n_select) {
+    const int j = __ldg(list + t);
+    if (j < -1 || j >= n_cap) atomicCAS(err, 0u, static_cast<uint32_t>(kDevBadInput));
+    else if (j >= 0 && j <= own) mine = j;
+    walk[t] = mine;
+  }
+  __syncthreads();
+  // lists from the block choice are ascending and close with their dropped
+  // entries; any other order is ranked
+  const bool in_place = t >= n_select || t == 0 || walk[t - 1] < mine || mine == kDropped;
+  int at = t;
+  if (!__syncthreads_and(in_place)) {
+    bool once = mine != kDropped;
+    for (int i = 0; once && i < t; ++i) once = walk[i] != mine;
+    __syncthreads();
+    if (t < n_select && !once) walk[t] = mine = kDropped;
+    __syncthreads();
+    at = 0;
+    if (mine != kDropped)
+      for (int i = 0; i < n_select; ++i) at += walk[i] < mine ? 1 : 0;
+    __syncthreads();
+    if (mine != kDropped) walk[at] = mine;
+  }
+  const int n = __syncthreads_count(mine != kDropped);
+  const bool starts = t < n && (t == 0 || walk[t - 1] / kSegTiles != walk[t] / kSegTiles);
+  if (starts) {
+    int s = 0;
+    for (int i = 1; i <= t; ++i) s += walk[i - 1] / kSegTiles != walk[i] / kSegTiles ? 1 : 0;
+    seg_first[s] = t;
+  }
+  const int ns = __syncthreads_count(starts);
+  if (t == 0) seg_first[ns] = n;
+  __syncthreads();
+  return make_int2(n, ns);
+}
+
+// kSparse (narrow, one query row per head): the row's key tiles are those of
+// its block list instead of 0..floor(p/128); its segments are the contract's
+// segments of which it lists a tile.
+template <bool kWide, int kNumSBufs, bool kSparse>
+__global__ void __launch_bounds__(PackedCfg<kWide, kNumSBufs, kSparse>::kThreads, 1)
 kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const PackedArgs args) {
-  using Cfg = PackedCfg<kWide, kNumSBufs>;
+  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse>;
+  static_assert(!kSparse || (!kWide && Cfg::kThreads > KB_MAX_SELECT), "sparse walks are narrow");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
@@ -203,12 +257,31 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   if (r1 - r0 <= 0) active = false;                     // the chunk does not reach a second tile
   const int n_rows = kGroup * Lc;                       // packed rows in use
   const int n_kv = (pos0 + r1 - 1) / kTileKeys + 1;     // C1: KV tiles 0..floor(last position / 128)
+  int* walk = reinterpret_cast<int*>(smem + Cfg::kWalkOff);
+  int* seg_first = reinterpret_cast<int*>(smem + Cfg::kSegFirstOff);
+  int2 walked = make_int2(0, 0);                        // sparse: entries and segments of the walk
+  if constexpr (kSparse) {
+    if (active)
+      walked = build_walk(args.blocks + (static_cast<size_t>(b) * args.Hkv + g) * args.n_select, args.n_select, n_kv - 1,
+                          (args.max_ctx + kTileKeys - 1) / kTileKeys, walk, seg_first, args.err);
+    if (active && walked.x == 0) {
+      // nothing listed: the rows are zero
+      if (rank == 0 && threadIdx.x < kGroup * 16)
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.o) +
+                                 (static_cast<size_t>(b) * args.Hq + g * kGroup) * kHeadDim)[threadIdx.x] =
+            make_uint4(0u, 0u, 0u, 0u);
+      active = false;
+    }
+  }
   // the tiles this CTA runs: one C5 segment (workspace mode) or a contiguous
   // block of segments (fold mode)
   const int seg_len = ws_mode ? args.seg_tiles : args.fold_seg;
-  const int ns = (n_kv + seg_len - 1) / seg_len;        // segments of the sub-chunk's rows
-  int j0, j1;
-  if (ws_mode) {
+  const int ns = kSparse ? walked.y : (n_kv + seg_len - 1) / seg_len;   // segments of the sub-chunk's rows
+  int j0, j1;                                           // tiles, or (sparse) entries of the walk
+  if constexpr (kSparse) {
+    j0 = active ? seg_first[seg_block_start(rank, ns, C)] : 0;
+    j1 = active ? seg_first[seg_block_start(rank + 1, ns, C)] : 0;
+  } else if (ws_mode) {
     j0 = seg_ws * seg_len;
     j1 = min(n_kv, j0 + seg_len);
   } else {
@@ -217,7 +290,12 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   if (j0 >= j1) active = false;
   const int nt = active ? j1 - j0 : 0;
-  const bool has_last = (j1 == n_kv);
+  // does this CTA run the row's own (last) tile?
+  const bool has_last = kSparse ? (nt > 0 && j1 == walked.x && walk[j1 - 1] == n_kv - 1) : (j1 == n_kv);
+  auto tile_at = [&](int jj) { return kSparse ? walk[j0 + jj] : j0 + jj; };     // key tile of this CTA's step jj
+  // sparse: is step jj the first or the last of its segment?
+  auto starts_seg = [&](int jj) { return jj == 0 || walk[j0 + jj - 1] / kSegTiles != walk[j0 + jj] / kSegTiles; };
+  auto ends_seg = [&](int jj) { return jj == nt - 1 || walk[j0 + jj + 1] / kSegTiles != walk[j0 + jj] / kSegTiles; };
   const bool zero_tail = (args.block_table != nullptr) || (args.ctx_lens != nullptr) || (args.starts != nullptr);
   const int tail_from = seq_kv - (n_kv - 1) * kTileKeys;   // first V row of the last tile past the sequence
   const uint32_t slot_bytes = static_cast<uint32_t>(n_rows) * kPartFloats * 4u;
@@ -312,7 +390,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         const int slot = jj % Cfg::kStages;
         const uint32_t use = jj / Cfg::kStages;
         int row = 0, plane = 0;
-        if (lane == 0) kv_tile_coords(args, b, g, j0 + jj, row, plane);
+        if (lane == 0) kv_tile_coords(args, b, g, tile_at(jj), row, plane);
         if (jj == Cfg::kStages) ok = no_error(args.err, abort_flag);   // the first loads are in flight
         if (ok && jj >= Cfg::kStages)
           ok = mbar_wait(bar(empty0 + slot), (use - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
@@ -401,7 +479,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           ok = mbar_wait(bar(Cfg::kBarVReady), 0, abort_flag, args.err, kDevTimeoutTma);
         else
           ok = mbar_wait(bar(Cfg::kBarVFull + slot), (j / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
-        const bool first = (js == 0);
+        const bool first = kSparse ? starts_seg(j) : (js == 0);
         if (++js == seg_len) js = 0;
         if (ok && first && F > 0)
           ok = mbar_wait(bar(Cfg::kBarORead), (F - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
@@ -660,8 +738,10 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     };
 
     int G = 0;
-    for (int jb = 0; jb < nt && ok; jb += seg_len, ++G) {
-      const int t_last = min(nt, jb + seg_len) - 1;           // local index of the segment's last tile
+    for (int jb = 0; jb < nt && ok; ++G) {
+      // local index of the segment's last tile
+      const int t_last = (kSparse ? seg_first[my_first + G + 1] - j0 : min(nt, jb + seg_len)) - 1;
+      jb = t_last + 1;
       // the stats are written after P(t_last), so P V(t_last - 3) is done and
       // the wait on P V(t_last) below is within one phase of its barrier
       ok = mbar_wait_idle(bar(Cfg::kBarStFull), G & 1, abort_flag, args.err, kDevTimeoutSoftmax, 128);
@@ -835,10 +915,10 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           x[16 + 2 * q + 1] = __uint_as_float(v1[4 * q + 1]);
         }
       }
-      const int jt = j0 + j;
-      const bool seg_start = (js == 0);
+      const int jt = tile_at(j);
+      const bool seg_start = kSparse ? starts_seg(j) : (js == 0);
       if (++js == seg_len) js = 0;
-      const bool seg_end = (js == 0) || (j == nt - 1);
+      const bool seg_end = kSparse ? ends_seg(j) : ((js == 0) || (j == nt - 1));
       if (seg_start) st = row_state_init();
       uint32_t p[16];
       const float alpha = (jt == n_kv - 1) ? row_softmax_tile_quad<true>(x, u, pos - jt * kTileKeys + 1, st, p)
@@ -899,7 +979,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const int r = threadIdx.x >> 4;
     const int cb = threadIdx.x & 15;
     bool ok = mbar_wait_cluster(bar(Cfg::kBarPart), 0, abort_flag, args.err, kDevTimeoutSoftmax);
-    ok = ok && (*abort_flag == 0);
+    ok = ok && run && (*abort_flag == 0);        // no rows (a bad context, an empty list): nothing to fold
     if (ok && r < n_rows) {
       const float* slots = reinterpret_cast<const float*>(smem + (push ? Cfg::kPartOff : Cfg::kKOff));
       const float* own = reinterpret_cast<const float*>(smem + Cfg::kPartOff);
@@ -956,17 +1036,17 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
 }
 
-template <bool kWide, int kNumSBufs>
+template <bool kWide, int kNumSBufs, bool kSparse = false>
 static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub,
                                    cudaStream_t s) {
-  using Cfg = PackedCfg<kWide, kNumSBufs>;
+  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse>;
   static_assert(Cfg::kSmemBytes <= 227u * 1024u, "shared memory budget");
   static int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(kb_decode_kernel<kWide, kNumSBufs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kb_decode_kernel<kWide, kNumSBufs, kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Cfg::kSmemBytes));
     if (e != cudaSuccess) return e;
     configured_device = dev;
@@ -975,7 +1055,7 @@ static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv,
   const int C = ws_mode ? 1 : a.cluster;
   const unsigned grid = static_cast<unsigned>((ws_mode ? a.n_seg : C) * n_sub * a.B * a.Hkv);
   if (C <= 1) {
-    kb_decode_kernel<kWide, kNumSBufs><<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
+    kb_decode_kernel<kWide, kNumSBufs, kSparse><<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
@@ -990,7 +1070,7 @@ static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kb_decode_kernel<kWide, kNumSBufs>, tk, tv, a);
+  e = cudaLaunchKernelEx(&cfg, kb_decode_kernel<kWide, kNumSBufs, kSparse>, tk, tv, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1000,19 +1080,20 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
   // narrow when at most 8 rows are packed (two query rows per head); wide
   // chunks fold their segments in TMEM (two S buffers) unless the partials
   // go to a workspace
+  if (a.blocks != nullptr) return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
   if (a.L <= 2) return launch_packed_t<false, 3>(tk, tv, a, n_sub, s);
   if (a.part != nullptr) return launch_packed_t<true, 3>(tk, tv, a, n_sub, s);
   return launch_packed_t<true, 2>(tk, tv, a, n_sub, s);
 }
 
-// How many clusters of 2, 4 and 8 CTAs of the narrow packed kernel the
-// current device runs at once (0 when it runs none): a cluster needs that
+// How many clusters of 2, 4 and 8 CTAs of the narrow packed kernel (the
+// block-sparse one has the same shape) the current device runs at once (0 when it runs none): a cluster needs that
 // many SMs of one GPC free together, so large clusters fit fewer times than
 // the SM count suggests.
 void packed_cluster_capacity(int (&active)[4]) {
   using Cfg = PackedCfg<false, 3>;
   for (int i = 0; i < 4; ++i) active[i] = 0;
-  if (cudaFuncSetAttribute(kb_decode_kernel<false, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(kb_decode_kernel<false, 3, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(Cfg::kSmemBytes)) != cudaSuccess) {
     (void)cudaGetLastError();
     return;
@@ -1030,7 +1111,7 @@ void packed_cluster_capacity(int (&active)[4]) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kb_decode_kernel<false, 3>, &cfg) == cudaSuccess) active[i] = n;
+    if (cudaOccupancyMaxActiveClusters(&n, kb_decode_kernel<false, 3, false>, &cfg) == cudaSuccess) active[i] = n;
     else (void)cudaGetLastError();
   }
 }

@@ -388,6 +388,7 @@ kb_status host_device(HostDevice* out) {
   out->index = static_cast<int>(st - g_dev);
   out->err = st->err;
   out->sm_count = st->sm_count;
+  out->cluster_fit = st->cluster_fit;
   return KB_OK;
 }
 

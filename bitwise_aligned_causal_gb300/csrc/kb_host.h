@@ -19,6 +19,7 @@ struct HostDevice {
   int index;
   uint32_t* err;       // the library's error word there
   int sm_count;
+  const int* cluster_fit;   // clusters of 2, 4, 8 narrow packed CTAs it runs at once (entries 1, 2, 3)
 };
 
 kb_status host_device(HostDevice* out);

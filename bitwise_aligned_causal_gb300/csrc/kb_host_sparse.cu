@@ -4,12 +4,14 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/kb_attn.h"
 #include "kb_contract.cuh"
 #include "kb_host.h"
 #include "kb_launch.h"
+#include "kb_sparse.cuh"
 
 namespace {
 
@@ -61,6 +63,129 @@ kb_status cache_rows(int* cap, int kv_cap, const int* block_table, int pages_per
   if (kv_cap > kMaxRows) return KB_ERR_UNSUPPORTED;
   *cap = kv_cap;
   return KB_OK;
+}
+
+// Position tiles of 32 that L consecutive positions can touch.
+long long max_tiles32(long long L) { return (L + kb::kUnitRows - 2) / kb::kUnitRows + 1; }
+
+long long align256(long long n) { return (n + 255) / 256 * 256; }
+
+// Workspace of a plan: the walks' lengths, then the walks.
+struct PlanSizes {
+  long long units, cap, bytes;
+};
+PlanSizes plan_sizes(int B, int Hkv, int L, int n_select, long long max_blocks) {
+  PlanSizes p;
+  p.units = static_cast<long long>(B) * Hkv * max_tiles32(L);
+  p.cap = std::min<long long>(static_cast<long long>(kb::kUnitRows) * n_select, max_blocks);
+  p.bytes = align256(p.units * 4) + p.units * p.cap * 8;
+  return p;
+}
+
+struct SparseCall {
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+  const int* blocks;
+  int n_select, B, Hq, Hkv, L, start;
+  const int *starts, *lens;
+  int kv_cap;
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+// Checks that every block-sparse forward makes; *cap gets the cache's positions.
+kb_status check_sparse(const SparseCall& c, int* cap, kb::HostDevice* dev) {
+  if (!c.q || !c.k || !c.v || !c.o || !c.blocks) return KB_ERR_INVALID_ARG;
+  for (const void* p : {c.q, c.k, c.v, static_cast<const void*>(c.o)})
+    if (!host_aligned(p, 16)) return KB_ERR_INVALID_ARG;
+  if (!host_aligned(c.blocks, 4) || !host_aligned(c.lse, 4)) return KB_ERR_INVALID_ARG;
+  kb_status s = kb::host_check_heads(c.B, c.Hq, c.Hkv);
+  if (s != KB_OK) return s;
+  if ((s = check_ragged(c.starts, c.lens)) != KB_OK) return s;
+  if (c.n_select < 1) return KB_ERR_INVALID_ARG;
+  if (c.n_select > KB_MAX_SELECT) return KB_ERR_UNSUPPORTED;
+  if ((s = cache_rows(cap, c.kv_cap, c.block_table, c.pages_per_seq, c.page_size, c.num_pages, c.Hkv)) != KB_OK) return s;
+  if (c.L < 1 || c.L > *cap || (c.starts == nullptr && (c.start < 0 || c.start > *cap - c.L))) return KB_ERR_INVALID_ARG;
+  if (static_cast<long long>(c.B) * c.Hkv * max_tiles32(c.L) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  if ((s = kb::host_device(dev)) != KB_OK) return s;
+  const void* p[] = {c.q, c.k, c.v, c.o, c.lse, c.blocks, c.starts, c.lens, c.block_table, c.workspace};
+  return device_pointers(p, 10);
+}
+
+// K/V maps: a contiguous uniform cache ends at the call's last key (later rows
+// read as zeros), a ragged batch maps the whole cache, a pool its pages.
+kb_status cache_maps(const SparseCall& c, CUtensorMap* tk, CUtensorMap* tv) {
+  const uint64_t row_bytes = kb::kHeadDim * 2u;
+  const bool paged = c.block_table != nullptr;
+  const uint64_t stride_rows = static_cast<uint64_t>(paged ? c.page_size : c.kv_cap);
+  const uint64_t rows = paged || c.starts != nullptr ? stride_rows : static_cast<uint64_t>(c.start) + c.L;
+  const uint64_t planes = static_cast<uint64_t>(paged ? c.num_pages : c.B) * c.Hkv;
+  const kb_status s = kb::host_rows_map(tk, c.k, rows, planes, stride_rows * row_bytes);
+  if (s != KB_OK) return s;
+  return kb::host_rows_map(tv, c.v, rows, planes, stride_rows * row_bytes);
+}
+
+// Units, walks and workspace of a call.
+kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, kb::SparseArgs* a) {
+  a->o = c.o;
+  a->lse = c.lse;
+  a->blocks = c.blocks;
+  a->n_select = c.n_select;
+  a->B = c.B;
+  a->Hq = c.Hq;
+  a->Hkv = c.Hkv;
+  a->L = c.L;
+  a->start = c.start;
+  a->starts = c.starts;
+  a->lens = c.lens;
+  a->kv_cap = cap;
+  a->max_blocks = ((c.starts != nullptr ? cap : c.start + c.L) + kb::kTileKeys - 1) / kb::kTileKeys;
+  a->block_table = c.block_table;
+  a->pages_per_seq = c.pages_per_seq;
+  a->page_size = c.page_size;
+  a->num_pages = c.num_pages;
+  a->err = err;
+  const PlanSizes full = plan_sizes(c.B, c.Hkv, c.L, c.n_select, a->max_blocks);
+  if (c.workspace == nullptr || !host_aligned(c.workspace, 256) || c.workspace_bytes < static_cast<size_t>(full.bytes))
+    return KB_ERR_INVALID_ARG;
+  a->n_tiles = static_cast<int>(c.starts != nullptr ? max_tiles32(c.L)
+                                                    : (c.start + c.L - 1) / kb::kUnitRows - c.start / kb::kUnitRows + 1);
+  a->n_units = c.B * c.Hkv * a->n_tiles;
+  a->walk_cap = static_cast<int>(full.cap);
+  a->walk_len = static_cast<int*>(c.workspace);
+  a->walks = reinterpret_cast<uint2*>(static_cast<char*>(c.workspace) + align256(full.units * 4));
+  return KB_OK;
+}
+
+kb_status sparse_forward(const SparseCall& c, void* stream) {
+  int cap = 0;
+  kb::HostDevice dev;
+  kb_status s = check_sparse(c, &cap, &dev);
+  if (s != KB_OK) return s;
+  kb::SparseArgs a{};
+  if ((s = fill_plan(c, cap, dev.err, &a)) != KB_OK) return s;
+  CUtensorMap tq, tk, tv;
+  if ((s = kb::host_group_map(&tq, c.q, static_cast<uint64_t>(c.L), static_cast<uint64_t>(c.B) * c.Hkv)) != KB_OK) return s;
+  if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
+  cudaError_t e = kb::launch_sparse_plan(a, dev.index, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = kb::launch_sparse_tile(tq, tk, tv, a, dev.index, static_cast<cudaStream_t>(stream));
+  return done(e);
+}
+
+// CTAs per (b, KV head) of a block-sparse token: the largest cluster whose
+// clusters all run at once, when the batch alone would leave SMs idle (the
+// rule of the dense token, with the segments a list can name).
+int sparse_cluster(const kb::HostDevice& dev, int B, int Hkv, int n_select, int max_blocks) {
+  const long long units = static_cast<long long>(B) * Hkv;
+  if (2 * units > dev.sm_count) return 1;
+  const int ns = std::min(n_select, (max_blocks + kb::kSegTiles - 1) / kb::kSegTiles);
+  const long long slots = kb::packed_partial_slots(kb::kGroup, true);
+  for (int i = 3, c = 8; i >= 1; --i, c /= 2)
+    if (c <= ns && units <= dev.cluster_fit[i] && (ns + c - 1) / c <= slots) return c;
+  return 1;
 }
 
 }  // namespace
@@ -240,6 +365,66 @@ kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, i
   a.num_pages = num_pages;
   a.err = dev.err;
   return done(kb::launch_select(a, dev.index, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kb_attn_sparse_workspace_bytes(int B, int Hkv, int L, int n_select, int kv_cap) {
+  if (B < 1 || Hkv < 1 || L < 1 || n_select < 1 || n_select > KB_MAX_SELECT || kv_cap < 1 || kv_cap > kMaxRows) return 0;
+  return static_cast<size_t>(plan_sizes(B, Hkv, L, n_select, (kv_cap + kb::kTileKeys - 1) / kb::kTileKeys).bytes);
+}
+
+kb_status kb_attn_sparse_chunk(const void* q, const void* k, const void* v, void* o, const int* blocks, int n_select,
+                               int B, int Hq, int Hkv, int L, int start, const int* starts, const int* lens, int kv_cap,
+                               const int* block_table, int pages_per_seq, int page_size, int num_pages, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const SparseCall c{q, k, v, o, nullptr, blocks, n_select, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table,
+                     pages_per_seq, page_size, num_pages, workspace, workspace_bytes};
+  return sparse_forward(c, stream);
+}
+
+kb_status kb_attn_sparse_prefill_lse(const void* q, const void* k, const void* v, void* o, float* lse,
+                                     const int* blocks, int n_select, int B, int Hq, int Hkv, int S, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (lse == nullptr) return KB_ERR_INVALID_ARG;
+  const SparseCall c{q, k, v, o, lse, blocks, n_select, B, Hq, Hkv, S, 0, nullptr, nullptr, S, nullptr, 0, 0, 0,
+                     workspace, workspace_bytes};
+  return sparse_forward(c, stream);
+}
+
+kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, void* o, const int* blocks, int n_select,
+                                int B, int Hq, int Hkv, int ctx_len, const int* ctx_lens, int kv_cap,
+                                const int* block_table, int pages_per_seq, int page_size, int num_pages, void* stream) {
+  if (ctx_lens == nullptr && ctx_len < 1) return KB_ERR_INVALID_ARG;
+  // ctx_lens plays the part of starts in the checks: device positions, whole cache mapped
+  const SparseCall c{q, k, v, o, nullptr, blocks, n_select, B, Hq, Hkv, 1, ctx_lens != nullptr ? 0 : ctx_len - 1, ctx_lens,
+                     nullptr, kv_cap, block_table, pages_per_seq, page_size, num_pages, nullptr, 0};
+  int cap = 0;
+  kb::HostDevice dev;
+  kb_status s = check_sparse(c, &cap, &dev);
+  if (s != KB_OK) return s;
+  CUtensorMap tk, tv;
+  if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
+  kb::PackedArgs a{};
+  a.q = q;
+  a.o = o;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.L = 1;
+  a.start = c.start;
+  a.ctx_lens = ctx_lens;
+  a.max_ctx = cap;
+  a.block_table = block_table;
+  a.pages_per_seq = pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.n_sub = 1;
+  a.fold_seg = kb::kSegTiles;
+  a.blocks = blocks;
+  a.n_select = n_select;
+  const int max_blocks = ((ctx_lens != nullptr ? cap : ctx_len) + kb::kTileKeys - 1) / kb::kTileKeys;
+  a.cluster = sparse_cluster(dev, B, Hkv, n_select, max_blocks);
+  a.err = dev.err;
+  return done(kb::launch_packed(tk, tv, a, 1, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

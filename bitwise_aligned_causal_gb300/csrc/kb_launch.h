@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "../../include/kb_attn.h"
+
 namespace kb {
 
 struct PrefillArgs {
@@ -51,6 +53,9 @@ struct PackedArgs {
   // partial (O[128], m, mc, l) to part[((b*Hq + h)*L + r)*n_seg + seg][132]
   int seg_tiles, n_seg;
   float* part;
+  // block-sparse tokens (L = 1, fold mode): device [B, Hkv, n_select] listed key blocks
+  const int* blocks;
+  int n_select;
   uint32_t* err;
 };
 
@@ -77,7 +82,7 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
                           cudaStream_t s);
 // Partials a CTA of the narrow packed kernel can keep in shared memory for
 // the cluster's first CTA, with n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows);
+uint32_t packed_partial_slots(int n_rows, bool sparse = false);
 // Clusters of 2, 4 and 8 CTAs (entries 1, 2, 3) of the narrow packed kernel
 // the current device runs at once; entry 0 is unused.
 void packed_cluster_capacity(int (&active)[4]);
@@ -162,6 +167,32 @@ struct SelectArgs {
   uint32_t* err;
 };
 cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s);
+
+// Block-sparse attention over listed key blocks (kb_sparse.cuh, kb_sparse*.cu).
+struct SparseArgs {
+  void* o;                     // [B, Hq, L, 128] bf16
+  float* lse;                  // optional [B, Hq, L]
+  const int* blocks;           // [B, Hkv, L, n_select]
+  int n_select;
+  int B, Hq, Hkv, L;
+  int start;
+  const int* starts;           // optional device [B] ...
+  const int* lens;             // ... and row counts (else L)
+  int kv_cap;                  // positions per sequence the cache can hold
+  int max_blocks;              // key blocks of the longest row the call can hold
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  int n_tiles;                 // units per (b, KV head): position tiles a sequence can touch
+  int n_units;                 // B * Hkv * n_tiles
+  int walk_cap;                // entries a unit's walk can have
+  int* walk_len;               // workspace [n_units]: entries (-1: no such unit)
+  uint2* walks;                // workspace [n_units][walk_cap]
+  uint32_t* err;
+};
+cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
+// tq: host_group_map of q; tk, tv: host_rows_map of the cache.
+cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const SparseArgs& a, int device, cudaStream_t s);
 
 cudaError_t launch_wait_probe(uint32_t* err, unsigned long long limit_ns, cudaStream_t s);
 

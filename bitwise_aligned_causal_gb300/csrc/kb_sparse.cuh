@@ -1,0 +1,57 @@
+// kb_sparse.cuh -- what the block-sparse kernels share: the plan that turns
+// per-row block lists into per-tile walks, and the units.
+//
+// A unit is 32 query positions (aligned to absolute multiples of 32) of one
+// KV head with its four query heads: 128 rows of one MMA tile, row
+// 32 * head + r.  The 32 positions lie in one key block, the unit's own.  The
+// unit walks the union of its rows' lists in ascending order; entry e of the
+// walk is a key block and a mask whose bit r says that row r listed it.
+#pragma once
+
+#include <cstdint>
+
+#include "kb_contract.cuh"
+#include "kb_launch.h"
+
+namespace kb {
+
+constexpr int kUnitRows = 32;
+constexpr uint32_t kEntrySegStart = 1u << 30;   // first entry of its C5 segment in this walk
+constexpr uint32_t kEntrySegEnd = 1u << 31;     // last entry of its C5 segment in this walk
+constexpr uint32_t kEntryBlock = kEntrySegStart - 1u;
+
+struct SparseUnit {
+  int b, g;              // batch, KV head
+  int t;                 // absolute position tile: positions 32t .. 32t+31
+  int own;               // the key block they lie in
+  int start, L;          // the sequence's first query position and row count
+  int kv_len;            // start + L
+  bool live;
+};
+
+// Unit `u` of the launch: (b, KV head) slowest, so the units that run at one
+// time share a group's K and V in L2; the last positions first (they can
+// have the longest walks).
+__device__ __forceinline__ SparseUnit sparse_unit(const SparseArgs& a, int u) {
+  SparseUnit w;
+  const int bg = u / a.n_tiles;
+  const int rank = u % a.n_tiles;
+  w.b = bg / a.Hkv;
+  w.g = bg % a.Hkv;
+  w.start = a.starts != nullptr ? a.starts[w.b] : a.start;
+  w.L = a.lens != nullptr ? a.lens[w.b] : a.L;
+  w.live = w.start >= 0 && w.L >= 1 && w.L <= a.L && w.start <= a.kv_cap - w.L;
+  const int first = w.live ? w.start / kUnitRows : 0;
+  const int n = w.live ? (w.start + w.L - 1) / kUnitRows - first + 1 : 0;
+  w.live = w.live && rank < n;
+  w.t = first + n - 1 - rank;
+  w.own = w.t * kUnitRows / kTileKeys;
+  w.kv_len = w.start + w.L;
+  return w;
+}
+
+__device__ __forceinline__ const uint2* unit_walk(const SparseArgs& a, int u) {
+  return a.walks + static_cast<size_t>(u) * a.walk_cap;
+}
+
+}  // namespace kb

@@ -1,0 +1,91 @@
+// kb_sparse_plan.cu -- the plan of a block-sparse call: for every unit (32
+// positions of one KV head, kb_sparse.cuh) the union of its rows' block lists
+// in ascending order, each with the mask of the rows that listed it.
+//
+// One CTA per unit keeps a row mask per key block in shared memory, so lists
+// may come in any order and name a block twice; blocks past a row's own are
+// dropped, since none of their keys is visible to it.  The lists are read
+// once (4 bytes an entry) and the walk written once (8 bytes): a few
+// microseconds beside the attention, bound by latency.
+#include "kb_sparse.cuh"
+
+namespace kb {
+
+constexpr int kPlanThreads = 256;
+
+__global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const SparseArgs args) {
+  extern __shared__ uint32_t row_mask[];              // per key block 0..own
+  __shared__ int warp_count[kPlanThreads / 32];
+  const int u = static_cast<int>(blockIdx.x);
+  if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) {
+    // the attention kernel must not walk what an earlier call left here, even
+    // if the error word is cleared before it starts
+    if (threadIdx.x == 0) args.walk_len[u] = -1;
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SparseUnit w = sparse_unit(args, u);
+  if (!w.live) {
+    // a start or length out of range (an absent unit of a shorter sequence is none)
+    if (threadIdx.x == 0) {
+      if (w.L < 0 || w.L > args.L || w.start < 0 || w.start > args.kv_cap - w.L)
+        atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
+      args.walk_len[u] = -1;
+    }
+    return;
+  }
+  const int nb = w.own + 1;
+  for (int j = threadIdx.x; j < nb; j += kPlanThreads) row_mask[j] = 0u;
+  __syncthreads();
+  const int i0 = w.t * kUnitRows - w.start;           // row index of the unit's first position (may be negative)
+  const int* lists = args.blocks + (static_cast<size_t>(w.b) * args.Hkv + w.g) * args.L * args.n_select;
+  const int n_cap = (args.kv_cap + kTileKeys - 1) / kTileKeys;
+  for (int e = threadIdx.x; e < kUnitRows * args.n_select; e += kPlanThreads) {
+    const int r = e / args.n_select;
+    const int i = i0 + r;
+    if (i < 0 || i >= w.L) continue;
+    const int j = lists[static_cast<size_t>(i) * args.n_select + e % args.n_select];
+    if (j < -1 || j >= n_cap) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
+    else if (j >= 0 && j <= w.own) atomicOr(&row_mask[j], 1u << r);
+  }
+  __syncthreads();
+  uint2* walk = args.walks + static_cast<size_t>(u) * args.walk_cap;
+  int n = 0;                                          // entries of the blocks before j0
+  for (int j0 = 0; j0 < nb; j0 += kPlanThreads) {
+    const int j = j0 + threadIdx.x;
+    const uint32_t m = j < nb ? row_mask[j] : 0u;
+    const uint32_t any = __ballot_sync(0xffffffffu, m != 0u);
+    if (lane == 0) warp_count[warp] = __popc(any);
+    __syncthreads();
+    int at = n;
+#pragma unroll
+    for (int k = 0; k < kPlanThreads / 32; ++k) {
+      const int c = warp_count[k];
+      if (k < warp) at += c;
+      n += c;
+    }
+    if (m != 0u) {
+      bool first = true, last = true;
+      for (int k = j / kSegTiles * kSegTiles; k < j; ++k) first = first && row_mask[k] == 0u;
+      for (int k = j + 1; k < nb && k / kSegTiles == j / kSegTiles; ++k) last = last && row_mask[k] == 0u;
+      walk[at + __popc(any & ((1u << lane) - 1u))] =
+          make_uint2(static_cast<uint32_t>(j) | (first ? kEntrySegStart : 0u) | (last ? kEntrySegEnd : 0u), m);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) args.walk_len[u] = n;
+}
+
+cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s) {
+  static bool configured[64] = {};
+  if (!configured[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(kb_sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+    configured[device] = true;
+  }
+  const int blocks = a.max_blocks;
+  kb_sparse_plan_kernel<<<static_cast<unsigned>(a.n_units), kPlanThreads, static_cast<size_t>(blocks) * 4, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace kb

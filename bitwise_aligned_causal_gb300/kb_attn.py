@@ -55,6 +55,11 @@ _SIGS = {
                        _P],
     "kb_attn_block_boxes": [_P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
     "kb_attn_select_blocks": [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_sparse_workspace_bytes": [_I, _I, _I, _I, _I],
+    "kb_attn_sparse_chunk": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P,
+                             ctypes.c_size_t, _P],
+    "kb_attn_sparse_prefill_lse": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, ctypes.c_size_t, _P],
+    "kb_attn_sparse_decode": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
     "kb_status_string": [_I],
     "kb_contract_version": [],
     "kb_attn_last_cuda_error": [],
@@ -187,6 +192,29 @@ def kb_attn_select_blocks(q, boxes, blocks, B, Hq, Hkv, L, n_select, keep_first,
                           n_blocks, block_table, pages_per_seq, page_size, num_pages, stream=None) -> int:
     return _lib.kb_attn_select_blocks(q, boxes, blocks, B, Hq, Hkv, L, n_select, keep_first, keep_last, start, starts,
                                       lens, n_blocks, block_table, pages_per_seq, page_size, num_pages, stream)
+
+
+def kb_attn_sparse_workspace_bytes(B, Hkv, L, n_select, kv_cap) -> int:
+    return int(_lib.kb_attn_sparse_workspace_bytes(B, Hkv, L, n_select, kv_cap))
+
+
+def kb_attn_sparse_chunk(q, k, v, o, blocks, n_select, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table,
+                         pages_per_seq, page_size, num_pages, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.kb_attn_sparse_chunk(q, k, v, o, blocks, n_select, B, Hq, Hkv, L, start, starts, lens, kv_cap,
+                                     block_table, pages_per_seq, page_size, num_pages, workspace, workspace_bytes,
+                                     stream)
+
+
+def kb_attn_sparse_prefill_lse(q, k, v, o, lse, blocks, n_select, B, Hq, Hkv, S, workspace, workspace_bytes,
+                               stream=None) -> int:
+    return _lib.kb_attn_sparse_prefill_lse(q, k, v, o, lse, blocks, n_select, B, Hq, Hkv, S, workspace,
+                                           workspace_bytes, stream)
+
+
+def kb_attn_sparse_decode(q, k, v, o, blocks, n_select, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table,
+                          pages_per_seq, page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_sparse_decode(q, k, v, o, blocks, n_select, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table,
+                                      pages_per_seq, page_size, num_pages, stream)
 
 
 def kb_attn_check_device_status(stream=None) -> int:
@@ -662,3 +690,104 @@ def select_blocks_varlen(q, boxes, starts, n, lens=None, block_table=None, keep_
     if starts is None:
         raise TypeError("starts must be a contiguous int32 CUDA tensor")
     return _select(q, boxes, 0, starts, lens, int(n), int(keep_first), int(keep_last), block_table, out, stream, check)
+
+
+# ------------------------------------------------------------- block-sparse attention
+
+def _sparse_args(q, k, v, blocks, block_table, out, positions):
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _check(t, n)
+    _check_i32(blocks, "blocks")
+    _optional(_check_i32, (block_table, "block_table"), *positions)
+    _optional(_check, (out, "out"))
+    sz = shapes.sparse(q.shape, k.shape, v.shape, blocks.shape, None if block_table is None else block_table.shape,
+                       None if out is None else out.shape)
+    for t, n in positions:
+        if t is not None:
+            shapes.per_sequence(sz[0], **{n: t.shape})
+    return sz
+
+
+def _stream_workspace(nbytes, device, workspace, stream):
+    """A workspace for one call on `stream`: memory of the allocator is kept from reuse until that stream is done."""
+    ws = _workspace(nbytes, device, workspace)
+    if workspace is None and stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _sparse_workspace(B, Hkv, L, n, cap, device, workspace, stream):
+    return _stream_workspace(kb_attn_sparse_workspace_bytes(B, Hkv, L, n, cap), device, workspace, stream)
+
+
+def _sparse_chunk(q, k, v, start, starts, lens, blocks, block_table, out, workspace, stream, check):
+    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(q, k, v, blocks, block_table, out,
+                                                               ((starts, "starts"), (lens, "lens")))
+    if starts is None and not 0 <= start <= cap - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
+    o = _torch().empty_like(q) if out is None else out
+    ws = _sparse_workspace(B, Hkv, L, n, cap, q.device, workspace, stream)
+    _finish(kb_attn_sparse_chunk(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
+                                 Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
+                                 ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+            "kb_attn_sparse_chunk", check, stream)
+    return o
+
+
+def sparse_chunk(q, k, v, start, blocks, out=None, workspace=None, stream=None, check=False):
+    """chunk over listed key blocks: row i of q [B,Hq,L,128] (position start + i) sees the keys of blocks
+    blocks[b, g, i] (int32 [B,Hkv,L,n], -1 for none) up to its position.  k/v caches [B,Hkv,cap,128]."""
+    return _sparse_chunk(q, k, v, int(start), None, None, blocks, None, out, workspace, stream, check)
+
+
+def sparse_chunk_varlen(q, k, v, starts, blocks, lens=None, block_table=None, out=None, workspace=None, stream=None,
+                        check=False):
+    """sparse_chunk with a start (and row count) per sequence, int32 [B] on the device, and optionally paged pools with
+    block_table [B,pages_per_seq].  Rows from lens[b] on are left as they were."""
+    if starts is None:
+        raise TypeError("starts must be a contiguous int32 CUDA tensor")
+    return _sparse_chunk(q, k, v, 0, starts, lens, blocks, block_table, out, workspace, stream, check)
+
+
+def _sparse_decode(q, k, v, ctx_len, ctx_lens, blocks, block_table, out, stream, check):
+    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(q, k, v, blocks, block_table, out,
+                                                               ((ctx_lens, "ctx_lens"),))
+    if L != 1:
+        raise ValueError(f"decode takes one query row per (batch, head), got {L}")
+    if ctx_lens is None and not 1 <= ctx_len <= cap:
+        raise ValueError(f"ctx_len must lie in 1..{cap} (the cache capacity), got {ctx_len}")
+    o = _torch().empty_like(q) if out is None else out
+    _finish(kb_attn_sparse_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
+                                  Hkv, ctx_len, _ptr(ctx_lens), cap, _ptr(block_table), pps, page, num_pages,
+                                  _stream(stream)), "kb_attn_sparse_decode", check, stream)
+    return o
+
+
+def sparse_decode(q, k, v, ctx_len, blocks, out=None, stream=None, check=False):
+    """decode over listed key blocks: q [B,Hq,1,128] at position ctx_len-1, blocks int32 [B,Hkv,1,n]."""
+    return _sparse_decode(q, k, v, int(ctx_len), None, blocks, None, out, stream, check)
+
+
+def sparse_decode_paged(q, k_pages, v_pages, block_table, ctx_lens, blocks, out=None, stream=None, check=False):
+    """decode_paged over listed key blocks: blocks int32 [B,Hkv,1,n], indices within each sequence."""
+    for t, n in ((block_table, "block_table"), (ctx_lens, "ctx_lens")):
+        _check_i32(t, n)
+    return _sparse_decode(q, k_pages, v_pages, 0, ctx_lens, blocks, block_table, out, stream, check)
+
+
+def sparse_prefill_lse(q, k, v, blocks, out=None, lse=None, workspace=None, stream=None, check=False):
+    """Training forward over listed key blocks of a whole sequence: (o, lse) as prefill_lse; a row that lists nothing
+    has o = 0 and lse = -inf."""
+    torch = _torch()
+    B, Hq, Hkv, S, n, cap, _, _, _ = _sparse_args(q, k, v, blocks, None, out, ())
+    shapes.prefill(q.shape, k.shape, v.shape)
+    o = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_f32(lse, "lse")
+    shapes.vector_f32("lse", lse.shape, B, Hq, S)
+    ws = _sparse_workspace(B, Hkv, S, n, cap, q.device, workspace, stream)
+    _finish(kb_attn_sparse_prefill_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                       blocks.data_ptr(), n, B, Hq, Hkv, S, ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), _stream(stream)),
+            "kb_attn_sparse_prefill_lse", check, stream)
+    return o, lse

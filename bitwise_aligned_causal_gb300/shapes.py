@@ -238,3 +238,18 @@ def select(q, boxes, n: int, keep_first: int, keep_last: int, block_table=None, 
     if out is not None:
         _need(_shape(out) == (q[0], bx[1], q[2], n), f"out must have shape {(q[0], bx[1], q[2], n)}, got {_shape(out)}")
     return q[0], q[1], bx[1], q[2], bx[2], num_pages, page, pps
+
+
+def sparse(q, k, v, blocks, block_table=None, out=None) -> tuple:
+    """q [B,Hq,L,128]; caches [B,Hkv,cap,128], or pools with block_table; blocks [B,Hkv,L,n].
+    Returns (B, Hq, Hkv, L, n, cap, num_pages, page_size, pages_per_seq)."""
+    if block_table is None:
+        B, Hq, Hkv, L, cap = query_and_cache(q, k, v, out)
+        num_pages = page = pps = 0
+    else:
+        B, Hq, Hkv, L, num_pages, page, pps = pools(q, k, v, block_table, out)
+        cap = pps * page
+    bl = _shape(blocks)
+    _need(len(bl) == 4 and bl[:3] == (B, Hkv, L), f"blocks must have shape [{B}, {Hkv}, {L}, n], got {bl}")
+    _need(1 <= bl[3] <= MAX_SELECT, f"blocks must list 1..{MAX_SELECT} per row, got {bl[3]}")
+    return B, Hq, Hkv, L, bl[3], cap, num_pages, page, pps

@@ -376,6 +376,49 @@ kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, i
                                 int page_size, int num_pages, void* stream);
 
 /*
+ * Block-sparse attention: as the dense entry points, but a row sees only the
+ * keys of its listed blocks of 128 (up to its own position).
+ *   blocks : device int32 [B, Hkv, L, n_select]: the key blocks of row i of KV
+ *            head g's four query heads, -1 for none, in any order (naming one
+ *            twice changes nothing; blocks past the row's own hold no visible
+ *            key).  An index below -1, or at or above the cache's number of
+ *            blocks, is found on the device and reported by the next
+ *            kb_attn_check_device_status as KB_ERR_INVALID_ARG.
+ * A row's result is the contract's walk over its listed blocks alone, with the
+ * contract's segments, so it has the same bits in a chunk of any split and as
+ * a new token, and equals the dense entry points' bits when its list holds
+ * every block.  A row that lists nothing is zero (log-sum-exp -inf).  K and V
+ * of the cache's visible rows must be finite: a neighbour's listed block is
+ * multiplied by weights of exactly zero.
+ *
+ * kb_attn_sparse_chunk: rows at start..start+L-1 of every sequence, or (starts
+ * != NULL) at starts[b].., lens[b] of them (L when lens is NULL), against a
+ * contiguous cache [B, Hkv, kv_cap, 128] or (block_table != NULL) pools
+ * [num_pages, Hkv, page_size, 128], as kb_attn_chunk, _paged and _varlen.
+ * kb_attn_sparse_prefill_lse: a whole sequence with lse [B, Hq, S] fp32, as
+ * kb_attn_prefill_lse.
+ * Both need a device workspace (256-byte aligned, caller-owned, contents
+ * scratch) of kb_attn_sparse_workspace_bytes(B, Hkv, L, n_select, kv_cap)
+ * bytes, kv_cap being the cache's positions per sequence (pages_per_seq *
+ * page_size of a paged one); calls that can overlap on the GPU need one each.
+ * kb_attn_sparse_decode: one token per sequence at position ctx_len - 1, or
+ * (ctx_lens != NULL, device int32 [B]) at ctx_lens[b] - 1; no workspace.
+ */
+size_t kb_attn_sparse_workspace_bytes(int B, int Hkv, int L, int n_select, int kv_cap);
+kb_status kb_attn_sparse_chunk(const void* q, const void* k, const void* v, void* o, const int* blocks,
+                               int n_select, int B, int Hq, int Hkv, int L, int start, const int* starts,
+                               const int* lens, int kv_cap, const int* block_table, int pages_per_seq,
+                               int page_size, int num_pages, void* workspace, size_t workspace_bytes,
+                               void* stream);
+kb_status kb_attn_sparse_prefill_lse(const void* q, const void* k, const void* v, void* o, float* lse,
+                                     const int* blocks, int n_select, int B, int Hq, int Hkv, int S,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, void* o, const int* blocks,
+                                int n_select, int B, int Hq, int Hkv, int ctx_len, const int* ctx_lens,
+                                int kv_cap, const int* block_table, int pages_per_seq, int page_size,
+                                int num_pages, void* stream);
+
+/*
  * Prefill/chunk with an explicit kernel shape, for tests of the contract:
  * q_tiles_per_cta = 3 runs the tile kernel (one 128-row query tile per CTA,
  * one CTA per SM, three score buffers, so Q K^T of later key tiles overlaps
