@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkb_attn.so")
 SOURCES = ["kb_host.cu", "kb_prefill2.cu", "kb_decode.cu", "kb_backward.cu", "kb_segment.cu",
-           "kb_host_sparse.cu", "kb_append.cu", "kb_select.cu", "kb_sparse_plan.cu", "kb_sparse.cu"]
+           "kb_host_sparse.cu", "kb_append.cu", "kb_select.cu", "kb_sparse_plan.cu", "kb_sparse.cu",
+           "kb_sparse_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -82,6 +82,9 @@ PlanSizes plan_sizes(int B, int Hkv, int L, int n_select, long long max_blocks) 
   return p;
 }
 
+// Where the backward's row masks start: one per unit and key block, behind the walks.
+long long masks_at(const PlanSizes& p) { return align256(p.bytes); }
+
 struct SparseCall {
   const void *q, *k, *v;
   void* o;
@@ -128,8 +131,8 @@ kb_status cache_maps(const SparseCall& c, CUtensorMap* tk, CUtensorMap* tv) {
   return kb::host_rows_map(tv, c.v, rows, planes, stride_rows * row_bytes);
 }
 
-// Units, walks and workspace of a call.
-kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, kb::SparseArgs* a) {
+// Units, walks and workspace of a call; with_masks: the backward's row masks too.
+kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, bool with_masks, kb::SparseArgs* a) {
   a->o = c.o;
   a->lse = c.lse;
   a->blocks = c.blocks;
@@ -149,7 +152,8 @@ kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, kb::SparseArgs*
   a->num_pages = c.num_pages;
   a->err = err;
   const PlanSizes full = plan_sizes(c.B, c.Hkv, c.L, c.n_select, a->max_blocks);
-  if (c.workspace == nullptr || !host_aligned(c.workspace, 256) || c.workspace_bytes < static_cast<size_t>(full.bytes))
+  const long long need = with_masks ? masks_at(full) + full.units * a->max_blocks * 4 : full.bytes;
+  if (c.workspace == nullptr || !host_aligned(c.workspace, 256) || c.workspace_bytes < static_cast<size_t>(need))
     return KB_ERR_INVALID_ARG;
   a->n_tiles = static_cast<int>(c.starts != nullptr ? max_tiles32(c.L)
                                                     : (c.start + c.L - 1) / kb::kUnitRows - c.start / kb::kUnitRows + 1);
@@ -157,6 +161,7 @@ kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, kb::SparseArgs*
   a->walk_cap = static_cast<int>(full.cap);
   a->walk_len = static_cast<int*>(c.workspace);
   a->walks = reinterpret_cast<uint2*>(static_cast<char*>(c.workspace) + align256(full.units * 4));
+  if (with_masks) a->masks = reinterpret_cast<uint32_t*>(static_cast<char*>(c.workspace) + masks_at(full));
   return KB_OK;
 }
 
@@ -166,7 +171,7 @@ kb_status sparse_forward(const SparseCall& c, void* stream) {
   kb_status s = check_sparse(c, &cap, &dev);
   if (s != KB_OK) return s;
   kb::SparseArgs a{};
-  if ((s = fill_plan(c, cap, dev.err, &a)) != KB_OK) return s;
+  if ((s = fill_plan(c, cap, dev.err, false, &a)) != KB_OK) return s;
   CUtensorMap tq, tk, tv;
   if ((s = kb::host_group_map(&tq, c.q, static_cast<uint64_t>(c.L), static_cast<uint64_t>(c.B) * c.Hkv)) != KB_OK) return s;
   if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
@@ -425,6 +430,48 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
   a.cluster = sparse_cluster(dev, B, Hkv, n_select, max_blocks);
   a.err = dev.err;
   return done(kb::launch_packed(tk, tv, a, 1, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select) {
+  if (kb_attn_sparse_workspace_bytes(B, Hkv, S, n_select, S) == 0) return 0;
+  const long long blocks = (S + kb::kTileKeys - 1) / kb::kTileKeys;
+  const PlanSizes p = plan_sizes(B, Hkv, S, n_select, blocks);
+  return static_cast<size_t>(masks_at(p) + p.units * blocks * 4);
+}
+
+kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                                  const float* lse, float* delta, const int* blocks, int n_select, void* dq, void* dk,
+                                  void* dv, int B, int Hq, int Hkv, int S, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (!dout || !lse || !delta || !dq || !dk || !dv) return KB_ERR_INVALID_ARG;
+  const void* outs[] = {dout, dq, dk, dv, lse, delta};
+  for (int i = 0; i < 6; ++i)
+    if (!host_aligned(outs[i], i < 4 ? 16 : 4)) return KB_ERR_INVALID_ARG;
+  const SparseCall c{q, k, v, const_cast<void*>(o), nullptr, blocks, n_select, B, Hq, Hkv, S, 0, nullptr, nullptr, S,
+                     nullptr, 0, 0, 0, workspace, workspace_bytes};
+  int cap = 0;
+  kb::HostDevice dev;
+  kb_status s = check_sparse(c, &cap, &dev);
+  if (s != KB_OK) return s;
+  if ((s = device_pointers(outs, 6)) != KB_OK) return s;
+  kb::SparseBwdArgs a{};
+  if ((s = fill_plan(c, cap, dev.err, true, &a.plan)) != KB_OK) return s;
+  if (static_cast<long long>(a.plan.max_blocks) * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  a.lse = lse;
+  a.delta = delta;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  CUtensorMap tq, tk, tv, tdo;
+  const uint64_t rows = static_cast<uint64_t>(S), groups = static_cast<uint64_t>(B) * Hkv;
+  if ((s = kb::host_group_map(&tq, q, rows, groups)) != KB_OK) return s;
+  if ((s = kb::host_group_map(&tdo, dout, rows, groups)) != KB_OK) return s;
+  if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = kb::launch_sparse_plan(a.plan, dev.index, st);
+  if (e == cudaSuccess) e = kb::launch_bwd_delta(o, dout, delta, static_cast<long long>(B) * Hq * S, st);
+  if (e == cudaSuccess) e = kb::launch_sparse_backward(tq, tk, tv, tdo, a, dev.index, st);
+  return done(e);
 }
 
 }  // extern "C"

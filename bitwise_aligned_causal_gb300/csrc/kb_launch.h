@@ -104,6 +104,8 @@ struct BwdArgs {
 // tq, tdo: [B*Hq planes, S rows]; tk, tv: [B*Hkv planes, S rows].
 cudaError_t launch_backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const BwdArgs& a, cudaStream_t s);
+// delta[row] = rowsum(dout * o) of `rows` rows of 128.
+cudaError_t launch_bwd_delta(const void* o, const void* dout, float* delta, long long rows, cudaStream_t s);
 // C5 fold of the packed kernel's per-segment partials, one warp per row
 // (rows = B*Hq*L, row r of a (b, h) at position start + r), then C4 into o.
 cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
@@ -187,12 +189,26 @@ struct SparseArgs {
   int walk_cap;                // entries a unit's walk can have
   int* walk_len;               // workspace [n_units]: entries (-1: no such unit)
   uint2* walks;                // workspace [n_units][walk_cap]
+  // backward: workspace [B * Hkv][max_blocks][n_tiles], the row mask of
+  // position tile t for key block j (written for the blocks up to the tile's own)
+  uint32_t* masks;
   uint32_t* err;
 };
 cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
 // tq: host_group_map of q; tk, tv: host_rows_map of the cache.
 cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const SparseArgs& a, int device, cudaStream_t s);
+
+// Gradient of whole-sequence block-sparse attention (kb_sparse_bwd.cu).
+struct SparseBwdArgs {
+  const float* lse;            // [B, Hq, S]
+  const float* delta;          // [B, Hq, S]
+  void *dq, *dk, *dv;
+  SparseArgs plan;             // units, walks and masks of the call
+};
+// tq, tdo: host_group_map of q and dout; tk, tv: host_rows_map of k and v.
+cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, cudaStream_t s);
 
 cudaError_t launch_wait_probe(uint32_t* err, unsigned long long limit_ns, cudaStream_t s);
 

@@ -78,16 +78,6 @@ __device__ __forceinline__ void drain_wait_s(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > 50000000ull) break;
 }
 
-// TMA box of query rows packed by GQA group (host_group_map): 32 rows of the
-// four heads of group `group`.
-__device__ __forceinline__ void tma_load_group(uint32_t dst, const void* tmap, int row, int group, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(0), "r"(0), "r"(group), "r"(bar)
-      : "memory");
-}
-
 // The last entry's V tile holds rows past the sequence (only a paged or
 // ragged cache maps them; a contiguous uniform one reads zeros there).
 __device__ __forceinline__ bool has_v_tail(const SparseArgs& a, const SparseUnit& w, uint32_t last_entry) {

@@ -54,4 +54,24 @@ __device__ __forceinline__ const uint2* unit_walk(const SparseArgs& a, int u) {
   return a.walks + static_cast<size_t>(u) * a.walk_cap;
 }
 
+// TMA box of query rows packed by GQA group (host_group_map): 32 rows of the
+// four heads of group `group`.
+__device__ __forceinline__ void tma_load_group(uint32_t dst, const void* tmap, int row, int group, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(0), "r"(0), "r"(group), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_group_hint(uint32_t dst, const void* tmap, int row, int group, uint32_t bar,
+                                                    uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(0), "r"(0), "r"(group), "r"(bar),
+        "l"(policy)
+      : "memory");
+}
+
 }  // namespace kb

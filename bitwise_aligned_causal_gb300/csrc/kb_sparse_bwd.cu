@@ -1,0 +1,651 @@
+// kb_sparse_bwd.cu -- gradient of block-sparse attention over a whole
+// sequence (row i at position i): the dense backward's formulas
+// (kb_backward.cu) over the listed keys alone,
+//   dS_ij = P_ij (dP_ij - delta_i),  dq_i = sum_j dS_ij k_j / sqrt(128),
+//   dk_j = sum_i dS_ij q_i / sqrt(128),  dv_j = sum_i P_ij dO_i,
+// j over row i's listed keys, i over the rows (of the four heads) that listed
+// key j's block.  A row that lists nothing and a block nobody lists have zero
+// gradients.
+//
+// Rows come in the units of the forward (32 positions times four heads, 128
+// rows).  The dq kernel runs one CTA per unit over the unit's walk; the dk/dv
+// kernel one CTA per (b, KV head, key block) over the units whose rows listed
+// it, found in the plan's row masks.  A row of a unit that did not list the
+// block at hand has P = 0 there.  No atomics: every gradient element is
+// summed by one CTA in one order.
+#include <type_traits>
+
+#include "kb_bwd.cuh"
+#include "kb_sparse.cuh"
+
+namespace kb {
+
+// -------------------------------------------------------------- dq kernel
+
+struct SparseBwdQCfg {
+  static constexpr int kThreads = 384;        // 8 elementwise warps, two producers, two MMA issuers
+  static constexpr int kLoadWarp = 8;         // Q, dO and the K ring
+  static constexpr int kMmaWarp = 9;          // TMEM allocator + S, dP issuer
+  static constexpr int kDqWarp = 10;          // dQ issuer
+  static constexpr int kLoadWarpV = 11;       // the V ring
+  // K(j) is read by S(j) and by dQ(j), V(j) only by dP(j): the K ring frees
+  // a slot after dQ(j), the V ring after S(j), dP(j), so V needs fewer slots
+  static constexpr int kKStages = 3;
+  static constexpr int kVStages = 2;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 384;
+  static constexpr uint32_t kQOff = 0;
+  static constexpr uint32_t kDOOff = kTileBytes;
+  static constexpr uint32_t kKOff = 2 * kTileBytes;
+  static constexpr uint32_t kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr uint32_t kBarOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kBarQD = 0;                         // Q and dO landed
+  static constexpr int kBarKFull = 1;                      // 3: K(j) landed in slot j%3
+  static constexpr int kBarKEmpty = kBarKFull + kKStages;  // 3: dQ(j) done, K slot j%3 free
+  static constexpr int kBarVFull = kBarKEmpty + kKStages;  // 2: V(j) landed in slot j%2
+  static constexpr int kBarVEmpty = kBarVFull + kVStages;  // 2: S(j), dP(j) done, V slot j%2 free
+  static constexpr int kBarSFull = kBarVEmpty + kVStages;  // S(j), dP(j) in TMEM
+  static constexpr int kBarSFree = kBarSFull + 1;          // S(j) read (256 arrivals)
+  static constexpr int kBarDSFull = kBarSFree + 1;         // dS(j) in TMEM (256 arrivals)
+  static constexpr int kBarDQDone = kBarDSFull + 1;        // dQ += dS(j) K(j) finished
+  static constexpr int kBarDrain = kBarDQDone + 1;          // 2: one per issuer
+  static constexpr int kBarDPFree = kBarDrain + 2;         // dP(j) read (256 arrivals)
+  static constexpr int kBarSDone = kBarDPFree + 1;         // S(j) in TMEM (kBarSFull: dP(j) too)
+  static constexpr int kNumBars = kBarSDone + 1;
+  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = kMiscOff + 16 + 1024;
+};
+
+__global__ void __launch_bounds__(SparseBwdQCfg::kThreads, 1)
+kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
+                 const SparseBwdArgs args) {
+  using Cfg = SparseBwdQCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kMiscOff);
+  volatile uint32_t* abort_flag = misc + 1;
+  auto bar = [&](int i) { return smem_addr(bars + i); };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  const int unit = static_cast<int>(blockIdx.x);
+  const SparseUnit w = sparse_unit(args.plan, unit);
+  const uint2* const walk = unit_walk(args.plan, unit);
+  const int n_kv = max(0, args.plan.walk_len[unit]);                // entries of the walk (-1: the plan was skipped)
+  const int group = w.b * args.plan.Hkv + w.g;
+  uint32_t* const err = args.plan.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg::kNumBars; ++i)
+      mbar_init(bar(i), (i == Cfg::kBarSFree || i == Cfg::kBarDSFull || i == Cfg::kBarDPFree) ? 256u : 1u);
+    misc[1] = (*reinterpret_cast<volatile uint32_t*>(err) != 0) ? 1u : 0u;
+    fence_mbar_init();
+  }
+  if (warp == Cfg::kMmaWarp) {
+    tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = misc[0];
+  const bool skip = (*abort_flag != 0);
+
+  if (warp == Cfg::kLoadWarp || warp == Cfg::kLoadWarpV) {
+    // ----------------------------------------------------------- producers
+    // One warp per ring: Q, dO and K; V.
+    const bool is_v = (warp == Cfg::kLoadWarpV);
+    if (!skip) {
+      const uint64_t keep = l2_policy_evict_last();
+      const int stages = is_v ? Cfg::kVStages : Cfg::kKStages;
+      const int full0 = is_v ? Cfg::kBarVFull : Cfg::kBarKFull;
+      const int empty0 = is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty;
+      const uint32_t ring = sbase + (is_v ? Cfg::kVOff : Cfg::kKOff);
+      const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
+      if (lane == 0) {
+        tma_prefetch_desc(tmap);
+        if (!is_v && n_kv > 0) {
+          tma_prefetch_desc(&tmap_q);
+          tma_prefetch_desc(&tmap_do);
+          mbar_arrive_expect_tx(bar(Cfg::kBarQD), 2 * kTileBytes);
+          tma_load_group(sbase + Cfg::kQOff, &tmap_q, w.t * kUnitRows, group, bar(Cfg::kBarQD));
+          tma_load_group(sbase + Cfg::kDOOff, &tmap_do, w.t * kUnitRows, group, bar(Cfg::kBarQD));
+        }
+      }
+      int issued = 0;
+      bool ok = true;
+      uint32_t next = n_kv > 0 ? __ldg(&walk[0].x) : 0u;
+      for (int j = 0; j < n_kv; ++j) {
+        const int slot = j % stages;
+        const int block = static_cast<int>(next & kEntryBlock);
+        if (j + 1 < n_kv) next = __ldg(&walk[j + 1].x);
+        if (j >= stages)
+          ok = mbar_wait(bar(empty0 + slot), ((j / stages) - 1) & 1, abort_flag, err, kDevTimeoutSlot);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(full0 + slot), kTileBytes);
+          tma_load_tile_hint(ring + slot * kTileBytes, tmap, block * kTileKeys, group, bar(full0 + slot), keep);
+        }
+        issued = j + 1;
+      }
+      if (!ok && lane == 0) {
+        if (!is_v && issued > 0) drain_wait_b(bar(Cfg::kBarQD), 0);
+        for (int x = (issued > stages ? issued - stages : 0); x < issued; ++x)
+          drain_wait_b(bar(full0 + x % stages), (x / stages) & 1);
+      }
+    }
+  } else if (warp == Cfg::kMmaWarp) {
+    // ------------------------------------------------------ S, dP issuer
+    // S(j+1), dP(j+1) go out as soon as the elementwise warps have read S(j),
+    // dP(j); a second thread issues the dQ products, so neither stream's
+    // barrier waits leave the tensor pipe idle.
+    if (lane == 0 && !skip && n_kv > 0) {
+      const uint32_t q_s = sbase + Cfg::kQOff, do_s = sbase + Cfg::kDOOff;
+      bool ok = mbar_wait(bar(Cfg::kBarQD), 0, abort_flag, err, kDevTimeoutTma);
+      for (int j = 0; j < n_kv && ok; ++j) {
+        const int ks = j % Cfg::kKStages, vs = j % Cfg::kVStages;
+        ok = mbar_wait_hint(bar(Cfg::kBarKFull + ks), (j / Cfg::kKStages) & 1, abort_flag, err, kDevTimeoutTma);
+        if (ok) ok = mbar_wait_hint(bar(Cfg::kBarVFull + vs), (j / Cfg::kVStages) & 1, abort_flag, err, kDevTimeoutTma);
+        if (ok && j > 0) ok = mbar_wait_hint(bar(Cfg::kBarSFree), (j - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        // S's first K step goes out once S(j-1) has been read, the rest, with
+        // dP's steps interleaved, once dP(j-1) has been read too
+        const uint32_t k_s = sbase + Cfg::kKOff + ks * kTileBytes, v_s = sbase + Cfg::kVOff + vs * kTileBytes;
+        mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, 0, 1024u, kSlabBytes), desc_kmajor(k_s, 0, 1024u, kSlabBytes),
+               kIdescQK, 0u);
+        if (j > 0) ok = mbar_wait_hint(bar(Cfg::kBarDPFree), (j - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          mma_ss(tmem_base + Cfg::kColDP, desc_kmajor(do_s, kk, 1024u, kSlabBytes), desc_kmajor(v_s, kk, 1024u, kSlabBytes),
+                 kIdescQK, kk > 0 ? 1u : 0u);
+          if (kk < 7)
+            mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, kk + 1, 1024u, kSlabBytes),
+                   desc_kmajor(k_s, kk + 1, 1024u, kSlabBytes), kIdescQK, 1u);
+          if (kk == 6) tc_commit(bar(Cfg::kBarSDone));             // S is complete before dP's last step
+        }
+        tc_commit(bar(Cfg::kBarSFull));
+        tc_commit(bar(Cfg::kBarVEmpty + vs));
+      }
+      if (!ok) {
+        tc_commit(bar(Cfg::kBarDrain));
+        drain_wait_b(bar(Cfg::kBarDrain), 0);
+      }
+    }
+  } else if (warp == Cfg::kDqWarp) {
+    // ---------------------------------------------------------- dQ issuer
+    // dQ(j) reads dS(j) and K(j); the K slot is released after it (S(j)
+    // finished before dS(j) existed).
+    if (lane == 0 && !skip) {
+      bool ok = true;
+      for (int j = 0; j < n_kv && ok; ++j) {
+        ok = mbar_wait_hint(bar(Cfg::kBarDSFull), j & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        const int ks = j % Cfg::kKStages;
+        issue_pv(tmem_base + Cfg::kColDQ, tmem_base + Cfg::kColDS, sbase + Cfg::kKOff + ks * kTileBytes, j == 0);
+        tc_commit(bar(Cfg::kBarDQDone));
+        tc_commit(bar(Cfg::kBarKEmpty + ks));
+      }
+      if (!ok) {
+        tc_commit(bar(Cfg::kBarDrain + 1));
+        drain_wait_b(bar(Cfg::kBarDrain + 1), 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------- elementwise
+    // Warp w owns TMEM lanes 32(w%4) + 16(w/4) .. +15: rows r0 .. of head
+    // w%4.  A thread holds the unit's rows r0 and r0 + 8 and, of each group of
+    // 8 keys, keys 2u and 2u+1 (u = lane % 4), as the 16x256b load lays them out.
+    const int head = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * head + 16 * (warp >> 2)) << 16;
+    const int u = lane & 3;
+    const int r0 = 16 * (warp >> 2) + (lane >> 2);
+    const uint32_t warp_rows = 0xFFFFu << (16 * (warp >> 2));
+    const int p0 = w.t * kUnitRows - w.own * kTileKeys;               // the unit's first row within its own block
+    const int S = args.plan.L;
+    const int iA = w.t * kUnitRows + r0, iB = iA + 8;                 // query positions
+    const bool vA = iA < S, vB = iB < S;
+    const size_t row0 = (static_cast<size_t>(w.b) * args.plan.Hq + w.g * kGroup + head) * static_cast<size_t>(S);
+    // rows past the sequence list nothing, as do rows with lse = -inf: every
+    // key of theirs is masked
+    const float lseA = vA ? __fmul_rn(args.lse[row0 + iA], kLog2e) : 0.0f;
+    const float lseB = vB ? __fmul_rn(args.lse[row0 + iB], kLog2e) : 0.0f;
+    const float dlA = vA ? args.delta[row0 + iA] : 0.0f;
+    const float dlB = vB ? args.delta[row0 + iB] : 0.0f;
+    const float2 c2 = make_float2(score_scale_log2(), score_scale_log2());
+    const float2 nlA = make_float2(-lseA, -lseA), nlB = make_float2(-lseB, -lseB);
+    const float2 ndA = make_float2(-dlA, -dlA), ndB = make_float2(-dlB, -dlB);
+    // a tile that some row of the warp did not list, and the own one, masks
+    // keys from nA, nB on; the others take no select
+    auto tile_ds = [&](auto mask_tag, const uint32_t (&sv)[32], const uint32_t (&pv)[32], int half, int nA, int nB,
+                       uint32_t (&ds)[32]) {
+      constexpr bool kMask = decltype(mask_tag)::value;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int key = 64 * half + 8 * r + 2 * u;                   // keys key, key + 1 within the tile
+        uint32_t unused;
+        p_ds_pair<kMask>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nlA, ndA, key >= nA, key + 1 >= nA,
+                         unused, ds[2 * (8 * half + r)]);
+        p_ds_pair<kMask>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nlB, ndB, key >= nB,
+                         key + 1 >= nB, unused, ds[2 * (8 * half + r) + 1]);
+      }
+    };
+    bool ok = !skip;
+    uint2 next = n_kv > 0 ? __ldg(&walk[0]) : make_uint2(0u, 0u);
+    for (int j = 0; j < n_kv && ok; ++j) {
+      const uint2 entry = next;
+      if (j + 1 < n_kv) next = __ldg(&walk[j + 1]);
+      ok = mbar_wait_hint(bar(Cfg::kBarSDone), j & 1, abort_flag, err, kDevTimeoutMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool diag = static_cast<int>(entry.x & kEntryBlock) == w.own;
+      const int nA = (entry.y >> r0) & 1u ? (diag ? p0 + r0 + 1 : kTileKeys) : 0;
+      const int nB = (entry.y >> (r0 + 8)) & 1u ? (diag ? p0 + r0 + 9 : kTileKeys) : 0;
+      uint32_t ds[32];
+      // all of S(j) and dP(j) into registers first, so S(j+1), dP(j+1) can be
+      // issued while this tile's dS is computed: S as soon as it is complete
+      // (before dP's last step), released on its own barrier so S(j+1) can
+      // start while dP is still being read
+      uint32_t sv0[32], pv0[32], sv1[32], pv1[32];
+      tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColS + lane_off, tmem_base + Cfg::kColS + lane_off + 64u, sv0,
+                                   sv1);
+      tc_fence_before();
+      mbar_arrive(bar(Cfg::kBarSFree));                              // S(j) fully read
+      ok = mbar_wait_hint(bar(Cfg::kBarSFull), j & 1, abort_flag, err, kDevTimeoutMma);   // dP(j) too
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColDP + lane_off, tmem_base + Cfg::kColDP + lane_off + 64u, pv0,
+                                   pv1);
+      tc_fence_before();
+      mbar_arrive(bar(Cfg::kBarDPFree));                             // dP(j) fully read
+      if (diag || (entry.y & warp_rows) != warp_rows) {
+        tile_ds(std::true_type{}, sv0, pv0, 0, nA, nB, ds);
+        tile_ds(std::true_type{}, sv1, pv1, 1, nA, nB, ds);
+      } else {
+        tile_ds(std::false_type{}, sv0, pv0, 0, nA, nB, ds);
+        tile_ds(std::false_type{}, sv1, pv1, 1, nA, nB, ds);
+      }
+      if (j > 0) {                                                   // dQ(j-1) has read dS(j-1)
+        ok = mbar_wait(bar(Cfg::kBarDQDone), (j - 1) & 1, abort_flag, err, kDevTimeoutMma);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tmem_st_16x128b_x16(tmem_base + Cfg::kColDS + lane_off, ds);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(Cfg::kBarDSFull));
+    }
+    if (ok && n_kv > 0) ok = mbar_wait(bar(Cfg::kBarDQDone), (n_kv - 1) & 1, abort_flag, err, kDevTimeoutMma);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      __nv_bfloat16* base = static_cast<__nv_bfloat16*>(args.dq) + row0 * kHeadDim;
+      uint32_t* dA = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vA ? iA : 0) * kHeadDim);
+      uint32_t* dB = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vB ? iB : 0) * kHeadDim);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[32];
+        tmem_ld_16x256b_x8_wait(tmem_base + Cfg::kColDQ + lane_off + 64u * half, v);
+        if (n_kv == 0) {                                              // nothing listed: the gradient is zero
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int col = 64 * half + 8 * r + 2 * u;
+          const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), kInvSqrtD),
+                                          __fmul_rn(__uint_as_float(v[4 * r + 1]), kInvSqrtD));
+          const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), kInvSqrtD),
+                                          __fmul_rn(__uint_as_float(v[4 * r + 3]), kInvSqrtD));
+          if (vA) dA[col >> 1] = wa;
+          if (vB) dB[col >> 1] = wb;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Cfg::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------- dk/dv kernel
+
+struct SparseBwdKVCfg {
+  static constexpr int kThreads = 320;
+  static constexpr int kLoadWarp = 8;
+  static constexpr int kMmaWarp = 9;
+  static constexpr int kStages = 2;           // Q/dO ring
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 384;
+  static constexpr uint32_t kKOff = 0;
+  static constexpr uint32_t kVOff = kTileBytes;
+  static constexpr uint32_t kQOff = 2 * kTileBytes;                   // slot s: Q at kQOff + s*2*tile,
+  static constexpr uint32_t kSlotBytes = 2 * kTileBytes;              //         dO right after it
+  static constexpr uint32_t kVecOff = kQOff + kStages * kSlotBytes;   // slot s: -lse2[128], -delta[128]
+  static constexpr uint32_t kVecBytes = 2 * 128 * 4 + 16;            // ... and the place of the first row
+  static constexpr uint32_t kBarOff = kVecOff + kStages * kVecBytes;
+  static constexpr int kBarKV = 0;                                    // K(jt), V(jt) landed
+  static constexpr int kBarQDFull = 1;                                // 2: Q, dO of step s landed
+  static constexpr int kBarQDEmpty = kBarQDFull + kStages;            // 2: dV, dK of step s done
+  static constexpr int kBarVecFull = kBarQDEmpty + kStages;           // 2: lse2, delta of step s (32 arrivals)
+  static constexpr int kBarSTFull = kBarVecFull + kStages;            // S^T, dP^T of step s in TMEM
+  static constexpr int kBarPDSFull = kBarSTFull + 1;                  // 4: P^T, dS^T of query quarter 0..3
+                                                                      //    stored (256 arrivals each)
+  static constexpr int kBarDone = kBarPDSFull + 4;                    // every dV, dK product finished
+  static constexpr int kBarDrain = kBarDone + 1;
+  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr uint32_t kSmemBytes = kMiscOff + 16 + 1024;
+};
+
+__global__ void __launch_bounds__(SparseBwdKVCfg::kThreads, 1)
+kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
+                   const SparseBwdArgs args) {
+  using Cfg = SparseBwdKVCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kMiscOff);
+  volatile uint32_t* abort_flag = misc + 1;
+  auto bar = [&](int i) { return smem_addr(bars + i); };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // (b, kv head g, key block jt), first blocks of every group first: they can
+  // be listed by the most units, so the longest CTAs start first
+  const int jt = static_cast<int>(blockIdx.x) / (args.plan.B * args.plan.Hkv);
+  const int group = static_cast<int>(blockIdx.x) % (args.plan.B * args.plan.Hkv);
+  const int S = args.plan.L;
+  const int n_tiles = args.plan.n_tiles;
+  uint32_t* const err = args.plan.err;
+  // units that listed this block, as row masks of the position tiles from the block's own on
+  const uint32_t* const masks =
+      args.plan.masks + (static_cast<size_t>(group) * args.plan.max_blocks + jt) * n_tiles;
+  const int t0 = jt * (kTileKeys / kUnitRows);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg::kNumBars; ++i) {
+      uint32_t count = 1u;
+      if (i >= Cfg::kBarPDSFull && i < Cfg::kBarPDSFull + 4) count = 256u;
+      if (i >= Cfg::kBarVecFull && i < Cfg::kBarVecFull + Cfg::kStages) count = 32u;
+      mbar_init(bar(i), count);
+    }
+    misc[1] = (*reinterpret_cast<volatile uint32_t*>(err) != 0) ? 1u : 0u;
+    fence_mbar_init();
+  }
+  if (warp == Cfg::kMmaWarp) {
+    tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = misc[0];
+  const bool skip = (*abort_flag != 0);
+  int n_steps = 0;                                    // one per unit that listed the block
+  if (!skip)
+    for (int t = t0; t < n_tiles; t += Cfg::kThreads) {
+      const int i = t + static_cast<int>(threadIdx.x);
+      n_steps += __syncthreads_count(i < n_tiles && __ldg(masks + i) != 0u);
+    }
+
+  if (warp == Cfg::kLoadWarp) {
+    // ------------------------------------------------------------ producer
+    if (!skip) {
+      const uint64_t keep = l2_policy_evict_last();
+      if (lane == 0) {
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_do);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        if (n_steps > 0) {
+          mbar_arrive_expect_tx(bar(Cfg::kBarKV), 2 * kTileBytes);
+          tma_load_tile(sbase + Cfg::kKOff, &tmap_k, jt * kTileKeys, group, bar(Cfg::kBarKV));
+          tma_load_tile(sbase + Cfg::kVOff, &tmap_v, jt * kTileKeys, group, bar(Cfg::kBarKV));
+        }
+      }
+      int issued = 0;
+      bool ok = true;
+      int tb = t0 - 32;                                                // 32 position tiles at a time: this lane's mask
+      uint32_t mine = 0u, left = 0u;                                   // and which of them are still to come
+      for (int s = 0; s < n_steps; ++s) {
+        const int slot = s % Cfg::kStages;
+        while (left == 0u && tb < n_tiles) {                           // n_steps counts the masks that are not zero
+          tb += 32;
+          mine = tb + lane < n_tiles ? __ldg(masks + tb + lane) : 0u;
+          left = __ballot_sync(0xffffffffu, mine != 0u);
+        }
+        ok = left != 0u;                                               // fewer than counted: the workspace was overwritten
+        if (!ok) break;
+        const int src = __ffs(left) - 1;
+        left &= left - 1u;
+        const int it = tb + src;
+        const uint32_t rows = __shfl_sync(0xffffffffu, mine, src);     // bit r: row r of the unit listed the block
+        if (s >= Cfg::kStages)
+          ok = mbar_wait(bar(Cfg::kBarQDEmpty + slot), ((s / Cfg::kStages) - 1) & 1, abort_flag, err,
+                         kDevTimeoutSlot);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = sbase + Cfg::kQOff + slot * Cfg::kSlotBytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(Cfg::kBarQDFull + slot), 2 * kTileBytes);
+          tma_load_group_hint(dst, &tmap_q, it * kUnitRows, group, bar(Cfg::kBarQDFull + slot), keep);
+          tma_load_group_hint(dst + kTileBytes, &tmap_do, it * kUnitRows, group, bar(Cfg::kBarQDFull + slot), keep);
+        }
+        issued = s + 1;
+        // -lse (base 2) and -delta of the step's 128 query rows (lane r: row r
+        // of the four heads); a row that did not list the block gets -lse2 =
+        // -inf, so its P (and dS) is exactly zero
+        float* vec = reinterpret_cast<float*>(smem + Cfg::kVecOff + slot * Cfg::kVecBytes);
+        const bool listed = ((rows >> lane) & 1u) && it * kUnitRows + lane < S;
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) {
+          const size_t at = (static_cast<size_t>(group) * kGroup + h) * static_cast<size_t>(S) + it * kUnitRows + lane;
+          vec[32 * h + lane] = listed ? -__fmul_rn(args.lse[at], kLog2e) : __int_as_float(0xFF800000);
+          vec[128 + 32 * h + lane] = listed ? -args.delta[at] : -0.0f;
+        }
+        // first row's place in the key block when the block is the unit's own
+        if (lane == 0) reinterpret_cast<int*>(vec)[256] = it * kUnitRows - jt * kTileKeys;
+        mbar_arrive(bar(Cfg::kBarVecFull + slot));
+      }
+      if (!ok && lane == 0) {
+        if (issued > 0) drain_wait_b(bar(Cfg::kBarKV), 0);
+        for (int x = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); x < issued; ++x)
+          drain_wait_b(bar(Cfg::kBarQDFull + x % Cfg::kStages), (x / Cfg::kStages) & 1);
+      }
+    }
+  } else if (warp == Cfg::kMmaWarp) {
+    // ---------------------------------------------------------- MMA issuer
+    // per step: S^T = K Q^T, dP^T = V dO^T, then for each quarter of the
+    // query columns (32 queries), once its P^T and dS^T are stored, K steps
+    // 2q and 2q+1 of dV += P^T dO and dK += dS^T Q.  A quarter's steps read
+    // only the columns that quarter wrote, so they run while the next quarter
+    // is computed.  P^T and dS^T overwrite S^T and dP^T, whose next values are
+    // issued after these products (in issue order).
+    if (lane == 0 && !skip) {
+      bool ok = n_steps == 0 || mbar_wait(bar(Cfg::kBarKV), 0, abort_flag, err, kDevTimeoutTma);
+      for (int s = 0; s < n_steps && ok; ++s) {
+        const int slot = s % Cfg::kStages;
+        const uint32_t q_s = sbase + Cfg::kQOff + slot * Cfg::kSlotBytes;
+        const uint32_t do_s = q_s + kTileBytes;
+        ok = mbar_wait_hint(bar(Cfg::kBarQDFull + slot), (s / Cfg::kStages) & 1, abort_flag, err, kDevTimeoutTma);
+        if (!ok) break;
+        tc_fence_after();
+        issue_qk_pair(tmem_base + Cfg::kColST, sbase + Cfg::kKOff, q_s, tmem_base + Cfg::kColDPT, sbase + Cfg::kVOff,
+                      do_s);
+        tc_commit(bar(Cfg::kBarSTFull));
+        ok = mbar_wait_hint(bar(Cfg::kBarPDSFull), s & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv_pair<0, 2>(tmem_base + Cfg::kColDV, tmem_base + Cfg::kColST, do_s, tmem_base + Cfg::kColDK,
+                            tmem_base + Cfg::kColDPT, q_s, s == 0);
+        ok = mbar_wait_hint(bar(Cfg::kBarPDSFull + 1), s & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv_pair<2, 4>(tmem_base + Cfg::kColDV, tmem_base + Cfg::kColST, do_s, tmem_base + Cfg::kColDK,
+                            tmem_base + Cfg::kColDPT, q_s, false);
+        ok = mbar_wait_hint(bar(Cfg::kBarPDSFull + 2), s & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv_pair<4, 6>(tmem_base + Cfg::kColDV, tmem_base + Cfg::kColST, do_s, tmem_base + Cfg::kColDK,
+                            tmem_base + Cfg::kColDPT, q_s, false);
+        ok = mbar_wait_hint(bar(Cfg::kBarPDSFull + 3), s & 1, abort_flag, err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv_pair<6, 8>(tmem_base + Cfg::kColDV, tmem_base + Cfg::kColST, do_s, tmem_base + Cfg::kColDK,
+                            tmem_base + Cfg::kColDPT, q_s, false);
+        tc_commit(bar(Cfg::kBarQDEmpty + slot));
+      }
+      if (ok) tc_commit(bar(Cfg::kBarDone));
+      if (!ok) {
+        tc_commit(bar(Cfg::kBarDrain));
+        drain_wait_b(bar(Cfg::kBarDrain), 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------------- elementwise
+    // rows are keys (lanes as in the dq kernel), columns are query rows
+    const int lane_base = 32 * (warp & 3) + 16 * (warp >> 2);
+    const uint32_t lane_off = static_cast<uint32_t>(lane_base) << 16;
+    const int u = lane & 3;
+    const int rA = lane_base + (lane >> 2);
+    const int rB = rA + 8;
+    const float2 c2 = make_float2(score_scale_log2(), score_scale_log2());
+    // one query quarter (the 32 rows of head qt): a step of the unit's own
+    // block masks keys past the query, the others take no select
+    auto quarter = [&](auto diag_tag, const uint32_t (&sv)[16], const uint32_t (&pv)[16], const float* vnl,
+                       const float* vnd, int qt, int p0, uint32_t (&pp)[8], uint32_t (&dd)[8]) {
+      constexpr bool kDiag = decltype(diag_tag)::value;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int qc = 32 * qt + 8 * r + 2 * u;                      // query rows qc, qc + 1 within their tile
+        const float2 nl = *reinterpret_cast<const float2*>(vnl + qc);
+        const float2 nd = *reinterpret_cast<const float2*>(vnd + qc);
+        const int at = p0 + 8 * r + 2 * u;                           // the query's place in the key block
+        p_ds_pair<kDiag>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nl, nd, rA > at, rA > at + 1,
+                         pp[2 * r], dd[2 * r]);
+        p_ds_pair<kDiag>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nl, nd, rB > at,
+                         rB > at + 1, pp[2 * r + 1], dd[2 * r + 1]);
+      }
+    };
+    bool ok = !skip;
+    for (int s = 0; s < n_steps && ok; ++s) {
+      const int slot = s % Cfg::kStages;
+      ok = mbar_wait_hint(bar(Cfg::kBarSTFull), s & 1, abort_flag, err, kDevTimeoutMma);
+      if (ok) ok = mbar_wait_hint(bar(Cfg::kBarVecFull + slot), (s / Cfg::kStages) & 1, abort_flag, err,
+                             kDevTimeoutTma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float* vnl = reinterpret_cast<const float*>(smem + Cfg::kVecOff + slot * Cfg::kVecBytes);
+      const float* vnd = vnl + 128;
+      const int p0 = reinterpret_cast<const int*>(vnl)[256];
+      const bool diag = p0 < kTileKeys;                              // the unit's own block: keys past the row masked
+#pragma unroll
+      for (int qt = 0; qt < 4; ++qt) {                                 // query quarter: 32 query columns
+        uint32_t sv[16], pv[16];
+        tmem_ld_16x256b_x4_pair_wait(tmem_base + Cfg::kColST + lane_off + 32u * qt,
+                                     tmem_base + Cfg::kColDPT + lane_off + 32u * qt, sv, pv);
+        uint32_t pp[8], dd[8];
+        if (diag) quarter(std::true_type{}, sv, pv, vnl, vnd, qt, p0, pp, dd);
+        else quarter(std::false_type{}, sv, pv, vnl, vnd, qt, p0, pp, dd);
+        // bf16 pairs of query columns 32*qt.. go to columns 16*qt.. of the
+        // same buffers; those fp32 columns were read in this quarter or an
+        // earlier one
+        tmem_st_16x128b_x4(tmem_base + Cfg::kColST + lane_off + 16u * qt, pp);
+        tmem_st_16x128b_x4(tmem_base + Cfg::kColDPT + lane_off + 16u * qt, dd);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::kBarPDSFull + qt));
+      }
+    }
+    if (ok) ok = mbar_wait(bar(Cfg::kBarDone), 0, abort_flag, err, kDevTimeoutMma);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const int jA = jt * kTileRows + rA, jB = jt * kTileRows + rB;
+      const bool vA = jA < S, vB = jB < S;
+      const size_t kv0 = static_cast<size_t>(group) * static_cast<size_t>(S);
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {                      // 0: dv, 1: dk (scaled by 1/sqrt(128))
+        __nv_bfloat16* base = static_cast<__nv_bfloat16*>(which ? args.dk : args.dv) + kv0 * kHeadDim;
+        uint32_t* oA = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vA ? jA : 0) * kHeadDim);
+        uint32_t* oB = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vB ? jB : 0) * kHeadDim);
+        const float sc = which ? kInvSqrtD : 1.0f;
+        const uint32_t col0 = which ? Cfg::kColDK : Cfg::kColDV;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
+          tmem_ld_16x256b_x8_wait(tmem_base + col0 + lane_off + 64u * half, v);
+          if (n_steps == 0) {                                        // listed by nobody: the gradient is zero
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int col = 64 * half + 8 * r + 2 * u;
+            const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), sc),
+                                            __fmul_rn(__uint_as_float(v[4 * r + 1]), sc));
+            const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), sc),
+                                            __fmul_rn(__uint_as_float(v[4 * r + 3]), sc));
+            if (vA) oA[col >> 1] = wa;
+            if (vB) oB[col >> 1] = wb;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Cfg::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------- launcher
+
+cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, cudaStream_t s) {
+  static_assert(SparseBwdQCfg::kSmemBytes <= 227u * 1024u, "shared memory budget (dq)");
+  static_assert(SparseBwdKVCfg::kSmemBytes <= 227u * 1024u, "shared memory budget (dk, dv)");
+  static bool configured[64] = {};
+  cudaError_t e;
+  if (!configured[device]) {
+    e = cudaFuncSetAttribute(kb_sparse_bwd_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SparseBwdQCfg::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kb_sparse_bwd_dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SparseBwdKVCfg::kSmemBytes));
+    if (e != cudaSuccess) return e;
+    configured[device] = true;
+  }
+  kb_sparse_bwd_dq_kernel<<<static_cast<unsigned>(a.plan.n_units), SparseBwdQCfg::kThreads, SparseBwdQCfg::kSmemBytes,
+                            s>>>(tq, tk, tv, tdo, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const unsigned grid_kv = static_cast<unsigned>(a.plan.max_blocks * a.plan.B * a.plan.Hkv);
+  kb_sparse_bwd_dkdv_kernel<<<grid_kv, SparseBwdKVCfg::kThreads, SparseBwdKVCfg::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
+  return cudaGetLastError();
+}
+
+}  // namespace kb

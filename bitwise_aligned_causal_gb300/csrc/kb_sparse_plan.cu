@@ -49,6 +49,10 @@ __global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const Spar
     else if (j >= 0 && j <= w.own) atomicOr(&row_mask[j], 1u << r);
   }
   __syncthreads();
+  if (args.masks != nullptr) {
+    uint32_t* m = args.masks + (static_cast<size_t>(w.b) * args.Hkv + w.g) * args.max_blocks * args.n_tiles + w.t;
+    for (int j = threadIdx.x; j < nb; j += kPlanThreads) m[static_cast<size_t>(j) * args.n_tiles] = row_mask[j];
+  }
   uint2* walk = args.walks + static_cast<size_t>(u) * args.walk_cap;
   int n = 0;                                          // entries of the blocks before j0
   for (int j0 = 0; j0 < nb; j0 += kPlanThreads) {

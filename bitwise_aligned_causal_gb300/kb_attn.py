@@ -60,6 +60,9 @@ _SIGS = {
                              ctypes.c_size_t, _P],
     "kb_attn_sparse_prefill_lse": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, ctypes.c_size_t, _P],
     "kb_attn_sparse_decode": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_sparse_backward_workspace_bytes": [_I, _I, _I, _I],
+    "kb_attn_sparse_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t,
+                                _P],
     "kb_status_string": [_I],
     "kb_contract_version": [],
     "kb_attn_last_cuda_error": [],
@@ -215,6 +218,16 @@ def kb_attn_sparse_decode(q, k, v, o, blocks, n_select, B, Hq, Hkv, ctx_len, ctx
                           pages_per_seq, page_size, num_pages, stream=None) -> int:
     return _lib.kb_attn_sparse_decode(q, k, v, o, blocks, n_select, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table,
                                       pages_per_seq, page_size, num_pages, stream)
+
+
+def kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n_select) -> int:
+    return int(_lib.kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n_select))
+
+
+def kb_attn_sparse_backward(q, k, v, o, dout, lse, delta, blocks, n_select, dq, dk, dv, B, Hq, Hkv, S, workspace,
+                            workspace_bytes, stream=None) -> int:
+    return _lib.kb_attn_sparse_backward(q, k, v, o, dout, lse, delta, blocks, n_select, dq, dk, dv, B, Hq, Hkv, S,
+                                        workspace, workspace_bytes, stream)
 
 
 def kb_attn_check_device_status(stream=None) -> int:
@@ -791,3 +804,30 @@ def sparse_prefill_lse(q, k, v, blocks, out=None, lse=None, workspace=None, stre
                                        ws.numel() * ws.element_size(), _stream(stream)),
             "kb_attn_sparse_prefill_lse", check, stream)
     return o, lse
+
+
+def sparse_backward(q, k, v, o, dout, lse, blocks, delta=None, dq=None, dk=None, dv=None, workspace=None, stream=None,
+                    check=False):
+    """Gradients (dq, dk, dv) of sparse_prefill_lse for output gradient dout; o, lse from it, blocks as given to it.
+    Also returns delta [B,Hq,S] float32 = rowsum(dout * o)."""
+    torch = _torch()
+    B, Hq, Hkv, S, n, _, _, _, _ = _sparse_args(q, k, v, blocks, None, None, ())
+    for t, name in ((o, "o"), (dout, "dout")):
+        _check(t, name)
+    _optional(_check, (dq, "dq"), (dk, "dk"), (dv, "dv"))
+    shapes.backward(q.shape, k.shape, v.shape, o.shape, dout.shape, None if dq is None else dq.shape,
+                    None if dk is None else dk.shape, None if dv is None else dv.shape)
+    delta = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if delta is None else delta
+    for t, name in ((lse, "lse"), (delta, "delta")):
+        _check_f32(t, name)
+        shapes.vector_f32(name, t.shape, B, Hq, S)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    ws = _stream_workspace(kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n), q.device, workspace, stream)
+    _finish(kb_attn_sparse_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                                    lse.data_ptr(), delta.data_ptr(), blocks.data_ptr(), n, dq.data_ptr(),
+                                    dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, S, ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), _stream(stream)),
+            "kb_attn_sparse_backward", check, stream)
+    return dq, dk, dv, delta

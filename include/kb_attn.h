@@ -419,6 +419,20 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
                                 int num_pages, void* stream);
 
 /*
+ * Backward of kb_attn_sparse_prefill_lse: as kb_attn_backward, over the listed
+ * keys (the lists themselves take no gradient).  o and lse from the forward
+ * with the same q, k, v and blocks; delta [B, Hq, S] fp32 is an output.  A row
+ * that lists nothing has dq = 0, a block that no row lists dk = dv = 0.  No
+ * atomics: repeated calls give identical bits.  workspace: 256-byte aligned
+ * scratch of kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n_select).
+ */
+size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select);
+kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                                  const float* lse, float* delta, const int* blocks, int n_select, void* dq,
+                                  void* dk, void* dv, int B, int Hq, int Hkv, int S, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * Prefill/chunk with an explicit kernel shape, for tests of the contract:
  * q_tiles_per_cta = 3 runs the tile kernel (one 128-row query tile per CTA,
  * one CTA per SM, three score buffers, so Q K^T of later key tiles overlaps

@@ -124,3 +124,40 @@ def test_boxes_and_select_abi(kb):
     assert s(start=253) == bad and s(start=-1) == bad and s(nb=0) == bad and s(L=257) == bad and s(lens=FAKE) == bad
     assert s(nb=40_000) == kb.KB_ERR_UNSUPPORTED
     assert s(bt=FAKE, pps=2, page=100, pages=4) == bad
+
+
+def test_sparse_shapes_and_abi(kb):
+    blocks = (2, 8, 5, 3)
+    assert shapes.sparse(Q, CACHE, CACHE, blocks) == (2, 32, 8, 5, 3, 300, 0, 0, 0)
+    assert shapes.sparse(Q, POOL, POOL, blocks, (2, 4))[5:] == (1024, 9, 256, 4)
+    for a in [(Q, CACHE, CACHE, (2, 8, 5, 129)), (Q, CACHE, CACHE, (2, 4, 5, 3)), (Q, CACHE, CACHE, (2, 8, 5)),
+              (Q, CACHE, (2, 8, 301, 128), blocks), (Q, POOL, POOL, blocks, (3, 4))]:
+        with pytest.raises(ValueError):
+            shapes.sparse(*a)
+    bad, ws = kb.KB_ERR_INVALID_ARG, kb.kb_attn_sparse_workspace_bytes(1, 8, 64, 4, 256)
+    assert ws == 256 + 8 * 3 * 2 * 8                                # three position tiles, two blocks at most
+    assert kb.kb_attn_sparse_workspace_bytes(1, 8, 64, 129, 256) == 0
+    assert kb.kb_attn_sparse_backward_workspace_bytes(1, 8, 64, 4) > kb.kb_attn_sparse_workspace_bytes(1, 8, 64, 4, 64)
+
+    def chunk(q=FAKE, blocks=FAKE, n=4, Hq=32, L=64, start=0, starts=None, lens=None, cap=256, bt=None, pps=0, page=0,
+              pages=0):
+        return kb.kb_attn_sparse_chunk(q, FAKE, FAKE, FAKE, blocks, n, 1, Hq, 8, L, start, starts, lens, cap, bt, pps, page,
+                                       pages, FAKE, ws)
+
+    assert chunk(q=None) == bad and chunk(blocks=None) == bad and chunk(blocks=FAKE + 2) == bad and chunk(n=0) == bad
+    assert chunk(n=129) == kb.KB_ERR_UNSUPPORTED and chunk(Hq=8) == kb.KB_ERR_UNSUPPORTED
+    assert chunk(start=193) == bad and chunk(start=-1) == bad and chunk(L=0) == bad and chunk(lens=FAKE) == bad
+    assert chunk(cap=1 << 23) == kb.KB_ERR_UNSUPPORTED and chunk(bt=FAKE, pps=2, page=64, pages=4) == bad
+
+    def decode(q=FAKE, n=4, ctx=10, lens=None, cap=256):
+        return kb.kb_attn_sparse_decode(q, FAKE, FAKE, FAKE, FAKE, n, 1, 32, 8, ctx, lens, cap, None, 0, 0, 0)
+
+    assert decode(q=None) == bad and decode(ctx=0) == bad and decode(ctx=257) == bad and decode(n=0) == bad
+    assert decode(lens=FAKE + 2) == bad
+    fwd = (FAKE,) * 4
+    assert kb.kb_attn_sparse_prefill_lse(*fwd, None, FAKE, 4, 1, 32, 8, 64, FAKE, ws) == bad
+    assert kb.kb_attn_sparse_prefill_lse(*fwd, FAKE, FAKE, 4, 1, 32, 8, 0, FAKE, ws) == bad
+    bwd = (FAKE,) * 8
+    assert kb.kb_attn_sparse_backward(*bwd, 4, FAKE, None, FAKE, 1, 32, 8, 64, FAKE, ws) == bad
+    assert kb.kb_attn_sparse_backward(*bwd, 4, FAKE + 8, FAKE, FAKE, 1, 32, 8, 64, FAKE, ws) == bad
+    assert kb.kb_attn_sparse_backward(*bwd, 4, FAKE, FAKE, FAKE, 1, 32, 4, 64, FAKE, ws) == kb.KB_ERR_UNSUPPORTED
