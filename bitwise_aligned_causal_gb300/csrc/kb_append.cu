@@ -187,7 +187,8 @@ template <bool kAppend>
 __global__ void __launch_bounds__(512) kb_append_kernel(const AppendArgs args) {
   __shared__ uint4 part[2][16][16];                     // [max, min][warp][chunk]
   __shared__ uint32_t amax_bits[4];
-  if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) return;
+  // one decision for the CTA: the word may change while its threads read it
+  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.err) != 0)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   const int u = lane & 7, r4 = lane >> 3;
   const int c = static_cast<int>(blockIdx.x) / (args.B * args.Hkv);    // which touched block

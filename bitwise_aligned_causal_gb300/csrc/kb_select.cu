@@ -136,15 +136,17 @@ __device__ __forceinline__ bool always_taken(const SelectArgs& a, int j, int nb)
 // ----------------------------------------------------------- a row per CTA
 //
 // One CTA of 16 warps per (row, batch, KV head); 16 lanes score a block (eight
-// channels of both bounds each), so a warp has two blocks of 512 bytes in
-// flight per step.
+// channels of both bounds each), so a warp has eight blocks of 512 bytes in
+// flight.
 constexpr int kSelectRowThreads = 512;
+constexpr int kSelectRowMax = 16;               // query rows per sequence up to which this kernel runs
 
 __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(const SelectArgs args) {
   extern __shared__ uint32_t sel_smem[];
   __shared__ float whole[kHeadDim];               // n
   __shared__ uint32_t amax_bits[8];
-  if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) return;
+  // one decision for the CTA: the word may change while its threads read it
+  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.err) != 0)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = blockIdx.x;
   const int g = static_cast<int>(item % args.Hkv);
@@ -195,21 +197,27 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
     np[e] = fmaxf(w, 0.0f);
     nm[e] = fminf(w, 0.0f);
   }
-  for (int j0 = warp * 2; j0 < nb; j0 += kSelectRowThreads / 16) {
-    const int j = j0 + (lane >> 4);
-    float s = 0.0f;
-    const bool scored = j < nb && !always_taken(args, j, nb);
-    if (scored) {
-      const __nv_bfloat16* box = box_of(args, b, g, j);
+  constexpr int kAtOnce = 4, kStep = kSelectRowThreads / 16;
+  for (int j0 = warp * 2 + (lane >> 4); j0 < nb + (lane >> 4); j0 += kStep * kAtOnce) {   // uniform over the warp
+    uint4 hi[kAtOnce], lo[kAtOnce];
+#pragma unroll
+    for (int a = 0; a < kAtOnce; ++a) {
+      const int j = j0 + a * kStep;
+      const __nv_bfloat16* box = j < nb && !always_taken(args, j, nb) ? box_of(args, b, g, j) : nullptr;
+      hi[a] = lo[a] = make_uint4(0u, 0u, 0u, 0u);
       if (box != nullptr) {
-        const uint4 hi = __ldg(reinterpret_cast<const uint4*>(box) + c);
-        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(box + kHeadDim) + c);
-        s = box_dot(hi, lo, np, nm);
+        hi[a] = __ldg(reinterpret_cast<const uint4*>(box) + c);
+        lo[a] = __ldg(reinterpret_cast<const uint4*>(box + kHeadDim) + c);
       }
     }
 #pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, m));
-    if (c == 0 && j < nb) sel_smem[j] = scored ? order_key(s) : kKeyForced;
+    for (int a = 0; a < kAtOnce; ++a) {
+      const int j = j0 + a * kStep;
+      float s = box_dot(hi[a], lo[a], np, nm);
+#pragma unroll
+      for (int m = 8; m >= 1; m >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, m));
+      if (c == 0 && j < nb) sel_smem[j] = always_taken(args, j, nb) ? kKeyForced : order_key(s);
+    }
   }
   __syncthreads();
   // rounds: every warp reduces chunks of 1024 keys to their n largest, until
@@ -243,17 +251,332 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
   }
 }
 
+// ------------------------------------------------------ 128 rows per CTA
+//
+// One CTA per (batch, KV head, 128 positions from a multiple of 128 on), so
+// its rows share their blocks 0 .. t.  Scores are one product of grid vectors,
+// [n+ | n-] (128 rows x 256) times [upper | lower] (blocks x 256), on the
+// tensor core, exact like every other order of summation.  They stay in TMEM
+// (a row per lane, a block per column), where one thread per row searches
+// its n largest: a trial value halves the range between the row's extremes
+// until exactly n scores are at or above it (ties: until the range is one
+// value).  Rows whose blocks exceed TMEM go on in passes of 256 blocks, the
+// winners of the earlier ones carried along in shared memory.
+// Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
+// half of TMEM let two CTAs share an SM, so one loads while the other
+// searches.
+struct SelectTileCfg {
+  static constexpr int kThreads = 256;
+  static constexpr int kChunk = 64;                         // blocks per MMA
+  static constexpr int kPass = 256;                         // blocks in TMEM at a time
+  static constexpr uint32_t kTmemCols = 256;
+  static constexpr uint32_t kASlab = 128 * 128;             // 64 of the 256 columns of n, 128 rows
+  static constexpr uint32_t kBSlab = kChunk * 128;
+  static constexpr uint32_t kAOff = 0;
+  static constexpr uint32_t kBOff = 4 * kASlab;
+  static constexpr uint32_t kBarOff = kBOff + 4 * kBSlab;
+  static constexpr uint32_t kMiscOff = kBarOff + 16;
+  static constexpr uint32_t kListOff = kMiscOff + 16;       // several passes: float score, int block per row and winner
+  static constexpr int kMaxListed = 32;
+};
+
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); }
+
+__global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_kernel(const SelectArgs args, int n_tiles) {
+  using Cfg = SelectTileCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kMiscOff);
+  volatile uint32_t* abort_flag = misc + 1;
+  const uint32_t bar = sbase + Cfg::kBarOff;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // one decision for the CTA: the word may change while its threads read it
+  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.err) != 0)) return;
+  const int bg = static_cast<int>(blockIdx.x) / n_tiles;
+  const int b = bg / args.Hkv, g = bg % args.Hkv;
+  int start = args.start, len = args.L;
+  if (args.starts != nullptr) {
+    start = args.starts[b];
+    if (args.lens != nullptr) len = args.lens[b];
+    if (start < 0 || len < 0 || len > args.L || start > args.kv_cap - len) {
+      if (threadIdx.x == 0) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
+      return;
+    }
+  }
+  const int t = start / kTileKeys + n_tiles - 1 - static_cast<int>(blockIdx.x) % n_tiles;   // last positions first
+  const int i0 = t * kTileKeys - start;                     // row index of the tile's first position (may be negative)
+  if (len == 0 || i0 >= len) return;
+  const int nb = t + 1;
+  const size_t out_row0 = (static_cast<size_t>(b) * args.Hkv + g) * args.L;
+  if (nb <= args.n) {
+    for (int e = threadIdx.x; e < kTileKeys * args.n; e += Cfg::kThreads) {
+      const int i = i0 + e / args.n, j = e % args.n;
+      if (i >= 0 && i < len) args.blocks[(out_row0 + i) * args.n + j] = j < nb ? j : -1;
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    misc[1] = 0u;
+    fence_mbar_init();
+  }
+  // by a warp that has not just branched on one thread: the allocation is one
+  // instruction of a whole, converged warp
+  if (warp == 4) {
+    __syncwarp();
+    tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+
+  // n of the tile's rows: 16 lanes per row, eight channels of the four heads
+  // each, written as the two halves n+ and n- of the A operand
+  {
+    const int c = lane & 15;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(args.q) +
+                                                    (static_cast<size_t>(b) * args.Hkv + g) * kGroup * args.L * kHeadDim);
+    const size_t head_step = static_cast<size_t>(args.L) * (kHeadDim / 8);
+    constexpr int kAtOnce = 2;                              // rows in flight per lane
+#pragma unroll 1
+    for (int m0 = 2 * warp + (lane >> 4); m0 < kTileKeys; m0 += 16 * kAtOnce) {
+      uint4 x[kAtOnce][kGroup];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int i = i0 + m0 + 16 * a;
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h)
+          x[a][h] = i >= 0 && i < len ? __ldg(q + h * head_step + static_cast<size_t>(i) * (kHeadDim / 8) + c)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) {
+          const uint32_t w[4] = {x[a][h].x, x[a][h].y, x[a][h].z, x[a][h].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        const float scale = exp2i(15 - grid_exponent(amax));
+        float u[8], umax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float v[kGroup];
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) {
+            const uint32_t w = e < 2 ? x[a][h].x : e < 4 ? x[a][h].y : e < 6 ? x[a][h].z : x[a][h].w;
+            v[h] = __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+          }
+          u[e] = whole_sum(v, scale);
+          umax = fmaxf(umax, fabsf(u[e]));
+        }
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1) umax = fmaxf(umax, __shfl_xor_sync(0xffffffffu, umax, m));
+        const float fit = exp2i(7 - grid_exponent(umax));
+        uint32_t np[4], nm[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w0 = rintf(__fmul_rn(u[2 * e], fit)), w1 = rintf(__fmul_rn(u[2 * e + 1], fit));
+          np[e] = pack_bf16x2(fmaxf(w0, 0.0f), fmaxf(w1, 0.0f));
+          nm[e] = pack_bf16x2(fminf(w0, 0.0f), fminf(w1, 0.0f));
+        }
+        const int m = m0 + 16 * a;
+        uint8_t* at = smem + Cfg::kAOff + (c >> 3) * Cfg::kASlab + (m >> 3) * 1024 + (m & 7) * 128 + (((c & 7) ^ (m & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(np[0], np[1], np[2], np[3]);
+        *reinterpret_cast<uint4*>(at + 2 * Cfg::kASlab) = make_uint4(nm[0], nm[1], nm[2], nm[3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = misc[0];
+
+  const int cand0 = args.keep_first, cand1 = nb - args.keep_last;      // blocks that are chosen by score
+  const int need = args.n - args.keep_first - args.keep_last;
+  const int passes = need > 0 ? (cand1 + Cfg::kPass - 1) / Cfg::kPass : 0;
+  float* list_s = reinterpret_cast<float*>(smem + Cfg::kListOff);        // [winner][row]
+  int* list_j = reinterpret_cast<int*>(smem + Cfg::kListOff) + Cfg::kMaxListed * 128;
+  int* staged = reinterpret_cast<int*>(smem + Cfg::kAOff);             // [row][n + 1], once A is no longer read
+  int listed = 0;                                                      // winners carried from earlier passes (any row's)
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int c0 = pass * Cfg::kPass, c1 = min(cand1, c0 + Cfg::kPass);
+    for (int j0 = c0; j0 < c1; j0 += Cfg::kChunk) {
+      // boxes of 64 blocks into the B operand (the layout of a box is its row)
+      for (int e = threadIdx.x; e < Cfg::kChunk * 32; e += Cfg::kThreads) {
+        const int r = e >> 5, c = e & 31, j = j0 + r;
+        uint4 val = make_uint4(0u, 0u, 0u, 0u);
+        if (j < c1) {
+          const __nv_bfloat16* box = box_of(args, b, g, j);
+          if (box != nullptr) val = __ldg(reinterpret_cast<const uint4*>(box) + c);
+        }
+        *reinterpret_cast<uint4*>(smem + Cfg::kBOff + (c >> 3) * Cfg::kBSlab + (r >> 3) * 1024 + (r & 7) * 128 +
+                                  (((c & 7) ^ (r & 7)) << 4)) = val;
+      }
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (threadIdx.x == 5 * 32) {                                        // warp 5 reads no TMEM
+        tc_fence_after();
+        constexpr uint32_t kIdesc = idesc_bf16_f32(128, Cfg::kChunk, 0);
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk)
+          mma_ss(tmem_base + static_cast<uint32_t>(j0 - c0), desc_kmajor(sbase + Cfg::kAOff, kk, 1024u, Cfg::kASlab),
+                 desc_kmajor(sbase + Cfg::kBOff, kk, 1024u, Cfg::kBSlab), kIdesc, kk > 0 ? 1u : 0u);
+        tc_commit(bar);
+      }
+      ok = mbar_wait(bar, phase, abort_flag, args.err, kDevTimeoutMma);   // the scores are there, B may be replaced
+      phase ^= 1u;
+      ok = __syncthreads_and(ok);
+      if (!ok) break;
+    }
+    if (!ok) break;
+    tc_fence_after();
+    if (warp < 4) {
+      const int row = 32 * warp + lane;
+      const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
+      const int cols = c1 - c0, skip = max(0, cand0 - c0);               // columns skip .. cols-1 are candidates
+      // fn(column, score) over the pass's candidates, 32 columns at a time;
+      // the whole warp calls it together
+      auto each32 = [&](auto fn) {
+        for (int k = 0; k < cols; k += 32) {
+          uint32_t x[32];
+          __syncwarp();
+          tmem_ld32_wait(s_tmem + static_cast<uint32_t>(k), x);
+          if (k < skip || k + 32 > cols) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (k + e < skip || k + e >= cols) x[e] = 0xFF800000u;      // -inf: below every trial
+          }
+          fn(k, x);
+        }
+      };
+      float hi = -INFINITY, lo = INFINITY;
+      each32([&](int k, const uint32_t (&x)[32]) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float v = __uint_as_float(x[e]);
+          hi = fmaxf(hi, v);
+          if (v != -INFINITY) lo = fminf(lo, v);
+        }
+      });
+      for (int w = 0; w < listed; ++w) {
+        const float v = list_s[w * 128 + row];
+        hi = fmaxf(hi, v);
+        lo = fminf(lo, v);
+      }
+      // the pass's winners: all of them when there are at most `need`, else
+      // those above the cut; ties at the cut from the lowest block on
+      const int have = cols - skip + listed;
+      uint32_t klo = order_key(lo), khi = order_key(hi) + 1u;            // count(>= klo) >= need > count(>= khi)
+      bool exact = have <= need;
+      int iter = 0;
+      while (true) {
+        const bool done = exact || khi - klo <= 1u;
+        if (__all_sync(0xffffffffu, done) || iter >= 80) break;         // 40 halvings of the values, 32 of the patterns
+        uint32_t kt = klo + ((khi - klo) >> 1);
+        const uint32_t kv = order_key(__fmaf_rn(0.5f, key_value(khi) - key_value(klo), key_value(klo)));
+        if (iter < 40 && kv > klo && kv < khi) kt = kv;                  // halve the values, not their bit patterns
+        const float trial = key_value(kt);
+        int count = 0;
+        each32([&](int k, const uint32_t (&x)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) count += __uint_as_float(x[e]) >= trial ? 1 : 0;
+        });
+        for (int w = 0; w < listed; ++w) count += list_s[w * 128 + row] >= trial ? 1 : 0;
+        if (!done) {
+          if (count >= need) klo = kt;
+          else khi = kt;
+          exact = count == need;
+        }
+        ++iter;
+      }
+      const float cut = key_value(klo);
+      int ties = 0x7FFFFFFF;                                             // scores equal to the cut that are taken
+      if (!__all_sync(0xffffffffu, exact)) {                               // the whole warp reads TMEM together
+        int above = 0;
+        each32([&](int k, const uint32_t (&x)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) above += __uint_as_float(x[e]) > cut ? 1 : 0;
+        });
+        for (int w = 0; w < listed; ++w) above += list_s[w * 128 + row] > cut ? 1 : 0;
+        if (!exact) ties = need - above;
+      }
+      const bool last = pass == passes - 1;
+      int* const mine = staged + row * (args.n + 1);
+      int at = 0;
+      auto take = [&](float v, int j) {
+        if (v > cut || (v == cut && ties-- > 0)) {
+          if (last) {
+            mine[args.keep_first + at] = j;
+          } else {
+            list_s[at * 128 + row] = v;
+            list_j[at * 128 + row] = j;
+          }
+          ++at;
+        }
+      };
+      for (int w = 0; w < listed; ++w) take(list_s[w * 128 + row], list_j[w * 128 + row]);
+      each32([&](int k, const uint32_t (&x)[32]) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (__uint_as_float(x[e]) >= cut) take(__uint_as_float(x[e]), c0 + k + e);
+      });
+      listed = min(need, have);
+    }
+    tc_fence_before();
+    __syncthreads();                                                     // TMEM has been read
+    tc_fence_after();
+  }
+  if (ok) {
+    // lists out, the kept blocks around the chosen ones
+    for (int e = threadIdx.x; e < kTileKeys * args.n; e += Cfg::kThreads) {
+      const int r = e / args.n, k = e % args.n, i = i0 + r;
+      if (i < 0 || i >= len) continue;
+      args.blocks[(out_row0 + i) * args.n + k] = k < args.keep_first ? k
+                                                 : k >= args.n - args.keep_last ? nb - args.n + k
+                                                                                : staged[r * (args.n + 1) + k];
+    }
+  }
+  __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  }
+}
+
 cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s) {
+  using Cfg = SelectTileCfg;
+  constexpr int kRowSmem = 200 * 1024, kTileSmem = static_cast<int>(Cfg::kListOff) + Cfg::kMaxListed * 128 * 8 + 1024;
   static bool configured[64] = {};
   if (!configured[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(kb_select_row_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(kb_select_row_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kb_select_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
     if (e != cudaSuccess) return e;
     configured[device] = true;
+  }
+  // A CTA of 128 rows pays from about 16 rows per sequence on.  Its lists of
+  // earlier passes hold 32 winners, so longer ones stay with it only while
+  // all blocks fit one pass.
+  const bool several = a.max_blocks - a.keep_last > Cfg::kPass;
+  if (a.L > kSelectRowMax && (!several || a.n - a.keep_first - a.keep_last <= Cfg::kMaxListed)) {
+    const int n_tiles = a.starts != nullptr ? (a.L + kTileKeys - 2) / kTileKeys + 1
+                                            : (a.start + a.L - 1) / kTileKeys - a.start / kTileKeys + 1;
+    const long long grid = static_cast<long long>(a.B) * a.Hkv * n_tiles;
+    const int smem = several ? kTileSmem : static_cast<int>(Cfg::kListOff) + 1024;
+    kb_select_tile_kernel<<<static_cast<unsigned>(grid), Cfg::kThreads, smem, s>>>(a, n_tiles);
+    return cudaGetLastError();
   }
   const int rounds = (a.max_blocks + kChunkKeys - 1) / kChunkKeys;
   const size_t smem = (static_cast<size_t>(a.max_blocks) + (a.max_blocks > kChunkKeys ? 4u * rounds * a.n : 0u)) * 4u;
   const long long rows = static_cast<long long>(a.B) * a.Hkv * a.L;
-  if (rows > 0x7FFFFFFFLL || smem > 200u * 1024u) return cudaErrorInvalidValue;
+  if (rows > 0x7FFFFFFFLL || smem > kRowSmem) return cudaErrorInvalidValue;
   kb_select_row_kernel<<<static_cast<unsigned>(rows), kSelectRowThreads, smem, s>>>(a);
   return cudaGetLastError();
 }

@@ -17,7 +17,8 @@ __global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const Spar
   extern __shared__ uint32_t row_mask[];              // per key block 0..own
   __shared__ int warp_count[kPlanThreads / 32];
   const int u = static_cast<int>(blockIdx.x);
-  if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) {
+  // one decision for the CTA: the word may change while its threads read it
+  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.err) != 0)) {
     // the attention kernel must not walk what an earlier call left here, even
     // if the error word is cleared before it starts
     if (threadIdx.x == 0) args.walk_len[u] = -1;

@@ -12,6 +12,7 @@ has not been built: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import shapes
@@ -251,10 +252,16 @@ def kb_attn_debug_wait_timeout(limit_us, stream=None) -> int:
 # the library's error word; until that word is cleared, later calls on the
 # device skip their work.  Pass check=True to call it after the launch.
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -538,9 +545,16 @@ def decode_seg_static(q, k, v, ctx_len, seg_tiles, out=None, stream=None, check=
 
 # ------------------------------------------------ rotation, cache append, block selection
 
-def _check_view(t, name):
+def _check_view(t, name, device):
     """A [*, *, *, 128] view whose last dimension is contiguous: slices of a fused projection need no copy."""
     torch = _torch()
+    try:
+        if t.dtype is torch.bfloat16 and t.get_device() == device and not t.data_ptr() % 16:
+            b, h, l, d = t.stride()
+            if d == 1 and not (b | h | l) & 7:
+                return
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
@@ -553,23 +567,64 @@ def _check_view(t, name):
     _on_current_device(t, name)
 
 
-def _strides(*tensors):
-    return (ctypes.c_longlong * (3 * len(tensors)))(*(x for t in tensors for x in
-                                                      ((0, 0, 0) if t is None else t.stride()[:3])))
+# A one-token call runs for a few microseconds on the GPU, so what a call costs on the host counts: a tensor that
+# passes the tests of _plain needs no closer look, shape rules are pure functions of shapes and remembered by them, and
+# the current stream's handle is read without making a stream object.
+
+def _plain(t, dtype, device):
+    try:
+        return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+    except AttributeError:
+        return False
+
+
+def _need_bf16(t, name, device, ndim=4):
+    if not _plain(t, _torch().bfloat16, device):
+        _check(t, name, ndim)
+
+
+def _need_i32(t, name, device):
+    if t is not None and not _plain(t, _torch().int32, device):
+        _check_i32(t, name)
+
+
+def _need_f32(t, name, device):
+    if t is not None and not _plain(t, _torch().float32, device):
+        _check_f32(t, name)
+
+
+_stride_array = functools.lru_cache(maxsize=1024)(lambda *strides: (ctypes.c_longlong * len(strides))(*strides))
+_shapes_append = functools.lru_cache(maxsize=1024)(shapes.append)
+_shapes_rope = functools.lru_cache(maxsize=1024)(shapes.rope)
+_shapes_select = functools.lru_cache(maxsize=1024)(shapes.select)
+_shapes_sparse = functools.lru_cache(maxsize=1024)(shapes.sparse)
+_shapes_backward = functools.lru_cache(maxsize=1024)(shapes.backward)
+
+
+def _stride3(t):
+    return (0, 0, 0) if t is None else t.stride()[:3]
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _optional(check, *pairs):
-    for t, name in pairs:
-        if t is not None:
-            check(t, name)
+def _shape(t):
+    return None if t is None else t.shape
 
 
-def _check_boxes(t, name):
-    _check(t, name, ndim=5)
+def _device():
+    return _torch().cuda.current_device()
+
+
+def _handle(stream, device):
+    """The stream's handle; None: that of the current device's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _per_sequence(B, t, name):
+    if t is not None and t.shape != (B,):
+        shapes.per_sequence(B, **{name: t.shape})
 
 
 def rope_table(n_pos, rot_dim=128, theta=10000.0, inv_freq=None, device=None, stream=None):
@@ -593,39 +648,52 @@ def rope_table(n_pos, rot_dim=128, theta=10000.0, inv_freq=None, device=None, st
 def rope(x, table, start=0, inverse=False, interleaved=False, out=None, stream=None, check=False):
     """Rotate x [B,H,L,128] (any strides, last dimension contiguous) by its positions start..start+L-1; inverse=True
     rotates by the negative angle, which turns the gradient of the result into the gradient of x."""
-    _check_view(x, "x")
-    _check_f32(table, "table")
-    _optional(_check, (out, "out"))
-    B, H, L, n_pos, rot_dim = shapes.rope(x.shape, table.shape, start, None if out is None else out.shape)
+    device = _device()
+    _check_view(x, "x", device)
+    if not _plain(table, _torch().float32, device):
+        _check_f32(table, "table")
+    if out is not None:
+        _need_bf16(out, "out", device)
+    start = int(start)
+    B, H, L, n_pos, rot_dim = _shapes_rope(x.shape, table.shape, start, _shape(out))
     o = _torch().empty((B, H, L, 128), dtype=x.dtype, device=x.device) if out is None else out
-    _finish(kb_attn_rope(x.data_ptr(), _strides(x), o.data_ptr(), table.data_ptr(), n_pos, rot_dim, int(interleaved),
-                         int(inverse), B, H, L, int(start), _stream(stream)), "kb_attn_rope", check, stream)
+    _finish(kb_attn_rope(x.data_ptr(), _stride_array(*x.stride()[:3]), o.data_ptr(), table.data_ptr(), n_pos, rot_dim,
+                         bool(interleaved), bool(inverse), B, H, L, start, _handle(stream, device)), "kb_attn_rope",
+            check, stream)
     return o
 
 
 def _append(q, k, v, k_cache, v_cache, table, start, starts, lens, block_table, boxes, interleaved, out, stream, check):
-    for t, n in ((k, "k"), (v, "v")):
-        _check_view(t, n)
-    _optional(_check_view, (q, "q"))
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, n)
-    _optional(_check_f32, (table, "table"))
-    _optional(_check_i32, (starts, "starts"), (lens, "lens"), (block_table, "block_table"))
-    _optional(_check_boxes, (boxes, "boxes"))
-    _optional(_check, (out, "out"))
-    shape = [None if t is None else t.shape for t in (q, k, v, k_cache, v_cache, table, boxes, block_table, out)]
-    B, Hq, Hkv, L, cap, num_pages, page, pps, n_pos, rot_dim = shapes.append(*shape)
-    shapes.per_sequence(B, starts=starts if starts is None else starts.shape, lens=lens if lens is None else lens.shape)
+    device = _device()
+    if q is not None:
+        _check_view(q, "q", device)
+    _check_view(k, "k", device)
+    _check_view(v, "v", device)
+    _need_bf16(k_cache, "k_cache", device)
+    _need_bf16(v_cache, "v_cache", device)
+    _need_f32(table, "table", device)
+    _need_i32(starts, "starts", device)
+    _need_i32(lens, "lens", device)
+    _need_i32(block_table, "block_table", device)
+    if boxes is not None:
+        _need_bf16(boxes, "boxes", device, 5)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    B, Hq, Hkv, L, cap, num_pages, page, pps, n_pos, rot_dim = _shapes_append(
+        _shape(q), k.shape, v.shape, k_cache.shape, v_cache.shape, _shape(table), _shape(boxes), _shape(block_table),
+        _shape(out))
+    _per_sequence(B, starts, "starts")
+    _per_sequence(B, lens, "lens")
     if starts is None and not 0 <= start <= cap - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
     if starts is None and table is not None and start > n_pos - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the table's 0..{n_pos - 1}")
     if q is not None and out is None:
         out = _torch().empty((B, Hq, L, 128), dtype=q.dtype, device=q.device)
-    _finish(kb_attn_append(_ptr(q), k.data_ptr(), v.data_ptr(), _strides(q, k, v), _ptr(out), k_cache.data_ptr(),
-                           v_cache.data_ptr(), _ptr(boxes), _ptr(table), n_pos, rot_dim, int(interleaved), B, Hq, Hkv,
-                           L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
-                           _stream(stream)), "kb_attn_append", check, stream)
+    _finish(kb_attn_append(_ptr(q), k.data_ptr(), v.data_ptr(), _stride_array(*_stride3(q), *_stride3(k), *_stride3(v)),
+                           _ptr(out), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(boxes), _ptr(table), n_pos, rot_dim,
+                           bool(interleaved), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table),
+                           pps, page, num_pages, _handle(stream, device)), "kb_attn_append", check, stream)
     return out
 
 
@@ -653,38 +721,44 @@ def block_boxes(k, kv_len=None, kv_lens=None, block_table=None, boxes=None, stre
     block_table: of its first kv_len keys (default: all), or kv_lens[b] of sequence b.  Returns bf16
     [B or num_pages, Hkv, blocks, 2, 128]; blocks beyond are zero in a new tensor and left as they were in `boxes`."""
     torch = _torch()
-    _check(k, "k")
-    _optional(_check_i32, (kv_lens, "kv_lens"), (block_table, "block_table"))
-    _optional(_check_boxes, (boxes, "boxes"))
-    B, Hkv, cap, num_pages, page, pps, box = shapes.block_boxes(
-        k.shape, None if block_table is None else block_table.shape, None if boxes is None else boxes.shape)
-    shapes.per_sequence(B, kv_lens=None if kv_lens is None else kv_lens.shape)
+    device = _device()
+    _need_bf16(k, "k", device)
+    _need_i32(kv_lens, "kv_lens", device)
+    _need_i32(block_table, "block_table", device)
+    if boxes is not None:
+        _need_bf16(boxes, "boxes", device, 5)
+    B, Hkv, cap, num_pages, page, pps, box = shapes.block_boxes(k.shape, _shape(block_table), _shape(boxes))
+    _per_sequence(B, kv_lens, "kv_lens")
     kv_len = cap if kv_len is None else int(kv_len)
     if not 1 <= kv_len <= cap:
         raise ValueError(f"kv_len must lie in 1..{cap} (the cache capacity), got {kv_len}")
     if boxes is None:
         boxes = torch.zeros(box, dtype=torch.bfloat16, device=k.device)
     _finish(kb_attn_block_boxes(k.data_ptr(), boxes.data_ptr(), B, Hkv, kv_len, _ptr(kv_lens), cap, _ptr(block_table),
-                                pps, page, num_pages, _stream(stream)), "kb_attn_block_boxes", check, stream)
+                                pps, page, num_pages, _handle(stream, device)), "kb_attn_block_boxes", check, stream)
     return boxes
 
 
 def _select(q, boxes, start, starts, lens, n, keep_first, keep_last, block_table, out, stream, check):
     torch = _torch()
-    _check(q, "q")
-    _check_boxes(boxes, "boxes")
-    _optional(_check_i32, (starts, "starts"), (lens, "lens"), (block_table, "block_table"), (out, "out"))
-    B, Hq, Hkv, L, per_plane, num_pages, page, pps = shapes.select(
-        q.shape, boxes.shape, n, keep_first, keep_last, None if block_table is None else block_table.shape,
-        None if out is None else out.shape)
-    shapes.per_sequence(B, starts=starts if starts is None else starts.shape, lens=lens if lens is None else lens.shape)
+    device = _device()
+    _need_bf16(q, "q", device)
+    _need_bf16(boxes, "boxes", device, 5)
+    _need_i32(starts, "starts", device)
+    _need_i32(lens, "lens", device)
+    _need_i32(block_table, "block_table", device)
+    _need_i32(out, "out", device)
+    B, Hq, Hkv, L, per_plane, num_pages, page, pps = _shapes_select(q.shape, boxes.shape, n, keep_first, keep_last,
+                                                                    _shape(block_table), _shape(out))
+    _per_sequence(B, starts, "starts")
+    _per_sequence(B, lens, "lens")
     if starts is None and not 0 <= start <= per_plane * shapes.BLOCK - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the boxes' 0..{per_plane * shapes.BLOCK - 1}")
     if out is None:
         out = torch.empty((B, Hkv, L, n), dtype=torch.int32, device=q.device)
     _finish(kb_attn_select_blocks(q.data_ptr(), boxes.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, n, keep_first,
                                   keep_last, start, _ptr(starts), _ptr(lens), per_plane, _ptr(block_table), pps, page,
-                                  num_pages, _stream(stream)), "kb_attn_select_blocks", check, stream)
+                                  num_pages, _handle(stream, device)), "kb_attn_select_blocks", check, stream)
     return out
 
 
@@ -707,17 +781,19 @@ def select_blocks_varlen(q, boxes, starts, n, lens=None, block_table=None, keep_
 
 # ------------------------------------------------------------- block-sparse attention
 
-def _sparse_args(q, k, v, blocks, block_table, out, positions):
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _check(t, n)
-    _check_i32(blocks, "blocks")
-    _optional(_check_i32, (block_table, "block_table"), *positions)
-    _optional(_check, (out, "out"))
-    sz = shapes.sparse(q.shape, k.shape, v.shape, blocks.shape, None if block_table is None else block_table.shape,
-                       None if out is None else out.shape)
-    for t, n in positions:
-        if t is not None:
-            shapes.per_sequence(sz[0], **{n: t.shape})
+def _sparse_args(device, q, k, v, blocks, block_table=None, out=None, positions=()):
+    _need_bf16(q, "q", device)
+    _need_bf16(k, "k", device)
+    _need_bf16(v, "v", device)
+    if not _plain(blocks, _torch().int32, device):
+        _check_i32(blocks, "blocks")
+    _need_i32(block_table, "block_table", device)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    sz = _shapes_sparse(q.shape, k.shape, v.shape, blocks.shape, _shape(block_table), _shape(out))
+    for t, name in positions:
+        _need_i32(t, name, device)
+        _per_sequence(sz[0], t, name)
     return sz
 
 
@@ -734,7 +810,8 @@ def _sparse_workspace(B, Hkv, L, n, cap, device, workspace, stream):
 
 
 def _sparse_chunk(q, k, v, start, starts, lens, blocks, block_table, out, workspace, stream, check):
-    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(q, k, v, blocks, block_table, out,
+    device = _device()
+    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(device, q, k, v, blocks, block_table, out,
                                                                ((starts, "starts"), (lens, "lens")))
     if starts is None and not 0 <= start <= cap - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
@@ -742,7 +819,7 @@ def _sparse_chunk(q, k, v, start, starts, lens, blocks, block_table, out, worksp
     ws = _sparse_workspace(B, Hkv, L, n, cap, q.device, workspace, stream)
     _finish(kb_attn_sparse_chunk(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
                                  Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
-                                 ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+                                 ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, device)),
             "kb_attn_sparse_chunk", check, stream)
     return o
 
@@ -763,7 +840,8 @@ def sparse_chunk_varlen(q, k, v, starts, blocks, lens=None, block_table=None, ou
 
 
 def _sparse_decode(q, k, v, ctx_len, ctx_lens, blocks, block_table, out, stream, check):
-    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(q, k, v, blocks, block_table, out,
+    device = _device()
+    B, Hq, Hkv, L, n, cap, num_pages, page, pps = _sparse_args(device, q, k, v, blocks, block_table, out,
                                                                ((ctx_lens, "ctx_lens"),))
     if L != 1:
         raise ValueError(f"decode takes one query row per (batch, head), got {L}")
@@ -772,7 +850,7 @@ def _sparse_decode(q, k, v, ctx_len, ctx_lens, blocks, block_table, out, stream,
     o = _torch().empty_like(q) if out is None else out
     _finish(kb_attn_sparse_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
                                   Hkv, ctx_len, _ptr(ctx_lens), cap, _ptr(block_table), pps, page, num_pages,
-                                  _stream(stream)), "kb_attn_sparse_decode", check, stream)
+                                  _handle(stream, device)), "kb_attn_sparse_decode", check, stream)
     return o
 
 
@@ -792,7 +870,8 @@ def sparse_prefill_lse(q, k, v, blocks, out=None, lse=None, workspace=None, stre
     """Training forward over listed key blocks of a whole sequence: (o, lse) as prefill_lse; a row that lists nothing
     has o = 0 and lse = -inf."""
     torch = _torch()
-    B, Hq, Hkv, S, n, cap, _, _, _ = _sparse_args(q, k, v, blocks, None, out, ())
+    device = _device()
+    B, Hq, Hkv, S, n, cap, _, _, _ = _sparse_args(device, q, k, v, blocks, None, out)
     shapes.prefill(q.shape, k.shape, v.shape)
     o = torch.empty_like(q) if out is None else out
     lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if lse is None else lse
@@ -801,7 +880,7 @@ def sparse_prefill_lse(q, k, v, blocks, out=None, lse=None, workspace=None, stre
     ws = _sparse_workspace(B, Hkv, S, n, cap, q.device, workspace, stream)
     _finish(kb_attn_sparse_prefill_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                        blocks.data_ptr(), n, B, Hq, Hkv, S, ws.data_ptr(),
-                                       ws.numel() * ws.element_size(), _stream(stream)),
+                                       ws.numel() * ws.element_size(), _handle(stream, device)),
             "kb_attn_sparse_prefill_lse", check, stream)
     return o, lse
 
@@ -811,12 +890,12 @@ def sparse_backward(q, k, v, o, dout, lse, blocks, delta=None, dq=None, dk=None,
     """Gradients (dq, dk, dv) of sparse_prefill_lse for output gradient dout; o, lse from it, blocks as given to it.
     Also returns delta [B,Hq,S] float32 = rowsum(dout * o)."""
     torch = _torch()
-    B, Hq, Hkv, S, n, _, _, _, _ = _sparse_args(q, k, v, blocks, None, None, ())
-    for t, name in ((o, "o"), (dout, "dout")):
-        _check(t, name)
-    _optional(_check, (dq, "dq"), (dk, "dk"), (dv, "dv"))
-    shapes.backward(q.shape, k.shape, v.shape, o.shape, dout.shape, None if dq is None else dq.shape,
-                    None if dk is None else dk.shape, None if dv is None else dv.shape)
+    device = _device()
+    B, Hq, Hkv, S, n, _, _, _, _ = _sparse_args(device, q, k, v, blocks)
+    for t, name in ((o, "o"), (dout, "dout"), (dq, "dq"), (dk, "dk"), (dv, "dv")):
+        if t is not None or name in ("o", "dout"):
+            _need_bf16(t, name, device)
+    _shapes_backward(q.shape, k.shape, v.shape, o.shape, dout.shape, _shape(dq), _shape(dk), _shape(dv))
     delta = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if delta is None else delta
     for t, name in ((lse, "lse"), (delta, "delta")):
         _check_f32(t, name)
@@ -828,6 +907,6 @@ def sparse_backward(q, k, v, o, dout, lse, blocks, delta=None, dq=None, dk=None,
     _finish(kb_attn_sparse_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                                     lse.data_ptr(), delta.data_ptr(), blocks.data_ptr(), n, dq.data_ptr(),
                                     dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, S, ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), _stream(stream)),
+                                    ws.numel() * ws.element_size(), _handle(stream, device)),
             "kb_attn_sparse_backward", check, stream)
     return dq, dk, dv, delta

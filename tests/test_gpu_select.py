@@ -48,6 +48,36 @@ def test_chunk_rows_equal_one_token_calls(kb, start, L, n):
         assert torch.equal(one[:, :, 0], got[:, :, i])
 
 
+@pytest.mark.parametrize("start,L,n,keep", [(39_000, 300, 16, {}), (39_000, 40, 40, {}), (20_000, 200, 128, {"keep_first": 0}),
+                                            (3000, 200, 2, {}), (70_000, 129, 34, {}), (33_000, 17, 5, {"keep_last": 4}),
+                                            (32_760, 30, 12, {"keep_first": 9})])
+def test_long_chunks_over_many_blocks(kb, start, L, n, keep):
+    """Around 256 blocks the scores of a chunk's rows take more than one pass."""
+    import torch
+
+    S = start + L
+    bx = kb.block_boxes(randn(250 + S, 1, 8, S, 128))
+    q = randn(251 + S, 1, 32, L, 128)
+    got = kb.select_blocks(q, bx, start, n, check=True, **keep)
+    rows = [0, L // 2, L - 1]
+    check_rows(got[0].cpu().numpy(), f64(q)[0], f64(bx)[0], np.arange(start, S), n, rows, **keep)
+    for i in range(0, L, 7):
+        one = kb.select_blocks(q[:, :, i:i + 1].contiguous(), bx, start + i, n, **keep)
+        assert torch.equal(one[:, :, 0], got[:, :, i])
+
+
+def test_ties_over_several_passes(kb):
+    import torch
+
+    bx = torch.ones(1, 8, 700, 2, 128, dtype=torch.bfloat16, device="cuda")
+    bx[:, :, 300] = 2.0
+    bx[:, :, 650] = 2.0
+    q = torch.ones(1, 32, 100, 128, dtype=torch.bfloat16, device="cuda")
+    got = kb.select_blocks(q, bx, 699 * 128, 8, check=True)
+    want = torch.tensor([0, 1, 2, 3, 4, 300, 650, 699], dtype=torch.int32)
+    assert bool((got.cpu() == want).all())
+
+
 def test_ties_go_to_the_lowest_block(kb):
     import torch
 
