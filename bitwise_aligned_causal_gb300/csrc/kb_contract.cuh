@@ -200,13 +200,17 @@ __device__ __forceinline__ float row_softmax_tile(const uint32_t (&s)[128], int 
 // bf16 pair of keys 8r+2u, 8r+2u+1 (TMEM column 4r+u of P).  All 32 lanes of
 // the warp must call it together.
 //
-// kMaybeNone: the row may see none of the tile's keys (n_valid <= 0, masked
-// tiles of block-sparse attention).  Such a tile leaves the state as it was
-// and gives p = 0: -inf scores never move m, and while m is still -inf the
-// exponent takes 0 in its place, since -inf + inf has no value.
+// kMaybeNone: the row may see none of the tile's keys (masked tiles of
+// block-sparse attention): n_valid <= 0 with kMasked, `on` false without.
+// Such a tile leaves the state as it was and gives p = 0.  With kMasked the
+// scores are -inf then, which never move m, and while m is still -inf the
+// exponent takes 0 in its place, since -inf + inf has no value.  Without, all
+// 128 keys of the tile are the row's or none is, and a row that is off takes
+// the factor 0 and the offset -inf instead of c and -mc: 2^(s 0 - inf) = 0
+// costs nothing per key (scores are finite).
 template <bool kMasked, bool kMaybeNone = false>
 __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, int n_valid, RowState& st,
-                                                       uint32_t (&p)[16]) {
+                                                       uint32_t (&p)[16], bool on = true) {
   const float c = score_scale_log2();
   if (kMasked) {
 #pragma unroll
@@ -227,6 +231,7 @@ __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, in
   float tile_max = fmaxf(max3(my[0], my[1], my[2]), my[3]);
   tile_max = fmaxf(tile_max, __shfl_xor_sync(0xffffffffu, tile_max, 1));
   tile_max = fmaxf(tile_max, __shfl_xor_sync(0xffffffffu, tile_max, 2));
+  if (kMaybeNone && !kMasked && !on) tile_max = -INFINITY;
 
   float alpha = 1.0f;
   if (__fsub_rn(tile_max, st.m) > kRescaleThresholdRaw) {
@@ -235,8 +240,9 @@ __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, in
     st.m = tile_max;
     st.mc = mc_new;
   }
-  const float2 c2 = make_float2(c, c);
-  const float nmc = (kMaybeNone && st.m == -INFINITY) ? 0.0f : -st.mc;
+  const float cu = (kMaybeNone && !kMasked && !on) ? 0.0f : c;
+  const float2 c2 = make_float2(cu, cu);
+  const float nmc = (kMaybeNone && !kMasked && !on) ? -INFINITY : (kMaybeNone && st.m == -INFINITY) ? 0.0f : -st.mc;
   const float2 nmc2 = make_float2(nmc, nmc);
   float2 acc;
 #pragma unroll

@@ -381,7 +381,6 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     const int r0 = 16 * (warp >> 2) + (lane >> 2);                  // the thread's rows of the unit: r0 and r0 + 8
     const uint32_t lane_off = static_cast<uint32_t>(32 * q4 + 16 * (warp >> 2)) << 16;
     const int u4 = lane & 3;
-    const uint32_t warp_rows = 0xFFFFu << (16 * (warp >> 2));       // the warp's rows in an entry's mask
     const uint32_t o_tmem = tmem_base + Cfg::kOCol + lane_off;
     float2* stats = reinterpret_cast<float2*>(smem + Cfg::kStatsOff);
     int T = 0, G = 0;                                               // tiles, segments
@@ -428,14 +427,13 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         const bool diag = static_cast<int>(entry.x & kEntryBlock) == w.own;
         uint32_t pkA[16], pkB[16];
         float aA, aB;
-        if (!diag && (entry.y & warp_rows) == warp_rows) {
-          aA = row_softmax_tile_quad<false>(xA, u4, kTileKeys, sA, pkA);
-          aB = row_softmax_tile_quad<false>(xB, u4, kTileKeys, sB, pkB);
+        const bool onA = (entry.y >> r0) & 1u, onB = (entry.y >> (r0 + 8)) & 1u;
+        if (!diag) {
+          aA = row_softmax_tile_quad<false, true>(xA, u4, kTileKeys, sA, pkA, onA);
+          aB = row_softmax_tile_quad<false, true>(xB, u4, kTileKeys, sB, pkB, onB);
         } else {
-          const int vA = (entry.y >> r0) & 1u ? (diag ? p0 + r0 + 1 : kTileKeys) : 0;
-          const int vB = (entry.y >> (r0 + 8)) & 1u ? (diag ? p0 + r0 + 9 : kTileKeys) : 0;
-          aA = row_softmax_tile_quad<true, true>(xA, u4, vA, sA, pkA);
-          aB = row_softmax_tile_quad<true, true>(xB, u4, vB, sB, pkB);
+          aA = row_softmax_tile_quad<true, true>(xA, u4, onA ? p0 + r0 + 1 : 0, sA, pkA);
+          aB = row_softmax_tile_quad<true, true>(xB, u4, onB ? p0 + r0 + 9 : 0, sB, pkB);
         }
         if (freshA) aA = 1.0f;
         if (freshB) aB = 1.0f;
