@@ -24,7 +24,10 @@
 //   warp 10      TMA producer of the V ring (zeroes a V tail)
 //   warp 11      P V issuer
 //   warps 12..15 fold and epilogue: warp 12+h owns head h, lane r row r
-// TMEM: S0, S1, S2 (P over the first half of each), O of the running segment.
+// TMEM: S0, S1 (P over the first half of each), O0, O1.  Scattered lists give
+// segments of one or two tiles, so a segment's fold must not hold up the next
+// one's P V: segments alternate between two O buffers and two sets of row
+// statistics, at the price of the dense kernel's third S buffer.
 #include "kb_sparse.cuh"
 
 namespace kb {
@@ -37,9 +40,9 @@ struct SparseCfg {
   static constexpr int kPvWarp = 11;
   static constexpr int kFoldWarp0 = 12;
   static constexpr int kStages = 3;
-  static constexpr int kSBufs = kStages;
+  static constexpr int kSBufs = 2;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kOCol = kSBufs * 128u;
+  static constexpr uint32_t kOCol = kSBufs * 128u;         // two of them: segment G in O buffer G%2
   // 256 softmax, 128 producer/issuer and 128 fold threads share the launch's 512 x 128 registers
   static constexpr uint32_t kSoftmaxRegs = 136;
   static constexpr uint32_t kOtherRegs = 64;
@@ -51,20 +54,23 @@ struct SparseCfg {
   static constexpr int kBarQFull = 0;
   static constexpr int kBarKFull = 1;
   static constexpr int kBarVFull = kBarKFull + kStages;
-  static constexpr int kBarSFull = kBarVFull + kStages;    // S(T) written, K slot T%3 free
+  static constexpr int kBarKEmpty = kBarVFull + kStages;   // Q K^T(T) done, K slot T%3 free
+  static constexpr int kBarVEmpty = kBarKEmpty + kStages;  // P V(T) done, V slot T%3 free
+  static constexpr int kBarSFull = kBarVEmpty + kStages;   // S(T) written, in S buffer T%2
   static constexpr int kBarPFull = kBarSFull + kSBufs;     // P(T) written (256 arrivals)
-  static constexpr int kBarOFull = kBarPFull + kSBufs;     // P V(T) done, V slot T%3 free
+  static constexpr int kBarOFull = kBarPFull + kSBufs;     // P V(T) done, S buffer T%2 free
   static constexpr int kBarVReady = kBarOFull + kSBufs;    // a unit's last V tile with its tail zeroed
   static constexpr int kBarQEmpty = kBarVReady + kStages;  // a unit's last Q K^T done
-  static constexpr int kBarORead = kBarQEmpty + 1;         // a finished segment's O was read (128 fold threads)
-  static constexpr int kBarStFull = kBarORead + 1;         // a finished segment's (m, l) written (256 softmax)
-  static constexpr int kBarStEmpty = kBarStFull + 1;       // ... and read (128 fold threads)
-  static constexpr int kBarDrain = kBarStEmpty + 1;        // 2: one per MMA issuer
+  static constexpr int kBarSegDone = kBarQEmpty + 1;       // 2: segment G's last P V done
+  static constexpr int kBarORead = kBarSegDone + 2;        // 2: segment G's O was read (128 fold threads)
+  static constexpr int kBarStFull = kBarORead + 2;         // 2: segment G's (m, l) written (256 softmax)
+  static constexpr int kBarStEmpty = kBarStFull + 2;       // 2: ... and read (128 fold threads)
+  static constexpr int kBarDrain = kBarStEmpty + 2;        // 2: one per MMA issuer
   static constexpr int kNumBars = kBarDrain + 2;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kStatsOff = kMiscOff + 16;     // float2 (m, l) per row
-  static constexpr uint32_t kSmemUsed = kStatsOff + kTileRows * 8;
-  static constexpr uint32_t kSmemBytes = kSmemUsed + 1024;
+  static constexpr uint32_t kStatsOff = (kMiscOff + 16u + 15u) & ~15u;   // 2: float2 (m, l) per row
+  static constexpr uint32_t kSmemUsed = kStatsOff + 2u * kTileRows * 8;
+  static constexpr uint32_t kSmemBytes = kSmemUsed;        // the array is declared 1 KB aligned: no room is left to round up
 };
 static_assert(8 * 32 * SparseCfg::kSoftmaxRegs + 4 * 32 * SparseCfg::kOtherRegs + 4 * 32 * SparseCfg::kFoldRegs <=
                   512 * 128,
@@ -98,8 +104,7 @@ __global__ void __launch_bounds__(SparseCfg::kThreads, 1)
 kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const SparseArgs args) {
   using Cfg = SparseCfg;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kMiscOff);
@@ -111,10 +116,12 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg::kNumBars; ++i) {
       uint32_t count = 1u;
-      if ((i >= Cfg::kBarPFull && i < Cfg::kBarPFull + Cfg::kSBufs) || i == Cfg::kBarStFull) count = 256u;
-      if (i == Cfg::kBarORead || i == Cfg::kBarStEmpty) count = 128u;
+      if ((i >= Cfg::kBarPFull && i < Cfg::kBarPFull + Cfg::kSBufs) || (i >= Cfg::kBarStFull && i < Cfg::kBarStFull + 2))
+        count = 256u;
+      if ((i >= Cfg::kBarORead && i < Cfg::kBarORead + 2) || (i >= Cfg::kBarStEmpty && i < Cfg::kBarStEmpty + 2)) count = 128u;
       mbar_init(bar(i), count);
     }
+    if ((sbase & 1023u) != 0u) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));   // never expected
     misc[1] = (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) ? 1u : 0u;
     fence_mbar_init();
   }
@@ -135,10 +142,10 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     regs_increase<Cfg::kFoldRegs>();
     const int head = warp - Cfg::kFoldWarp0;
     const int row = 32 * head + lane;                                // TMEM lane
-    const uint32_t o_tmem = tmem_base + Cfg::kOCol + (static_cast<uint32_t>(32 * head) << 16);
+    const uint32_t o_tmem0 = tmem_base + Cfg::kOCol + (static_cast<uint32_t>(32 * head) << 16);
     const float2* stats = reinterpret_cast<const float2*>(smem + Cfg::kStatsOff);
     const float c = score_scale_log2();
-    int T = 0, G = 0;                                                // tiles, segments
+    int G = 0;                                                       // segments
     bool ok = !skip;
     KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
       if (!ok) break;
@@ -149,15 +156,16 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
       for (int i = 0; i < 128; ++i) oacc[i] = 0u;
       for (int j = 0; j < n && ok; ++j) {
         if (!(__ldg(&walk[j].x) & kEntrySegEnd)) continue;
-        const int t_last = T + j;                                    // the segment's last tile
-        ok = mbar_wait_idle(bar(Cfg::kBarStFull), G & 1, abort_flag, args.err, kDevTimeoutSoftmax, 256);
+        const int buf = G & 1;                                       // segment G's O and stats buffers
+        const uint32_t turn = (G >> 1) & 1;
+        const uint32_t o_tmem = o_tmem0 + 128u * buf;
+        ok = mbar_wait_idle(bar(Cfg::kBarStFull + buf), turn, abort_flag, args.err, kDevTimeoutSoftmax, 64);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float2 st = stats[row];
+        const float2 st = stats[kTileRows * buf + row];
         const RowState sg{st.x, __fmul_rn(st.x, c), st.y};
-        mbar_arrive(bar(Cfg::kBarStEmpty));
-        ok = mbar_wait_idle(bar(Cfg::kBarOFull + t_last % Cfg::kSBufs), (t_last / Cfg::kSBufs) & 1, abort_flag,
-                            args.err, kDevTimeoutMma, 32);
+        mbar_arrive(bar(Cfg::kBarStEmpty + buf));
+        ok = mbar_wait_idle(bar(Cfg::kBarSegDone + buf), turn, abort_flag, args.err, kDevTimeoutMma, 32);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -184,6 +192,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 #pragma unroll
             for (int i = 0; i < 16; ++i) oacc[base + i] = o[i];
           }
+          __syncwarp();                                              // rows differ; the next TMEM load is the whole warp's
         };
         tmem_ld16_issue(o_tmem, oa);
 #pragma unroll
@@ -196,10 +205,9 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           chunk(16 * (q + 1), ob);
         }
         tc_fence_before();
-        mbar_arrive(bar(Cfg::kBarORead));
+        mbar_arrive(bar(Cfg::kBarORead + buf));
         ++G;
       }
-      T += n;
       if (!ok) break;
       const int i = w.t * kUnitRows + lane - w.start;                // query row index in q / o
       if (i >= 0 && i < w.L) {
@@ -230,7 +238,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         const uint64_t keep = l2_policy_evict_last();
         const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
         const int full0 = is_v ? Cfg::kBarVFull : Cfg::kBarKFull;
-        const int empty0 = is_v ? Cfg::kBarOFull : Cfg::kBarSFull;   // slot T%3 free: P V(T) / Q K^T(T) done
+        const int empty0 = is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty;
         const uint32_t ring = sbase + (is_v ? Cfg::kVOff : Cfg::kKOff);
         if (lane == 0) {
           tma_prefetch_desc(tmap);
@@ -315,15 +323,15 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           if (n == 0) continue;
           ok = mbar_wait(bar(Cfg::kBarQFull), U & 1, abort_flag, args.err, kDevTimeoutTma);
           for (int j = 0; j < n && ok; ++j, ++T) {
-            const int sb = T % Cfg::kSBufs;
-            const uint32_t use = T / Cfg::kSBufs;
-            ok = mbar_wait(bar(Cfg::kBarKFull + sb), use & 1, abort_flag, args.err, kDevTimeoutTma);
+            const int sb = T % Cfg::kSBufs, slot = T % Cfg::kStages;
+            ok = mbar_wait(bar(Cfg::kBarKFull + slot), (T / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
             if (ok && T >= Cfg::kSBufs)
-              ok = mbar_wait(bar(Cfg::kBarOFull + sb), (use - 1) & 1, abort_flag, args.err, kDevTimeoutMma);
+              ok = mbar_wait(bar(Cfg::kBarOFull + sb), (T / Cfg::kSBufs - 1) & 1, abort_flag, args.err, kDevTimeoutMma);
             if (!ok) break;
             tc_fence_after();
-            issue_qk(tmem_base + sb * 128u, q_saddr, 1024u, kSlabBytes, sbase + Cfg::kKOff + sb * kTileBytes);
+            issue_qk(tmem_base + sb * 128u, q_saddr, 1024u, kSlabBytes, sbase + Cfg::kKOff + slot * kTileBytes);
             tc_commit(bar(Cfg::kBarSFull + sb));
+            tc_commit(bar(Cfg::kBarKEmpty + slot));
           }
           if (ok) tc_commit(bar(Cfg::kBarQEmpty));
           ++U;
@@ -336,7 +344,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     } else {
       // -------------------------------------------------------- P V issuer
       if (lane == 0 && !skip) {
-        int T = 0, F = 0;                                           // F: segments started
+        int T = 0, F = 0;                                           // F: segments finished
         uint32_t zero_parity = 0;                                   // bit s: zero-tail phases of V slot s, mod 2
         bool ok = true;
         KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
@@ -346,26 +354,30 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           for (int j = 0; j < n && ok; ++j, ++T) {
             const uint32_t entry = next;
             if (j + 1 < n) next = __ldg(&walk[j + 1].x);
-            const int sb = T % Cfg::kSBufs;
-            const uint32_t use = T / Cfg::kSBufs;
-            ok = mbar_wait_hint(bar(Cfg::kBarPFull + sb), use & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+            const int sb = T % Cfg::kSBufs, slot = T % Cfg::kStages;
+            ok = mbar_wait_hint(bar(Cfg::kBarPFull + sb), (T / Cfg::kSBufs) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             if (ok) {
               if (j == n - 1 && has_v_tail(args, w, entry)) {
-                ok = mbar_wait(bar(Cfg::kBarVReady + sb), (zero_parity >> sb) & 1u, abort_flag, args.err,
+                ok = mbar_wait(bar(Cfg::kBarVReady + slot), (zero_parity >> slot) & 1u, abort_flag, args.err,
                                kDevTimeoutTma);
-                zero_parity ^= 1u << sb;
+                zero_parity ^= 1u << slot;
               } else {
-                ok = mbar_wait(bar(Cfg::kBarVFull + sb), use & 1, abort_flag, args.err, kDevTimeoutTma);
+                ok = mbar_wait(bar(Cfg::kBarVFull + slot), (T / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
               }
             }
             const bool first = (entry & kEntrySegStart) != 0u;
-            if (ok && first && F > 0)
-              ok = mbar_wait(bar(Cfg::kBarORead), (F - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+            const int buf = F & 1;                                  // the segment's O buffer
+            if (ok && first && F >= 2)
+              ok = mbar_wait(bar(Cfg::kBarORead + buf), ((F >> 1) - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(tmem_base + Cfg::kOCol, tmem_base + sb * 128u, sbase + Cfg::kVOff + sb * kTileBytes, first);
+            issue_pv(tmem_base + Cfg::kOCol + 128u * buf, tmem_base + sb * 128u, sbase + Cfg::kVOff + slot * kTileBytes, first);
             tc_commit(bar(Cfg::kBarOFull + sb));
-            if (first) ++F;
+            tc_commit(bar(Cfg::kBarVEmpty + slot));
+            if (entry & kEntrySegEnd) {
+              tc_commit(bar(Cfg::kBarSegDone + buf));
+              ++F;
+            }
           }
         }
         if (!ok) {
@@ -381,7 +393,6 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     const int r0 = 16 * (warp >> 2) + (lane >> 2);                  // the thread's rows of the unit: r0 and r0 + 8
     const uint32_t lane_off = static_cast<uint32_t>(32 * q4 + 16 * (warp >> 2)) << 16;
     const int u4 = lane & 3;
-    const uint32_t o_tmem = tmem_base + Cfg::kOCol + lane_off;
     float2* stats = reinterpret_cast<float2*>(smem + Cfg::kStatsOff);
     int T = 0, G = 0;                                               // tiles, segments
     bool ok = !skip;
@@ -443,6 +454,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
+          const uint32_t o_tmem = tmem_base + Cfg::kOCol + 128u * (G & 1) + lane_off;
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             uint32_t o[32];
@@ -472,17 +484,18 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         mbar_arrive(bar(Cfg::kBarPFull + sb));
         if (entry.x & kEntrySegEnd) {
           // hand the finished segment's (m, l) to the fold warps, once they
-          // have read the previous segment's
-          if (G > 0) {
-            ok = mbar_wait(bar(Cfg::kBarStEmpty), (G - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+          // have read those of the segment two before
+          const int buf = G & 1;
+          if (G >= 2) {
+            ok = mbar_wait(bar(Cfg::kBarStEmpty + buf), ((G >> 1) - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
           if (u4 == 0) {
-            stats[32 * q4 + r0] = make_float2(sA.m, sA.l);
-            stats[32 * q4 + r0 + 8] = make_float2(sB.m, sB.l);
+            stats[kTileRows * buf + 32 * q4 + r0] = make_float2(sA.m, sA.l);
+            stats[kTileRows * buf + 32 * q4 + r0 + 8] = make_float2(sB.m, sB.l);
           }
-          mbar_arrive(bar(Cfg::kBarStFull));
+          mbar_arrive(bar(Cfg::kBarStFull + buf));
           ++G;
         }
       }
