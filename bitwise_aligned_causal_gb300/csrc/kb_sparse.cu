@@ -24,10 +24,12 @@
 //   warp 10      TMA producer of the V ring (zeroes a V tail)
 //   warp 11      P V issuer
 //   warps 12..15 fold and epilogue: warp 12+h owns head h, lane r row r
-// TMEM: S0, S1 (P over the first half of each), O0, O1.  Scattered lists give
-// segments of one or two tiles, so a segment's fold must not hold up the next
-// one's P V: segments alternate between two O buffers and two sets of row
-// statistics, at the price of the dense kernel's third S buffer.
+// TMEM: S, P0, P1 (64 columns each), O0, O1.  Scattered lists give segments of
+// one or two tiles, so a segment's fold must not hold up the next one's P V:
+// segments alternate between two O buffers and two sets of row statistics.
+// One S buffer is enough beside them, because P has columns of its own: the
+// softmax warps read a tile's scores at once and release them before they
+// compute, so Q K^T of the next tile runs under the softmax of this one.
 #include "kb_sparse.cuh"
 
 namespace kb {
@@ -40,9 +42,9 @@ struct SparseCfg {
   static constexpr int kPvWarp = 11;
   static constexpr int kFoldWarp0 = 12;
   static constexpr int kStages = 3;
-  static constexpr int kSBufs = 2;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kOCol = kSBufs * 128u;         // two of them: segment G in O buffer G%2
+  static constexpr uint32_t kPCol = 128u;                  // S in columns 0..127, then P(T) in P buffer T%2, 64 columns
+  static constexpr uint32_t kOCol = 256u;                  // two of them: segment G in O buffer G%2
   // 256 softmax, 128 producer/issuer and 128 fold threads share the launch's 512 x 128 registers
   static constexpr uint32_t kSoftmaxRegs = 136;
   static constexpr uint32_t kOtherRegs = 64;
@@ -56,10 +58,11 @@ struct SparseCfg {
   static constexpr int kBarVFull = kBarKFull + kStages;
   static constexpr int kBarKEmpty = kBarVFull + kStages;   // Q K^T(T) done, K slot T%3 free
   static constexpr int kBarVEmpty = kBarKEmpty + kStages;  // P V(T) done, V slot T%3 free
-  static constexpr int kBarSFull = kBarVEmpty + kStages;   // S(T) written, in S buffer T%2
-  static constexpr int kBarPFull = kBarSFull + kSBufs;     // P(T) written (256 arrivals)
-  static constexpr int kBarOFull = kBarPFull + kSBufs;     // P V(T) done, S buffer T%2 free
-  static constexpr int kBarVReady = kBarOFull + kSBufs;    // a unit's last V tile with its tail zeroed
+  static constexpr int kBarSFull = kBarVEmpty + kStages;   // S(T) written
+  static constexpr int kBarSRead = kBarSFull + 1;          // S(T) read (256 arrivals)
+  static constexpr int kBarPFull = kBarSRead + 1;          // 2: P(T) written (256 arrivals)
+  static constexpr int kBarPDone = kBarPFull + 2;          // 2: P V(T) done, P buffer T%2 free
+  static constexpr int kBarVReady = kBarPDone + 2;         // a unit's last V tile with its tail zeroed
   static constexpr int kBarQEmpty = kBarVReady + kStages;  // a unit's last Q K^T done
   static constexpr int kBarSegDone = kBarQEmpty + 1;       // 2: segment G's last P V done
   static constexpr int kBarORead = kBarSegDone + 2;        // 2: segment G's O was read (128 fold threads)
@@ -116,7 +119,8 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg::kNumBars; ++i) {
       uint32_t count = 1u;
-      if ((i >= Cfg::kBarPFull && i < Cfg::kBarPFull + Cfg::kSBufs) || (i >= Cfg::kBarStFull && i < Cfg::kBarStFull + 2))
+      if (i == Cfg::kBarSRead || (i >= Cfg::kBarPFull && i < Cfg::kBarPFull + 2) ||
+          (i >= Cfg::kBarStFull && i < Cfg::kBarStFull + 2))
         count = 256u;
       if ((i >= Cfg::kBarORead && i < Cfg::kBarORead + 2) || (i >= Cfg::kBarStEmpty && i < Cfg::kBarStEmpty + 2)) count = 128u;
       mbar_init(bar(i), count);
@@ -323,14 +327,13 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           if (n == 0) continue;
           ok = mbar_wait(bar(Cfg::kBarQFull), U & 1, abort_flag, args.err, kDevTimeoutTma);
           for (int j = 0; j < n && ok; ++j, ++T) {
-            const int sb = T % Cfg::kSBufs, slot = T % Cfg::kStages;
+            const int slot = T % Cfg::kStages;
             ok = mbar_wait(bar(Cfg::kBarKFull + slot), (T / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
-            if (ok && T >= Cfg::kSBufs)
-              ok = mbar_wait(bar(Cfg::kBarOFull + sb), (T / Cfg::kSBufs - 1) & 1, abort_flag, args.err, kDevTimeoutMma);
+            if (ok && T > 0) ok = mbar_wait_hint(bar(Cfg::kBarSRead), (T - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             if (!ok) break;
             tc_fence_after();
-            issue_qk(tmem_base + sb * 128u, q_saddr, 1024u, kSlabBytes, sbase + Cfg::kKOff + slot * kTileBytes);
-            tc_commit(bar(Cfg::kBarSFull + sb));
+            issue_qk(tmem_base, q_saddr, 1024u, kSlabBytes, sbase + Cfg::kKOff + slot * kTileBytes);
+            tc_commit(bar(Cfg::kBarSFull));
             tc_commit(bar(Cfg::kBarKEmpty + slot));
           }
           if (ok) tc_commit(bar(Cfg::kBarQEmpty));
@@ -354,8 +357,8 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
           for (int j = 0; j < n && ok; ++j, ++T) {
             const uint32_t entry = next;
             if (j + 1 < n) next = __ldg(&walk[j + 1].x);
-            const int sb = T % Cfg::kSBufs, slot = T % Cfg::kStages;
-            ok = mbar_wait_hint(bar(Cfg::kBarPFull + sb), (T / Cfg::kSBufs) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+            const int pb = T & 1, slot = T % Cfg::kStages;
+            ok = mbar_wait_hint(bar(Cfg::kBarPFull + pb), (T >> 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             if (ok) {
               if (j == n - 1 && has_v_tail(args, w, entry)) {
                 ok = mbar_wait(bar(Cfg::kBarVReady + slot), (zero_parity >> slot) & 1u, abort_flag, args.err,
@@ -371,8 +374,9 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
               ok = mbar_wait(bar(Cfg::kBarORead + buf), ((F >> 1) - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(tmem_base + Cfg::kOCol + 128u * buf, tmem_base + sb * 128u, sbase + Cfg::kVOff + slot * kTileBytes, first);
-            tc_commit(bar(Cfg::kBarOFull + sb));
+            issue_pv(tmem_base + Cfg::kOCol + 128u * buf, tmem_base + Cfg::kPCol + 64u * pb,
+                     sbase + Cfg::kVOff + slot * kTileBytes, first);
+            tc_commit(bar(Cfg::kBarPDone + pb));
             tc_commit(bar(Cfg::kBarVEmpty + slot));
             if (entry & kEntrySegEnd) {
               tc_commit(bar(Cfg::kBarSegDone + buf));
@@ -405,12 +409,11 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
       for (int j = 0; j < n && ok; ++j, ++T) {
         const uint2 entry = next;
         if (j + 1 < n) next = __ldg(&walk[j + 1]);
-        const int sb = T % Cfg::kSBufs;
-        ok = mbar_wait_hint(bar(Cfg::kBarSFull + sb), (T / Cfg::kSBufs) & 1, abort_flag, args.err, kDevTimeoutMma);
+        ok = mbar_wait_hint(bar(Cfg::kBarSFull), T & 1, abort_flag, args.err, kDevTimeoutMma);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t s_tmem = tmem_base + sb * 128u + lane_off;
+        const uint32_t s_tmem = tmem_base + lane_off;
         float xA[32], xB[32];
         {
           uint32_t v0[32], v1[32];
@@ -427,6 +430,9 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             xB[16 + 2 * r + 1] = __uint_as_float(v1[4 * r + 3]);
           }
         }
+        // S is in registers: the next tile's Q K^T may overwrite it
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::kBarSRead));
         const bool seg_start = (entry.x & kEntrySegStart) != 0u;
         if (seg_start) {                                            // C5: each segment starts fresh
           sA = row_state_init();
@@ -449,8 +455,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         if (freshA) aA = 1.0f;
         if (freshB) aB = 1.0f;
         if (!seg_start && __any_sync(0xffffffffu, aA != 1.0f || aB != 1.0f)) {
-          ok = mbar_wait(bar(Cfg::kBarOFull + (T - 1) % Cfg::kSBufs), ((T - 1) / Cfg::kSBufs) & 1, abort_flag,
-                         args.err, kDevTimeoutMma);
+          ok = mbar_wait(bar(Cfg::kBarPDone + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag, args.err, kDevTimeoutMma);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -473,15 +478,22 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             tmem_st_16x256b_x8(o_tmem + 64u * half, o);
           }
         }
+        const int pb = T & 1;
+        if (T >= 2) {                                               // P V(T-2) has read this P buffer
+          ok = mbar_wait(bar(Cfg::kBarPDone + pb), ((T >> 1) - 1) & 1, abort_flag, args.err, kDevTimeoutMma);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
         {
           uint32_t pv[32];
 #pragma unroll
           for (int r = 0; r < 16; ++r) { pv[2 * r] = pkA[r]; pv[2 * r + 1] = pkB[r]; }
-          tmem_st_16x128b_x16(s_tmem, pv);
+          tmem_st_16x128b_x16(tmem_base + Cfg::kPCol + 64u * pb + lane_off, pv);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar(Cfg::kBarPFull + sb));
+        mbar_arrive(bar(Cfg::kBarPFull + pb));
         if (entry.x & kEntrySegEnd) {
           // hand the finished segment's (m, l) to the fold warps, once they
           // have read those of the segment two before
