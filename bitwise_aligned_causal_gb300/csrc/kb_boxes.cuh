@@ -23,14 +23,18 @@ __device__ __forceinline__ int grid_exponent(float amax) {
 // 2^n for n in [-126, 127].
 __device__ __forceinline__ float exp2i(int n) { return __int_as_float((n + 127) << 23); }
 
+// rint of |x| < 2^22 (ties to even): at 1.5 * 2^23 and above fp32 has no
+// fraction bits, so the sum rounds to a whole number.  Two additions, where a
+// conversion instruction takes a quarter-rate pipe.
+__device__ __forceinline__ float rint_small(float x) { return __fsub_rn(__fadd_rn(x, 12582912.0f), 12582912.0f); }
+
 // The four heads' values of one channel as whole numbers of 2^(E-15), summed
-// (below 2^17, so every step is exact); values beyond the grid saturate and
-// NaN counts as 0.
+// (below 2^17, so every step is exact); values beyond the grid saturate.
 __device__ __forceinline__ float whole_sum(const float (&q)[4], float scale) {
   float u = 0.0f;
 #pragma unroll
   for (int h = 0; h < 4; ++h)
-    u = __fadd_rn(u, static_cast<float>(min(max(__float2int_rn(__fmul_rn(q[h], scale)), -32512), 32512)));
+    u = __fadd_rn(u, rint_small(fminf(fmaxf(__fmul_rn(q[h], scale), -32512.0f), 32512.0f)));
   return u;
 }
 

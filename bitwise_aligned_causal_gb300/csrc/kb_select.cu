@@ -18,9 +18,10 @@
 // the others by score, ties to the lowest block, until n are taken.  They go
 // out in ascending order, -1 behind the last when there are fewer than n.
 //
-// The n largest keys are found without sorting: scores become unsigned whole
-// numbers of the same order, and the n-th largest is built bit by bit from
-// the counts of the keys at or above a trial value.
+// The n largest scores are found without sorting: a trial value halves the
+// range between the smallest and the largest score until exactly n scores are
+// at or above it; only ties keep the search going until the range is a single
+// value, of which the first blocks are then taken.
 #include "kb_boxes.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
@@ -29,65 +30,82 @@ namespace kb {
 
 namespace {
 
-constexpr uint32_t kKeyForced = 0xFFFFFFFFu;    // above every score
-constexpr int kChunkKeys = 1024;                // keys a warp searches at once: 32 registers per lane
+constexpr int kChunkKeys = 1024;                // scores a warp searches at once: 32 registers per lane
 
 // Scores (finite) as unsigned keys of the same order; -0 counts as +0.
 __device__ __forceinline__ uint32_t order_key(float s) {
   const uint32_t b = __float_as_uint(__fadd_rn(s, 0.0f));
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); }
 
-// The warp's n largest of m <= 1024 keys, in place order (ties: the first
-// ones), handed to emit(place among the chosen, place among the keys).
-// Returns how many there are (min(n, m)).
+// Search for the value that exactly `need` scores are at or above: the range
+// [lo, hi) of keys with count(>= lo) >= need > count(>= hi).
+struct CutSearch {
+  uint32_t lo, hi;
+  bool exact;                                   // exactly `need` scores are at or above lo's value
+  __device__ __forceinline__ bool done() const { return exact || hi - lo <= 1u; }
+  // The next key to try: the middle of the values, and after 40 halvings that
+  // of their bit patterns (32 more end any search).
+  __device__ __forceinline__ uint32_t trial(int iter) const {
+    const float a = key_value(lo), b = key_value(hi);
+    const uint32_t mid = order_key(__fmaf_rn(0.5f, __fsub_rn(b, a), a));
+    return iter < 40 && mid > lo && mid < hi ? mid : lo + ((hi - lo) >> 1);
+  }
+  __device__ __forceinline__ void counted(uint32_t key, int count, int need) {
+    if (count >= need) lo = key;
+    else hi = key;
+    exact = count == need;
+  }
+  __device__ __forceinline__ float cut() const { return key_value(lo); }
+};
+constexpr int kMaxTrials = 80;
+
+// The warp's n largest of m <= 1024 scores, in place order (ties: the first
+// ones), handed to emit(place among the chosen, place among the scores).
 template <class Emit>
-__device__ __forceinline__ int warp_largest(const uint32_t* keys, int m, int n, int lane, Emit emit) {
-  uint32_t r[kChunkKeys / 32];
+__device__ __forceinline__ void warp_largest(const float* scores, int m, int n, int lane, Emit emit) {
+  float r[kChunkKeys / 32];
+  float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kChunkKeys / 32; ++i) {
     if (i * 32 >= m) break;
-    r[i] = i * 32 + lane < m ? keys[i * 32 + lane] : 0u;
+    const bool in = i * 32 + lane < m;
+    r[i] = in ? scores[i * 32 + lane] : -INFINITY;          // below every trial
+    hi = fmaxf(hi, r[i]);
+    lo = fminf(lo, in ? r[i] : INFINITY);
   }
-  uint32_t T = 0;
-  int ties = 0;                                   // keys equal to T that are taken; < 0: all
-  if (m > n) {
-    bool exact = false;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t trial = T | (1u << bit);
-      int c = 0;
+  CutSearch c{__reduce_min_sync(0xffffffffu, order_key(lo)), __reduce_max_sync(0xffffffffu, order_key(hi)) + 1u, m <= n};
+  for (int iter = 0; iter < kMaxTrials && !c.done(); ++iter) {
+    const uint32_t key = c.trial(iter);
+    const float t = key_value(key);
+    int count = 0;
 #pragma unroll
-      for (int i = 0; i < kChunkKeys / 32; ++i) {
-        if (i * 32 >= m) break;
-        c += r[i] >= trial ? 1 : 0;
-      }
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c >= n) T = trial;
-      if (c == n) { exact = true; break; }
+    for (int i = 0; i < kChunkKeys / 32; ++i) {
+      if (i * 32 >= m) break;
+      count += r[i] >= t ? 1 : 0;
     }
-    if (exact) {
-      ties = -1;
-    } else {
-      int above = 0;
+    c.counted(key, __reduce_add_sync(0xffffffffu, count), n);
+  }
+  const float cut = c.cut();
+  int ties = 0;                                             // scores equal to the cut that are taken
+  if (!c.exact) {
+    int above = 0;
 #pragma unroll
-      for (int i = 0; i < kChunkKeys / 32; ++i) {
-        if (i * 32 >= m) break;
-        above += r[i] > T ? 1 : 0;
-      }
-      ties = n - __reduce_add_sync(0xffffffffu, above);
+    for (int i = 0; i < kChunkKeys / 32; ++i) {
+      if (i * 32 >= m) break;
+      above += r[i] > cut ? 1 : 0;
     }
-  } else {
-    ties = -1;
+    ties = n - __reduce_add_sync(0xffffffffu, above);
   }
   int taken = 0, tied = 0;
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int i = 0; i < kChunkKeys / 32; ++i) {
     if (i * 32 >= m) break;
-    const bool in = i * 32 + lane < m;
-    bool take = in && r[i] >= T;
-    if (ties >= 0) {
-      const bool eq = in && r[i] == T;
+    bool take = i * 32 + lane < m && r[i] >= cut;
+    if (!c.exact) {
+      const bool eq = take && r[i] == cut;
       const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
       if (eq) take = tied + __popc(eqs & below) < ties;
       tied += __popc(eqs);
@@ -96,7 +114,6 @@ __device__ __forceinline__ int warp_largest(const uint32_t* keys, int m, int n, 
     if (take) emit(taken + __popc(mask & below), i * 32 + lane);
     taken += __popc(mask);
   }
-  return taken;
 }
 
 // Position of row i of sequence b, or -1 when the row does not exist; a bad
@@ -127,54 +144,76 @@ __device__ __forceinline__ const __nv_bfloat16* box_of(const SelectArgs& a, int 
   return boxes + ((static_cast<size_t>(pg) * a.Hkv + g) * a.blocks_per_plane + j % a.blocks_per_plane) * 2 * kHeadDim;
 }
 
-__device__ __forceinline__ bool always_taken(const SelectArgs& a, int j, int nb) {
-  return j < a.keep_first || j >= nb - a.keep_last;
-}
-
 }  // namespace
 
 // ----------------------------------------------------------- a row per CTA
 //
 // One CTA of 16 warps per (row, batch, KV head); 16 lanes score a block (eight
 // channels of both bounds each), so a warp has eight blocks of 512 bytes in
-// flight.
+// flight, the first of them while the query is still on its way to whole
+// numbers.  For one token the boxes are read once and nothing else counts.
 constexpr int kSelectRowThreads = 512;
 constexpr int kSelectRowMax = 16;               // query rows per sequence up to which this kernel runs
 
 __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(const SelectArgs args) {
-  extern __shared__ uint32_t sel_smem[];
+  extern __shared__ float sel_smem[];
   __shared__ float whole[kHeadDim];               // n
   __shared__ uint32_t amax_bits[8];
-  // one decision for the CTA: the word may change while its threads read it
-  if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.err) != 0)) return;
+  const bool failed = *reinterpret_cast<volatile uint32_t*>(args.err) != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = blockIdx.x;
   const int g = static_cast<int>(item % args.Hkv);
   const int b = static_cast<int>(item / args.Hkv % args.B);
   const int i = static_cast<int>(item / (static_cast<long long>(args.Hkv) * args.B));
   const int pos = row_position(args, b, i);
-  if (pos < 0) return;
-  const int nb = pos / kTileKeys + 1;
+  const int nb = pos < 0 ? 0 : pos / kTileKeys + 1;
+  const int c0 = args.keep_first, m = nb - args.keep_first - args.keep_last;   // blocks c0 .. c0+m-1 are chosen by score
+  const int need = args.n - args.keep_first - args.keep_last;
+  // the first boxes and the query leave together
+  constexpr int kAtOnce = 4, kStep = kSelectRowThreads / 16;
+  const int c = lane & 15;
+  uint4 hi[kAtOnce], lo[kAtOnce];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int a = 0; a < kAtOnce; ++a) {
+      const int j = j0 + a * kStep;
+      const __nv_bfloat16* box = j < m ? box_of(args, b, g, c0 + j) : nullptr;
+      hi[a] = lo[a] = make_uint4(0u, 0u, 0u, 0u);
+      if (box != nullptr) {
+        hi[a] = __ldg(reinterpret_cast<const uint4*>(box) + c);
+        lo[a] = __ldg(reinterpret_cast<const uint4*>(box + kHeadDim) + c);
+      }
+    }
+  };
+  const int j_first = warp * 2 + (lane >> 4);
+  const bool scored = nb > args.n && need > 0;
+  float q[kGroup];
+  if (scored) {
+    fetch(j_first);
+    if (warp < 4) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int h = 0; h < kGroup; ++h) {
+        q[h] = __bfloat162float(static_cast<const __nv_bfloat16*>(
+            args.q)[((static_cast<size_t>(b) * args.Hkv + g) * kGroup + h) * args.L * kHeadDim +
+                    static_cast<size_t>(i) * kHeadDim + threadIdx.x]);
+        mx = fmaxf(mx, fabsf(q[h]));
+      }
+      const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      if (lane == 0) amax_bits[warp] = mb;
+    }
+  }
+  // one decision for the CTA: the word may change while its threads read it
+  if (__syncthreads_or(failed) || pos < 0) return;
   int* out = args.blocks + ((static_cast<size_t>(b) * args.Hkv + g) * args.L + i) * args.n;
-  if (nb <= args.n) {
-    for (int t = threadIdx.x; t < args.n; t += kSelectRowThreads) out[t] = t < nb ? t : -1;
+  if (!scored) {
+    if (nb > args.n)                              // nothing is scored, but a bad page is still found
+      for (int j = threadIdx.x; j < m; j += kSelectRowThreads) (void)box_of(args, b, g, c0 + j);
+    for (int t = threadIdx.x; t < args.n; t += kSelectRowThreads)
+      out[t] = nb <= args.n ? (t < nb ? t : -1) : t < args.keep_first ? t : nb - args.n + t;
     return;
   }
   // the whole-number query: thread d < 128 holds channel d
-  float q[kGroup];
-  if (warp < 4) {
-    float m = 0.0f;
-#pragma unroll
-    for (int h = 0; h < kGroup; ++h) {
-      q[h] = __bfloat162float(static_cast<const __nv_bfloat16*>(
-          args.q)[((static_cast<size_t>(b) * args.Hkv + g) * kGroup + h) * args.L * kHeadDim +
-                  static_cast<size_t>(i) * kHeadDim + threadIdx.x]);
-      m = fmaxf(m, fabsf(q[h]));
-    }
-    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (lane == 0) amax_bits[warp] = mb;
-  }
-  __syncthreads();
   float u = 0.0f;
   if (warp < 4) {
     const uint32_t mb = max(max(amax_bits[0], amax_bits[1]), max(amax_bits[2], amax_bits[3]));
@@ -185,11 +224,9 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
   __syncthreads();
   if (warp < 4) {
     const uint32_t ub = max(max(amax_bits[4], amax_bits[5]), max(amax_bits[6], amax_bits[7]));
-    whole[threadIdx.x] = rintf(__fmul_rn(u, exp2i(7 - grid_exponent(__uint_as_float(ub)))));
+    whole[threadIdx.x] = rint_small(__fmul_rn(u, exp2i(7 - grid_exponent(__uint_as_float(ub)))));
   }
   __syncthreads();
-  // scores
-  const int c = lane & 15;
   float np[8], nm[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -197,57 +234,51 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
     np[e] = fmaxf(w, 0.0f);
     nm[e] = fminf(w, 0.0f);
   }
-  constexpr int kAtOnce = 4, kStep = kSelectRowThreads / 16;
-  for (int j0 = warp * 2 + (lane >> 4); j0 < nb + (lane >> 4); j0 += kStep * kAtOnce) {   // uniform over the warp
-    uint4 hi[kAtOnce], lo[kAtOnce];
+  for (int j0 = j_first; j0 < m + (lane >> 4); j0 += kStep * kAtOnce) {        // uniform over the warp
+    float s[kAtOnce];
 #pragma unroll
-    for (int a = 0; a < kAtOnce; ++a) {
-      const int j = j0 + a * kStep;
-      const __nv_bfloat16* box = j < nb && !always_taken(args, j, nb) ? box_of(args, b, g, j) : nullptr;
-      hi[a] = lo[a] = make_uint4(0u, 0u, 0u, 0u);
-      if (box != nullptr) {
-        hi[a] = __ldg(reinterpret_cast<const uint4*>(box) + c);
-        lo[a] = __ldg(reinterpret_cast<const uint4*>(box + kHeadDim) + c);
-      }
-    }
+    for (int a = 0; a < kAtOnce; ++a) s[a] = box_dot(hi[a], lo[a], np, nm);
+    if (j0 + kStep * kAtOnce < m + (lane >> 4)) fetch(j0 + kStep * kAtOnce);
 #pragma unroll
-    for (int a = 0; a < kAtOnce; ++a) {
-      const int j = j0 + a * kStep;
-      float s = box_dot(hi[a], lo[a], np, nm);
+    for (int k = 8; k >= 1; k >>= 1)
 #pragma unroll
-      for (int m = 8; m >= 1; m >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, m));
-      if (c == 0 && j < nb) sel_smem[j] = always_taken(args, j, nb) ? kKeyForced : order_key(s);
-    }
+      for (int a = 0; a < kAtOnce; ++a) s[a] = __fadd_rn(s[a], __shfl_xor_sync(0xffffffffu, s[a], k));
+#pragma unroll
+    for (int a = 0; a < kAtOnce; ++a)
+      if (c == 0 && j0 + a * kStep < m) sel_smem[j0 + a * kStep] = s[a];
   }
   __syncthreads();
-  // rounds: every warp reduces chunks of 1024 keys to their n largest, until
-  // one chunk is left.  Round 0 reads the keys in block order, later rounds
-  // (key, block) pairs in the same order.
-  int m = nb;
-  uint32_t* keys = sel_smem;
+  // rounds: every warp reduces chunks of 1024 scores to their `need` largest,
+  // until one chunk is left.  Round 0 reads the scores in block order, later
+  // rounds (score, block) pairs in the same order.
+  int left = m;
+  float* scores = sel_smem;
   int* ids = nullptr;
   const int half = (args.max_blocks + kChunkKeys - 1) / kChunkKeys * args.n;     // pairs a round can leave
   int which = 0;
-  while (m > kChunkKeys) {
-    uint32_t* nk = sel_smem + args.max_blocks + which * 2 * half;
+  while (left > kChunkKeys) {
+    float* nk = sel_smem + args.max_blocks + which * 2 * half;
     int* ni = reinterpret_cast<int*>(nk + half);
-    const int chunks = (m + kChunkKeys - 1) / kChunkKeys;
+    const int chunks = (left + kChunkKeys - 1) / kChunkKeys;
     for (int k = warp; k < chunks; k += kSelectRowThreads / 32) {
-      const int from = k * kChunkKeys, mk = min(kChunkKeys, m - from);
-      warp_largest(keys + from, mk, args.n, lane, [&](int to, int at) {
-        nk[k * args.n + to] = keys[from + at];
-        ni[k * args.n + to] = ids == nullptr ? from + at : ids[from + at];
+      const int from = k * kChunkKeys;
+      warp_largest(scores + from, min(kChunkKeys, left - from), need, lane, [&](int to, int at) {
+        nk[k * need + to] = scores[from + at];
+        ni[k * need + to] = ids == nullptr ? from + at : ids[from + at];
       });
     }
-    const int last = m - (chunks - 1) * kChunkKeys;
-    m = (chunks - 1) * args.n + min(args.n, last);
-    keys = nk;
+    left = (chunks - 1) * need + min(need, left - (chunks - 1) * kChunkKeys);
+    scores = nk;
     ids = ni;
     which ^= 1;
     __syncthreads();
   }
   if (warp == 0) {
-    warp_largest(keys, m, args.n, lane, [&](int to, int at) { out[to] = ids == nullptr ? at : ids[at]; });
+    warp_largest(scores, left, need, lane, [&](int to, int at) { out[c0 + to] = c0 + (ids == nullptr ? at : ids[at]); });
+  } else if (warp == 1) {
+    for (int t = lane; t < args.keep_first + args.keep_last; t += 32)
+      if (t < args.keep_first) out[t] = t;
+      else out[args.n - args.keep_last + t - args.keep_first] = nb - args.keep_last + t - args.keep_first;
   }
 }
 
@@ -257,11 +288,11 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
 // its rows share their blocks 0 .. t.  Scores are one product of grid vectors,
 // [n+ | n-] (128 rows x 256) times [upper | lower] (blocks x 256), on the
 // tensor core, exact like every other order of summation.  They stay in TMEM
-// (a row per lane, a block per column), where one thread per row searches
-// its n largest: a trial value halves the range between the row's extremes
-// until exactly n scores are at or above it (ties: until the range is one
-// value).  Rows whose blocks exceed TMEM go on in passes of 256 blocks, the
-// winners of the earlier ones carried along in shared memory.
+// (a row per lane, a block per column).  Two threads search a row, each over
+// half of its blocks, the first 64 of which it keeps in registers; they add
+// their counts through shared memory.  Rows whose blocks exceed TMEM go on in
+// passes of 256 blocks, the winners of the earlier ones carried along in
+// shared memory.
 // Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
 // half of TMEM let two CTAs share an SM, so one loads while the other
 // searches.
@@ -276,11 +307,10 @@ struct SelectTileCfg {
   static constexpr uint32_t kBOff = 4 * kASlab;
   static constexpr uint32_t kBarOff = kBOff + 4 * kBSlab;
   static constexpr uint32_t kMiscOff = kBarOff + 16;
-  static constexpr uint32_t kListOff = kMiscOff + 16;       // several passes: float score, int block per row and winner
+  static constexpr uint32_t kCountOff = kMiscOff + 16;      // [parity][half][row] counts
+  static constexpr uint32_t kListOff = kCountOff + 2 * 2 * 128 * 4;   // several passes: score and block per winner and row
   static constexpr int kMaxListed = 32;
 };
-
-__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); }
 
 __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_kernel(const SelectArgs args, int n_tiles) {
   using Cfg = SelectTileCfg;
@@ -309,10 +339,15 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   if (len == 0 || i0 >= len) return;
   const int nb = t + 1;
   const size_t out_row0 = (static_cast<size_t>(b) * args.Hkv + g) * args.L;
-  if (nb <= args.n) {
+  const int cand0 = args.keep_first, cand1 = nb - args.keep_last;      // blocks that are chosen by score
+  const int need = args.n - args.keep_first - args.keep_last;
+  if (nb <= args.n || need == 0) {
+    if (nb > args.n)                                        // nothing is scored, but a bad page is still found
+      for (int j = cand0 + threadIdx.x; j < cand1; j += Cfg::kThreads) (void)box_of(args, b, g, j);
     for (int e = threadIdx.x; e < kTileKeys * args.n; e += Cfg::kThreads) {
-      const int i = i0 + e / args.n, j = e % args.n;
-      if (i >= 0 && i < len) args.blocks[(out_row0 + i) * args.n + j] = j < nb ? j : -1;
+      const int i = i0 + e / args.n, k = e % args.n;
+      if (i >= 0 && i < len)
+        args.blocks[(out_row0 + i) * args.n + k] = nb <= args.n ? (k < nb ? k : -1) : k < args.keep_first ? k : nb - args.n + k;
     }
     return;
   }
@@ -329,6 +364,23 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
     tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
     tmem_relinquish();
   }
+  // boxes of the 64 blocks from j0 on into the B operand (a box is a row of it)
+  auto load_boxes = [&](int j0, int j1) {
+    uint4 val[Cfg::kChunk * 32 / Cfg::kThreads];
+#pragma unroll
+    for (int k = 0; k < Cfg::kChunk * 32 / Cfg::kThreads; ++k) {
+      const int e = threadIdx.x + k * Cfg::kThreads, j = j0 + (e >> 5);
+      const __nv_bfloat16* box = j < j1 ? box_of(args, b, g, j) : nullptr;
+      val[k] = box != nullptr ? __ldg(reinterpret_cast<const uint4*>(box) + (e & 31)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < Cfg::kChunk * 32 / Cfg::kThreads; ++k) {
+      const int e = threadIdx.x + k * Cfg::kThreads, r = e >> 5, c = e & 31;
+      *reinterpret_cast<uint4*>(smem + Cfg::kBOff + (c >> 3) * Cfg::kBSlab + (r >> 3) * 1024 + (r & 7) * 128 +
+                                (((c & 7) ^ (r & 7)) << 4)) = val[k];
+    }
+  };
+  load_boxes(0, min(cand1, Cfg::kPass));
 
   // n of the tile's rows: 16 lanes per row, eight channels of the four heads
   // each, written as the two halves n+ and n- of the A operand
@@ -380,7 +432,7 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
         uint32_t np[4], nm[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w0 = rintf(__fmul_rn(u[2 * e], fit)), w1 = rintf(__fmul_rn(u[2 * e + 1], fit));
+          const float w0 = rint_small(__fmul_rn(u[2 * e], fit)), w1 = rint_small(__fmul_rn(u[2 * e + 1], fit));
           np[e] = pack_bf16x2(fmaxf(w0, 0.0f), fmaxf(w1, 0.0f));
           nm[e] = pack_bf16x2(fminf(w0, 0.0f), fminf(w1, 0.0f));
         }
@@ -396,32 +448,32 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   tc_fence_after();
   const uint32_t tmem_base = misc[0];
 
-  const int cand0 = args.keep_first, cand1 = nb - args.keep_last;      // blocks that are chosen by score
-  const int need = args.n - args.keep_first - args.keep_last;
-  const int passes = need > 0 ? (cand1 + Cfg::kPass - 1) / Cfg::kPass : 0;
+  const int passes = (cand1 + Cfg::kPass - 1) / Cfg::kPass;
+  const int row = 32 * (warp & 3) + lane, side = warp >> 2;            // the thread's row, and which half of its blocks
+  int* counts = reinterpret_cast<int*>(smem + Cfg::kCountOff);
+  int turn = 0;
+  // both sides' values of the row, side 0's in .x
+  auto exchange = [&](int mine) {
+    counts[(turn * 2 + side) * 128 + row] = mine;
+    __syncwarp();
+    named_bar_sync(1u + (warp & 3), 64u);
+    const int2 v = make_int2(counts[turn * 2 * 128 + row], counts[(turn * 2 + 1) * 128 + row]);
+    turn ^= 1;                                                           // the other buffer next: one barrier is enough
+    return v;
+  };
   float* list_s = reinterpret_cast<float*>(smem + Cfg::kListOff);        // [winner][row]
   int* list_j = reinterpret_cast<int*>(smem + Cfg::kListOff) + Cfg::kMaxListed * 128;
   int* staged = reinterpret_cast<int*>(smem + Cfg::kAOff);             // [row][n + 1], once A is no longer read
-  int listed = 0;                                                      // winners carried from earlier passes (any row's)
+  int listed = 0;                                                      // winners carried from earlier passes (every row's)
   uint32_t phase = 0;
   bool ok = true;
   for (int pass = 0; pass < passes; ++pass) {
     const int c0 = pass * Cfg::kPass, c1 = min(cand1, c0 + Cfg::kPass);
     for (int j0 = c0; j0 < c1; j0 += Cfg::kChunk) {
-      // boxes of 64 blocks into the B operand (the layout of a box is its row)
-      for (int e = threadIdx.x; e < Cfg::kChunk * 32; e += Cfg::kThreads) {
-        const int r = e >> 5, c = e & 31, j = j0 + r;
-        uint4 val = make_uint4(0u, 0u, 0u, 0u);
-        if (j < c1) {
-          const __nv_bfloat16* box = box_of(args, b, g, j);
-          if (box != nullptr) val = __ldg(reinterpret_cast<const uint4*>(box) + c);
-        }
-        *reinterpret_cast<uint4*>(smem + Cfg::kBOff + (c >> 3) * Cfg::kBSlab + (r >> 3) * 1024 + (r & 7) * 128 +
-                                  (((c & 7) ^ (r & 7)) << 4)) = val;
-      }
+      if (j0 > 0) load_boxes(j0, c1);
       fence_proxy_async_smem();
       __syncthreads();
-      if (threadIdx.x == 5 * 32) {                                        // warp 5 reads no TMEM
+      if (threadIdx.x == 7 * 32) {
         tc_fence_after();
         constexpr uint32_t kIdesc = idesc_bf16_f32(128, Cfg::kChunk, 0);
 #pragma unroll
@@ -437,100 +489,133 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
     }
     if (!ok) break;
     tc_fence_after();
-    if (warp < 4) {
-      const int row = 32 * warp + lane;
-      const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(32 * warp) << 16);
-      const int cols = c1 - c0, skip = max(0, cand0 - c0);               // columns skip .. cols-1 are candidates
-      // fn(column, score) over the pass's candidates, 32 columns at a time;
-      // the whole warp calls it together
-      auto each32 = [&](auto fn) {
-        for (int k = 0; k < cols; k += 32) {
-          uint32_t x[32];
-          __syncwarp();
-          tmem_ld32_wait(s_tmem + static_cast<uint32_t>(k), x);
-          if (k < skip || k + 32 > cols) {
+    {
+      // side 0 has the winners of earlier passes and columns skip .. mid-1 of
+      // this one, side 1 columns mid .. cols-1
+      const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      const int cols = c1 - c0, skip = max(0, cand0 - c0);
+      const int mid = min(cols, (cols / 2 + 31) & ~31);
+      const int k0 = side ? mid : 0, k1 = side ? cols : mid;
+      const int carried = side ? 0 : listed;
+      auto load32 = [&](int k, uint32_t (&x)[32]) {
+        __syncwarp();                                                     // TMEM is read by the whole warp together
+        tmem_ld32_wait(s_tmem + static_cast<uint32_t>(k), x);
+        if (k < skip || k + 32 > k1) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k + e < skip || k + e >= cols) x[e] = 0xFF800000u;      // -inf: below every trial
-          }
+          for (int e = 0; e < 32; ++e)
+            if (k + e < skip || k + e >= k1) x[e] = 0xFF800000u;          // -inf: below every trial
+        }
+      };
+      uint32_t x0[32], x1[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0xFF800000u;
+      if (k0 < k1) load32(k0, x0);
+      if (k0 + 32 < k1) load32(k0 + 32, x1);
+      // fn(column of x[0], x) over the side's columns; the whole warp together
+      auto each32 = [&](auto fn) {
+        fn(k0, x0);
+        if (k0 + 32 < k1) fn(k0 + 32, x1);
+        for (int k = k0 + 64; k < k1; k += 32) {
+          uint32_t x[32];
+          load32(k, x);
           fn(k, x);
         }
       };
       float hi = -INFINITY, lo = INFINITY;
-      each32([&](int k, const uint32_t (&x)[32]) {
+      each32([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float v = __uint_as_float(x[e]);
           hi = fmaxf(hi, v);
-          if (v != -INFINITY) lo = fminf(lo, v);
+          lo = fminf(lo, v == -INFINITY ? INFINITY : v);
         }
       });
-      for (int w = 0; w < listed; ++w) {
+      for (int w = 0; w < carried; ++w) {
         const float v = list_s[w * 128 + row];
         hi = fmaxf(hi, v);
         lo = fminf(lo, v);
       }
+      const int2 his = exchange(__float_as_int(hi)), los = exchange(__float_as_int(lo));
+      hi = fmaxf(__int_as_float(his.x), __int_as_float(his.y));
+      lo = fminf(__int_as_float(los.x), __int_as_float(los.y));
       // the pass's winners: all of them when there are at most `need`, else
       // those above the cut; ties at the cut from the lowest block on
-      const int have = cols - skip + listed;
-      uint32_t klo = order_key(lo), khi = order_key(hi) + 1u;            // count(>= klo) >= need > count(>= khi)
-      bool exact = have <= need;
-      int iter = 0;
-      while (true) {
-        const bool done = exact || khi - klo <= 1u;
-        if (__all_sync(0xffffffffu, done) || iter >= 80) break;         // 40 halvings of the values, 32 of the patterns
-        uint32_t kt = klo + ((khi - klo) >> 1);
-        const uint32_t kv = order_key(__fmaf_rn(0.5f, key_value(khi) - key_value(klo), key_value(klo)));
-        if (iter < 40 && kv > klo && kv < khi) kt = kv;                  // halve the values, not their bit patterns
-        const float trial = key_value(kt);
+      const int have = cols - min(cols, skip) + listed;
+      CutSearch c{order_key(lo), order_key(hi) + 1u, have <= need};
+      for (int iter = 0; iter < kMaxTrials; ++iter) {
+        const bool done = c.done();
+        if (__all_sync(0xffffffffu, done)) break;                         // the same on both sides: they hold the same rows
+        const uint32_t key = c.trial(iter);
+        const float trial = key_value(key);
         int count = 0;
-        each32([&](int k, const uint32_t (&x)[32]) {
+        each32([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) count += __uint_as_float(x[e]) >= trial ? 1 : 0;
         });
-        for (int w = 0; w < listed; ++w) count += list_s[w * 128 + row] >= trial ? 1 : 0;
-        if (!done) {
-          if (count >= need) klo = kt;
-          else khi = kt;
-          exact = count == need;
-        }
-        ++iter;
+        for (int w = 0; w < carried; ++w) count += list_s[w * 128 + row] >= trial ? 1 : 0;
+        const int2 both = exchange(count);
+        if (!done) c.counted(key, both.x + both.y, need);
       }
-      const float cut = key_value(klo);
-      int ties = 0x7FFFFFFF;                                             // scores equal to the cut that are taken
-      if (!__all_sync(0xffffffffu, exact)) {                               // the whole warp reads TMEM together
-        int above = 0;
-        each32([&](int k, const uint32_t (&x)[32]) {
+      const float cut = c.cut();
+      // counts of the scores above the cut and at it, and of side 0's share
+      int above = 0, equal = 0;
+      each32([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) above += __uint_as_float(x[e]) > cut ? 1 : 0;
-        });
-        for (int w = 0; w < listed; ++w) above += list_s[w * 128 + row] > cut ? 1 : 0;
-        if (!exact) ties = need - above;
+        for (int e = 0; e < 32; ++e) {
+          above += __uint_as_float(x[e]) > cut ? 1 : 0;
+          equal += __uint_as_float(x[e]) == cut ? 1 : 0;
+        }
+      });
+      for (int w = 0; w < carried; ++w) {
+        above += list_s[w * 128 + row] > cut ? 1 : 0;
+        equal += list_s[w * 128 + row] == cut ? 1 : 0;
       }
+      const int2 aboves = exchange(above), equals = exchange(equal);
+      const int ties_all = c.exact ? equals.x + equals.y : need - aboves.x - aboves.y;
+      const int ties0 = min(ties_all, equals.x);
+      int ties = side ? ties_all - ties0 : ties0;
+      int at = side ? aboves.x + ties0 : 0;                               // place of the side's first winner
       const bool last = pass == passes - 1;
-      int* const mine = staged + row * (args.n + 1);
-      int at = 0;
+      int* const mine = staged + row * (args.n + 1) + args.keep_first;
       auto take = [&](float v, int j) {
-        if (v > cut || (v == cut && ties-- > 0)) {
-          if (last) {
-            mine[args.keep_first + at] = j;
-          } else {
-            list_s[at * 128 + row] = v;
-            list_j[at * 128 + row] = j;
-          }
-          ++at;
+        if (v == cut && ties-- <= 0) return;
+        if (last) {
+          mine[at] = j;
+        } else {
+          list_s[at * 128 + row] = v;
+          list_j[at * 128 + row] = j;
         }
+        ++at;
       };
-      for (int w = 0; w < listed; ++w) take(list_s[w * 128 + row], list_j[w * 128 + row]);
+      // carried winners first (side 0 moves them down in place), then the
+      // columns: their winners as a mask, so only those cost a store
+      for (int w = 0; w < carried; ++w) {
+        const float v = list_s[w * 128 + row];
+        if (v >= cut) take(v, list_j[w * 128 + row]);
+      }
+      __syncwarp();
+      if (!last) named_bar_sync(1u + (warp & 3), 64u);                    // side 1 writes behind them
       each32([&](int k, const uint32_t (&x)[32]) {
+        uint32_t mask = 0u;
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (__uint_as_float(x[e]) >= cut) take(__uint_as_float(x[e]), c0 + k + e);
+        for (int e = 0; e < 32; ++e) mask |= __uint_as_float(x[e]) >= cut ? 1u << e : 0u;
+        while (mask != 0u) {
+          const int e = __ffs(mask) - 1;
+          mask &= mask - 1u;
+          float v = cut;
+          if (!last || !c.exact) {                                        // the score is only needed for these
+#pragma unroll
+            for (int f = 0; f < 32; ++f) v = f == e ? __uint_as_float(x[f]) : v;
+          } else {
+            v = INFINITY;
+          }
+          take(v, c0 + k + e);
+        }
       });
       listed = min(need, have);
     }
     tc_fence_before();
-    __syncthreads();                                                     // TMEM has been read
+    __syncthreads();                                                     // TMEM has been read, the lists are written
     tc_fence_after();
   }
   if (ok) {
