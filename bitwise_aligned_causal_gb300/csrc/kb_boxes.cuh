@@ -23,32 +23,37 @@ __device__ __forceinline__ int grid_exponent(float amax) {
 // 2^n for n in [-126, 127].
 __device__ __forceinline__ float exp2i(int n) { return __int_as_float((n + 127) << 23); }
 
-// rint of |x| < 2^22 (ties to even): at 1.5 * 2^23 and above fp32 has no
-// fraction bits, so the sum rounds to a whole number.  Two additions, where a
-// conversion instruction takes a quarter-rate pipe.
-__device__ __forceinline__ float rint_small(float x) { return __fsub_rn(__fadd_rn(x, 12582912.0f), 12582912.0f); }
+// Rounding to whole numbers without conversion instructions (a quarter-rate
+// pipe): for |x| < 2^22, x + 1.5 * 2^23 has no fraction bits left, so the sum
+// rounds to a whole number (ties to even) and its bit pattern is that of
+// 1.5 * 2^23 plus the number.
+constexpr float kWholeAt = 12582912.0f;              // 1.5 * 2^23
+constexpr uint32_t kWholeBits = 0x4B400000u;         // its bit pattern
+// rint(x * scale), scale a power of two.
+__device__ __forceinline__ float rint_scaled(float x, float scale) { return __fsub_rn(__fmaf_rn(x, scale, kWholeAt), kWholeAt); }
+// Beyond this magnitude a value lies off the grid (E stops at 100) and saturates.
+constexpr float kGridMax = 127.0f * 9.903520314283042e27f;   // 127 * 2^93
 
 // The four heads' values of one channel as whole numbers of 2^(E-15), summed
 // (below 2^17, so every step is exact); values beyond the grid saturate.
-__device__ __forceinline__ float whole_sum(const float (&q)[4], float scale) {
-  float u = 0.0f;
-#pragma unroll
-  for (int h = 0; h < 4; ++h)
-    u = __fadd_rn(u, rint_small(fminf(fmaxf(__fmul_rn(q[h], scale), -32512.0f), 32512.0f)));
-  return u;
+__device__ __forceinline__ float whole_sum(float q0, float q1, float q2, float q3, float scale) {
+  const uint32_t u = __float_as_uint(__fmaf_rn(q0, scale, kWholeAt)) + __float_as_uint(__fmaf_rn(q1, scale, kWholeAt)) +
+                     __float_as_uint(__fmaf_rn(q2, scale, kWholeAt)) + __float_as_uint(__fmaf_rn(q3, scale, kWholeAt));
+  return __fsub_rn(__uint_as_float(u - 3u * kWholeBits), kWholeAt);        // modulo 2^32
 }
+__device__ __forceinline__ float saturated(float q) { return fminf(fmaxf(q, -kGridMax), kGridMax); }
 
-// Share of a block's score of eight channels: box bounds hi, lo (bf16 pairs),
-// np and nm the positive and negative parts of n.
-__device__ __forceinline__ float box_dot(const uint4& hi, const uint4& lo, const float (&np)[8], const float (&nm)[8]) {
+// The bounds that count in the score of two channels (bf16 pairs): the upper
+// one where n is positive, the lower one elsewhere; `up` has all bits of a
+// positive channel's half set.
+__device__ __forceinline__ float box_dot(const uint4& hi, const uint4& lo, const uint32_t (&up)[4], const float (&n)[8]) {
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    s = __fmaf_rn(np[2 * i], __uint_as_float(h[i] << 16), s);
-    s = __fmaf_rn(nm[2 * i], __uint_as_float(l[i] << 16), s);
-    s = __fmaf_rn(np[2 * i + 1], __uint_as_float(h[i] & 0xFFFF0000u), s);
-    s = __fmaf_rn(nm[2 * i + 1], __uint_as_float(l[i] & 0xFFFF0000u), s);
+    const uint32_t w = (h[i] & up[i]) | (l[i] & ~up[i]);
+    s = __fmaf_rn(n[2 * i], __uint_as_float(w << 16), s);
+    s = __fmaf_rn(n[2 * i + 1], __uint_as_float(w & 0xFFFF0000u), s);
   }
   return s;
 }

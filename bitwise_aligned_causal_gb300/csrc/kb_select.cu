@@ -20,8 +20,10 @@
 //
 // The n largest scores are found without sorting: a trial value halves the
 // range between the smallest and the largest score until exactly n scores are
-// at or above it; only ties keep the search going until the range is a single
-// value, of which the first blocks are then taken.
+// at or above it (about 7 trials for a row, 12 for the slowest of 32; trials
+// placed by the counts at both ends took as many); only ties keep the search
+// going until the range is a single value, of which the first blocks are then
+// taken.
 #include "kb_boxes.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
@@ -30,91 +32,30 @@ namespace kb {
 
 namespace {
 
-constexpr int kChunkKeys = 1024;                // scores a warp searches at once: 32 registers per lane
-
-// Scores (finite) as unsigned keys of the same order; -0 counts as +0.
-__device__ __forceinline__ uint32_t order_key(float s) {
-  const uint32_t b = __float_as_uint(__fadd_rn(s, 0.0f));
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); }
-
 // Search for the value that exactly `need` scores are at or above: the range
-// [lo, hi) of keys with count(>= lo) >= need > count(>= hi).
+// [lo, hi) of values with count(>= lo) >= need > count(>= hi).
 struct CutSearch {
-  uint32_t lo, hi;
-  bool exact;                                   // exactly `need` scores are at or above lo's value
-  __device__ __forceinline__ bool done() const { return exact || hi - lo <= 1u; }
-  // The next key to try: the middle of the values, and after 40 halvings that
-  // of their bit patterns (32 more end any search).
-  __device__ __forceinline__ uint32_t trial(int iter) const {
-    const float a = key_value(lo), b = key_value(hi);
-    const uint32_t mid = order_key(__fmaf_rn(0.5f, __fsub_rn(b, a), a));
-    return iter < 40 && mid > lo && mid < hi ? mid : lo + ((hi - lo) >> 1);
+  float lo, hi;
+  bool exact;                                   // exactly `need` scores are at or above lo
+  __device__ __forceinline__ CutSearch(float least, float most, bool all)
+      : lo(least), hi(next_above(most)), exact(all) {}
+  __device__ __forceinline__ static float next_above(float x) {
+    const int b = __float_as_int(__fadd_rn(x, 0.0f));       // -0 counts as +0
+    return __int_as_float(b >= 0 ? b + 1 : b - 1);
   }
-  __device__ __forceinline__ void counted(uint32_t key, int count, int need) {
-    if (count >= need) lo = key;
-    else hi = key;
+  __device__ __forceinline__ float trial() const { return __fmaf_rn(0.5f, __fsub_rn(hi, lo), lo); }
+  // No value lies between lo and hi, or the cut is exact.
+  __device__ __forceinline__ bool done(float t) const { return exact || !(t > lo && t < hi); }
+  __device__ __forceinline__ void counted(float t, int count, int need) {
+    if (count >= need) lo = t;
+    else hi = t;
     exact = count == need;
   }
-  __device__ __forceinline__ float cut() const { return key_value(lo); }
 };
-constexpr int kMaxTrials = 80;
-
-// The warp's n largest of m <= 1024 scores, in place order (ties: the first
-// ones), handed to emit(place among the chosen, place among the scores).
-template <class Emit>
-__device__ __forceinline__ void warp_largest(const float* scores, int m, int n, int lane, Emit emit) {
-  float r[kChunkKeys / 32];
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kChunkKeys / 32; ++i) {
-    if (i * 32 >= m) break;
-    const bool in = i * 32 + lane < m;
-    r[i] = in ? scores[i * 32 + lane] : -INFINITY;          // below every trial
-    hi = fmaxf(hi, r[i]);
-    lo = fminf(lo, in ? r[i] : INFINITY);
-  }
-  CutSearch c{__reduce_min_sync(0xffffffffu, order_key(lo)), __reduce_max_sync(0xffffffffu, order_key(hi)) + 1u, m <= n};
-  for (int iter = 0; iter < kMaxTrials && !c.done(); ++iter) {
-    const uint32_t key = c.trial(iter);
-    const float t = key_value(key);
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < kChunkKeys / 32; ++i) {
-      if (i * 32 >= m) break;
-      count += r[i] >= t ? 1 : 0;
-    }
-    c.counted(key, __reduce_add_sync(0xffffffffu, count), n);
-  }
-  const float cut = c.cut();
-  int ties = 0;                                             // scores equal to the cut that are taken
-  if (!c.exact) {
-    int above = 0;
-#pragma unroll
-    for (int i = 0; i < kChunkKeys / 32; ++i) {
-      if (i * 32 >= m) break;
-      above += r[i] > cut ? 1 : 0;
-    }
-    ties = n - __reduce_add_sync(0xffffffffu, above);
-  }
-  int taken = 0, tied = 0;
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-  for (int i = 0; i < kChunkKeys / 32; ++i) {
-    if (i * 32 >= m) break;
-    bool take = i * 32 + lane < m && r[i] >= cut;
-    if (!c.exact) {
-      const bool eq = take && r[i] == cut;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-      if (eq) take = tied + __popc(eqs & below) < ties;
-      tied += __popc(eqs);
-    }
-    const uint32_t mask = __ballot_sync(0xffffffffu, take);
-    if (take) emit(taken + __popc(mask & below), i * 32 + lane);
-    taken += __popc(mask);
-  }
-}
+// Scores are whole multiples of a power of two and below 2^22 of them, so
+// halving ends within a few dozen steps of 22 bits, except around zero, where
+// floats go on down to 2^-149: 264 halvings at most.
+constexpr int kMaxTrials = 300;
 
 // Position of row i of sequence b, or -1 when the row does not exist; a bad
 // start or length is recorded.
@@ -129,6 +70,16 @@ __device__ __forceinline__ int row_position(const SelectArgs& a, int b, int i) {
     }
   }
   return i < len ? start + i : -1;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));       // NaN goes through
+  return r;
+}
+// All ones in the half of every negative value of a bf16 pair.
+__device__ __forceinline__ uint32_t bf16x2_sign_mask(uint32_t w) {
+  return ((w & 0x8000u) ? 0x0000FFFFu : 0u) | ((w & 0x80000000u) ? 0xFFFF0000u : 0u);
 }
 
 // Box of block j of sequence b, KV head g, or null for a page out of range.
@@ -149,8 +100,8 @@ __device__ __forceinline__ const __nv_bfloat16* box_of(const SelectArgs& a, int 
 // ----------------------------------------------------------- a row per CTA
 //
 // One CTA of 16 warps per (row, batch, KV head); 16 lanes score a block (eight
-// channels of both bounds each), so a warp has eight blocks of 512 bytes in
-// flight, the first of them while the query is still on its way to whole
+// channels of both bounds each), so a warp has twelve blocks of 512 bytes
+// in flight, the first of them while the query is still on its way to whole
 // numbers.  For one token the boxes are read once and nothing else counts.
 constexpr int kSelectRowThreads = 512;
 constexpr int kSelectRowMax = 16;               // query rows per sequence up to which this kernel runs
@@ -159,6 +110,7 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
   extern __shared__ float sel_smem[];
   __shared__ float whole[kHeadDim];               // n
   __shared__ uint32_t amax_bits[8];
+  __shared__ int warp_sums[2][kSelectRowThreads / 32];
   const bool failed = *reinterpret_cast<volatile uint32_t*>(args.err) != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = blockIdx.x;
@@ -170,7 +122,7 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
   const int c0 = args.keep_first, m = nb - args.keep_first - args.keep_last;   // blocks c0 .. c0+m-1 are chosen by score
   const int need = args.n - args.keep_first - args.keep_last;
   // the first boxes and the query leave together
-  constexpr int kAtOnce = 4, kStep = kSelectRowThreads / 16;
+  constexpr int kAtOnce = 6, kStep = kSelectRowThreads / 16;
   const int c = lane & 15;
   uint4 hi[kAtOnce], lo[kAtOnce];
   auto fetch = [&](int j0) {
@@ -194,9 +146,9 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
       float mx = 0.0f;
 #pragma unroll
       for (int h = 0; h < kGroup; ++h) {
-        q[h] = __bfloat162float(static_cast<const __nv_bfloat16*>(
+        q[h] = saturated(__bfloat162float(static_cast<const __nv_bfloat16*>(
             args.q)[((static_cast<size_t>(b) * args.Hkv + g) * kGroup + h) * args.L * kHeadDim +
-                    static_cast<size_t>(i) * kHeadDim + threadIdx.x]);
+                    static_cast<size_t>(i) * kHeadDim + threadIdx.x]));
         mx = fmaxf(mx, fabsf(q[h]));
       }
       const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
@@ -217,27 +169,26 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
   float u = 0.0f;
   if (warp < 4) {
     const uint32_t mb = max(max(amax_bits[0], amax_bits[1]), max(amax_bits[2], amax_bits[3]));
-    u = whole_sum(q, exp2i(15 - grid_exponent(__uint_as_float(mb))));
+    u = whole_sum(q[0], q[1], q[2], q[3], exp2i(15 - grid_exponent(__uint_as_float(mb))));
     const uint32_t ub = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(u)));
     if (lane == 0) amax_bits[4 + warp] = ub;
   }
   __syncthreads();
   if (warp < 4) {
     const uint32_t ub = max(max(amax_bits[4], amax_bits[5]), max(amax_bits[6], amax_bits[7]));
-    whole[threadIdx.x] = rint_small(__fmul_rn(u, exp2i(7 - grid_exponent(__uint_as_float(ub)))));
+    whole[threadIdx.x] = rint_scaled(u, exp2i(7 - grid_exponent(__uint_as_float(ub))));
   }
   __syncthreads();
-  float np[8], nm[8];
+  float n[8];
+  uint32_t up[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float w = whole[8 * c + e];
-    np[e] = fmaxf(w, 0.0f);
-    nm[e] = fminf(w, 0.0f);
-  }
+  for (int e = 0; e < 8; ++e) n[e] = whole[8 * c + e];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) up[e] = (n[2 * e] > 0.0f ? 0x0000FFFFu : 0u) | (n[2 * e + 1] > 0.0f ? 0xFFFF0000u : 0u);
   for (int j0 = j_first; j0 < m + (lane >> 4); j0 += kStep * kAtOnce) {        // uniform over the warp
     float s[kAtOnce];
 #pragma unroll
-    for (int a = 0; a < kAtOnce; ++a) s[a] = box_dot(hi[a], lo[a], np, nm);
+    for (int a = 0; a < kAtOnce; ++a) s[a] = box_dot(hi[a], lo[a], up, n);
     if (j0 + kStep * kAtOnce < m + (lane >> 4)) fetch(j0 + kStep * kAtOnce);
 #pragma unroll
     for (int k = 8; k >= 1; k >>= 1)
@@ -248,38 +199,77 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
       if (c == 0 && j0 + a * kStep < m) sel_smem[j0 + a * kStep] = s[a];
   }
   __syncthreads();
-  // rounds: every warp reduces chunks of 1024 scores to their `need` largest,
-  // until one chunk is left.  Round 0 reads the scores in block order, later
-  // rounds (score, block) pairs in the same order.
-  int left = m;
-  float* scores = sel_smem;
-  int* ids = nullptr;
-  const int half = (args.max_blocks + kChunkKeys - 1) / kChunkKeys * args.n;     // pairs a round can leave
-  int which = 0;
-  while (left > kChunkKeys) {
-    float* nk = sel_smem + args.max_blocks + which * 2 * half;
-    int* ni = reinterpret_cast<int*>(nk + half);
-    const int chunks = (left + kChunkKeys - 1) / kChunkKeys;
-    for (int k = warp; k < chunks; k += kSelectRowThreads / 32) {
-      const int from = k * kChunkKeys;
-      warp_largest(scores + from, min(kChunkKeys, left - from), need, lane, [&](int to, int at) {
-        nk[k * need + to] = scores[from + at];
-        ni[k * need + to] = ids == nullptr ? from + at : ids[from + at];
-      });
+  // the cut, by all threads: thread t holds scores t, t + 512, ..
+  int turn = 0;
+  auto sum_of = [&](int mine) {                   // over the CTA
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) warp_sums[turn][warp] = mine;
+    __syncthreads();
+    const int all = __reduce_add_sync(0xffffffffu, lane < kSelectRowThreads / 32 ? warp_sums[turn][lane] : 0);
+    turn ^= 1;                                    // the other buffer next: one barrier is enough
+    return all;
+  };
+  float least = INFINITY, most = -INFINITY;
+  for (int j = threadIdx.x; j < m; j += kSelectRowThreads) {
+    least = fminf(least, sel_smem[j]);
+    most = fmaxf(most, sel_smem[j]);
+  }
+  {
+    // extremes over the CTA, as unsigned numbers of the same order
+    auto key = [](float x) {
+      const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+      return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    };
+    auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); };
+    const uint32_t klo = __reduce_min_sync(0xffffffffu, key(least)), khi = __reduce_max_sync(0xffffffffu, key(most));
+    if (lane == 0) {
+      warp_sums[0][warp] = static_cast<int>(klo);
+      warp_sums[1][warp] = static_cast<int>(khi);
     }
-    left = (chunks - 1) * need + min(need, left - (chunks - 1) * kChunkKeys);
-    scores = nk;
-    ids = ni;
-    which ^= 1;
+    __syncthreads();
+    const int from = lane & (kSelectRowThreads / 32 - 1);
+    least = value(__reduce_min_sync(0xffffffffu, static_cast<uint32_t>(warp_sums[0][from])));
+    most = value(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(warp_sums[1][from])));
     __syncthreads();
   }
-  if (warp == 0) {
-    warp_largest(scores, left, need, lane, [&](int to, int at) { out[c0 + to] = c0 + (ids == nullptr ? at : ids[at]); });
-  } else if (warp == 1) {
-    for (int t = lane; t < args.keep_first + args.keep_last; t += 32)
-      if (t < args.keep_first) out[t] = t;
-      else out[args.n - args.keep_last + t - args.keep_first] = nb - args.keep_last + t - args.keep_first;
+  CutSearch s(least, most, m <= need);
+#pragma unroll 1
+  for (int iter = 0; iter < kMaxTrials; ++iter) {
+    const float t = s.trial();
+    if (s.done(t)) break;                         // the same in every thread
+    int count = 0;
+    for (int j = threadIdx.x; j < m; j += kSelectRowThreads) count += sel_smem[j] >= t ? 1 : 0;
+    s.counted(t, sum_of(count), need);
   }
+  int ties = 0;                                   // scores equal to the cut that are taken
+  if (!s.exact) {
+    int above = 0;
+    for (int j = threadIdx.x; j < m; j += kSelectRowThreads) above += sel_smem[j] > s.lo ? 1 : 0;
+    ties = need - sum_of(above);
+  }
+  // winners out in block order: a place is the number of winners before it
+  int before = 0, tied_before = 0;                // of the blocks of earlier slabs of 512
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j0 = 0; j0 < m; j0 += kSelectRowThreads) {
+    const int j = j0 + static_cast<int>(threadIdx.x);
+    const float v = j < m ? sel_smem[j] : -INFINITY;
+    const bool tied = !s.exact && v == s.lo;
+    const uint32_t win = __ballot_sync(0xffffffffu, v >= s.lo && !tied), eq = __ballot_sync(0xffffffffu, tied);
+    if (lane == 0) warp_sums[turn][warp] = __popc(win) | (__popc(eq) << 16);
+    __syncthreads();
+    const int theirs = lane < kSelectRowThreads / 32 ? warp_sums[turn][lane] : 0;
+    const int earlier = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);      // two sums in one word: at most 512 each
+    const int all = __reduce_add_sync(0xffffffffu, theirs);
+    turn ^= 1;
+    const int n_win = before + (earlier & 0xFFFF) + __popc(win & below);
+    const int n_eq = tied_before + (earlier >> 16) + __popc(eq & below);
+    if (tied ? n_eq < ties : v >= s.lo) out[c0 + n_win + min(n_eq, ties)] = c0 + j;
+    before += all & 0xFFFF;
+    tied_before += all >> 16;
+  }
+  for (int t = threadIdx.x; t < args.keep_first + args.keep_last; t += kSelectRowThreads)
+    if (t < args.keep_first) out[t] = t;
+    else out[args.n - args.keep_last + t - args.keep_first] = nb - args.keep_last + t - args.keep_first;
 }
 
 // ------------------------------------------------------ 128 rows per CTA
@@ -288,10 +278,11 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
 // its rows share their blocks 0 .. t.  Scores are one product of grid vectors,
 // [n+ | n-] (128 rows x 256) times [upper | lower] (blocks x 256), on the
 // tensor core, exact like every other order of summation.  They stay in TMEM
-// (a row per lane, a block per column).  Two threads search a row, each over
-// half of its blocks, the first 64 of which it keeps in registers; they add
-// their counts through shared memory.  Rows whose blocks exceed TMEM go on in
-// passes of 256 blocks, the winners of the earlier ones carried along in
+// (a row per lane, a block per column).  A quad of threads searches a row: the
+// 16x256b TMEM load gives thread u columns 8r + 2u and 8r + 2u + 1 of every
+// group of 8, for two rows, so counts are added by two shuffles, and 128
+// blocks of both rows are 64 registers.  Rows whose blocks exceed TMEM go on
+// in passes of 256 blocks, the winners of the earlier ones carried along in
 // shared memory.
 // Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
 // half of TMEM let two CTAs share an SM, so one loads while the other
@@ -307,8 +298,8 @@ struct SelectTileCfg {
   static constexpr uint32_t kBOff = 4 * kASlab;
   static constexpr uint32_t kBarOff = kBOff + 4 * kBSlab;
   static constexpr uint32_t kMiscOff = kBarOff + 16;
-  static constexpr uint32_t kCountOff = kMiscOff + 16;      // [parity][half][row] counts
-  static constexpr uint32_t kListOff = kCountOff + 2 * 2 * 128 * 4;   // several passes: score and block per winner and row
+  static constexpr uint32_t kMaskOff = kMiscOff + 16;       // [row][9] chosen columns of a pass, 32 to a word
+  static constexpr uint32_t kListOff = kMaskOff + 128 * 9 * 4;        // several passes: score and block per winner and row
   static constexpr int kMaxListed = 32;
 };
 
@@ -344,9 +335,10 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   if (nb <= args.n || need == 0) {
     if (nb > args.n)                                        // nothing is scored, but a bad page is still found
       for (int j = cand0 + threadIdx.x; j < cand1; j += Cfg::kThreads) (void)box_of(args, b, g, j);
-    for (int e = threadIdx.x; e < kTileKeys * args.n; e += Cfg::kThreads) {
-      const int i = i0 + e / args.n, k = e % args.n;
-      if (i >= 0 && i < len)
+    for (int r = warp; r < kTileKeys; r += Cfg::kThreads / 32) {
+      const int i = i0 + r;
+      if (i < 0 || i >= len) continue;
+      for (int k = lane; k < args.n; k += 32)
         args.blocks[(out_row0 + i) * args.n + k] = nb <= args.n ? (k < nb ? k : -1) : k < args.keep_first ? k : nb - args.n + k;
     }
     return;
@@ -390,30 +382,40 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
                                                     (static_cast<size_t>(b) * args.Hkv + g) * kGroup * args.L * kHeadDim);
     const size_t head_step = static_cast<size_t>(args.L) * (kHeadDim / 8);
     constexpr int kAtOnce = 2;                              // rows in flight per lane
-#pragma unroll 1
-    for (int m0 = 2 * warp + (lane >> 4); m0 < kTileKeys; m0 += 16 * kAtOnce) {
-      uint4 x[kAtOnce][kGroup];
+    auto fetch = [&](int m0, uint4 (&x)[kAtOnce][kGroup]) {
 #pragma unroll
       for (int a = 0; a < kAtOnce; ++a) {
         const int i = i0 + m0 + 16 * a;
+        const bool in = m0 + 16 * a < kTileKeys && i >= 0 && i < len;
 #pragma unroll
         for (int h = 0; h < kGroup; ++h)
-          x[a][h] = i >= 0 && i < len ? __ldg(q + h * head_step + static_cast<size_t>(i) * (kHeadDim / 8) + c)
-                                      : make_uint4(0u, 0u, 0u, 0u);
+          x[a][h] = in ? __ldg(q + h * head_step + static_cast<size_t>(i) * (kHeadDim / 8) + c) : make_uint4(0u, 0u, 0u, 0u);
       }
+    };
+    uint4 x[kAtOnce][kGroup], ahead[kAtOnce][kGroup];
+    fetch(2 * warp + (lane >> 4), ahead);
+#pragma unroll 1
+    for (int m0 = 2 * warp + (lane >> 4); m0 < kTileKeys; m0 += 16 * kAtOnce) {
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a)
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h) x[a][h] = ahead[a][h];
+      fetch(m0 + 16 * kAtOnce, ahead);                      // the next rows are on their way while these are rounded
 #pragma unroll
       for (int a = 0; a < kAtOnce; ++a) {
-        float amax = 0.0f;
+        uint32_t top = 0u;                                  // largest magnitudes, a bf16 pair
 #pragma unroll
         for (int h = 0; h < kGroup; ++h) {
           const uint32_t w[4] = {x[a][h].x, x[a][h].y, x[a][h].z, x[a][h].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+          for (int e = 0; e < 4; ++e) top = bf16x2_max(top, w[e] & 0x7FFF7FFFu);
         }
+        uint32_t top32 = max(top << 16, top & 0xFFFF0000u);  // as fp32 bits, whose order is that of the magnitudes
 #pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        for (int m = 8; m >= 1; m >>= 1) top32 = max(top32, __shfl_xor_sync(0xffffffffu, top32, m));
+        const float amax = __uint_as_float(top32);
         const float scale = exp2i(15 - grid_exponent(amax));
+        const bool off_grid = !(amax <= kGridMax);          // beyond the grid, infinite or NaN
         float u[8], umax = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -422,8 +424,9 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
           for (int h = 0; h < kGroup; ++h) {
             const uint32_t w = e < 2 ? x[a][h].x : e < 4 ? x[a][h].y : e < 6 ? x[a][h].z : x[a][h].w;
             v[h] = __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+            if (off_grid) v[h] = saturated(v[h]);
           }
-          u[e] = whole_sum(v, scale);
+          u[e] = whole_sum(v[0], v[1], v[2], v[3], scale);
           umax = fmaxf(umax, fabsf(u[e]));
         }
 #pragma unroll
@@ -432,9 +435,10 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
         uint32_t np[4], nm[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w0 = rint_small(__fmul_rn(u[2 * e], fit)), w1 = rint_small(__fmul_rn(u[2 * e + 1], fit));
-          np[e] = pack_bf16x2(fmaxf(w0, 0.0f), fmaxf(w1, 0.0f));
-          nm[e] = pack_bf16x2(fminf(w0, 0.0f), fminf(w1, 0.0f));
+          const uint32_t w = pack_bf16x2(rint_scaled(u[2 * e], fit), rint_scaled(u[2 * e + 1], fit));
+          const uint32_t neg = bf16x2_sign_mask(w);         // n- has the negative channels, n+ the others
+          np[e] = w & ~neg;
+          nm[e] = w & neg;
         }
         const int m = m0 + 16 * a;
         uint8_t* at = smem + Cfg::kAOff + (c >> 3) * Cfg::kASlab + (m >> 3) * 1024 + (m & 7) * 128 + (((c & 7) ^ (m & 7)) << 4);
@@ -449,18 +453,10 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   const uint32_t tmem_base = misc[0];
 
   const int passes = (cand1 + Cfg::kPass - 1) / Cfg::kPass;
-  const int row = 32 * (warp & 3) + lane, side = warp >> 2;            // the thread's row, and which half of its blocks
-  int* counts = reinterpret_cast<int*>(smem + Cfg::kCountOff);
-  int turn = 0;
-  // both sides' values of the row, side 0's in .x
-  auto exchange = [&](int mine) {
-    counts[(turn * 2 + side) * 128 + row] = mine;
-    __syncwarp();
-    named_bar_sync(1u + (warp & 3), 64u);
-    const int2 v = make_int2(counts[turn * 2 * 128 + row], counts[(turn * 2 + 1) * 128 + row]);
-    turn ^= 1;                                                           // the other buffer next: one barrier is enough
-    return v;
-  };
+  // rows of this thread: rA and rA + 8 of the warp's 16, shared by its quad
+  const int lane_base = 32 * (warp & 3) + 16 * (warp >> 2);
+  const int u4 = lane & 3, rA = lane_base + (lane >> 2);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(smem + Cfg::kMaskOff);
   float* list_s = reinterpret_cast<float*>(smem + Cfg::kListOff);        // [winner][row]
   int* list_j = reinterpret_cast<int*>(smem + Cfg::kListOff) + Cfg::kMaxListed * 128;
   int* staged = reinterpret_cast<int*>(smem + Cfg::kAOff);             // [row][n + 1], once A is no longer read
@@ -490,128 +486,216 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
     if (!ok) break;
     tc_fence_after();
     {
-      // side 0 has the winners of earlier passes and columns skip .. mid-1 of
-      // this one, side 1 columns mid .. cols-1
-      const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-      const int cols = c1 - c0, skip = max(0, cand0 - c0);
-      const int mid = min(cols, (cols / 2 + 31) & ~31);
-      const int k0 = side ? mid : 0, k1 = side ? cols : mid;
-      const int carried = side ? 0 : listed;
-      auto load32 = [&](int k, uint32_t (&x)[32]) {
-        __syncwarp();                                                     // TMEM is read by the whole warp together
-        tmem_ld32_wait(s_tmem + static_cast<uint32_t>(k), x);
-        if (k < skip || k + 32 > k1) {
+      const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(lane_base) << 16);
+      const int cols = c1 - c0, skip = max(0, cand0 - c0);               // columns skip .. cols-1 are candidates
+      // 64 columns from k on: x[4r], x[4r+1] of row A, x[4r+2], x[4r+3] of row
+      // B, columns k + 8r + 2 u4 and the next; other columns as -inf, below
+      // every trial.  The whole warp reads TMEM together.
+      auto load64 = [&](int k, uint32_t (&x)[32]) {
+        __syncwarp();
+        tmem_ld_16x256b_x8_wait(s_tmem + static_cast<uint32_t>(k), x);
+        if (k < skip || k + 64 > cols) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (k + e < skip || k + e >= k1) x[e] = 0xFF800000u;          // -inf: below every trial
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int col = k + 8 * r + 2 * u4 + e;
+              if (col < skip || col >= cols) x[4 * r + e] = x[4 * r + 2 + e] = 0xFF800000u;
+            }
         }
       };
       uint32_t x0[32], x1[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x0[e] = x1[e] = 0xFF800000u;
-      if (k0 < k1) load32(k0, x0);
-      if (k0 + 32 < k1) load32(k0 + 32, x1);
-      // fn(column of x[0], x) over the side's columns; the whole warp together
-      auto each32 = [&](auto fn) {
-        fn(k0, x0);
-        if (k0 + 32 < k1) fn(k0 + 32, x1);
-        for (int k = k0 + 64; k < k1; k += 32) {
+      load64(0, x0);
+      if (cols > 64) load64(64, x1);
+      // fn(first column, x) over the pass's columns; the first 128 stay in registers
+      auto each64 = [&](auto fn) {
+        fn(0, x0);
+        if (cols > 64) fn(64, x1);
+        for (int k = 128; k < cols; k += 64) {
           uint32_t x[32];
-          load32(k, x);
+          load64(k, x);
           fn(k, x);
         }
       };
-      float hi = -INFINITY, lo = INFINITY;
-      each32([&](int, const uint32_t (&x)[32]) {
+      auto quad_sum = [](int v) {
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        return v + __shfl_xor_sync(0xffffffffu, v, 2);
+      };
+      // carried winners of a row: the quad takes every fourth
+      auto carried = [&](int r, auto fn) {
+        for (int w = u4; w < listed; w += 4) fn(list_s[w * 128 + r], list_j[w * 128 + r]);
+      };
+      float hiA = -INFINITY, hiB = -INFINITY, loA = INFINITY, loB = INFINITY;
+      each64([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = __uint_as_float(x[e]);
-          hi = fmaxf(hi, v);
-          lo = fminf(lo, v == -INFINITY ? INFINITY : v);
-        }
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = __uint_as_float(x[4 * r + e]), z = __uint_as_float(x[4 * r + 2 + e]);
+            hiA = fmaxf(hiA, a);
+            hiB = fmaxf(hiB, z);
+            loA = fminf(loA, a == -INFINITY ? INFINITY : a);
+            loB = fminf(loB, z == -INFINITY ? INFINITY : z);
+          }
       });
-      for (int w = 0; w < carried; ++w) {
-        const float v = list_s[w * 128 + row];
-        hi = fmaxf(hi, v);
-        lo = fminf(lo, v);
+      carried(rA, [&](float v, int) { hiA = fmaxf(hiA, v); loA = fminf(loA, v); });
+      carried(rA + 8, [&](float v, int) { hiB = fmaxf(hiB, v); loB = fminf(loB, v); });
+      __syncwarp();
+#pragma unroll
+      for (int k = 1; k <= 2; k <<= 1) {
+        hiA = fmaxf(hiA, __shfl_xor_sync(0xffffffffu, hiA, k));
+        hiB = fmaxf(hiB, __shfl_xor_sync(0xffffffffu, hiB, k));
+        loA = fminf(loA, __shfl_xor_sync(0xffffffffu, loA, k));
+        loB = fminf(loB, __shfl_xor_sync(0xffffffffu, loB, k));
       }
-      const int2 his = exchange(__float_as_int(hi)), los = exchange(__float_as_int(lo));
-      hi = fmaxf(__int_as_float(his.x), __int_as_float(his.y));
-      lo = fminf(__int_as_float(los.x), __int_as_float(los.y));
       // the pass's winners: all of them when there are at most `need`, else
       // those above the cut; ties at the cut from the lowest block on
       const int have = cols - min(cols, skip) + listed;
-      CutSearch c{order_key(lo), order_key(hi) + 1u, have <= need};
+      CutSearch sA(loA, hiA, have <= need), sB(loB, hiB, have <= need);
       for (int iter = 0; iter < kMaxTrials; ++iter) {
-        const bool done = c.done();
-        if (__all_sync(0xffffffffu, done)) break;                         // the same on both sides: they hold the same rows
-        const uint32_t key = c.trial(iter);
-        const float trial = key_value(key);
-        int count = 0;
-        each32([&](int, const uint32_t (&x)[32]) {
+        const float tA = sA.trial(), tB = sB.trial();
+        const bool doneA = sA.done(tA), doneB = sB.done(tB);
+        if (__all_sync(0xffffffffu, doneA && doneB)) break;
+        int nA = 0, nB = 0;
+        each64([&](int, const uint32_t (&x)[32]) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) count += __uint_as_float(x[e]) >= trial ? 1 : 0;
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              nA += __uint_as_float(x[4 * r + e]) >= tA ? 1 : 0;
+              nB += __uint_as_float(x[4 * r + 2 + e]) >= tB ? 1 : 0;
+            }
         });
-        for (int w = 0; w < carried; ++w) count += list_s[w * 128 + row] >= trial ? 1 : 0;
-        const int2 both = exchange(count);
-        if (!done) c.counted(key, both.x + both.y, need);
+        if (listed > 0) {
+          carried(rA, [&](float v, int) { nA += v >= tA ? 1 : 0; });
+          carried(rA + 8, [&](float v, int) { nB += v >= tB ? 1 : 0; });
+          __syncwarp();
+        }
+        nA = quad_sum(nA | (nB << 16));                                   // two counts of at most 288 in one word
+        if (!doneA) sA.counted(tA, nA & 0xFFFF, need);
+        if (!doneB) sB.counted(tB, nA >> 16, need);
       }
-      const float cut = c.cut();
-      // counts of the scores above the cut and at it, and of side 0's share
-      int above = 0, equal = 0;
-      each32([&](int, const uint32_t (&x)[32]) {
+      // the chosen columns as bit masks, a word for 32 columns: a thread's
+      // share of a word are bits 8(r%4) + 2 u4 + e; the quad's shares are ORed
+      // and thread u4 stores the words u4, u4 + 4, ..
+      const bool tied = __any_sync(0xffffffffu, !sA.exact || !sB.exact);
+      auto put_masks = [&](int k, const uint32_t (&x)[32], int half, bool strict, int word0) {
+        // half 0: row A, 1: row B; strict: above the cut only, else at or above
+        const float cut = half ? sB.lo : sA.lo;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          above += __uint_as_float(x[e]) > cut ? 1 : 0;
-          equal += __uint_as_float(x[e]) == cut ? 1 : 0;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w = 0u;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float v = __uint_as_float(x[4 * (4 * h + r) + 2 * half + e]);
+              if (strict ? v > cut : v >= cut) w |= 1u << (8 * r + e);
+            }
+          w <<= 2 * u4;
+          w |= __shfl_xor_sync(0xffffffffu, w, 1);
+          w |= __shfl_xor_sync(0xffffffffu, w, 2);
+          const int word = word0 + k / 32 + h;
+          if (u4 == (word & 3)) masks[(rA + 8 * half) * 9 + word] = w;
         }
-      });
-      for (int w = 0; w < carried; ++w) {
-        above += list_s[w * 128 + row] > cut ? 1 : 0;
-        equal += list_s[w * 128 + row] == cut ? 1 : 0;
-      }
-      const int2 aboves = exchange(above), equals = exchange(equal);
-      const int ties_all = c.exact ? equals.x + equals.y : need - aboves.x - aboves.y;
-      const int ties0 = min(ties_all, equals.x);
-      int ties = side ? ties_all - ties0 : ties0;
-      int at = side ? aboves.x + ties0 : 0;                               // place of the side's first winner
-      const bool last = pass == passes - 1;
-      int* const mine = staged + row * (args.n + 1) + args.keep_first;
-      auto take = [&](float v, int j) {
-        if (v == cut && ties-- <= 0) return;
-        if (last) {
-          mine[at] = j;
-        } else {
-          list_s[at * 128 + row] = v;
-          list_j[at * 128 + row] = j;
-        }
-        ++at;
       };
-      // carried winners first (side 0 moves them down in place), then the
-      // columns: their winners as a mask, so only those cost a store
-      for (int w = 0; w < carried; ++w) {
-        const float v = list_s[w * 128 + row];
-        if (v >= cut) take(v, list_j[w * 128 + row]);
-      }
-      __syncwarp();
-      if (!last) named_bar_sync(1u + (warp & 3), 64u);                    // side 1 writes behind them
-      each32([&](int k, const uint32_t (&x)[32]) {
-        uint32_t mask = 0u;
+      auto write_masks = [&](bool strict) {
+        each64([&](int k, const uint32_t (&x)[32]) {
+          put_masks(k, x, 0, strict, 0);
+          put_masks(k, x, 1, strict, 0);
+        });
+        __syncwarp();
+      };
+      const bool last = pass == passes - 1;
+      const int words = (cols + 31) / 32;
+      write_masks(false);
+      if (tied) {
+        // rows whose cut is tied: the words now hold the columns at or above
+        // it; keep the strict ones and the first of the tied ones.  Rare, so
+        // thread 0 and 1 of a quad do it serially, a row each.
+        uint32_t at_or_above[8];
+        const int rr = rA + 8 * u4;
+        if (u4 < 2)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mask |= __uint_as_float(x[e]) >= cut ? 1u << e : 0u;
-        while (mask != 0u) {
-          const int e = __ffs(mask) - 1;
-          mask &= mask - 1u;
-          float v = cut;
-          if (!last || !c.exact) {                                        // the score is only needed for these
+          for (int k = 0; k < 8; ++k) at_or_above[k] = k < words ? masks[rr * 9 + k] : 0u;
+        __syncwarp();
+        write_masks(true);
+        if (u4 < 2) {
+          const bool exact = u4 ? sB.exact : sA.exact;
+          const float cut = u4 ? sB.lo : sA.lo;
+          int above = 0;
+          for (int k = 0; k < words; ++k) above += __popc(masks[rr * 9 + k]);
+          for (int w = 0; w < listed; ++w) above += list_s[w * 128 + rr] > cut ? 1 : 0;
+          int left = exact ? 0x7FFFFFFF : need - above;
+          for (int w = 0; w < listed; ++w)                                // carried ones come first
+            if (list_s[w * 128 + rr] == cut && left-- <= 0) list_s[w * 128 + rr] = -INFINITY;
+          left = max(left, 0);
 #pragma unroll
-            for (int f = 0; f < 32; ++f) v = f == e ? __uint_as_float(x[f]) : v;
-          } else {
-            v = INFINITY;
+          for (int k = 0; k < 8; ++k) {
+            if (k >= words) break;
+            uint32_t eq = at_or_above[k] & ~masks[rr * 9 + k], keep = 0u;
+            for (; eq != 0u && left > 0; --left) {
+              keep |= eq & (0u - eq);
+              eq &= eq - 1u;
+            }
+            masks[rr * 9 + k] |= keep;
           }
-          take(v, c0 + k + e);
         }
-      });
+        __syncwarp();
+      }
+      if (last) {
+        // a row's winners in block order: carried ones (thread 0 of the quad),
+        // then those of words 2 u4 and 2 u4 + 1
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int r = rA + 8 * half;
+          const float cut = half ? sB.lo : sA.lo;
+          int* const mine = staged + r * (args.n + 1) + args.keep_first;
+          int at = 0;
+          for (int w = 0; w < listed; ++w)
+            if (list_s[w * 128 + r] >= cut) {
+              if (u4 == 0) mine[at] = list_j[w * 128 + r];
+              ++at;
+            }
+          for (int k = 0; k < min(words, 2 * u4); ++k) at += __popc(masks[r * 9 + k]);
+          for (int k = 2 * u4; k < min(words, 2 * u4 + 2); ++k)
+            for (uint32_t m = masks[r * 9 + k]; m != 0u; m &= m - 1u) mine[at++] = c0 + 32 * k + __ffs(m) - 1;
+          __syncwarp();
+        }
+      } else {
+        // carry the winners on: the earlier ones move down (in place, by
+        // thread 0), then each column's score goes to its place
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = rA + 8 * half;
+          const float cut = half ? sB.lo : sA.lo;
+          int kept = 0;
+          if (u4 == 0)
+            for (int w = 0; w < listed; ++w) {
+              const float v = list_s[w * 128 + r];
+              if (v < cut) continue;
+              list_s[kept * 128 + r] = v;
+              list_j[kept * 128 + r] = list_j[w * 128 + r];
+              ++kept;
+            }
+          __syncwarp();
+          kept = __shfl_sync(0xffffffffu, kept, lane & ~3);
+          each64([&](int k, const uint32_t (&x)[32]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = k + 8 * i + 2 * u4 + e;
+                if (col >= cols || !((masks[r * 9 + col / 32] >> (col & 31)) & 1u)) continue;
+                int at = kept + __popc(masks[r * 9 + col / 32] & ((1u << (col & 31)) - 1u));
+                for (int w = 0; w < col / 32; ++w) at += __popc(masks[r * 9 + w]);
+                list_s[at * 128 + r] = __uint_as_float(x[4 * i + 2 * half + e]);
+                list_j[at * 128 + r] = c0 + col;
+              }
+          });
+          __syncwarp();
+        }
+      }
       listed = min(need, have);
     }
     tc_fence_before();
@@ -620,12 +704,12 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   }
   if (ok) {
     // lists out, the kept blocks around the chosen ones
-    for (int e = threadIdx.x; e < kTileKeys * args.n; e += Cfg::kThreads) {
-      const int r = e / args.n, k = e % args.n, i = i0 + r;
+    for (int r = warp; r < kTileKeys; r += Cfg::kThreads / 32) {
+      const int i = i0 + r;
       if (i < 0 || i >= len) continue;
-      args.blocks[(out_row0 + i) * args.n + k] = k < args.keep_first ? k
-                                                 : k >= args.n - args.keep_last ? nb - args.n + k
-                                                                                : staged[r * (args.n + 1) + k];
+      int* out = args.blocks + (out_row0 + i) * args.n;
+      for (int k = lane; k < args.n; k += 32)
+        out[k] = k < args.keep_first ? k : k >= args.n - args.keep_last ? nb - args.n + k : staged[r * (args.n + 1) + k];
     }
   }
   __syncthreads();
@@ -637,7 +721,7 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
 
 cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s) {
   using Cfg = SelectTileCfg;
-  constexpr int kRowSmem = 200 * 1024, kTileSmem = static_cast<int>(Cfg::kListOff) + Cfg::kMaxListed * 128 * 8 + 1024;
+  constexpr int kRowSmem = 128 * 1024, kTileSmem = static_cast<int>(Cfg::kListOff) + Cfg::kMaxListed * 128 * 8 + 1024;
   static bool configured[64] = {};
   if (!configured[device]) {
     cudaError_t e = cudaFuncSetAttribute(kb_select_row_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
@@ -658,8 +742,7 @@ cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s) {
     kb_select_tile_kernel<<<static_cast<unsigned>(grid), Cfg::kThreads, smem, s>>>(a, n_tiles);
     return cudaGetLastError();
   }
-  const int rounds = (a.max_blocks + kChunkKeys - 1) / kChunkKeys;
-  const size_t smem = (static_cast<size_t>(a.max_blocks) + (a.max_blocks > kChunkKeys ? 4u * rounds * a.n : 0u)) * 4u;
+  const size_t smem = static_cast<size_t>(a.max_blocks) * 4u;
   const long long rows = static_cast<long long>(a.B) * a.Hkv * a.L;
   if (rows > 0x7FFFFFFFLL || smem > kRowSmem) return cudaErrorInvalidValue;
   kb_select_row_kernel<<<static_cast<unsigned>(rows), kSelectRowThreads, smem, s>>>(a);
