@@ -457,6 +457,8 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   kb::SparseBwdArgs a{};
   if ((s = fill_plan(c, cap, dev.err, true, &a.plan)) != KB_OK) return s;
   if (static_cast<long long>(a.plan.max_blocks) * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  a.q = q;
+  a.dout = dout;
   a.lse = lse;
   a.delta = delta;
   a.dq = dq;

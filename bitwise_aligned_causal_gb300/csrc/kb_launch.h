@@ -201,6 +201,7 @@ cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, con
 
 // Gradient of whole-sequence block-sparse attention (kb_sparse_bwd.cu).
 struct SparseBwdArgs {
+  const void *q, *dout;        // [B, Hq, S, 128] bf16
   const float* lse;            // [B, Hq, S]
   const float* delta;          // [B, Hq, S]
   void *dq, *dk, *dv;

@@ -74,4 +74,12 @@ __device__ __forceinline__ void tma_load_group_hint(uint32_t dst, const void* tm
       : "memory");
 }
 
+// Asynchronous copy of 16 bytes into shared memory, `size` (0 or 16) of them
+// from global memory and zeros after that.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+// Wait for every such copy of this thread.
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 }  // namespace kb

@@ -9,10 +9,10 @@
 //
 // Rows come in the units of the forward (32 positions times four heads, 128
 // rows).  The dq kernel runs one CTA per unit over the unit's walk; the dk/dv
-// kernel one CTA per (b, KV head, key block) over the units whose rows listed
-// it, found in the plan's row masks.  A row of a unit that did not list the
-// block at hand has P = 0 there.  No atomics: every gradient element is
-// summed by one CTA in one order.
+// kernel one CTA per (b, KV head, key block) over the rows that listed it,
+// found in the plan's row masks and packed 32 positions to a step.  A row of a
+// unit that did not list the dq kernel's block at hand has P = 0 there.  No
+// atomics: every gradient element is summed by one CTA in one order.
 #include <type_traits>
 
 #include "kb_bwd.cuh"
@@ -324,11 +324,21 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
 }
 
 // ----------------------------------------------------------- dk/dv kernel
-
+//
+// A step takes 32 positions that listed the key block, whichever units they
+// come from, with their four heads: row 4r + h of the step's Q and dO tiles is
+// head h of its r-th position, so no row of a step is idle but in the last
+// one.  Four producer warps find the positions in the plan's row masks and
+// copy their rows with 16-byte asynchronous copies into the swizzled tiles: a
+// TMA box per position (four heads, 512 bytes) took 11,000 cycles a step, and
+// whole units (all 32 rows of a unit of which some listed the block) 1.5 times
+// the steps.  At S = 8192 with 16 blocks per row: 565 us, against 1127 and
+// 688 us.
 struct SparseBwdKVCfg {
-  static constexpr int kThreads = 320;
-  static constexpr int kLoadWarp = 8;
-  static constexpr int kMmaWarp = 9;
+  static constexpr int kThreads = 416;        // 8 elementwise warps, 4 producers, the MMA issuer
+  static constexpr int kLoadWarp0 = 8;
+  static constexpr int kLoadWarps = 4;
+  static constexpr int kMmaWarp = 12;
   static constexpr int kStages = 2;           // Q/dO ring
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColST = 0, kColDPT = 128, kColDV = 256, kColDK = 384;
@@ -337,8 +347,10 @@ struct SparseBwdKVCfg {
   static constexpr uint32_t kQOff = 2 * kTileBytes;                   // slot s: Q at kQOff + s*2*tile,
   static constexpr uint32_t kSlotBytes = 2 * kTileBytes;              //         dO right after it
   static constexpr uint32_t kVecOff = kQOff + kStages * kSlotBytes;   // slot s: -lse2[128], -delta[128]
-  static constexpr uint32_t kVecBytes = 2 * 128 * 4 + 16;            // ... and the place of the first row
-  static constexpr uint32_t kBarOff = kVecOff + kStages * kVecBytes;
+  static constexpr uint32_t kVecBytes = (2 * 128 + 32 + 4) * 4;       // ... the positions' places, "own block" flag
+  static constexpr int kQueue = 32 + 1024;                            // positions found and not yet used, per producer warp
+  static constexpr uint32_t kQueueOff = kVecOff + kStages * kVecBytes;
+  static constexpr uint32_t kBarOff = kQueueOff + kLoadWarps * kQueue * 4;
   static constexpr int kBarKV = 0;                                    // K(jt), V(jt) landed
   static constexpr int kBarQDFull = 1;                                // 2: Q, dO of step s landed
   static constexpr int kBarQDEmpty = kBarQDFull + kStages;            // 2: dV, dK of step s done
@@ -354,9 +366,8 @@ struct SparseBwdKVCfg {
 };
 
 __global__ void __launch_bounds__(SparseBwdKVCfg::kThreads, 1)
-kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
-                   const SparseBwdArgs args) {
+kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                          const SparseBwdArgs args) {
   using Cfg = SparseBwdKVCfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -375,7 +386,7 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
   const int S = args.plan.L;
   const int n_tiles = args.plan.n_tiles;
   uint32_t* const err = args.plan.err;
-  // units that listed this block, as row masks of the position tiles from the block's own on
+  // rows that listed this block, as masks of the position tiles from the block's own on
   const uint32_t* const masks =
       args.plan.masks + (static_cast<size_t>(group) * args.plan.max_blocks + jt) * n_tiles;
   const int t0 = jt * (kTileKeys / kUnitRows);
@@ -385,9 +396,11 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
       uint32_t count = 1u;
       if (i >= Cfg::kBarPDSFull && i < Cfg::kBarPDSFull + 4) count = 256u;
       if (i >= Cfg::kBarVecFull && i < Cfg::kBarVecFull + Cfg::kStages) count = 32u;
+      if (i >= Cfg::kBarQDFull && i < Cfg::kBarQDFull + Cfg::kStages) count = 32u * Cfg::kLoadWarps;
       mbar_init(bar(i), count);
     }
     misc[1] = (*reinterpret_cast<volatile uint32_t*>(err) != 0) ? 1u : 0u;
+    misc[2] = 0u;
     fence_mbar_init();
   }
   if (warp == Cfg::kMmaWarp) {
@@ -399,20 +412,22 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
   tc_fence_after();
   const uint32_t tmem_base = misc[0];
   const bool skip = (*abort_flag != 0);
-  int n_steps = 0;                                    // one per unit that listed the block
+  int found = 0;                                      // rows that listed the block
   if (!skip)
-    for (int t = t0; t < n_tiles; t += Cfg::kThreads) {
-      const int i = t + static_cast<int>(threadIdx.x);
-      n_steps += __syncthreads_count(i < n_tiles && __ldg(masks + i) != 0u);
-    }
+    for (int t = t0 + static_cast<int>(threadIdx.x); t < n_tiles; t += Cfg::kThreads) found += __popc(__ldg(masks + t));
+  found = __reduce_add_sync(0xffffffffu, found);
+  if (lane == 0) atomicAdd(reinterpret_cast<int*>(smem + Cfg::kMiscOff) + 2, found);
+  __syncthreads();
+  const int n_rows = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff)[2];
+  const int n_steps = (n_rows + kUnitRows - 1) / kUnitRows;
 
-  if (warp == Cfg::kLoadWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp >= Cfg::kLoadWarp0 && warp < Cfg::kLoadWarp0 + Cfg::kLoadWarps) {
+    // ----------------------------------------------------------- producers
+    // Every warp finds the step's positions for itself and copies the rows of
+    // eight of them.
     if (!skip) {
-      const uint64_t keep = l2_policy_evict_last();
-      if (lane == 0) {
-        tma_prefetch_desc(&tmap_q);
-        tma_prefetch_desc(&tmap_do);
+      const int lw = warp - Cfg::kLoadWarp0;
+      if (lw == 0 && lane == 0) {
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
         if (n_steps > 0) {
@@ -421,55 +436,83 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
           tma_load_tile(sbase + Cfg::kVOff, &tmap_v, jt * kTileKeys, group, bar(Cfg::kBarKV));
         }
       }
-      int issued = 0;
       bool ok = true;
-      int tb = t0 - 32;                                                // 32 position tiles at a time: this lane's mask
-      uint32_t mine = 0u, left = 0u;                                   // and which of them are still to come
+      int* queue = reinterpret_cast<int*>(smem + Cfg::kQueueOff) + lw * Cfg::kQueue;
+      int tb = t0, queued = 0, used = 0;                               // next masks; the queue holds used .. queued-1
       for (int s = 0; s < n_steps; ++s) {
         const int slot = s % Cfg::kStages;
-        while (left == 0u && tb < n_tiles) {                           // n_steps counts the masks that are not zero
+        // the next 32 positions: what is left moves to the front, then the
+        // set bits of 32 masks at a time join it
+        while (queued - used < kUnitRows && tb < n_tiles) {
+          const int rest = queued - used;
+          const int keep_pos = lane < rest ? queue[used + lane] : 0;
+          __syncwarp();
+          if (lane < rest) queue[lane] = keep_pos;
+          uint32_t m = tb + lane < n_tiles ? __ldg(masks + tb + lane) : 0u;
+          int at = __popc(m);
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, at, d);
+            if (lane >= d) at += v;
+          }
+          const int total = __shfl_sync(0xffffffffu, at, 31);
+          at += rest - __popc(m);
+          for (; m != 0u; m &= m - 1u) queue[at++] = (tb + lane) * kUnitRows + __ffs(m) - 1;
+          __syncwarp();
+          used = 0;
+          queued = rest + total;
           tb += 32;
-          mine = tb + lane < n_tiles ? __ldg(masks + tb + lane) : 0u;
-          left = __ballot_sync(0xffffffffu, mine != 0u);
         }
-        ok = left != 0u;                                               // fewer than counted: the workspace was overwritten
-        if (!ok) break;
-        const int src = __ffs(left) - 1;
-        left &= left - 1u;
-        const int it = tb + src;
-        const uint32_t rows = __shfl_sync(0xffffffffu, mine, src);     // bit r: row r of the unit listed the block
+        // a step short of positions is filled up with rows past the sequence,
+        // which read as zeros; a position there was not listed by this call
+        int pos = lane < queued - used ? queue[used + lane] : S;
+        const bool listed = pos < S;
+        if (!listed) pos = S;
+        used = min(queued, used + kUnitRows);
         if (s >= Cfg::kStages)
           ok = mbar_wait(bar(Cfg::kBarQDEmpty + slot), ((s / Cfg::kStages) - 1) & 1, abort_flag, err,
                          kDevTimeoutSlot);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = sbase + Cfg::kQOff + slot * Cfg::kSlotBytes;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(Cfg::kBarQDFull + slot), 2 * kTileBytes);
-          tma_load_group_hint(dst, &tmap_q, it * kUnitRows, group, bar(Cfg::kBarQDFull + slot), keep);
-          tma_load_group_hint(dst + kTileBytes, &tmap_do, it * kUnitRows, group, bar(Cfg::kBarQDFull + slot), keep);
-        }
-        issued = s + 1;
-        // -lse (base 2) and -delta of the step's 128 query rows (lane r: row r
-        // of the four heads); a row that did not list the block gets -lse2 =
-        // -inf, so its P (and dS) is exactly zero
-        float* vec = reinterpret_cast<float*>(smem + Cfg::kVecOff + slot * Cfg::kVecBytes);
-        const bool listed = ((rows >> lane) & 1u) && it * kUnitRows + lane < S;
+        // 16 lanes a row, two rows a copy: rows 32 lw .. 32 lw + 31 of both tiles
+        const int c = lane & 15;
+        const uint32_t dst = sbase + Cfg::kQOff + slot * Cfg::kSlotBytes + static_cast<uint32_t>(c >> 3) * kSlabBytes;
 #pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
-          const size_t at = (static_cast<size_t>(group) * kGroup + h) * static_cast<size_t>(S) + it * kUnitRows + lane;
-          vec[32 * h + lane] = listed ? -__fmul_rn(args.lse[at], kLog2e) : __int_as_float(0xFF800000);
-          vec[128 + 32 * h + lane] = listed ? -args.delta[at] : -0.0f;
+        for (int k = 0; k < 16; ++k) {
+          const int row = 32 * lw + 2 * k + (lane >> 4);
+          const int p = __shfl_sync(0xffffffffu, pos, 8 * lw + (k >> 1));
+          const uint32_t size = p < S ? 16u : 0u;                      // a filler row is written as zeros
+          const size_t from = ((static_cast<size_t>(group) * kGroup + (row & 3)) * static_cast<size_t>(S) + (p < S ? p : 0)) *
+                                  kHeadDim + 8 * c;
+          const uint32_t at = dst + static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + (((c & 7) ^ (row & 7)) << 4));
+          cp_async16(at, static_cast<const __nv_bfloat16*>(args.q) + from, size);
+          cp_async16(at + kTileBytes, static_cast<const __nv_bfloat16*>(args.dout) + from, size);
         }
-        // first row's place in the key block when the block is the unit's own
-        if (lane == 0) reinterpret_cast<int*>(vec)[256] = it * kUnitRows - jt * kTileKeys;
-        mbar_arrive(bar(Cfg::kBarVecFull + slot));
+        // -lse (base 2) and -delta of the step's 128 query rows; a filler gets
+        // -lse2 = -inf, so its P (and dS) is exactly zero
+        if (lw == 0) {
+          float* vec = reinterpret_cast<float*>(smem + Cfg::kVecOff + slot * Cfg::kVecBytes);
+          float nl[kGroup], nd[kGroup];
+  #pragma unroll
+          for (int h = 0; h < kGroup; ++h) {
+            const size_t at = (static_cast<size_t>(group) * kGroup + h) * static_cast<size_t>(S) + pos;
+            nl[h] = listed ? -__fmul_rn(args.lse[at], kLog2e) : __int_as_float(0xFF800000);
+            nd[h] = listed ? -args.delta[at] : -0.0f;
+          }
+          reinterpret_cast<float4*>(vec)[lane] = make_float4(nl[0], nl[1], nl[2], nl[3]);
+          reinterpret_cast<float4*>(vec + 128)[lane] = make_float4(nd[0], nd[1], nd[2], nd[3]);
+          // the position's place in the key block, if the block is its own
+          const int place = pos - jt * kTileKeys;
+          reinterpret_cast<int*>(vec)[256 + lane] = place;
+          const uint32_t own = __ballot_sync(0xffffffffu, place < kTileKeys);
+          if (lane == 0) reinterpret_cast<uint32_t*>(vec)[288] = own;
+          mbar_arrive(bar(Cfg::kBarVecFull + slot));
+        }
+        cp_async_wait();
+        fence_proxy_async_smem();                                      // the copies -> visible to the tensor core
+        mbar_arrive(bar(Cfg::kBarQDFull + slot));
       }
-      if (!ok && lane == 0) {
-        if (issued > 0) drain_wait_b(bar(Cfg::kBarKV), 0);
-        for (int x = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); x < issued; ++x)
-          drain_wait_b(bar(Cfg::kBarQDFull + x % Cfg::kStages), (x / Cfg::kStages) & 1);
-      }
+      if (!ok && lw == 0 && lane == 0) drain_wait_b(bar(Cfg::kBarKV), 0);
     }
   } else if (warp == Cfg::kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
@@ -528,21 +571,21 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
     const int rA = lane_base + (lane >> 2);
     const int rB = rA + 8;
     const float2 c2 = make_float2(score_scale_log2(), score_scale_log2());
-    // one query quarter (the 32 rows of head qt): a step of the unit's own
-    // block masks keys past the query, the others take no select
+    // one query quarter (eight positions): a step with positions of the block
+    // itself masks keys past them, the others take no select
     auto quarter = [&](auto diag_tag, const uint32_t (&sv)[16], const uint32_t (&pv)[16], const float* vnl,
-                       const float* vnd, int qt, int p0, uint32_t (&pp)[8], uint32_t (&dd)[8]) {
+                       const float* vnd, int qt, const int* place, uint32_t (&pp)[8], uint32_t (&dd)[8]) {
       constexpr bool kDiag = decltype(diag_tag)::value;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int qc = 32 * qt + 8 * r + 2 * u;                      // query rows qc, qc + 1 within their tile
         const float2 nl = *reinterpret_cast<const float2*>(vnl + qc);
         const float2 nd = *reinterpret_cast<const float2*>(vnd + qc);
-        const int at = p0 + 8 * r + 2 * u;                           // the query's place in the key block
-        p_ds_pair<kDiag>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nl, nd, rA > at, rA > at + 1,
+        const int at = kDiag ? place[qc >> 2] : 0;                   // both columns are heads of one position
+        p_ds_pair<kDiag>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nl, nd, rA > at, rA > at,
                          pp[2 * r], dd[2 * r]);
         p_ds_pair<kDiag>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nl, nd, rB > at,
-                         rB > at + 1, pp[2 * r + 1], dd[2 * r + 1]);
+                         rB > at, pp[2 * r + 1], dd[2 * r + 1]);
       }
     };
     bool ok = !skip;
@@ -556,16 +599,16 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __gr
       tc_fence_after();
       const float* vnl = reinterpret_cast<const float*>(smem + Cfg::kVecOff + slot * Cfg::kVecBytes);
       const float* vnd = vnl + 128;
-      const int p0 = reinterpret_cast<const int*>(vnl)[256];
-      const bool diag = p0 < kTileKeys;                              // the unit's own block: keys past the row masked
+      const int* place = reinterpret_cast<const int*>(vnl) + 256;
+      const bool diag = reinterpret_cast<const uint32_t*>(vnl)[288] != 0u;
 #pragma unroll
       for (int qt = 0; qt < 4; ++qt) {                                 // query quarter: 32 query columns
         uint32_t sv[16], pv[16];
         tmem_ld_16x256b_x4_pair_wait(tmem_base + Cfg::kColST + lane_off + 32u * qt,
                                      tmem_base + Cfg::kColDPT + lane_off + 32u * qt, sv, pv);
         uint32_t pp[8], dd[8];
-        if (diag) quarter(std::true_type{}, sv, pv, vnl, vnd, qt, p0, pp, dd);
-        else quarter(std::false_type{}, sv, pv, vnl, vnd, qt, p0, pp, dd);
+        if (diag) quarter(std::true_type{}, sv, pv, vnl, vnd, qt, place, pp, dd);
+        else quarter(std::false_type{}, sv, pv, vnl, vnd, qt, place, pp, dd);
         // bf16 pairs of query columns 32*qt.. go to columns 16*qt.. of the
         // same buffers; those fp32 columns were read in this quarter or an
         // earlier one
@@ -644,7 +687,7 @@ cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid_kv = static_cast<unsigned>(a.plan.max_blocks * a.plan.B * a.plan.Hkv);
-  kb_sparse_bwd_dkdv_kernel<<<grid_kv, SparseBwdKVCfg::kThreads, SparseBwdKVCfg::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
+  kb_sparse_bwd_dkdv_kernel<<<grid_kv, SparseBwdKVCfg::kThreads, SparseBwdKVCfg::kSmemBytes, s>>>(tk, tv, a);
   return cudaGetLastError();
 }
 
