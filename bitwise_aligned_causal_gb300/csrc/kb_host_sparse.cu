@@ -85,6 +85,23 @@ PlanSizes plan_sizes(int B, int Hkv, int L, int n_select, long long max_blocks) 
 // Where the backward's row masks start: one per unit and key block, behind the walks.
 long long masks_at(const PlanSizes& p) { return align256(p.bytes); }
 
+// The backward's workspace behind the plan's: row masks, tickets, fp32 sums.
+struct BwdSizes {
+  long long n_split, masks, tickets, sums, bytes;      // key blocks that two CTAs may share, offsets, size
+};
+BwdSizes bwd_sizes(const PlanSizes& p, int B, int Hkv, int S) {
+  BwdSizes b;
+  const long long blocks = (S + kb::kTileKeys - 1) / kb::kTileKeys, groups = static_cast<long long>(B) * Hkv;
+  // rows S - 128 j and more can list block j: at least 32 * (split - 1) + 1
+  const long long spare = S - (kb::kSparseSplitSteps - 1LL) * kb::kUnitRows;
+  b.n_split = spare > 0 ? std::min((spare + kb::kTileKeys - 1) / kb::kTileKeys, blocks) : 0;
+  b.masks = masks_at(p);
+  b.tickets = align256(b.masks + p.units * blocks * 4);
+  b.sums = align256(b.tickets + groups * b.n_split * 4);
+  b.bytes = b.sums + groups * b.n_split * 2 * (2LL * kb::kTileKeys * kb::kHeadDim * 4);
+  return b;
+}
+
 struct SparseCall {
   const void *q, *k, *v;
   void* o;
@@ -152,7 +169,8 @@ kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, bool with_masks
   a->num_pages = c.num_pages;
   a->err = err;
   const PlanSizes full = plan_sizes(c.B, c.Hkv, c.L, c.n_select, a->max_blocks);
-  const long long need = with_masks ? masks_at(full) + full.units * a->max_blocks * 4 : full.bytes;
+  const BwdSizes bwd = bwd_sizes(full, c.B, c.Hkv, c.L);
+  const long long need = with_masks ? bwd.bytes : full.bytes;
   if (c.workspace == nullptr || !host_aligned(c.workspace, 256) || c.workspace_bytes < static_cast<size_t>(need))
     return KB_ERR_INVALID_ARG;
   a->n_tiles = static_cast<int>(c.starts != nullptr ? max_tiles32(c.L)
@@ -161,7 +179,11 @@ kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, bool with_masks
   a->walk_cap = static_cast<int>(full.cap);
   a->walk_len = static_cast<int*>(c.workspace);
   a->walks = reinterpret_cast<uint2*>(static_cast<char*>(c.workspace) + align256(full.units * 4));
-  if (with_masks) a->masks = reinterpret_cast<uint32_t*>(static_cast<char*>(c.workspace) + masks_at(full));
+  if (with_masks) {
+    a->masks = reinterpret_cast<uint32_t*>(static_cast<char*>(c.workspace) + bwd.masks);
+    a->tickets = reinterpret_cast<int*>(static_cast<char*>(c.workspace) + bwd.tickets);
+    a->n_split = static_cast<int>(bwd.n_split);
+  }
   return KB_OK;
 }
 
@@ -435,8 +457,7 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
 size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select) {
   if (kb_attn_sparse_workspace_bytes(B, Hkv, S, n_select, S) == 0) return 0;
   const long long blocks = (S + kb::kTileKeys - 1) / kb::kTileKeys;
-  const PlanSizes p = plan_sizes(B, Hkv, S, n_select, blocks);
-  return static_cast<size_t>(masks_at(p) + p.units * blocks * 4);
+  return static_cast<size_t>(bwd_sizes(plan_sizes(B, Hkv, S, n_select, blocks), B, Hkv, S).bytes);
 }
 
 kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -456,9 +477,13 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   if ((s = device_pointers(outs, 6)) != KB_OK) return s;
   kb::SparseBwdArgs a{};
   if ((s = fill_plan(c, cap, dev.err, true, &a.plan)) != KB_OK) return s;
-  if (static_cast<long long>(a.plan.max_blocks) * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  if (2LL * a.plan.max_blocks * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   a.q = q;
   a.dout = dout;
+  a.n_split = a.plan.n_split;
+  a.tickets = a.plan.tickets;
+  a.sums = reinterpret_cast<float4*>(static_cast<char*>(workspace) +
+                                     bwd_sizes(plan_sizes(B, Hkv, S, n_select, a.plan.max_blocks), B, Hkv, S).sums);
   a.lse = lse;
   a.delta = delta;
   a.dq = dq;

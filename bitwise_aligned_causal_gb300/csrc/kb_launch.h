@@ -192,6 +192,8 @@ struct SparseArgs {
   // backward: workspace [B * Hkv][max_blocks][n_tiles], the row mask of
   // position tile t for key block j (written for the blocks up to the tile's own)
   uint32_t* masks;
+  int* tickets;                // backward: [B * Hkv][n_split] counters to zero
+  int n_split;
   uint32_t* err;
 };
 cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
@@ -199,12 +201,18 @@ cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
 cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const SparseArgs& a, int device, cudaStream_t s);
 
+// Steps of 32 positions from which on two CTAs share a key block's gradient.
+constexpr int kSparseSplitSteps = 128;
+
 // Gradient of whole-sequence block-sparse attention (kb_sparse_bwd.cu).
 struct SparseBwdArgs {
   const void *q, *dout;        // [B, Hq, S, 128] bf16
   const float* lse;            // [B, Hq, S]
   const float* delta;          // [B, Hq, S]
   void *dq, *dk, *dv;
+  int n_split;                 // key blocks 0 .. n_split-1 may have kSparseSplitSteps steps or more
+  float4* sums;                // workspace [B * Hkv][n_split][2 CTAs]: fp32 dv and dk, 128 KB each
+  int* tickets;                // workspace [B * Hkv][n_split], zeroed by the plan
   SparseArgs plan;             // units, walks and masks of the call
 };
 // tq, tdo: host_group_map of q and dout; tk, tv: host_rows_map of k and v.

@@ -334,6 +334,16 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
 // whole units (all 32 rows of a unit of which some listed the block) 1.5 times
 // the steps.  At S = 8192 with 16 blocks per row: 565 us, against 1127 and
 // 688 us.
+//
+// Blocks differ in how many rows list them (the first block is kept by all),
+// and one CTA for the longest would hold up the launch.  So a block of
+// kSparseSplitSteps steps or more is shared by two CTAs, half of its steps each:
+// both leave their fp32 sums in the workspace, and whichever is done last adds
+// the other's to its own.  Neither waits, and a sum of two terms has one value
+// in either order.  What is summed how depends on the block's rows alone, not
+// on the batch or the width of the lists.  Clusters of two CTAs per block, the
+// second leaving at once where there is nothing to share, took 579 us: a
+// cluster needs two free SMs at a time.
 struct SparseBwdKVCfg {
   static constexpr int kThreads = 416;        // 8 elementwise warps, 4 producers, the MMA issuer
   static constexpr int kLoadWarp0 = 8;
@@ -381,8 +391,12 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
 
   // (b, kv head g, key block jt), first blocks of every group first: they can
   // be listed by the most units, so the longest CTAs start first
-  const int jt = static_cast<int>(blockIdx.x) / (args.plan.B * args.plan.Hkv);
-  const int group = static_cast<int>(blockIdx.x) % (args.plan.B * args.plan.Hkv);
+  const int groups = args.plan.B * args.plan.Hkv;
+  const int shared = args.n_split * groups;           // CTAs 0 .. 2 shared - 1: blocks that two CTAs may share
+  const int bid = static_cast<int>(blockIdx.x);
+  const int share = bid < 2 * shared ? bid / groups % 2 : 0;
+  const int jt = bid < 2 * shared ? bid / (2 * groups) : (bid - shared) / groups;
+  const int group = bid % groups;
   const int S = args.plan.L;
   const int n_tiles = args.plan.n_tiles;
   uint32_t* const err = args.plan.err;
@@ -403,7 +417,21 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
     misc[2] = 0u;
     fence_mbar_init();
   }
+  __syncthreads();
+  int found = 0;                                      // rows that listed the block
+  for (int t = t0 + static_cast<int>(threadIdx.x); t < n_tiles; t += Cfg::kThreads) found += __popc(__ldg(masks + t));
+  found = __reduce_add_sync(0xffffffffu, found);
+  if (lane == 0) atomicAdd(reinterpret_cast<int*>(smem + Cfg::kMiscOff) + 2, found);
+  __syncthreads();
+  const int n_rows = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff)[2];
+  const int block_steps = (n_rows + kUnitRows - 1) / kUnitRows;
+  const bool split = jt < args.n_split && block_steps >= kSparseSplitSteps;
+  const int step0 = share ? (split ? block_steps / 2 : block_steps) : 0;
+  const int n_steps = (split && !share ? block_steps / 2 : block_steps) - step0;
+
+  if (share == 1 && !split) return;
   if (warp == Cfg::kMmaWarp) {
+    __syncwarp();
     tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -412,14 +440,6 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
   tc_fence_after();
   const uint32_t tmem_base = misc[0];
   const bool skip = (*abort_flag != 0);
-  int found = 0;                                      // rows that listed the block
-  if (!skip)
-    for (int t = t0 + static_cast<int>(threadIdx.x); t < n_tiles; t += Cfg::kThreads) found += __popc(__ldg(masks + t));
-  found = __reduce_add_sync(0xffffffffu, found);
-  if (lane == 0) atomicAdd(reinterpret_cast<int*>(smem + Cfg::kMiscOff) + 2, found);
-  __syncthreads();
-  const int n_rows = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff)[2];
-  const int n_steps = (n_rows + kUnitRows - 1) / kUnitRows;
 
   if (warp >= Cfg::kLoadWarp0 && warp < Cfg::kLoadWarp0 + Cfg::kLoadWarps) {
     // ----------------------------------------------------------- producers
@@ -439,6 +459,7 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
       bool ok = true;
       int* queue = reinterpret_cast<int*>(smem + Cfg::kQueueOff) + lw * Cfg::kQueue;
       int tb = t0, queued = 0, used = 0;                               // next masks; the queue holds used .. queued-1
+      int skip_rows = step0 * kUnitRows;                               // positions of the share before this one
       for (int s = 0; s < n_steps; ++s) {
         const int slot = s % Cfg::kStages;
         // the next 32 positions: what is left moves to the front, then the
@@ -456,12 +477,17 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
             if (lane >= d) at += v;
           }
           const int total = __shfl_sync(0xffffffffu, at, 31);
-          at += rest - __popc(m);
-          for (; m != 0u; m &= m - 1u) queue[at++] = (tb + lane) * kUnitRows + __ffs(m) - 1;
-          __syncwarp();
-          used = 0;
-          queued = rest + total;
           tb += 32;
+          if (total <= skip_rows) {                                    // nothing is queued yet
+            skip_rows -= total;
+            continue;
+          }
+          at += rest - __popc(m);
+          for (; m != 0u; m &= m - 1u) queue[at++] = (tb - 32 + lane) * kUnitRows + __ffs(m) - 1;
+          __syncwarp();
+          used = skip_rows;
+          skip_rows = 0;
+          queued = rest + total;
         }
         // a step short of positions is filled up with rows past the sequence,
         // which read as zeros; a position there was not listed by this call
@@ -621,36 +647,73 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
     }
     if (ok) ok = mbar_wait(bar(Cfg::kBarDone), 0, abort_flag, err, kDevTimeoutMma);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      const int jA = jt * kTileRows + rA, jB = jt * kTileRows + rB;
+    tc_fence_after();
+    // A shared block: this thread's sums, part by part (dv's halves, then
+    // dk's), as a float4 of registers 4r .. 4r+3 per r
+    float4* const sums = args.sums + ((static_cast<size_t>(group) * args.n_split + jt) * 2) * (32 * 256);
+    bool writes = ok && (share == 0 || split);
+    if (split) {                                                     // every elementwise warp meets the barriers
+      float4* const mine = sums + share * (32 * 256);
+#pragma unroll 1
+      for (int part = 0; part < 4 && ok; ++part) {
+        uint32_t v[32];
+        tmem_ld_16x256b_x8_wait(tmem_base + (part < 2 ? Cfg::kColDV : Cfg::kColDK) + lane_off + 64u * (part & 1), v);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          mine[(8 * part + r) * 256 + threadIdx.x] =
+              make_float4(__uint_as_float(v[4 * r]), __uint_as_float(v[4 * r + 1]), __uint_as_float(v[4 * r + 2]),
+                          __uint_as_float(v[4 * r + 3]));
+      }
+      // all 256 threads' sums, then one ticket: the second to draw finds the
+      // other CTA's sums complete
+      __threadfence();
+      named_bar_sync(1u, 256u);
+      if (threadIdx.x == 0) {
+        misc[3] = *abort_flag != 0 ? 0u
+                                   : static_cast<uint32_t>(
+                                         atomicAdd(args.tickets + static_cast<size_t>(group) * args.n_split + jt, 1));
+        __threadfence();
+      }
+      named_bar_sync(1u, 256u);
+      writes = writes && misc[3] == 1u;
+    }
+    if (writes) {
+      const int jA = jt * kTileKeys + rA, jB = jt * kTileKeys + rB;
       const bool vA = jA < S, vB = jB < S;
       const size_t kv0 = static_cast<size_t>(group) * static_cast<size_t>(S);
+      const float4* const theirs = sums + (1 - share) * (32 * 256);
 #pragma unroll 1
-      for (int which = 0; which < 2; ++which) {                      // 0: dv, 1: dk (scaled by 1/sqrt(128))
+      for (int part = 0; part < 4; ++part) {                         // dk is scaled by 1/sqrt(128)
+        const int which = part >> 1, half = part & 1;
         __nv_bfloat16* base = static_cast<__nv_bfloat16*>(which ? args.dk : args.dv) + kv0 * kHeadDim;
         uint32_t* oA = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vA ? jA : 0) * kHeadDim);
         uint32_t* oB = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vB ? jB : 0) * kHeadDim);
         const float sc = which ? kInvSqrtD : 1.0f;
-        const uint32_t col0 = which ? Cfg::kColDK : Cfg::kColDV;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[32];
-          tmem_ld_16x256b_x8_wait(tmem_base + col0 + lane_off + 64u * half, v);
-          if (n_steps == 0) {                                        // listed by nobody: the gradient is zero
+        uint32_t v[32];
+        tmem_ld_16x256b_x8_wait(tmem_base + (which ? Cfg::kColDK : Cfg::kColDV) + lane_off + 64u * half, v);
+        if (n_steps == 0) {                                          // listed by nobody: the gradient is zero
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-          }
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+        if (split) {
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            const int col = 64 * half + 8 * r + 2 * u;
-            const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), sc),
-                                            __fmul_rn(__uint_as_float(v[4 * r + 1]), sc));
-            const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), sc),
-                                            __fmul_rn(__uint_as_float(v[4 * r + 3]), sc));
-            if (vA) oA[col >> 1] = wa;
-            if (vB) oB[col >> 1] = wb;
+            const float4 x = __ldcg(theirs + (8 * part + r) * 256 + threadIdx.x);
+            v[4 * r] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * r]), x.x));
+            v[4 * r + 1] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * r + 1]), x.y));
+            v[4 * r + 2] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * r + 2]), x.z));
+            v[4 * r + 3] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * r + 3]), x.w));
           }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int col = 64 * half + 8 * r + 2 * u;
+          const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), sc),
+                                          __fmul_rn(__uint_as_float(v[4 * r + 1]), sc));
+          const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), sc),
+                                          __fmul_rn(__uint_as_float(v[4 * r + 3]), sc));
+          if (vA) oA[col >> 1] = wa;
+          if (vB) oB[col >> 1] = wb;
         }
       }
     }
@@ -686,7 +749,7 @@ cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk,
                             s>>>(tq, tk, tv, tdo, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const unsigned grid_kv = static_cast<unsigned>(a.plan.max_blocks * a.plan.B * a.plan.Hkv);
+  const unsigned grid_kv = static_cast<unsigned>((a.plan.max_blocks + a.n_split) * a.plan.B * a.plan.Hkv);
   kb_sparse_bwd_dkdv_kernel<<<grid_kv, SparseBwdKVCfg::kThreads, SparseBwdKVCfg::kSmemBytes, s>>>(tk, tv, a);
   return cudaGetLastError();
 }

@@ -140,6 +140,30 @@ def test_repeats_order_and_streams_give_the_same_bits(kb):
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, want))
 
 
+def test_long_blocks_shared_by_two_ctas(kb):
+    """Rows enough for a block's gradient to be summed in two halves: every row keeps the first block, and the batch and the
+    lists' width change no bit."""
+    import torch
+
+    S, n = 4500, 3
+    q, k, v, dout = (randn(3700 + i, 2, h, S, 128) for i, h in enumerate((32, 8, 8, 32)))
+    lists = random_lists(3704, 1, S, 0, n).repeat(2, 1, 1, 1)
+    lists[..., 2] = 0
+    o, lse = kb.sparse_prefill_lse(q, k, v, lists)
+    got = kb.sparse_backward(q, k, v, o, dout, lse, lists, check=True)
+    one = [x[1:].contiguous() for x in (q, k, v, o, dout, lse, lists)]
+    wide = torch.cat([one[6], torch.full_like(one[6], -1)], -1).contiguous()
+    alone = kb.sparse_backward(*one[:6], wide, check=True)
+    for x, y in zip(got, alone):
+        assert torch.equal(x[1:].contiguous().view(torch.uint8), y.view(torch.uint8))
+    for g in (0, 7):
+        h = slice(4 * g, 4 * g + 4)
+        args = f64(q)[1, h], f64(k)[1, g], f64(v)[1, g], f64(dout)[1, h], lists[1, g].cpu().numpy()
+        want, tol = plain.gradients(*args), tolerances(*args)
+        for x, y, t in zip((got[0][1, h], got[1][1, g], got[2][1, g]), want, tol):
+            assert np.all(np.abs(f64(x) - y) <= t + 1e-7)
+
+
 def test_a_training_step(kb):
     """Rotation, boxes, selection, forward, backward and the rotation's gradient together."""
     import torch
