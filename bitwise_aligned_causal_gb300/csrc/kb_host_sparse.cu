@@ -85,19 +85,23 @@ PlanSizes plan_sizes(int B, int Hkv, int L, int n_select, long long max_blocks) 
 // Where the backward's row masks start: one per unit and key block, behind the walks.
 long long masks_at(const PlanSizes& p) { return align256(p.bytes); }
 
-// The backward's workspace behind the plan's: row masks, tickets, fp32 sums.
+// The backward's workspace behind the plan's: row masks; counts and tickets
+// (zeroed by every call); jobs and their number; fp32 sums.
 struct BwdSizes {
-  long long n_split, masks, tickets, sums, bytes;      // key blocks that two CTAs may share, offsets, size
+  long long n_split;                                   // key blocks that two CTAs may share
+  long long masks, counts, tickets, jobs, sums, bytes; // offsets, size
 };
 BwdSizes bwd_sizes(const PlanSizes& p, int B, int Hkv, int S) {
   BwdSizes b;
   const long long blocks = (S + kb::kTileKeys - 1) / kb::kTileKeys, groups = static_cast<long long>(B) * Hkv;
-  // rows S - 128 j and more can list block j: at least 32 * (split - 1) + 1
+  // rows from 128 j on can list block j, and a shared one has 32 * (kSparseSplitSteps - 1) + 1 at least
   const long long spare = S - (kb::kSparseSplitSteps - 1LL) * kb::kUnitRows;
   b.n_split = spare > 0 ? std::min((spare + kb::kTileKeys - 1) / kb::kTileKeys, blocks) : 0;
   b.masks = masks_at(p);
-  b.tickets = align256(b.masks + p.units * blocks * 4);
-  b.sums = align256(b.tickets + groups * b.n_split * 4);
+  b.counts = align256(b.masks + p.units * blocks * 4);
+  b.tickets = b.counts + groups * blocks * 4;
+  b.jobs = align256(b.tickets + groups * b.n_split * 4);
+  b.sums = align256(b.jobs + 8 + groups * (blocks + b.n_split) * 8);
   b.bytes = b.sums + groups * b.n_split * 2 * (2LL * kb::kTileKeys * kb::kHeadDim * 4);
   return b;
 }
@@ -181,8 +185,7 @@ kb_status fill_plan(const SparseCall& c, int cap, uint32_t* err, bool with_masks
   a->walks = reinterpret_cast<uint2*>(static_cast<char*>(c.workspace) + align256(full.units * 4));
   if (with_masks) {
     a->masks = reinterpret_cast<uint32_t*>(static_cast<char*>(c.workspace) + bwd.masks);
-    a->tickets = reinterpret_cast<int*>(static_cast<char*>(c.workspace) + bwd.tickets);
-    a->n_split = static_cast<int>(bwd.n_split);
+    a->row_counts = reinterpret_cast<int*>(static_cast<char*>(c.workspace) + bwd.counts);
   }
   return KB_OK;
 }
@@ -480,10 +483,13 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   if (2LL * a.plan.max_blocks * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   a.q = q;
   a.dout = dout;
-  a.n_split = a.plan.n_split;
-  a.tickets = a.plan.tickets;
-  a.sums = reinterpret_cast<float4*>(static_cast<char*>(workspace) +
-                                     bwd_sizes(plan_sizes(B, Hkv, S, n_select, a.plan.max_blocks), B, Hkv, S).sums);
+  const BwdSizes bwd = bwd_sizes(plan_sizes(B, Hkv, S, n_select, a.plan.max_blocks), B, Hkv, S);
+  char* const ws = static_cast<char*>(workspace);
+  a.n_split = static_cast<int>(bwd.n_split);
+  a.tickets = reinterpret_cast<int*>(ws + bwd.tickets);
+  a.n_jobs = reinterpret_cast<int*>(ws + bwd.jobs);
+  a.jobs = reinterpret_cast<int2*>(ws + bwd.jobs + 8);
+  a.sums = reinterpret_cast<float4*>(ws + bwd.sums);
   a.lse = lse;
   a.delta = delta;
   a.dq = dq;
@@ -495,7 +501,8 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   if ((s = kb::host_group_map(&tdo, dout, rows, groups)) != KB_OK) return s;
   if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = kb::launch_sparse_plan(a.plan, dev.index, st);
+  cudaError_t e = cudaMemsetAsync(a.plan.row_counts, 0, static_cast<size_t>(bwd.jobs - bwd.counts), st);
+  if (e == cudaSuccess) e = kb::launch_sparse_plan(a.plan, dev.index, st);
   if (e == cudaSuccess) e = kb::launch_bwd_delta(o, dout, delta, static_cast<long long>(B) * Hq * S, st);
   if (e == cudaSuccess) e = kb::launch_sparse_backward(tq, tk, tv, tdo, a, dev.index, st);
   return done(e);

@@ -192,8 +192,7 @@ struct SparseArgs {
   // backward: workspace [B * Hkv][max_blocks][n_tiles], the row mask of
   // position tile t for key block j (written for the blocks up to the tile's own)
   uint32_t* masks;
-  int* tickets;                // backward: [B * Hkv][n_split] counters to zero
-  int n_split;
+  int* row_counts;             // backward: workspace [B * Hkv][max_blocks], rows that listed a block (zeroed before)
   uint32_t* err;
 };
 cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
@@ -212,7 +211,9 @@ struct SparseBwdArgs {
   void *dq, *dk, *dv;
   int n_split;                 // key blocks 0 .. n_split-1 may have kSparseSplitSteps steps or more
   float4* sums;                // workspace [B * Hkv][n_split][2 CTAs]: fp32 dv and dk, 128 KB each
-  int* tickets;                // workspace [B * Hkv][n_split], zeroed by the plan
+  int* tickets;                // workspace [B * Hkv][n_split], zeroed before
+  int2* jobs;                  // workspace: the dk/dv kernel's jobs, longest first ...
+  int* n_jobs;                 // ... and how many
   SparseArgs plan;             // units, walks and masks of the call
 };
 // tq, tdo: host_group_map of q and dout; tk, tv: host_rows_map of k and v.

@@ -341,9 +341,59 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
 // both leave their fp32 sums in the workspace, and whichever is done last adds
 // the other's to its own.  Neither waits, and a sum of two terms has one value
 // in either order.  What is summed how depends on the block's rows alone, not
-// on the batch or the width of the lists.  Clusters of two CTAs per block, the
-// second leaving at once where there is nothing to share, took 579 us: a
-// cluster needs two free SMs at a time.
+// on the batch or the width of the lists.  The shares are dealt longest first
+// (kb_sparse_order_kernel).  Clusters of two CTAs per block, the second leaving
+// at once where there is nothing to share, took 579 us: a cluster needs two
+// free SMs at a time.
+
+// A job: x the (b, KV head), y the key block, whether it is shared, and which
+// half this is.
+constexpr uint32_t kJobSplit = 1u << 31, kJobSecond = 1u << 30, kJobBlock = kJobSecond - 1u;
+
+// The launch's jobs, longest first, by one CTA: a counting sort on the number
+// of steps (capped at 1023).  The order within one length is that of atomics;
+// it decides only which SM runs what.  A few microseconds; blocks taken as they
+// come left the last CTAs with 240 steps where 201 are the even share.
+constexpr int kOrderThreads = 1024;
+__global__ void __launch_bounds__(kOrderThreads, 1) kb_sparse_order_kernel(const SparseBwdArgs args) {
+  __shared__ int first[kOrderThreads];                // per length (1023 - steps): jobs, then where they start
+  __shared__ int warp_sum[kOrderThreads / 32];
+  const int t = static_cast<int>(threadIdx.x), warp = t >> 5, lane = t & 31;
+  const int groups = args.plan.B * args.plan.Hkv, blocks = args.plan.max_blocks;
+  first[t] = 0;
+  __syncthreads();
+  auto each_job = [&](auto fn) {
+    for (long long i = t; i < static_cast<long long>(groups) * blocks; i += kOrderThreads) {
+      const int group = static_cast<int>(i / blocks), jt = static_cast<int>(i % blocks);
+      const int steps = (__ldg(args.plan.row_counts + i) + kUnitRows - 1) / kUnitRows;
+      const bool split = jt < args.n_split && steps >= kSparseSplitSteps;
+      const int y = jt | (split ? static_cast<int>(kJobSplit) : 0);
+      fn(split ? steps / 2 : steps, group, y);
+      if (split) fn(steps - steps / 2, group, y | static_cast<int>(kJobSecond));
+    }
+  };
+  each_job([&](int steps, int, int) { atomicAdd(&first[kOrderThreads - 1 - min(steps, kOrderThreads - 1)], 1); });
+  __syncthreads();
+  // exclusive sums over the lengths
+  const int mine = first[t];
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  first[t] = before + upto - mine;
+  if (t == kOrderThreads - 1) *args.n_jobs = before + upto;
+  __syncthreads();
+  each_job([&](int steps, int group, int y) {
+    args.jobs[atomicAdd(&first[kOrderThreads - 1 - min(steps, kOrderThreads - 1)], 1)] = make_int2(group, y);
+  });
+}
+
 struct SparseBwdKVCfg {
   static constexpr int kThreads = 416;        // 8 elementwise warps, 4 producers, the MMA issuer
   static constexpr int kLoadWarp0 = 8;
@@ -389,14 +439,12 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // (b, kv head g, key block jt), first blocks of every group first: they can
-  // be listed by the most units, so the longest CTAs start first
-  const int groups = args.plan.B * args.plan.Hkv;
-  const int shared = args.n_split * groups;           // CTAs 0 .. 2 shared - 1: blocks that two CTAs may share
-  const int bid = static_cast<int>(blockIdx.x);
-  const int share = bid < 2 * shared ? bid / groups % 2 : 0;
-  const int jt = bid < 2 * shared ? bid / (2 * groups) : (bid - shared) / groups;
-  const int group = bid % groups;
+  // this CTA's job: (b, KV head), key block and share of its steps
+  if (static_cast<int>(blockIdx.x) >= __ldg(args.n_jobs)) return;
+  const int2 job = __ldg(args.jobs + blockIdx.x);
+  const int group = job.x;
+  const int jt = job.y & static_cast<int>(kJobBlock);
+  const int share = (job.y & static_cast<int>(kJobSecond)) ? 1 : 0;
   const int S = args.plan.L;
   const int n_tiles = args.plan.n_tiles;
   uint32_t* const err = args.plan.err;
@@ -414,22 +462,14 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
       mbar_init(bar(i), count);
     }
     misc[1] = (*reinterpret_cast<volatile uint32_t*>(err) != 0) ? 1u : 0u;
-    misc[2] = 0u;
     fence_mbar_init();
   }
-  __syncthreads();
-  int found = 0;                                      // rows that listed the block
-  for (int t = t0 + static_cast<int>(threadIdx.x); t < n_tiles; t += Cfg::kThreads) found += __popc(__ldg(masks + t));
-  found = __reduce_add_sync(0xffffffffu, found);
-  if (lane == 0) atomicAdd(reinterpret_cast<int*>(smem + Cfg::kMiscOff) + 2, found);
-  __syncthreads();
-  const int n_rows = reinterpret_cast<volatile int*>(smem + Cfg::kMiscOff)[2];
+  const int n_rows = __ldg(args.plan.row_counts + static_cast<size_t>(group) * args.plan.max_blocks + jt);
   const int block_steps = (n_rows + kUnitRows - 1) / kUnitRows;
-  const bool split = jt < args.n_split && block_steps >= kSparseSplitSteps;
+  const bool split = job.y < 0;                       // kJobSplit
   const int step0 = share ? (split ? block_steps / 2 : block_steps) : 0;
   const int n_steps = (split && !share ? block_steps / 2 : block_steps) - step0;
 
-  if (share == 1 && !split) return;
   if (warp == Cfg::kMmaWarp) {
     __syncwarp();
     tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
@@ -747,6 +787,9 @@ cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk,
   }
   kb_sparse_bwd_dq_kernel<<<static_cast<unsigned>(a.plan.n_units), SparseBwdQCfg::kThreads, SparseBwdQCfg::kSmemBytes,
                             s>>>(tq, tk, tv, tdo, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  kb_sparse_order_kernel<<<1, kOrderThreads, 0, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned grid_kv = static_cast<unsigned>((a.plan.max_blocks + a.n_split) * a.plan.B * a.plan.Hkv);

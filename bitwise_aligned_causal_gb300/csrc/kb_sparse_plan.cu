@@ -51,11 +51,12 @@ __global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const Spar
   }
   __syncthreads();
   if (args.masks != nullptr) {
-    // the block's first unit zeroes its ticket
-    if (threadIdx.x == 0 && w.own < args.n_split && w.t * kUnitRows == w.own * kTileKeys)
-      args.tickets[(static_cast<size_t>(w.b) * args.Hkv + w.g) * args.n_split + w.own] = 0;
+    int* counts = args.row_counts + (static_cast<size_t>(w.b) * args.Hkv + w.g) * args.max_blocks;
     uint32_t* m = args.masks + (static_cast<size_t>(w.b) * args.Hkv + w.g) * args.max_blocks * args.n_tiles + w.t;
-    for (int j = threadIdx.x; j < nb; j += kPlanThreads) m[static_cast<size_t>(j) * args.n_tiles] = row_mask[j];
+    for (int j = threadIdx.x; j < nb; j += kPlanThreads) {
+      m[static_cast<size_t>(j) * args.n_tiles] = row_mask[j];
+      if (row_mask[j] != 0u) atomicAdd(counts + j, __popc(row_mask[j]));     // whole numbers: any order
+    }
   }
   uint2* walk = args.walks + static_cast<size_t>(u) * args.walk_cap;
   int n = 0;                                          // entries of the blocks before j0
