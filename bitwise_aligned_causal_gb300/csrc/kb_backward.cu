@@ -13,7 +13,7 @@
 //
 // Three kernels, no atomics (every gradient element is summed by one CTA in
 // one fixed order, so repeated runs give the same bits):
-//   kb_bwd_delta_kernel  one warp per row: delta = rowsum(dO * O)
+//   kb_bwd_delta_kernel  half a warp per row: delta = rowsum(dO * O)
 //   kb_bwd_dq_kernel     one CTA per (b, head, query tile): walks key tiles
 //                        0..t; S = Q K^T and dP = dO V^T on the tensor core,
 //                        dS in TMEM, dQ += dS K
@@ -32,22 +32,44 @@ namespace kb {
 
 // ------------------------------------------------------------------ delta
 
-// One warp per row of 128: lane l takes elements 4l..4l+3; the four products
-// are summed in pairs, then across lanes by a fixed butterfly.
+// Sixteen lanes per row of 128, four rows of a half warp in flight: lane l
+// takes elements 4l..4l+3 and 64+4l..64+4l+3; the four products of each are
+// summed in pairs, then the two, then across lanes by a fixed butterfly.
+// Bound: both tensors are read once.  One row per warp and 8 bytes in flight
+// per lane took 32 us for [1, 32, 8192, 128] (4.2 TB/s), this 25.7 us.
+constexpr int kDeltaRows = 4;                   // rows per half warp
+
 __global__ void __launch_bounds__(256) kb_bwd_delta_kernel(const __nv_bfloat16* __restrict__ o,
                                                            const __nv_bfloat16* __restrict__ dout,
                                                            float* __restrict__ delta, long long rows) {
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int lane = threadIdx.x & 31;
-  const uint2 a = reinterpret_cast<const uint2*>(o + row * kHeadDim)[lane];
-  const uint2 g = reinterpret_cast<const uint2*>(dout + row * kHeadDim)[lane];
-  const float p01 = __fmaf_rn(bf16_lo(a.x), bf16_lo(g.x), __fmul_rn(bf16_hi(a.x), bf16_hi(g.x)));
-  const float p23 = __fmaf_rn(bf16_lo(a.y), bf16_lo(g.y), __fmul_rn(bf16_hi(a.y), bf16_hi(g.y)));
-  float s = __fadd_rn(p01, p23);
+  const int lane = threadIdx.x & 15;
+  const long long row0 = static_cast<long long>(blockIdx.x) * (16 * kDeltaRows) + (threadIdx.x >> 4);
+  uint2 a[kDeltaRows][2], g[kDeltaRows][2];
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, m));
-  if (lane == 0) delta[row] = s;
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const long long row = row0 + 16 * i;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      a[i][e] = row < rows ? __ldg(reinterpret_cast<const uint2*>(o + row * kHeadDim) + lane + 16 * e) : make_uint2(0u, 0u);
+      g[i][e] = row < rows ? __ldg(reinterpret_cast<const uint2*>(dout + row * kHeadDim) + lane + 16 * e) : make_uint2(0u, 0u);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    float part[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint2 x = a[i][e], y = g[i][e];
+      const float p01 = __fmaf_rn(bf16_lo(x.x), bf16_lo(y.x), __fmul_rn(bf16_hi(x.x), bf16_hi(y.x)));
+      const float p23 = __fmaf_rn(bf16_lo(x.y), bf16_lo(y.y), __fmul_rn(bf16_hi(x.y), bf16_hi(y.y)));
+      part[e] = __fadd_rn(p01, p23);
+    }
+    float s = __fadd_rn(part[0], part[1]);
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, m));
+    const long long row = row0 + 16 * i;
+    if (lane == 0 && row < rows) delta[row] = s;
+  }
 }
 
 // -------------------------------------------------------------- dq kernel
@@ -642,7 +664,8 @@ kb_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 // --------------------------------------------------------------- launcher
 
 cudaError_t launch_bwd_delta(const void* o, const void* dout, float* delta, long long rows, cudaStream_t s) {
-  kb_bwd_delta_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(
+  constexpr long long kPerCta = 16 * kDeltaRows;
+  kb_bwd_delta_kernel<<<static_cast<unsigned>((rows + kPerCta - 1) / kPerCta), 256, 0, s>>>(
       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dout), delta, rows);
   return cudaGetLastError();
 }
