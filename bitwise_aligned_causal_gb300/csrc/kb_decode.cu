@@ -53,8 +53,11 @@
 
 namespace kb {
 
+// kSparse with one S buffer is the lean shape: half of TMEM and of shared
+// memory, so that two CTAs share an SM.
 template <bool kWide, int kNumSBufs, bool kSparse = false>
 struct PackedCfg {
+  static constexpr bool kLean = kSparse && kNumSBufs == 1;
   static constexpr int kSoftmaxWarps = kWide ? 4 : 1;
   static constexpr int kKProdWarp = kWide ? 4 : 1;
   static constexpr int kQkWarp = kWide ? 5 : 2;             // TMEM allocator + Q K^T issuer
@@ -62,24 +65,25 @@ struct PackedCfg {
   static constexpr int kPvWarp = kWide ? 7 : 5;
   static constexpr int kFoldWarp = kWide ? -1 : 4;          // narrow: folds and epilogue
   static constexpr int kThreads = (kWide ? 8 : 6) * 32;
-  static constexpr int kStages = 3;
+  static constexpr int kKStages = kLean ? 2 : 3;
+  static constexpr int kVStages = kLean ? 1 : 3;
   static constexpr int kQRows = kWide ? 128 : 8;
   static constexpr int kSBufs = kNumSBufs;
   static constexpr bool kFoldTmem = kWide && kNumSBufs == 2;  // wide fold mode: folded O in TMEM
-  static constexpr uint32_t kTmemCols = 512;                  // S buffers, O (and the folded O)
+  static constexpr uint32_t kTmemCols = kLean ? 256 : 512;    // S buffers, O (and the folded O)
   static constexpr uint32_t kOCol = kSBufs * 128u;
   static constexpr uint32_t kOAccCol = 384u;                  // kFoldTmem only
   static constexpr uint32_t kQSlab = kQRows * 128;            // bytes of one 64-column slab of Q
   static constexpr uint32_t kQSbo = kWide ? 1024u : 0u;
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kKOff = 2 * kQSlab;
-  static constexpr uint32_t kVOff = kKOff + kStages * kTileBytes;
-  static constexpr uint32_t kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr uint32_t kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr uint32_t kBarOff = kVOff + kVStages * kTileBytes;
   static constexpr int kBarKFull = 0;
-  static constexpr int kBarKEmpty = kBarKFull + kStages;
-  static constexpr int kBarVFull = kBarKEmpty + kStages;
-  static constexpr int kBarVEmpty = kBarVFull + kStages;
-  static constexpr int kBarSFull = kBarVEmpty + kStages;   // one per S buffer
+  static constexpr int kBarKEmpty = kBarKFull + kKStages;
+  static constexpr int kBarVFull = kBarKEmpty + kKStages;
+  static constexpr int kBarVEmpty = kBarVFull + kVStages;
+  static constexpr int kBarSFull = kBarVEmpty + kVStages;  // one per S buffer
   static constexpr int kBarPFull = kBarSFull + kSBufs;     // one per S buffer: P of a tile using it written
   static constexpr int kBarOFull = kBarPFull + kSBufs;     // one per S buffer: P V of a tile using it done
   static constexpr int kBarVReady = kBarOFull + kSBufs;    // last V tile with its tail zeroed
@@ -104,7 +108,7 @@ struct PackedCfg {
   static constexpr uint32_t kSegFirstOff = kWalkOff + (kSparse ? KB_MAX_SELECT * 4u : 0u);
   static constexpr uint32_t kPartOff = (kSegFirstOff + (kSparse ? (KB_MAX_SELECT + 1u) * 4u : 0u) + 15u) & ~15u;
   static constexpr uint32_t kSmemCap = 227u * 1024u - 1024u;   // usable once the base is 1 KB aligned
-  static constexpr uint32_t kPartBytes = kWide ? 0u : ((kSmemCap - kPartOff) & ~15u);
+  static constexpr uint32_t kPartBytes = kWide || kLean ? 0u : ((kSmemCap - kPartOff) & ~15u);
   static constexpr uint32_t kSmemUsed = kPartOff + kPartBytes;
   static constexpr uint32_t kSmemBytes = kSmemUsed + 1024;
 };
@@ -201,6 +205,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                  const PackedArgs args) {
   using Cfg = PackedCfg<kWide, kNumSBufs, kSparse>;
   static_assert(!kSparse || (!kWide && Cfg::kThreads > KB_MAX_SELECT), "sparse walks are narrow");
+  static_assert(!Cfg::kLean || 2 * Cfg::kSmemBytes <= 226u * 1024u, "two lean CTAs share an SM");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
@@ -312,7 +317,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const bool push = C > 1 && !ws_mode &&
                     static_cast<uint32_t>(ns - s_first + 1) * slot_bytes <= static_cast<uint32_t>(Cfg::kPartBytes);
   const bool gather = !kWide && C > 1 && !ws_mode && !push &&
-                      static_cast<uint32_t>(ns - s_first) * slot_bytes <= 2u * Cfg::kStages * kTileBytes;
+                      static_cast<uint32_t>(ns - s_first) * slot_bytes <= (Cfg::kKStages + Cfg::kVStages) * kTileBytes;
   const bool pull_sync = C > 1 && !ws_mode && !push && !gather;   // the pull path's cluster barrier
 
   if (threadIdx.x == 0) {
@@ -384,15 +389,16 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int full0 = is_v ? Cfg::kBarVFull : Cfg::kBarKFull;
       const int empty0 = is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty;
       const uint32_t ring = sbase + (is_v ? Cfg::kVOff : Cfg::kKOff);
+      const int stages = is_v ? Cfg::kVStages : Cfg::kKStages;
       int issued = 0;
       bool ok = true;
       for (int jj = 0; jj < nt && ok; ++jj) {
-        const int slot = jj % Cfg::kStages;
-        const uint32_t use = jj / Cfg::kStages;
+        const int slot = jj % stages;
+        const uint32_t use = jj / stages;
         int row = 0, plane = 0;
         if (lane == 0) kv_tile_coords(args, b, g, tile_at(jj), row, plane);
-        if (jj == Cfg::kStages) ok = no_error(args.err, abort_flag);   // the first loads are in flight
-        if (ok && jj >= Cfg::kStages)
+        if (jj == stages) ok = no_error(args.err, abort_flag);         // the first loads are in flight
+        if (ok && jj >= stages)
           ok = mbar_wait(bar(empty0 + slot), (use - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -402,14 +408,14 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         issued = jj + 1;
       }
-      if (ok && nt <= Cfg::kStages) ok = no_error(args.err, abort_flag);
+      if (ok && nt <= stages) ok = no_error(args.err, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (ok && is_v && zero_tail && has_last) {
         // V rows past the sequence in its last tile may hold anything (another
         // sequence's data, NaN): make them zero so P = 0 contributes nothing.
         const int jl = nt - 1;
-        const int slot = jl % Cfg::kStages;
-        ok = mbar_wait(bar(Cfg::kBarVFull + slot), (jl / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+        const int slot = jl % Cfg::kVStages;
+        ok = mbar_wait(bar(Cfg::kBarVFull + slot), (jl / Cfg::kVStages) & 1, abort_flag, args.err, kDevTimeoutTma);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           uint8_t* vt = smem + Cfg::kVOff + slot * kTileBytes;
@@ -425,8 +431,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
       }
       if (!ok && lane == 0) {
-        for (int x = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); x < issued; ++x)
-          packed_drain_wait(bar(full0 + x % Cfg::kStages), (x / Cfg::kStages) & 1);
+        for (int x = (issued > stages ? issued - stages : 0); x < issued; ++x)
+          packed_drain_wait(bar(full0 + x % stages), (x / stages) & 1);
       }
     }
     if (C > 1) {
@@ -442,9 +448,9 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       bool ok = no_error(args.err, abort_flag) &&
                 mbar_wait(bar(Cfg::kBarQReady), 0, abort_flag, args.err, kDevTimeoutTma);
       for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
-        const int slot = j % Cfg::kStages;
+        const int slot = j % Cfg::kKStages;
         const int sb = j % Cfg::kSBufs;
-        ok = mbar_wait(bar(Cfg::kBarKFull + slot), (j / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+        ok = mbar_wait(bar(Cfg::kBarKFull + slot), (j / Cfg::kKStages) & 1, abort_flag, args.err, kDevTimeoutTma);
         if (ok && j >= Cfg::kSBufs)
           ok = mbar_wait(bar(Cfg::kBarOFull + sb), ((j - Cfg::kSBufs) / Cfg::kSBufs) & 1, abort_flag, args.err,
                          kDevTimeoutMma);
@@ -473,12 +479,12 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       int js = 0;                                           // tile index within its segment (j0 starts one)
       bool ok = no_error(args.err, abort_flag);
       for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
-        const int slot = j % Cfg::kStages;
+        const int slot = j % Cfg::kVStages;
         const int sb = j % Cfg::kSBufs;
         if (zero_tail && has_last && j == nt - 1)
           ok = mbar_wait(bar(Cfg::kBarVReady), 0, abort_flag, args.err, kDevTimeoutTma);
         else
-          ok = mbar_wait(bar(Cfg::kBarVFull + slot), (j / Cfg::kStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+          ok = mbar_wait(bar(Cfg::kBarVFull + slot), (j / Cfg::kVStages) & 1, abort_flag, args.err, kDevTimeoutTma);
         const bool first = kSparse ? starts_seg(j) : (js == 0);
         if (++js == seg_len) js = 0;
         if (ok && first && F > 0)
@@ -1080,7 +1086,13 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
   // narrow when at most 8 rows are packed (two query rows per head); wide
   // chunks fold their segments in TMEM (two S buffers) unless the partials
   // go to a workspace
-  if (a.blocks != nullptr) return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
+  if (a.blocks != nullptr) {
+    // more units than SMs: two lean CTAs share an SM, so that all of them run
+    // at once and no second wave leaves SMs idle (B = 32, 16 blocks of 16K:
+    // 50.8 us in two waves, 48 us)
+    if (a.lean) return launch_packed_t<false, 1, true>(tk, tv, a, n_sub, s);
+    return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
+  }
   if (a.L <= 2) return launch_packed_t<false, 3>(tk, tv, a, n_sub, s);
   if (a.part != nullptr) return launch_packed_t<true, 3>(tk, tv, a, n_sub, s);
   return launch_packed_t<true, 2>(tk, tv, a, n_sub, s);

@@ -453,6 +453,7 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
   a.n_select = n_select;
   const int max_blocks = ((ctx_lens != nullptr ? cap : ctx_len) + kb::kTileKeys - 1) / kb::kTileKeys;
   a.cluster = sparse_cluster(dev, B, Hkv, n_select, max_blocks);
+  a.lean = a.cluster == 1 && static_cast<long long>(B) * Hkv > dev.sm_count;
   a.err = dev.err;
   return done(kb::launch_packed(tk, tv, a, 1, static_cast<cudaStream_t>(stream)));
 }

@@ -56,6 +56,7 @@ struct PackedArgs {
   // block-sparse tokens (L = 1, fold mode): device [B, Hkv, n_select] listed key blocks
   const int* blocks;
   int n_select;
+  bool lean;               // more units than SMs (cluster 1): the shape of which two CTAs share an SM
   uint32_t* err;
 };
 

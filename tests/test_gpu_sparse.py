@@ -130,6 +130,38 @@ def test_one_token_equals_its_row_of_a_chunk(kb, ctx, n, B):
     check_rows(f64(got)[0], f64(q)[0], f64(k)[0], f64(v)[0], lists[0].cpu().numpy(), [ctx - 1])
 
 
+@pytest.mark.parametrize("page", [0, 128])
+def test_many_tokens_with_ragged_contexts(kb, page):
+    """More (sequence, KV head) units than SMs, contexts of their own, cache rows past them NaN, a row without blocks."""
+    import torch
+
+    B, cap, n = 24, 1280, 4
+    k_cache, v_cache, _, table, seq = caches(B, cap, page, seed=1450)
+    rng = np.random.default_rng(1451)
+    ctx = rng.integers(1, cap + 1, size=B)
+    ctx[:4] = (1, 128, 129, cap)
+    lists = torch.cat([random_lists(1452 + b, 1, 1, int(ctx[b]) - 1, n) for b in range(B)])
+    lists[5] = -1
+    for b in range(B):
+        for c in (k_cache, v_cache):
+            if not page:
+                c[b, :, ctx[b]:] = float("nan")
+            else:
+                for j in range(cap // page):
+                    c[table[b, j], :, max(0, min(page, ctx[b] - j * page)):] = float("nan")
+    q = randn(1453, B, 32, 1, 128)
+    lens = torch.from_numpy(ctx.astype(np.int32)).cuda()
+    if page:
+        got = kb.sparse_decode_paged(q, k_cache, v_cache, table, lens, lists, check=True)
+    else:
+        got = kb.sparse_chunk_varlen(q, k_cache, v_cache, lens - 1, lists, check=True)
+    assert bool((got[5] == 0).all())
+    for b in range(B):
+        kc, vc = (seq(x, b)[:, :ctx[b]].contiguous()[None] for x in (k_cache, v_cache))
+        want = kb.sparse_decode(q[b:b + 1], kc, vc, int(ctx[b]), lists[b:b + 1], check=True)
+        assert torch.equal(bits(got[b:b + 1]), bits(want)), b
+
+
 @pytest.mark.parametrize("L", [1, 70])
 def test_order_repeats_and_later_blocks_change_nothing(kb, L):
     import torch
