@@ -622,6 +622,16 @@ def _handle(stream, device):
     return _torch()._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`, from that stream's memory: the allocator may hand out memory that an earlier
+    owner's kernels on another stream still use."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _per_sequence(B, t, name):
     if t is not None and t.shape != (B,):
         shapes.per_sequence(B, **{name: t.shape})
@@ -636,8 +646,9 @@ def rope_table(n_pos, rot_dim=128, theta=10000.0, inv_freq=None, device=None, st
         inv_freq = float(theta) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
     if inv_freq.dim() != 1 or 2 * inv_freq.numel() != rot_dim:
         raise ValueError(f"inv_freq must have shape ({rot_dim // 2},), got {tuple(inv_freq.shape)}")
-    inv_freq = inv_freq.to(device=device, dtype=torch.float64).contiguous()
-    table = torch.empty((int(n_pos), rot_dim // 2, 2), dtype=torch.float32, device=device)
+    with torch.cuda.stream(stream):
+        inv_freq = inv_freq.to(device=device, dtype=torch.float64).contiguous()
+        table = torch.empty((int(n_pos), rot_dim // 2, 2), dtype=torch.float32, device=device)
     shapes.rope_table(table.shape)
     _on_current_device(table, "table")
     _raise(kb_attn_rope_table(table.data_ptr(), int(n_pos), int(rot_dim), inv_freq.data_ptr(), _stream(stream)),
@@ -656,7 +667,7 @@ def rope(x, table, start=0, inverse=False, interleaved=False, out=None, stream=N
         _need_bf16(out, "out", device)
     start = int(start)
     B, H, L, n_pos, rot_dim = _shapes_rope(x.shape, table.shape, start, _shape(out))
-    o = _torch().empty((B, H, L, 128), dtype=x.dtype, device=x.device) if out is None else out
+    o = _empty((B, H, L, 128), x.dtype, x.device, stream) if out is None else out
     _finish(kb_attn_rope(x.data_ptr(), _stride_array(*x.stride()[:3]), o.data_ptr(), table.data_ptr(), n_pos, rot_dim,
                          bool(interleaved), bool(inverse), B, H, L, start, _handle(stream, device)), "kb_attn_rope",
             check, stream)
@@ -689,7 +700,7 @@ def _append(q, k, v, k_cache, v_cache, table, start, starts, lens, block_table, 
     if starts is None and table is not None and start > n_pos - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the table's 0..{n_pos - 1}")
     if q is not None and out is None:
-        out = _torch().empty((B, Hq, L, 128), dtype=q.dtype, device=q.device)
+        out = _empty((B, Hq, L, 128), q.dtype, q.device, stream)
     _finish(kb_attn_append(_ptr(q), k.data_ptr(), v.data_ptr(), _stride_array(*_stride3(q), *_stride3(k), *_stride3(v)),
                            _ptr(out), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(boxes), _ptr(table), n_pos, rot_dim,
                            bool(interleaved), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table),
@@ -733,7 +744,9 @@ def block_boxes(k, kv_len=None, kv_lens=None, block_table=None, boxes=None, stre
     if not 1 <= kv_len <= cap:
         raise ValueError(f"kv_len must lie in 1..{cap} (the cache capacity), got {kv_len}")
     if boxes is None:
-        boxes = torch.zeros(box, dtype=torch.bfloat16, device=k.device)
+        boxes = _empty(box, torch.bfloat16, k.device, stream)
+        with torch.cuda.stream(stream):
+            boxes.zero_()
     _finish(kb_attn_block_boxes(k.data_ptr(), boxes.data_ptr(), B, Hkv, kv_len, _ptr(kv_lens), cap, _ptr(block_table),
                                 pps, page, num_pages, _handle(stream, device)), "kb_attn_block_boxes", check, stream)
     return boxes
@@ -755,7 +768,7 @@ def _select(q, boxes, start, starts, lens, n, keep_first, keep_last, block_table
     if starts is None and not 0 <= start <= per_plane * shapes.BLOCK - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the boxes' 0..{per_plane * shapes.BLOCK - 1}")
     if out is None:
-        out = torch.empty((B, Hkv, L, n), dtype=torch.int32, device=q.device)
+        out = _empty((B, Hkv, L, n), torch.int32, q.device, stream)
     _finish(kb_attn_select_blocks(q.data_ptr(), boxes.data_ptr(), out.data_ptr(), B, Hq, Hkv, L, n, keep_first,
                                   keep_last, start, _ptr(starts), _ptr(lens), per_plane, _ptr(block_table), pps, page,
                                   num_pages, _handle(stream, device)), "kb_attn_select_blocks", check, stream)
@@ -798,11 +811,9 @@ def _sparse_args(device, q, k, v, blocks, block_table=None, out=None, positions=
 
 
 def _stream_workspace(nbytes, device, workspace, stream):
-    """A workspace for one call on `stream`: memory of the allocator is kept from reuse until that stream is done."""
-    ws = _workspace(nbytes, device, workspace)
-    if workspace is None and stream is not None:
-        ws.record_stream(stream)
-    return ws
+    if workspace is not None:
+        return _workspace(nbytes, device, workspace)
+    return _empty(max(int(nbytes), 256), _torch().uint8, device, stream)
 
 
 def _sparse_workspace(B, Hkv, L, n, cap, device, workspace, stream):
@@ -815,7 +826,7 @@ def _sparse_chunk(q, k, v, start, starts, lens, blocks, block_table, out, worksp
                                                                ((starts, "starts"), (lens, "lens")))
     if starts is None and not 0 <= start <= cap - L:
         raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
-    o = _torch().empty_like(q) if out is None else out
+    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
     ws = _sparse_workspace(B, Hkv, L, n, cap, q.device, workspace, stream)
     _finish(kb_attn_sparse_chunk(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
                                  Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
@@ -847,7 +858,7 @@ def _sparse_decode(q, k, v, ctx_len, ctx_lens, blocks, block_table, out, stream,
         raise ValueError(f"decode takes one query row per (batch, head), got {L}")
     if ctx_lens is None and not 1 <= ctx_len <= cap:
         raise ValueError(f"ctx_len must lie in 1..{cap} (the cache capacity), got {ctx_len}")
-    o = _torch().empty_like(q) if out is None else out
+    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
     _finish(kb_attn_sparse_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), blocks.data_ptr(), n, B, Hq,
                                   Hkv, ctx_len, _ptr(ctx_lens), cap, _ptr(block_table), pps, page, num_pages,
                                   _handle(stream, device)), "kb_attn_sparse_decode", check, stream)
@@ -873,8 +884,8 @@ def sparse_prefill_lse(q, k, v, blocks, out=None, lse=None, workspace=None, stre
     device = _device()
     B, Hq, Hkv, S, n, cap, _, _, _ = _sparse_args(device, q, k, v, blocks, None, out)
     shapes.prefill(q.shape, k.shape, v.shape)
-    o = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
+    lse = _empty((B, Hq, S), torch.float32, q.device, stream) if lse is None else lse
     _check_f32(lse, "lse")
     shapes.vector_f32("lse", lse.shape, B, Hq, S)
     ws = _sparse_workspace(B, Hkv, S, n, cap, q.device, workspace, stream)
@@ -896,13 +907,13 @@ def sparse_backward(q, k, v, o, dout, lse, blocks, delta=None, dq=None, dk=None,
         if t is not None or name in ("o", "dout"):
             _need_bf16(t, name, device)
     _shapes_backward(q.shape, k.shape, v.shape, o.shape, dout.shape, _shape(dq), _shape(dk), _shape(dv))
-    delta = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device) if delta is None else delta
+    delta = _empty((B, Hq, S), torch.float32, q.device, stream) if delta is None else delta
     for t, name in ((lse, "lse"), (delta, "delta")):
         _check_f32(t, name)
         shapes.vector_f32(name, t.shape, B, Hq, S)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
     ws = _stream_workspace(kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n), q.device, workspace, stream)
     _finish(kb_attn_sparse_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                                     lse.data_ptr(), delta.data_ptr(), blocks.data_ptr(), n, dq.data_ptr(),

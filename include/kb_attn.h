@@ -304,7 +304,8 @@ kb_status kb_attn_rope(const void* x, const long long* strides, void* out, const
  *             then k's, then v's (multiples of 8, last dimension contiguous),
  *             so slices of one fused projection need no copy.  q and q_out may
  *             be NULL together.
- *   q_out   : [B, Hq, L, 128] contiguous
+ *   q_out   : [B, Hq, L, 128] contiguous; may be q itself when q is contiguous,
+ *             and must not overlap it otherwise
  *   k_cache,
  *   v_cache : block_table == NULL: [B, Hkv, kv_cap, 128], else pools
  *             [num_pages, Hkv, page_size, 128] as in kb_attn_chunk_paged
@@ -319,8 +320,9 @@ kb_status kb_attn_rope(const void* x, const long long* strides, void* out, const
  *             NULL) of sequence b goes to position starts[b] + i; rows from
  *             lens[b] on are neither read nor written
  * A block whose first key is among the new ones gets a new box; any other
- * touched block's box is widened, so keys overwritten inside a block leave
- * their old bounds in its box until kb_attn_block_boxes makes it anew.
+ * touched block's box must hold its earlier keys' bounds and is widened, so
+ * keys overwritten inside a block leave their old bounds in its box until
+ * kb_attn_block_boxes makes it anew.
  * Keys, queries and boxes have the same bits for any split of a sequence into
  * appends.  No two sequences may append to the same page.  Out-of-range
  * starts, lens or page indices are found on the device: that sequence (or
