@@ -316,7 +316,7 @@ kb_status kb_attn_append(const void* q, const void* k, const void* v, const long
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return done(kb::launch_append(a, false, static_cast<cudaStream_t>(stream)));
+  return done(kb::launch_append(a, false, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, int kv_len, const int* kv_lens,
@@ -348,7 +348,7 @@ kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, 
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return done(kb::launch_append(a, true, static_cast<cudaStream_t>(stream)));
+  return done(kb::launch_append(a, true, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, int B, int Hq, int Hkv, int L,

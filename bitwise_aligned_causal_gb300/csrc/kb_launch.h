@@ -150,7 +150,7 @@ struct AppendArgs {
 };
 // only_boxes: read the cache's keys at the rows' positions and make their
 // blocks' boxes anew (q, k, v unused).
-cudaError_t launch_append(const AppendArgs& a, bool only_boxes, cudaStream_t s);
+cudaError_t launch_append(const AppendArgs& a, bool only_boxes, int sm_count, cudaStream_t s);
 
 // Choice of key blocks per query row (kb_select.cu).
 struct SelectArgs {
