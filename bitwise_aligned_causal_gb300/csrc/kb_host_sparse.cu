@@ -201,7 +201,7 @@ kb_status sparse_forward(const SparseCall& c, void* stream) {
   if ((s = kb::host_group_map(&tq, c.q, static_cast<uint64_t>(c.L), static_cast<uint64_t>(c.B) * c.Hkv)) != KB_OK) return s;
   if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
   cudaError_t e = kb::launch_sparse_plan(a, dev.index, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = kb::launch_sparse_tile(tq, tk, tv, a, dev.index, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = kb::launch_sparse_tile(tq, tk, tv, a, dev.index, dev.sm_count, static_cast<cudaStream_t>(stream));
   return done(e);
 }
 
@@ -505,7 +505,7 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   cudaError_t e = cudaMemsetAsync(a.plan.row_counts, 0, static_cast<size_t>(bwd.jobs - bwd.counts), st);
   if (e == cudaSuccess) e = kb::launch_sparse_plan(a.plan, dev.index, st);
   if (e == cudaSuccess) e = kb::launch_bwd_delta(o, dout, delta, static_cast<long long>(B) * Hq * S, st);
-  if (e == cudaSuccess) e = kb::launch_sparse_backward(tq, tk, tv, tdo, a, dev.index, st);
+  if (e == cudaSuccess) e = kb::launch_sparse_backward(tq, tk, tv, tdo, a, dev.index, dev.sm_count, st);
   return done(e);
 }
 

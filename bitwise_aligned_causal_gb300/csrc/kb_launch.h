@@ -199,7 +199,7 @@ struct SparseArgs {
 cudaError_t launch_sparse_plan(const SparseArgs& a, int device, cudaStream_t s);
 // tq: host_group_map of q; tk, tv: host_rows_map of the cache.
 cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const SparseArgs& a, int device, cudaStream_t s);
+                               const SparseArgs& a, int device, int sm_count, cudaStream_t s);
 
 // Steps of 32 positions from which on two CTAs share a key block's gradient.
 constexpr int kSparseSplitSteps = 128;
@@ -219,7 +219,8 @@ struct SparseBwdArgs {
 };
 // tq, tdo: host_group_map of q and dout; tk, tv: host_rows_map of k and v.
 cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, cudaStream_t s);
+                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, int sm_count,
+                                   cudaStream_t s);
 
 cudaError_t launch_wait_probe(uint32_t* err, unsigned long long limit_ns, cudaStream_t s);
 

@@ -96,13 +96,6 @@ __device__ __forceinline__ bool has_v_tail(const SparseArgs& a, const SparseUnit
 
 }  // namespace
 
-// Every role of a CTA walks the same units in the same order.
-#define KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk)                                                              \
-  for (int u = static_cast<int>(blockIdx.x); u < args.n_units; u += static_cast<int>(gridDim.x))            \
-    if (const int n = __ldg(args.walk_len + u); n >= 0)                                                     \
-      if (const SparseUnit w = sparse_unit(args, u); true)                                                  \
-        if (const uint2* const walk = unit_walk(args, u); true)
-
 __global__ void __launch_bounds__(SparseCfg::kThreads, 1)
 kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const SparseArgs args) {
@@ -151,7 +144,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     const float c = score_scale_log2();
     int G = 0;                                                       // segments
     bool ok = !skip;
-    KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
+    KB_FOR_EACH_SPARSE_UNIT(args, u, w, n, walk) {
       if (!ok) break;
       RowState acc = row_state_init();
       bool none = true;                                              // the row has folded no segment yet
@@ -250,7 +243,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         }
         int T = 0, U = 0;                                            // tiles; units with tiles
         bool ok = true;
-        KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
+        KB_FOR_EACH_SPARSE_UNIT(args, u, w, n, walk) {
           if (!ok) break;
           if (n == 0) continue;
           if (!is_v) {
@@ -322,7 +315,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         const uint32_t q_saddr = sbase + Cfg::kQOff;
         int T = 0, U = 0;
         bool ok = true;
-        KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
+        KB_FOR_EACH_SPARSE_UNIT(args, u, w, n, walk) {
           if (!ok) break;
           if (n == 0) continue;
           ok = mbar_wait(bar(Cfg::kBarQFull), U & 1, abort_flag, args.err, kDevTimeoutTma);
@@ -350,7 +343,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         int T = 0, F = 0;                                           // F: segments finished
         uint32_t zero_parity = 0;                                   // bit s: zero-tail phases of V slot s, mod 2
         bool ok = true;
-        KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
+        KB_FOR_EACH_SPARSE_UNIT(args, u, w, n, walk) {
           if (!ok) break;
           if (n == 0) continue;
           uint32_t next = __ldg(&walk[0].x);
@@ -400,7 +393,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     float2* stats = reinterpret_cast<float2*>(smem + Cfg::kStatsOff);
     int T = 0, G = 0;                                               // tiles, segments
     bool ok = !skip;
-    KB_FOR_EACH_SPARSE_UNIT(u, w, n, walk) {
+    KB_FOR_EACH_SPARSE_UNIT(args, u, w, n, walk) {
       if (!ok) break;
       if (n == 0) continue;
       RowState sA = row_state_init(), sB = row_state_init();
@@ -524,7 +517,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 }
 
 cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const SparseArgs& a, int device, cudaStream_t s) {
+                               const SparseArgs& a, int device, int sm_count, cudaStream_t s) {
   using Cfg = SparseCfg;
   static_assert(Cfg::kSmemBytes <= 227u * 1024u, "shared memory budget");
   static bool configured[64] = {};
@@ -534,7 +527,7 @@ cudaError_t launch_sparse_tile(const CUtensorMap& tq, const CUtensorMap& tk, con
     if (e != cudaSuccess) return e;
     configured[device] = true;
   }
-  kb_sparse_tile_kernel<<<static_cast<unsigned>(a.n_units), Cfg::kThreads, Cfg::kSmemBytes, s>>>(tq, tk, tv, a);
+  kb_sparse_tile_kernel<<<static_cast<unsigned>(unit_grid(a, sm_count, 16)), Cfg::kThreads, Cfg::kSmemBytes, s>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 

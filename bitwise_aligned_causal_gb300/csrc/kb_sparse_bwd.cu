@@ -51,11 +51,14 @@ struct SparseBwdQCfg {
   static constexpr int kBarDrain = kBarDQDone + 1;          // 2: one per issuer
   static constexpr int kBarDPFree = kBarDrain + 2;         // dP(j) read (256 arrivals)
   static constexpr int kBarSDone = kBarDPFree + 1;         // S(j) in TMEM (kBarSFull: dP(j) too)
-  static constexpr int kNumBars = kBarSDone + 1;
+  static constexpr int kBarQDEmpty = kBarSDone + 1;        // a unit's last S, dP done
+  static constexpr int kNumBars = kBarQDEmpty + 1;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
   static constexpr uint32_t kSmemBytes = kMiscOff + 16 + 1024;
 };
 
+// Every role of a CTA walks the same units in the same order; T counts tiles
+// (ring slots and parities follow from it), U units with tiles.
 __global__ void __launch_bounds__(SparseBwdQCfg::kThreads, 1)
 kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
@@ -71,11 +74,6 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  const int unit = static_cast<int>(blockIdx.x);
-  const SparseUnit w = sparse_unit(args.plan, unit);
-  const uint2* const walk = unit_walk(args.plan, unit);
-  const int n_kv = max(0, args.plan.walk_len[unit]);                // entries of the walk (-1: the plan was skipped)
-  const int group = w.b * args.plan.Hkv + w.g;
   uint32_t* const err = args.plan.err;
 
   if (threadIdx.x == 0) {
@@ -107,34 +105,46 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
       const CUtensorMap* tmap = is_v ? &tmap_v : &tmap_k;
       if (lane == 0) {
         tma_prefetch_desc(tmap);
-        if (!is_v && n_kv > 0) {
+        if (!is_v) {
           tma_prefetch_desc(&tmap_q);
           tma_prefetch_desc(&tmap_do);
-          mbar_arrive_expect_tx(bar(Cfg::kBarQD), 2 * kTileBytes);
-          tma_load_group(sbase + Cfg::kQOff, &tmap_q, w.t * kUnitRows, group, bar(Cfg::kBarQD));
-          tma_load_group(sbase + Cfg::kDOOff, &tmap_do, w.t * kUnitRows, group, bar(Cfg::kBarQD));
         }
       }
-      int issued = 0;
+      int T = 0, U = 0;
       bool ok = true;
-      uint32_t next = n_kv > 0 ? __ldg(&walk[0].x) : 0u;
-      for (int j = 0; j < n_kv; ++j) {
-        const int slot = j % stages;
-        const int block = static_cast<int>(next & kEntryBlock);
-        if (j + 1 < n_kv) next = __ldg(&walk[j + 1].x);
-        if (j >= stages)
-          ok = mbar_wait(bar(empty0 + slot), ((j / stages) - 1) & 1, abort_flag, err, kDevTimeoutSlot);
-        ok = __all_sync(0xffffffffu, ok);
+      KB_FOR_EACH_SPARSE_UNIT(args.plan, u, w, n, walk) {
         if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(full0 + slot), kTileBytes);
-          tma_load_tile_hint(ring + slot * kTileBytes, tmap, block * kTileKeys, group, bar(full0 + slot), keep);
+        if (n == 0) continue;
+        const int group = w.b * args.plan.Hkv + w.g;
+        if (!is_v) {
+          if (U > 0) ok = mbar_wait(bar(Cfg::kBarQDEmpty), (U - 1) & 1, abort_flag, err, kDevTimeoutSlot);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(Cfg::kBarQD), 2 * kTileBytes);
+            tma_load_group(sbase + Cfg::kQOff, &tmap_q, w.t * kUnitRows, group, bar(Cfg::kBarQD));
+            tma_load_group(sbase + Cfg::kDOOff, &tmap_do, w.t * kUnitRows, group, bar(Cfg::kBarQD));
+          }
         }
-        issued = j + 1;
+        ++U;
+        uint32_t next = __ldg(&walk[0].x);
+        for (int j = 0; j < n; ++j, ++T) {
+          const int slot = T % stages;
+          const int block = static_cast<int>(next & kEntryBlock);
+          if (j + 1 < n) next = __ldg(&walk[j + 1].x);
+          if (T >= stages)
+            ok = mbar_wait(bar(empty0 + slot), ((T / stages) - 1) & 1, abort_flag, err, kDevTimeoutSlot);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(full0 + slot), kTileBytes);
+            tma_load_tile_hint(ring + slot * kTileBytes, tmap, block * kTileKeys, group, bar(full0 + slot), keep);
+          }
+        }
       }
       if (!ok && lane == 0) {
-        if (!is_v && issued > 0) drain_wait_b(bar(Cfg::kBarQD), 0);
-        for (int x = (issued > stages ? issued - stages : 0); x < issued; ++x)
+        if (!is_v && U > 0) drain_wait_b(bar(Cfg::kBarQD), (U - 1) & 1);
+        for (int x = (T > stages ? T - stages : 0); x < T; ++x)
           drain_wait_b(bar(full0 + x % stages), (x / stages) & 1);
       }
     }
@@ -143,35 +153,43 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     // S(j+1), dP(j+1) go out as soon as the elementwise warps have read S(j),
     // dP(j); a second thread issues the dQ products, so neither stream's
     // barrier waits leave the tensor pipe idle.
-    if (lane == 0 && !skip && n_kv > 0) {
+    if (lane == 0 && !skip) {
       const uint32_t q_s = sbase + Cfg::kQOff, do_s = sbase + Cfg::kDOOff;
-      bool ok = mbar_wait(bar(Cfg::kBarQD), 0, abort_flag, err, kDevTimeoutTma);
-      for (int j = 0; j < n_kv && ok; ++j) {
-        const int ks = j % Cfg::kKStages, vs = j % Cfg::kVStages;
-        ok = mbar_wait_hint(bar(Cfg::kBarKFull + ks), (j / Cfg::kKStages) & 1, abort_flag, err, kDevTimeoutTma);
-        if (ok) ok = mbar_wait_hint(bar(Cfg::kBarVFull + vs), (j / Cfg::kVStages) & 1, abort_flag, err, kDevTimeoutTma);
-        if (ok && j > 0) ok = mbar_wait_hint(bar(Cfg::kBarSFree), (j - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
+      int T = 0, U = 0;
+      bool ok = true;
+      KB_FOR_EACH_SPARSE_UNIT(args.plan, u, w, n, walk) {
         if (!ok) break;
-        tc_fence_after();
-        // S's first K step goes out once S(j-1) has been read, the rest, with
-        // dP's steps interleaved, once dP(j-1) has been read too
-        const uint32_t k_s = sbase + Cfg::kKOff + ks * kTileBytes, v_s = sbase + Cfg::kVOff + vs * kTileBytes;
-        mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, 0, 1024u, kSlabBytes), desc_kmajor(k_s, 0, 1024u, kSlabBytes),
-               kIdescQK, 0u);
-        if (j > 0) ok = mbar_wait_hint(bar(Cfg::kBarDPFree), (j - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
-        if (!ok) break;
-        tc_fence_after();
+        if (n == 0) continue;
+        ok = mbar_wait(bar(Cfg::kBarQD), U & 1, abort_flag, err, kDevTimeoutTma);
+        for (int j = 0; j < n && ok; ++j, ++T) {
+          const int ks = T % Cfg::kKStages, vs = T % Cfg::kVStages;
+          ok = mbar_wait_hint(bar(Cfg::kBarKFull + ks), (T / Cfg::kKStages) & 1, abort_flag, err, kDevTimeoutTma);
+          if (ok) ok = mbar_wait_hint(bar(Cfg::kBarVFull + vs), (T / Cfg::kVStages) & 1, abort_flag, err, kDevTimeoutTma);
+          if (ok && T > 0) ok = mbar_wait_hint(bar(Cfg::kBarSFree), (T - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
+          if (!ok) break;
+          tc_fence_after();
+          // S's first K step goes out once S(j-1) has been read, the rest, with
+          // dP's steps interleaved, once dP(j-1) has been read too
+          const uint32_t k_s = sbase + Cfg::kKOff + ks * kTileBytes, v_s = sbase + Cfg::kVOff + vs * kTileBytes;
+          mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, 0, 1024u, kSlabBytes), desc_kmajor(k_s, 0, 1024u, kSlabBytes),
+                 kIdescQK, 0u);
+          if (T > 0) ok = mbar_wait_hint(bar(Cfg::kBarDPFree), (T - 1) & 1, abort_flag, err, kDevTimeoutSoftmax);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          mma_ss(tmem_base + Cfg::kColDP, desc_kmajor(do_s, kk, 1024u, kSlabBytes), desc_kmajor(v_s, kk, 1024u, kSlabBytes),
-                 kIdescQK, kk > 0 ? 1u : 0u);
-          if (kk < 7)
-            mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, kk + 1, 1024u, kSlabBytes),
-                   desc_kmajor(k_s, kk + 1, 1024u, kSlabBytes), kIdescQK, 1u);
-          if (kk == 6) tc_commit(bar(Cfg::kBarSDone));             // S is complete before dP's last step
+          for (int kk = 0; kk < 8; ++kk) {
+            mma_ss(tmem_base + Cfg::kColDP, desc_kmajor(do_s, kk, 1024u, kSlabBytes), desc_kmajor(v_s, kk, 1024u, kSlabBytes),
+                   kIdescQK, kk > 0 ? 1u : 0u);
+            if (kk < 7)
+              mma_ss(tmem_base + Cfg::kColS, desc_kmajor(q_s, kk + 1, 1024u, kSlabBytes),
+                     desc_kmajor(k_s, kk + 1, 1024u, kSlabBytes), kIdescQK, 1u);
+            if (kk == 6) tc_commit(bar(Cfg::kBarSDone));             // S is complete before dP's last step
+          }
+          tc_commit(bar(Cfg::kBarSFull));
+          tc_commit(bar(Cfg::kBarVEmpty + vs));
         }
-        tc_commit(bar(Cfg::kBarSFull));
-        tc_commit(bar(Cfg::kBarVEmpty + vs));
+        if (ok) tc_commit(bar(Cfg::kBarQDEmpty));
+        ++U;
       }
       if (!ok) {
         tc_commit(bar(Cfg::kBarDrain));
@@ -183,15 +201,20 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     // dQ(j) reads dS(j) and K(j); the K slot is released after it (S(j)
     // finished before dS(j) existed).
     if (lane == 0 && !skip) {
+      int T = 0;
       bool ok = true;
-      for (int j = 0; j < n_kv && ok; ++j) {
-        ok = mbar_wait_hint(bar(Cfg::kBarDSFull), j & 1, abort_flag, err, kDevTimeoutSoftmax);
+      KB_FOR_EACH_SPARSE_UNIT(args.plan, u, w, n, walk) {
         if (!ok) break;
-        tc_fence_after();
-        const int ks = j % Cfg::kKStages;
-        issue_pv(tmem_base + Cfg::kColDQ, tmem_base + Cfg::kColDS, sbase + Cfg::kKOff + ks * kTileBytes, j == 0);
-        tc_commit(bar(Cfg::kBarDQDone));
-        tc_commit(bar(Cfg::kBarKEmpty + ks));
+        // a unit's first dS comes after the same warps have read the last unit's dQ
+        for (int j = 0; j < n && ok; ++j, ++T) {
+          ok = mbar_wait_hint(bar(Cfg::kBarDSFull), T & 1, abort_flag, err, kDevTimeoutSoftmax);
+          if (!ok) break;
+          tc_fence_after();
+          const int ks = T % Cfg::kKStages;
+          issue_pv(tmem_base + Cfg::kColDQ, tmem_base + Cfg::kColDS, sbase + Cfg::kKOff + ks * kTileBytes, j == 0);
+          tc_commit(bar(Cfg::kBarDQDone));
+          tc_commit(bar(Cfg::kBarKEmpty + ks));
+        }
       }
       if (!ok) {
         tc_commit(bar(Cfg::kBarDrain + 1));
@@ -208,107 +231,111 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     const int u = lane & 3;
     const int r0 = 16 * (warp >> 2) + (lane >> 2);
     const uint32_t warp_rows = 0xFFFFu << (16 * (warp >> 2));
-    const int p0 = w.t * kUnitRows - w.own * kTileKeys;               // the unit's first row within its own block
     const int S = args.plan.L;
-    const int iA = w.t * kUnitRows + r0, iB = iA + 8;                 // query positions
-    const bool vA = iA < S, vB = iB < S;
-    const size_t row0 = (static_cast<size_t>(w.b) * args.plan.Hq + w.g * kGroup + head) * static_cast<size_t>(S);
-    // rows past the sequence list nothing, as do rows with lse = -inf: every
-    // key of theirs is masked
-    const float lseA = vA ? __fmul_rn(args.lse[row0 + iA], kLog2e) : 0.0f;
-    const float lseB = vB ? __fmul_rn(args.lse[row0 + iB], kLog2e) : 0.0f;
-    const float dlA = vA ? args.delta[row0 + iA] : 0.0f;
-    const float dlB = vB ? args.delta[row0 + iB] : 0.0f;
     const float2 c2 = make_float2(score_scale_log2(), score_scale_log2());
-    const float2 nlA = make_float2(-lseA, -lseA), nlB = make_float2(-lseB, -lseB);
-    const float2 ndA = make_float2(-dlA, -dlA), ndB = make_float2(-dlB, -dlB);
-    // a tile that some row of the warp did not list, and the own one, masks
-    // keys from nA, nB on; the others take no select
-    auto tile_ds = [&](auto mask_tag, const uint32_t (&sv)[32], const uint32_t (&pv)[32], int half, int nA, int nB,
-                       uint32_t (&ds)[32]) {
-      constexpr bool kMask = decltype(mask_tag)::value;
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int key = 64 * half + 8 * r + 2 * u;                   // keys key, key + 1 within the tile
-        uint32_t unused;
-        p_ds_pair<kMask>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nlA, ndA, key >= nA, key + 1 >= nA,
-                         unused, ds[2 * (8 * half + r)]);
-        p_ds_pair<kMask>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nlB, ndB, key >= nB,
-                         key + 1 >= nB, unused, ds[2 * (8 * half + r) + 1]);
-      }
-    };
+    int T = 0;
     bool ok = !skip;
-    uint2 next = n_kv > 0 ? __ldg(&walk[0]) : make_uint2(0u, 0u);
-    for (int j = 0; j < n_kv && ok; ++j) {
-      const uint2 entry = next;
-      if (j + 1 < n_kv) next = __ldg(&walk[j + 1]);
-      ok = mbar_wait_hint(bar(Cfg::kBarSDone), j & 1, abort_flag, err, kDevTimeoutMma);
-      ok = __all_sync(0xffffffffu, ok);
+    KB_FOR_EACH_SPARSE_UNIT(args.plan, unit, w, n, walk) {
       if (!ok) break;
-      tc_fence_after();
-      const bool diag = static_cast<int>(entry.x & kEntryBlock) == w.own;
-      const int nA = (entry.y >> r0) & 1u ? (diag ? p0 + r0 + 1 : kTileKeys) : 0;
-      const int nB = (entry.y >> (r0 + 8)) & 1u ? (diag ? p0 + r0 + 9 : kTileKeys) : 0;
-      uint32_t ds[32];
-      // all of S(j) and dP(j) into registers first, so S(j+1), dP(j+1) can be
-      // issued while this tile's dS is computed: S as soon as it is complete
-      // (before dP's last step), released on its own barrier so S(j+1) can
-      // start while dP is still being read
-      uint32_t sv0[32], pv0[32], sv1[32], pv1[32];
-      tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColS + lane_off, tmem_base + Cfg::kColS + lane_off + 64u, sv0,
-                                   sv1);
-      tc_fence_before();
-      mbar_arrive(bar(Cfg::kBarSFree));                              // S(j) fully read
-      ok = mbar_wait_hint(bar(Cfg::kBarSFull), j & 1, abort_flag, err, kDevTimeoutMma);   // dP(j) too
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColDP + lane_off, tmem_base + Cfg::kColDP + lane_off + 64u, pv0,
-                                   pv1);
-      tc_fence_before();
-      mbar_arrive(bar(Cfg::kBarDPFree));                             // dP(j) fully read
-      if (diag || (entry.y & warp_rows) != warp_rows) {
-        tile_ds(std::true_type{}, sv0, pv0, 0, nA, nB, ds);
-        tile_ds(std::true_type{}, sv1, pv1, 1, nA, nB, ds);
-      } else {
-        tile_ds(std::false_type{}, sv0, pv0, 0, nA, nB, ds);
-        tile_ds(std::false_type{}, sv1, pv1, 1, nA, nB, ds);
-      }
-      if (j > 0) {                                                   // dQ(j-1) has read dS(j-1)
-        ok = mbar_wait(bar(Cfg::kBarDQDone), (j - 1) & 1, abort_flag, err, kDevTimeoutMma);
+      const int p0 = w.t * kUnitRows - w.own * kTileKeys;               // the unit's first row within its own block
+      const int iA = w.t * kUnitRows + r0, iB = iA + 8;                 // query positions
+      const bool vA = iA < S, vB = iB < S;
+      const size_t row0 = (static_cast<size_t>(w.b) * args.plan.Hq + w.g * kGroup + head) * static_cast<size_t>(S);
+      // rows past the sequence list nothing, as do rows with lse = -inf: every
+      // key of theirs is masked
+      const float lseA = vA ? __fmul_rn(args.lse[row0 + iA], kLog2e) : 0.0f;
+      const float lseB = vB ? __fmul_rn(args.lse[row0 + iB], kLog2e) : 0.0f;
+      const float dlA = vA ? args.delta[row0 + iA] : 0.0f;
+      const float dlB = vB ? args.delta[row0 + iB] : 0.0f;
+      const float2 nlA = make_float2(-lseA, -lseA), nlB = make_float2(-lseB, -lseB);
+      const float2 ndA = make_float2(-dlA, -dlA), ndB = make_float2(-dlB, -dlB);
+      // a tile that some row of the warp did not list, and the own one, masks
+      // keys from nA, nB on; the others take no select
+      auto tile_ds = [&](auto mask_tag, const uint32_t (&sv)[32], const uint32_t (&pv)[32], int half, int nA, int nB,
+                         uint32_t (&ds)[32]) {
+        constexpr bool kMask = decltype(mask_tag)::value;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int key = 64 * half + 8 * r + 2 * u;                   // keys key, key + 1 within the tile
+          uint32_t unused;
+          p_ds_pair<kMask>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nlA, ndA, key >= nA, key + 1 >= nA,
+                           unused, ds[2 * (8 * half + r)]);
+          p_ds_pair<kMask>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nlB, ndB, key >= nB,
+                           key + 1 >= nB, unused, ds[2 * (8 * half + r) + 1]);
+        }
+      };
+      uint2 next = n > 0 ? __ldg(&walk[0]) : make_uint2(0u, 0u);
+      for (int j = 0; j < n && ok; ++j, ++T) {
+        const uint2 entry = next;
+        if (j + 1 < n) next = __ldg(&walk[j + 1]);
+        ok = mbar_wait_hint(bar(Cfg::kBarSDone), T & 1, abort_flag, err, kDevTimeoutMma);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-      }
-      tmem_st_16x128b_x16(tmem_base + Cfg::kColDS + lane_off, ds);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bar(Cfg::kBarDSFull));
-    }
-    if (ok && n_kv > 0) ok = mbar_wait(bar(Cfg::kBarDQDone), (n_kv - 1) & 1, abort_flag, err, kDevTimeoutMma);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      __nv_bfloat16* base = static_cast<__nv_bfloat16*>(args.dq) + row0 * kHeadDim;
-      uint32_t* dA = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vA ? iA : 0) * kHeadDim);
-      uint32_t* dB = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vB ? iB : 0) * kHeadDim);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint32_t v[32];
-        tmem_ld_16x256b_x8_wait(tmem_base + Cfg::kColDQ + lane_off + 64u * half, v);
-        if (n_kv == 0) {                                              // nothing listed: the gradient is zero
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        const bool diag = static_cast<int>(entry.x & kEntryBlock) == w.own;
+        const int nA = (entry.y >> r0) & 1u ? (diag ? p0 + r0 + 1 : kTileKeys) : 0;
+        const int nB = (entry.y >> (r0 + 8)) & 1u ? (diag ? p0 + r0 + 9 : kTileKeys) : 0;
+        uint32_t ds[32];
+        // all of S(j) and dP(j) into registers first, so S(j+1), dP(j+1) can be
+        // issued while this tile's dS is computed: S as soon as it is complete
+        // (before dP's last step), released on its own barrier so S(j+1) can
+        // start while dP is still being read
+        uint32_t sv0[32], pv0[32], sv1[32], pv1[32];
+        tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColS + lane_off, tmem_base + Cfg::kColS + lane_off + 64u, sv0,
+                                     sv1);
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::kBarSFree));                              // S(j) fully read
+        ok = mbar_wait_hint(bar(Cfg::kBarSFull), T & 1, abort_flag, err, kDevTimeoutMma);   // dP(j) too
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld_16x256b_x8_pair_wait(tmem_base + Cfg::kColDP + lane_off, tmem_base + Cfg::kColDP + lane_off + 64u, pv0,
+                                     pv1);
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::kBarDPFree));                             // dP(j) fully read
+        if (diag || (entry.y & warp_rows) != warp_rows) {
+          tile_ds(std::true_type{}, sv0, pv0, 0, nA, nB, ds);
+          tile_ds(std::true_type{}, sv1, pv1, 1, nA, nB, ds);
+        } else {
+          tile_ds(std::false_type{}, sv0, pv0, 0, nA, nB, ds);
+          tile_ds(std::false_type{}, sv1, pv1, 1, nA, nB, ds);
         }
+        if (T > 0) {                                                   // dQ(j-1) has read dS(j-1)
+          ok = mbar_wait(bar(Cfg::kBarDQDone), (T - 1) & 1, abort_flag, err, kDevTimeoutMma);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st_16x128b_x16(tmem_base + Cfg::kColDS + lane_off, ds);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(Cfg::kBarDSFull));
+      }
+      if (ok && n > 0) ok = mbar_wait(bar(Cfg::kBarDQDone), (T - 1) & 1, abort_flag, err, kDevTimeoutMma);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        __nv_bfloat16* base = static_cast<__nv_bfloat16*>(args.dq) + row0 * kHeadDim;
+        uint32_t* dA = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vA ? iA : 0) * kHeadDim);
+        uint32_t* dB = reinterpret_cast<uint32_t*>(base + static_cast<size_t>(vB ? iB : 0) * kHeadDim);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
+          tmem_ld_16x256b_x8_wait(tmem_base + Cfg::kColDQ + lane_off + 64u * half, v);
+          if (n == 0) {                                              // nothing listed: the gradient is zero
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int col = 64 * half + 8 * r + 2 * u;
-          const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), kInvSqrtD),
-                                          __fmul_rn(__uint_as_float(v[4 * r + 1]), kInvSqrtD));
-          const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), kInvSqrtD),
-                                          __fmul_rn(__uint_as_float(v[4 * r + 3]), kInvSqrtD));
-          if (vA) dA[col >> 1] = wa;
-          if (vB) dB[col >> 1] = wb;
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int col = 64 * half + 8 * r + 2 * u;
+            const uint32_t wa = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r]), kInvSqrtD),
+                                            __fmul_rn(__uint_as_float(v[4 * r + 1]), kInvSqrtD));
+            const uint32_t wb = pack_bf16x2(__fmul_rn(__uint_as_float(v[4 * r + 2]), kInvSqrtD),
+                                            __fmul_rn(__uint_as_float(v[4 * r + 3]), kInvSqrtD));
+            if (vA) dA[col >> 1] = wa;
+            if (vB) dB[col >> 1] = wb;
+          }
         }
       }
     }
@@ -771,7 +798,8 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
 // --------------------------------------------------------------- launcher
 
 cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, cudaStream_t s) {
+                                   const CUtensorMap& tdo, const SparseBwdArgs& a, int device, int sm_count,
+                                   cudaStream_t s) {
   static_assert(SparseBwdQCfg::kSmemBytes <= 227u * 1024u, "shared memory budget (dq)");
   static_assert(SparseBwdKVCfg::kSmemBytes <= 227u * 1024u, "shared memory budget (dk, dv)");
   static bool configured[64] = {};
@@ -785,8 +813,8 @@ cudaError_t launch_sparse_backward(const CUtensorMap& tq, const CUtensorMap& tk,
     if (e != cudaSuccess) return e;
     configured[device] = true;
   }
-  kb_sparse_bwd_dq_kernel<<<static_cast<unsigned>(a.plan.n_units), SparseBwdQCfg::kThreads, SparseBwdQCfg::kSmemBytes,
-                            s>>>(tq, tk, tv, tdo, a);
+  kb_sparse_bwd_dq_kernel<<<static_cast<unsigned>(unit_grid(a.plan, sm_count, 32)), SparseBwdQCfg::kThreads,
+                            SparseBwdQCfg::kSmemBytes, s>>>(tq, tk, tv, tdo, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   kb_sparse_order_kernel<<<1, kOrderThreads, 0, s>>>(a);

@@ -321,3 +321,21 @@ def test_serving_run_equals_the_training_forward(kb, page):
         kb.check_device_status()
         assert torch.equal(bits(got), bits(want[:, :, cut])), at
         at += L
+
+
+@pytest.mark.parametrize("S", [4860, 4864])
+def test_ctas_that_go_from_unit_to_unit(kb, S):
+    """8 KV heads x 152 position tiles are a whole number of units for every SM of this GPU, so a CTA takes several; cut
+    into chunks of 500 rows, one each.  Same bits, with rows and whole units that list nothing among them."""
+    import torch
+
+    q, k, v = randn(150, 1, 32, S, 128), randn(151, 1, 8, S, 128), randn(152, 1, 8, S, 128)
+    blocks = random_lists(153, 1, S, 0, 3, none=0.2)
+    blocks[:, :, 640:800] = -1
+    o, lse = kb.sparse_prefill_lse(q, k, v, blocks, check=True)
+    for a in range(0, S, 500):
+        z = min(a + 500, S)
+        part = kb.sparse_chunk(q[:, :, a:z].contiguous(), k, v, a, blocks[:, :, a:z].contiguous(), check=True)
+        assert torch.equal(bits(part), bits(o[:, :, a:z]))
+    empty = (blocks < 0).all(-1).repeat_interleave(4, 1)
+    assert torch.equal(torch.isneginf(lse), empty) and not o[empty].any()

@@ -212,3 +212,20 @@ def test_refusals(kb):
     kb.sparse_backward(q, k, v, o, dout, lse, lists)
     with pytest.raises(kb.KBError):
         kb.check_device_status()
+
+
+def test_ctas_that_go_from_unit_to_unit(kb):
+    """8 KV heads x 152 position tiles are a whole number of units for every SM of this GPU, so a CTA takes several; a
+    shorter sequence's are not, and it has the same rows' dq, bit for bit."""
+    import torch
+
+    S, short, n = 4864, 2000, 3
+    q, k, v, dout = (randn(3800 + i, 1, h, S, 128) for i, h in enumerate((32, 8, 8, 32)))
+    lists = random_lists(3804, 1, S, 0, n, none=0.2)
+    lists[:, :, 640:800] = -1
+    o, lse = kb.sparse_prefill_lse(q, k, v, lists)
+    whole = kb.sparse_backward(q, k, v, o, dout, lse, lists, check=True)[0]
+    cut = [x[:, :, :short].contiguous() for x in (q, k, v, o, dout, lse, lists)]
+    dq = kb.sparse_backward(*cut, check=True)[0]
+    assert torch.equal(whole[:, :, :short].contiguous().view(torch.uint8), dq.view(torch.uint8))
+    assert not whole[:, :, 640:800].any()
