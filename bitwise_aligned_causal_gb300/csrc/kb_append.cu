@@ -23,7 +23,10 @@
 // Bound: memory.  Everything is read once and written once (a token: 40 rows
 // of 256 B in and 40 out, 8 value rows in and out, 512 B of table); a thread
 // holds eight planes of a row, so the table's 64 bytes are fetched once for
-// the five or six rows it turns.
+// the five or six rows it turns.  Measured: the rotation of 32 heads x 16384
+// positions 43.9 us (6.3 TB/s of bytes read and written; HBM copies at 6.8);
+// an append of four ragged prompts of up to 4096, 39 to 50 us from GPU to GPU
+// (5.5 to 7.0 TB/s), of one token of 16 sequences 5.0 us, a launch's latency.
 #include <algorithm>
 
 #include "kb_boxes.cuh"

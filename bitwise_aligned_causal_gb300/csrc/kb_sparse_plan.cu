@@ -5,8 +5,9 @@
 // One CTA per unit keeps a row mask per key block in shared memory, so lists
 // may come in any order and name a block twice; blocks past a row's own are
 // dropped, since none of their keys is visible to it.  The lists are read
-// once (4 bytes an entry) and the walk written once (8 bytes): a few
-// microseconds beside the attention, bound by latency.
+// once (4 bytes an entry) and the walk written once (8 bytes): 8.5 us for 512
+// units and 512 blocks, 12 us for 2048 units and 64, beside 234 and 338 us of
+// attention; bound by the latency of its steps.
 #include "kb_sparse.cuh"
 
 namespace kb {

@@ -341,8 +341,8 @@ kb_status kb_attn_append(const void* q, const void* k, const void* v, const long
  * integer in -100..100 for which the block's largest |key| is at most
  * 127 * 2^(E-7), the upper bound of a channel is ceil(max 2^(7-E)) 2^(E-7)
  * and the lower one floor(min 2^(7-E)) 2^(E-7).  Layouts as in kb_attn_append;
- * boxes of blocks beyond are left as they were.  Keys are finite (infinities
- * saturate, a NaN does not count).
+ * boxes of blocks beyond are left as they were.  Keys are finite: infinities
+ * saturate, and the bounds of a block with a NaN are unspecified.
  */
 kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, int kv_len,
                               const int* kv_lens, int kv_cap, const int* block_table, int pages_per_seq,
@@ -424,9 +424,12 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
  * Backward of kb_attn_sparse_prefill_lse: as kb_attn_backward, over the listed
  * keys (the lists themselves take no gradient).  o and lse from the forward
  * with the same q, k, v and blocks; delta [B, Hq, S] fp32 is an output.  A row
- * that lists nothing has dq = 0, a block that no row lists dk = dv = 0.  No
- * atomics: repeated calls give identical bits.  workspace: 256-byte aligned
- * scratch of kb_attn_sparse_backward_workspace_bytes(B, Hkv, S, n_select).
+ * that lists nothing has dq = 0, a block that no row lists dk = dv = 0.
+ * Every sum has one order: repeated calls give identical bits, and a
+ * sequence's gradients do not depend on the batch or on n_select.  workspace:
+ * 256-byte aligned scratch of kb_attn_sparse_backward_workspace_bytes(B, Hkv,
+ * S, n_select), which from S = 4065 on includes 256 KB per KV head for every
+ * block with 4065 positions or more from its first on.
  */
 size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select);
 kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
