@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
 // shared memory.
 // Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
 // half of TMEM let two CTAs share an SM, so one loads while the other
-// searches.  A 16K prompt (134 MB of q) takes 94 us, 1.5 TB/s: rounding q to
+// searches.  A 16K prompt (134 MB of q) takes 90 us, 1.6 TB/s: rounding q to
 // whole numbers and the search are instructions (56 % of issue slots), and a
 // tile's slowest row holds up its CTA.  Sixteen rows per warp with register
 // products of 16 x 8 in place of tcgen05, so that no warp waits for another,
@@ -362,23 +362,30 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
     tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
     tmem_relinquish();
   }
-  // boxes of the 64 blocks from j0 on into the B operand (a box is a row of it)
-  auto load_boxes = [&](int j0, int j1) {
-    uint4 val[Cfg::kChunk * 32 / Cfg::kThreads];
+  // boxes of the 64 blocks from j0 on: into registers, then into the B operand
+  // (a box is a row of it)
+  constexpr int kBoxLoads = Cfg::kChunk * 32 / Cfg::kThreads;
+  auto fetch_boxes = [&](int j0, int j1, uint4 (&val)[kBoxLoads]) {
 #pragma unroll
-    for (int k = 0; k < Cfg::kChunk * 32 / Cfg::kThreads; ++k) {
+    for (int k = 0; k < kBoxLoads; ++k) {
       const int e = threadIdx.x + k * Cfg::kThreads, j = j0 + (e >> 5);
       const __nv_bfloat16* box = j < j1 ? box_of(args, b, g, j) : nullptr;
       val[k] = box != nullptr ? __ldg(reinterpret_cast<const uint4*>(box) + (e & 31)) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  auto put_boxes = [&](const uint4 (&val)[kBoxLoads]) {
 #pragma unroll
-    for (int k = 0; k < Cfg::kChunk * 32 / Cfg::kThreads; ++k) {
+    for (int k = 0; k < kBoxLoads; ++k) {
       const int e = threadIdx.x + k * Cfg::kThreads, r = e >> 5, c = e & 31;
       *reinterpret_cast<uint4*>(smem + Cfg::kBOff + (c >> 3) * Cfg::kBSlab + (r >> 3) * 1024 + (r & 7) * 128 +
                                 (((c & 7) ^ (r & 7)) << 4)) = val[k];
     }
   };
-  load_boxes(0, min(cand1, Cfg::kPass));
+  {
+    uint4 val[kBoxLoads];
+    fetch_boxes(0, min(cand1, Cfg::kPass), val);
+    put_boxes(val);
+  }
 
   // n of the tile's rows: 16 lanes per row, eight channels of the four heads
   // each, written as the two halves n+ and n- of the A operand
@@ -471,8 +478,12 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
   bool ok = true;
   for (int pass = 0; pass < passes; ++pass) {
     const int c0 = pass * Cfg::kPass, c1 = min(cand1, c0 + Cfg::kPass);
+    uint4 val[kBoxLoads];
     for (int j0 = c0; j0 < c1; j0 += Cfg::kChunk) {
-      if (j0 > 0) load_boxes(j0, c1);
+      if (j0 > 0) {
+        fetch_boxes(j0, c1, val);
+        put_boxes(val);
+      }
       fence_proxy_async_smem();
       __syncthreads();
       if (threadIdx.x == 7 * 32) {
@@ -651,21 +662,28 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
       }
       if (last) {
         // a row's winners in block order: carried ones (thread 0 of the quad),
-        // then those of words 2 u4 and 2 u4 + 1
+        // then those of words u4 and u4 + 4
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int r = rA + 8 * half;
           const float cut = half ? sB.lo : sA.lo;
-          int* const mine = staged + r * (args.n + 1) + args.keep_first;
-          int at = 0;
+          int* const mine = staged + r * (args.n + 1);
+          for (int k = u4; k < args.keep_first; k += 4) mine[k] = k;
+          for (int k = u4; k < args.keep_last; k += 4) mine[args.n - 1 - k] = nb - 1 - k;
+          int at = args.keep_first;
           for (int w = 0; w < listed; ++w)
             if (list_s[w * 128 + r] >= cut) {
               if (u4 == 0) mine[at] = list_j[w * 128 + r];
               ++at;
             }
-          for (int k = 0; k < min(words, 2 * u4); ++k) at += __popc(masks[r * 9 + k]);
-          for (int k = 2 * u4; k < min(words, 2 * u4 + 2); ++k)
-            for (uint32_t m = masks[r * 9 + k]; m != 0u; m &= m - 1u) mine[at++] = c0 + 32 * k + __ffs(m) - 1;
+          for (int k = 0; k < words; ++k) {
+            uint32_t m = masks[r * 9 + k];
+            if ((k & 3) != u4) {
+              at += __popc(m);
+              continue;
+            }
+            for (; m != 0u; m &= m - 1u) mine[at++] = c0 + 32 * k + __ffs(m) - 1;
+          }
           __syncwarp();
         }
       } else {
@@ -704,20 +722,26 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
       }
       listed = min(need, have);
     }
-    tc_fence_before();
-    __syncthreads();                                                     // TMEM has been read, the lists are written
-    tc_fence_after();
-  }
-  if (ok) {
-    // lists out, the kept blocks around the chosen ones
-    for (int r = warp; r < kTileKeys; r += Cfg::kThreads / 32) {
-      const int i = i0 + r;
-      if (i < 0 || i >= len) continue;
-      int* out = args.blocks + (out_row0 + i) * args.n;
-      for (int k = lane; k < args.n; k += 32)
-        out[k] = k < args.keep_first ? k : k >= args.n - args.keep_last ? nb - args.n + k : staged[r * (args.n + 1) + k];
+    if (pass + 1 < passes) {
+      tc_fence_before();
+      __syncthreads();                                                   // TMEM has been read
+      tc_fence_after();
     }
   }
+  if (ok) {
+    // the warp's sixteen lists out, one after another
+    for (int rr = lane / args.n, k = lane % args.n; rr < 16;) {
+      const int i = i0 + lane_base + rr;
+      if (i >= 0 && i < len) args.blocks[(out_row0 + i) * args.n + k] = staged[(lane_base + rr) * (args.n + 1) + k];
+      rr += 32 / args.n;
+      k += 32 % args.n;
+      if (k >= args.n) {
+        k -= args.n;
+        ++rr;
+      }
+    }
+  }
+  tc_fence_before();
   __syncthreads();
   if (warp == 4) {
     __syncwarp();
