@@ -15,15 +15,17 @@
 // Every gradient element is summed in one order, by one CTA, or by two of which
 // the second adds both halves; atomics count rows and draw tickets, no more.
 //
-// Roundings: P and dS go to the tensor core as bf16, like the dense backward's,
-// with fp32 sums.  dS's rounding and delta's (from the forward's bf16 o) put dq
-// 0.0027 to 0.0030 off the 64-bit formula (relative, root mean square; its own
-// rounding to bf16 alone is 0.0017).  dS split into two bf16 parts would give
-// 0.0021 for a second product per tile.
+// Roundings: P and dS go to the tensor core as bf16, with fp32 sums, but for dq
+// dS goes as two bf16 parts.  delta comes from the forward's bf16 o, and its
+// error is common to a row's keys: with dS's own rounding on top dq was 0.0027
+// to 0.0030 off the 64-bit formula (relative, root mean square), where rounding
+// the result to bf16 alone is 0.0017; with the second product it is at most
+// 0.0024, for 7 % of the kernel's time (455 us without it).  In dk the rows'
+// errors average out.
 //
-// Measured for 8192 rows of 32 heads, 16 blocks a row: delta 25 us, dq 455 us
-// (42,700 tiles: about 3,100 cycles a tile and SM, the dense kernel's pace),
-// dk/dv 459 us (201 steps an SM: 4,400 cycles a step, also the dense pace),
+// Measured for 8192 rows of 32 heads, 16 blocks a row: delta 25 us, dq 488 us
+// (42,700 tiles: about 3,350 cycles a tile and SM; the dense kernel 3,200),
+// dk/dv 459 us (201 steps an SM: 4,400 cycles a step, the dense kernel's pace),
 // plan and order 16 us.
 #include <type_traits>
 
@@ -45,7 +47,8 @@ struct SparseBwdQCfg {
   static constexpr int kKStages = 3;
   static constexpr int kVStages = 2;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256, kColDS = 384;
+  static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256;
+  static constexpr uint32_t kColDS = 384, kColDSLow = 448;      // dS as the sum of two bf16 parts, 64 columns each
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kDOOff = kTileBytes;
   static constexpr uint32_t kKOff = 2 * kTileBytes;
@@ -224,6 +227,7 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
           tc_fence_after();
           const int ks = T % Cfg::kKStages;
           issue_pv(tmem_base + Cfg::kColDQ, tmem_base + Cfg::kColDS, sbase + Cfg::kKOff + ks * kTileBytes, j == 0);
+          issue_pv(tmem_base + Cfg::kColDQ, tmem_base + Cfg::kColDSLow, sbase + Cfg::kKOff + ks * kTileBytes, false);
           tc_commit(bar(Cfg::kBarDQDone));
           tc_commit(bar(Cfg::kBarKEmpty + ks));
         }
@@ -264,16 +268,16 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
       // a tile that some row of the warp did not list, and the own one, masks
       // keys from nA, nB on; the others take no select
       auto tile_ds = [&](auto mask_tag, const uint32_t (&sv)[32], const uint32_t (&pv)[32], int half, int nA, int nB,
-                         uint32_t (&ds)[32]) {
+                         uint32_t (&ds)[32], uint32_t (&low)[32]) {
         constexpr bool kMask = decltype(mask_tag)::value;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const int key = 64 * half + 8 * r + 2 * u;                   // keys key, key + 1 within the tile
-          uint32_t unused;
-          p_ds_pair<kMask>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nlA, ndA, key >= nA, key + 1 >= nA,
-                           unused, ds[2 * (8 * half + r)]);
-          p_ds_pair<kMask>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nlB, ndB, key >= nB,
-                           key + 1 >= nB, unused, ds[2 * (8 * half + r) + 1]);
+          const int at = 2 * (8 * half + r);
+          ds_split_pair<kMask>(sv[4 * r], sv[4 * r + 1], pv[4 * r], pv[4 * r + 1], c2, nlA, ndA, key >= nA, key + 1 >= nA,
+                               ds[at], low[at]);
+          ds_split_pair<kMask>(sv[4 * r + 2], sv[4 * r + 3], pv[4 * r + 2], pv[4 * r + 3], c2, nlB, ndB, key >= nB,
+                               key + 1 >= nB, ds[at + 1], low[at + 1]);
         }
       };
       uint2 next = n > 0 ? __ldg(&walk[0]) : make_uint2(0u, 0u);
@@ -287,7 +291,7 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         const bool diag = static_cast<int>(entry.x & kEntryBlock) == w.own;
         const int nA = (entry.y >> r0) & 1u ? (diag ? p0 + r0 + 1 : kTileKeys) : 0;
         const int nB = (entry.y >> (r0 + 8)) & 1u ? (diag ? p0 + r0 + 9 : kTileKeys) : 0;
-        uint32_t ds[32];
+        uint32_t ds[32], low[32];
         // all of S(j) and dP(j) into registers first, so S(j+1), dP(j+1) can be
         // issued while this tile's dS is computed: S as soon as it is complete
         // (before dP's last step), released on its own barrier so S(j+1) can
@@ -306,11 +310,11 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         tc_fence_before();
         mbar_arrive(bar(Cfg::kBarDPFree));                             // dP(j) fully read
         if (diag || (entry.y & warp_rows) != warp_rows) {
-          tile_ds(std::true_type{}, sv0, pv0, 0, nA, nB, ds);
-          tile_ds(std::true_type{}, sv1, pv1, 1, nA, nB, ds);
+          tile_ds(std::true_type{}, sv0, pv0, 0, nA, nB, ds, low);
+          tile_ds(std::true_type{}, sv1, pv1, 1, nA, nB, ds, low);
         } else {
-          tile_ds(std::false_type{}, sv0, pv0, 0, nA, nB, ds);
-          tile_ds(std::false_type{}, sv1, pv1, 1, nA, nB, ds);
+          tile_ds(std::false_type{}, sv0, pv0, 0, nA, nB, ds, low);
+          tile_ds(std::false_type{}, sv1, pv1, 1, nA, nB, ds, low);
         }
         if (T > 0) {                                                   // dQ(j-1) has read dS(j-1)
           ok = mbar_wait(bar(Cfg::kBarDQDone), (T - 1) & 1, abort_flag, err, kDevTimeoutMma);
@@ -319,6 +323,7 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
           tc_fence_after();
         }
         tmem_st_16x128b_x16(tmem_base + Cfg::kColDS + lane_off, ds);
+        tmem_st_16x128b_x16(tmem_base + Cfg::kColDSLow + lane_off, low);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar(Cfg::kBarDSFull));
