@@ -26,7 +26,7 @@
 // Measured for 8192 rows of 32 heads, 16 blocks a row: delta 25 us, dq 488 us
 // (42,700 tiles: about 3,350 cycles a tile and SM; the dense kernel 3,200),
 // dk/dv 459 us (201 steps an SM: 4,400 cycles a step, the dense kernel's pace),
-// plan and order 16 us.
+// plan and order 15 us.
 #include <type_traits>
 
 #include "kb_bwd.cuh"

@@ -5,8 +5,8 @@
 // One CTA per unit keeps a row mask per key block in shared memory, so lists
 // may come in any order and name a block twice; blocks past a row's own are
 // dropped, since none of their keys is visible to it.  The lists are read
-// once (4 bytes an entry) and the walk written once (8 bytes): 8.5 us for 512
-// units and 512 blocks, 12 us for 2048 units and 64, beside 234 and 338 us of
+// once (4 bytes an entry) and the walk written once (8 bytes): 6.6 us for 512
+// units and 512 blocks, 10.8 us for 2048 units and 64, beside 234 and 334 us of
 // attention; bound by the latency of its steps.
 #include "kb_sparse.cuh"
 
@@ -40,15 +40,22 @@ __global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const Spar
   for (int j = threadIdx.x; j < nb; j += kPlanThreads) row_mask[j] = 0u;
   __syncthreads();
   const int i0 = w.t * kUnitRows - w.start;           // row index of the unit's first position (may be negative)
-  const int* lists = args.blocks + (static_cast<size_t>(w.b) * args.Hkv + w.g) * args.L * args.n_select;
+  const int* lists = args.blocks + ((static_cast<size_t>(w.b) * args.Hkv + w.g) * args.L + max(i0, 0)) * args.n_select;
   const int n_cap = (args.kv_cap + kTileKeys - 1) / kTileKeys;
-  for (int e = threadIdx.x; e < kUnitRows * args.n_select; e += kPlanThreads) {
-    const int r = e / args.n_select;
-    const int i = i0 + r;
-    if (i < 0 || i >= w.L) continue;
-    const int j = lists[static_cast<size_t>(i) * args.n_select + e % args.n_select];
+  // the unit's rows lie one after another; entry e of them is of row `r`
+  const int r0 = max(0, -i0), rows = min(kUnitRows - r0, w.L - max(i0, 0));
+  int r = r0 + static_cast<int>(threadIdx.x) / args.n_select, k = static_cast<int>(threadIdx.x) % args.n_select;
+  const int r_step = kPlanThreads / args.n_select, k_step = kPlanThreads % args.n_select;
+  for (int e = threadIdx.x; e < rows * args.n_select; e += kPlanThreads) {
+    const int j = __ldg(lists + e);
     if (j < -1 || j >= n_cap) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
     else if (j >= 0 && j <= w.own) atomicOr(&row_mask[j], 1u << r);
+    r += r_step;
+    k += k_step;
+    if (k >= args.n_select) {
+      k -= args.n_select;
+      ++r;
+    }
   }
   __syncthreads();
   if (args.masks != nullptr) {
@@ -75,9 +82,9 @@ __global__ void __launch_bounds__(kPlanThreads) kb_sparse_plan_kernel(const Spar
       n += c;
     }
     if (m != 0u) {
-      bool first = true, last = true;
-      for (int k = j / kSegTiles * kSegTiles; k < j; ++k) first = first && row_mask[k] == 0u;
-      for (int k = j + 1; k < nb && k / kSegTiles == j / kSegTiles; ++k) last = last && row_mask[k] == 0u;
+      // the warp's 32 blocks are four whole segments
+      const uint32_t seg = (any >> (lane & ~(kSegTiles - 1))) & ((1u << kSegTiles) - 1u), place = lane % kSegTiles;
+      const bool first = (seg & ((1u << place) - 1u)) == 0u, last = (seg >> place) == 1u;
       walk[at + __popc(any & ((1u << lane) - 1u))] =
           make_uint2(static_cast<uint32_t>(j) | (first ? kEntrySegStart : 0u) | (last ? kEntrySegEnd : 0u), m);
     }
