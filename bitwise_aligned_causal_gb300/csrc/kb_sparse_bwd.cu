@@ -18,10 +18,11 @@
 // Roundings: P and dS go to the tensor core as bf16, with fp32 sums, but for dq
 // dS goes as two bf16 parts.  delta comes from the forward's bf16 o, and its
 // error is common to a row's keys: with dS's own rounding on top dq was 0.0027
-// to 0.0030 off the 64-bit formula (relative, root mean square), where rounding
-// the result to bf16 alone is 0.0017; with the second product it is at most
-// 0.0024, for 7 % of the kernel's time (455 us without it).  In dk the rows'
-// errors average out.
+// to 0.0031 off the 64-bit formula (relative, root mean square), where rounding
+// the result to bf16 alone is 0.0017; with the second product it is 0.0022 to
+// 0.0026, for 7 % of the kernel's time (455 us without it).  dk, whose rows'
+// errors are independent, is there with one part.  The rest is delta's, and an
+// exact delta would take a pass over the tiles of its own.
 //
 // Measured for 8192 rows of 32 heads, 16 blocks a row: delta 25 us, dq 488 us
 // (42,700 tiles: about 3,350 cycles a tile and SM; the dense kernel 3,200),
