@@ -148,3 +148,29 @@ def test_bad_device_arguments(kb):
     with pytest.raises(kb.KBError):
         kb.check_device_status()
     kb.check_device_status()
+
+
+@pytest.mark.parametrize("L", [1, 200])
+def test_on_two_streams_and_replayed(kb, L):
+    """Two calls at once have their own lists, and a captured one reads what its tensors hold at the replay."""
+    import torch
+
+    start, n = 2000, 5
+    q = [randn(670 + i, 1, 32, L, 128) for i in range(3)]
+    bx = kb.block_boxes(randn(675, 1, 8, start + L, 128), check=True)
+    want = [kb.select_blocks(x, bx, start, n, check=True) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in q]
+    got = [kb.select_blocks(x, bx, start, n, stream=s) for _ in range(4) for x, s in zip(q, streams)]
+    torch.cuda.synchronize()
+    kb.check_device_status()
+    assert all(torch.equal(x, want[i % 3]) for i, x in enumerate(got))
+    held, out = q[0].clone(), torch.zeros_like(want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kb.select_blocks(held, bx, start, n, out=out)
+    for x, y in zip(q, want):
+        held.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
