@@ -554,6 +554,10 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
           const int keep_pos = lane < rest ? queue[used + lane] : 0;
           __syncwarp();
           if (lane < rest) queue[lane] = keep_pos;
+          // at once, not only when the window adds positions: a window without any
+          // would let the next one move from where this move has written
+          used = 0;
+          queued = rest;
           uint32_t m = tb + lane < n_tiles ? __ldg(masks + tb + lane) : 0u;
           int at = __popc(m);
 #pragma unroll
@@ -563,14 +567,14 @@ kb_sparse_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_k, const __gr
           }
           const int total = __shfl_sync(0xffffffffu, at, 31);
           tb += 32;
-          if (total <= skip_rows) {                                    // nothing is queued yet
+          if (total <= skip_rows) {                                    // all of the other share's, or an empty window
             skip_rows -= total;
             continue;
           }
           at += rest - __popc(m);
           for (; m != 0u; m &= m - 1u) queue[at++] = (tb - 32 + lane) * kUnitRows + __ffs(m) - 1;
           __syncwarp();
-          used = skip_rows;
+          used = skip_rows;                                            // > 0 only where the share begins: rest is 0 there
           skip_rows = 0;
           queued = rest + total;
         }
