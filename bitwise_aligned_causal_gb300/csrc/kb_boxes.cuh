@@ -42,6 +42,18 @@ __device__ __forceinline__ float whole_sum(float q0, float q1, float q2, float q
   return __fsub_rn(__uint_as_float(u - 3u * kWholeBits), kWholeAt);        // modulo 2^32
 }
 __device__ __forceinline__ float saturated(float q) { return fminf(fmaxf(q, -kGridMax), kGridMax); }
+// Both bounds of a bf16 pair within the grid (127 * 2^93 is bf16 0x717E): infinities saturate, NaN becomes the least value.
+// The library's own boxes lie there; others must not make scores without a place in an order.
+__device__ __forceinline__ uint32_t saturated_bf16x2(uint32_t w) {
+  asm("max.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0xF17EF17Eu));
+  asm("min.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(0x717E717Eu));
+  return w;
+}
+// The same for a finished score: on the grid it is below 2^114 (128 * 127 * 127 * 2^93).
+__device__ __forceinline__ float saturated_score(float s) {
+  constexpr float kScoreMax = 1.329227995784916e36f;   // 2^120
+  return fminf(fmaxf(s, -kScoreMax), kScoreMax);
+}
 
 // The bounds that count in the score of two channels (bf16 pairs): the upper
 // one where n is positive, the lower one elsewhere; `up` has all bits of a

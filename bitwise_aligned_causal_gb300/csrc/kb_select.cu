@@ -54,7 +54,10 @@ struct CutSearch {
 };
 // Scores are whole multiples of a power of two and below 2^22 of them, so
 // halving ends within a few dozen steps of 22 bits, except around zero, where
-// floats go on down to 2^-149: 264 halvings at most.
+// floats go on down to 2^-149: 264 halvings at most, 271 between the bounds to
+// which scores of boxes that are no boxes saturate.  Scores must be finite:
+// with an infinite or NaN one the range has no middle, or fewer than `need`
+// scores reach any value, and a row's winners would not fill its places exactly.
 constexpr int kMaxTrials = 300;
 
 // Position of row i of sequence b, or -1 when the row does not exist; a bad
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
       for (int a = 0; a < kAtOnce; ++a) s[a] = __fadd_rn(s[a], __shfl_xor_sync(0xffffffffu, s[a], k));
 #pragma unroll
     for (int a = 0; a < kAtOnce; ++a)
-      if (c == 0 && j0 + a * kStep < m) sel_smem[j0 + a * kStep] = s[a];
+      if (c == 0 && j0 + a * kStep < m) sel_smem[j0 + a * kStep] = saturated_score(s[a]);
   }
   __syncthreads();
   // the cut, by all threads: thread t holds scores t, t + 512, ..
@@ -378,7 +381,8 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
     for (int k = 0; k < kBoxLoads; ++k) {
       const int e = threadIdx.x + k * Cfg::kThreads, r = e >> 5, c = e & 31;
       *reinterpret_cast<uint4*>(smem + Cfg::kBOff + (c >> 3) * Cfg::kBSlab + (r >> 3) * 1024 + (r & 7) * 128 +
-                                (((c & 7) ^ (r & 7)) << 4)) = val[k];
+                                (((c & 7) ^ (r & 7)) << 4)) =
+          make_uint4(saturated_bf16x2(val[k].x), saturated_bf16x2(val[k].y), saturated_bf16x2(val[k].z), saturated_bf16x2(val[k].w));
     }
   };
   {

@@ -366,7 +366,11 @@ kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, 
  * block.  Score: t_h = rint(q_h 2^(15-E)) of the group's four heads with their
  * common E (as for a box), u = sum_h t_h, n = rint(u 2^(7-E')) with E' that of
  * u, score = sum_d max(n_d upper_d, n_d lower_d).  Every step is exact, so the
- * choice does not depend on the batch, the split or the kernel.
+ * choice does not depend on the batch, the split or the kernel.  This holds for
+ * boxes from kb_attn_append and kb_attn_block_boxes; where `boxes` holds
+ * anything else (infinities, NaN, memory that was never written) a row's list
+ * is some n_select distinct blocks of its own, ascending, the kept ones among
+ * them.
  * keep_first + keep_last <= n_select <= KB_MAX_SELECT.  Out-of-range starts or
  * lens are found on the device (that sequence's rows are not written), as are
  * page indices (the row's list is then any list within its blocks); the next
