@@ -36,18 +36,20 @@ __device__ __forceinline__ void p_ds_pair(uint32_t s0, uint32_t s1, uint32_t dp0
 }
 
 // dS alone of the same pair, as the sum of two bf16 values each (16 bits of
-// mantissa), for a product that must not lose it to rounding.
+// mantissa), for a product that must not lose it to rounding.  The mask comes
+// last: a row that lists nothing has lse = -inf, and its q, dO and delta may be
+// anything (a padded row's NaN).
 template <bool kMask>
 __device__ __forceinline__ void ds_split_pair(uint32_t s0, uint32_t s1, uint32_t dp0, uint32_t dp1, float2 c2,
                                               float2 nl, float2 nd, bool m0, bool m1, uint32_t& high,
                                               uint32_t& low) {
   const float2 a = __ffma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), c2, nl);
-  float2 pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+  const float2 pp = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+  float2 d = __fmul2_rn(pp, __fadd2_rn(make_float2(__uint_as_float(dp0), __uint_as_float(dp1)), nd));
   if (kMask) {
-    if (m0) pp.x = 0.0f;
-    if (m1) pp.y = 0.0f;
+    if (m0) d.x = 0.0f;
+    if (m1) d.y = 0.0f;
   }
-  const float2 d = __fmul2_rn(pp, __fadd2_rn(make_float2(__uint_as_float(dp0), __uint_as_float(dp1)), nd));
   high = pack_bf16x2(d.x, d.y);
   const float2 rest = __fadd2_rn(d, make_float2(-__uint_as_float(high << 16), -__uint_as_float(high & 0xFFFF0000u)));
   low = pack_bf16x2(rest.x, rest.y);

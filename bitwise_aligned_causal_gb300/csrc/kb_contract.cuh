@@ -207,7 +207,9 @@ __device__ __forceinline__ float row_softmax_tile(const uint32_t (&s)[128], int 
 // exponent takes 0 in its place, since -inf + inf has no value.  Without, all
 // 128 keys of the tile are the row's or none is, and a row that is off takes
 // the factor 0 and the offset -inf instead of c and -mc: 2^(s 0 - inf) = 0
-// costs nothing per key (scores are finite).
+// costs nothing per key.  A score that is not finite (a padded row's NaN query,
+// an overflow against a block that only neighbours listed) gives NaN that way,
+// which l then shows: the caller takes l back and sets p to zero.
 template <bool kMasked, bool kMaybeNone = false>
 __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, int n_valid, RowState& st,
                                                        uint32_t (&p)[16], bool on = true) {

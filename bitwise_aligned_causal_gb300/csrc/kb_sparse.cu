@@ -451,6 +451,7 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         uint32_t pkA[16], pkB[16];
         float aA, aB;
         const bool onA = (entry.y >> r0) & 1u, onB = (entry.y >> (r0 + 8)) & 1u;
+        const float lA = sA.l, lB = sB.l;
         if (!diag) {
           aA = row_softmax_tile_quad<false, true>(xA, u4, kTileKeys, sA, pkA, onA);
           aB = row_softmax_tile_quad<false, true>(xB, u4, kTileKeys, sB, pkB, onB);
@@ -460,6 +461,18 @@ kb_sparse_tile_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         }
         if (freshA) aA = 1.0f;
         if (freshB) aB = 1.0f;
+        // a row that did not list the tile, but whose sum moved: its scores were
+        // not finite, and its weights are zero all the same
+        const bool moved_off = (!onA && !(sA.l == lA)) || (!onB && !(sB.l == lB));
+        if (__any_sync(0xffffffffu, moved_off)) {
+          if (!onA) sA.l = lA;
+          if (!onB) sB.l = lB;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            pkA[r] = onA ? pkA[r] : 0u;
+            pkB[r] = onB ? pkB[r] : 0u;
+          }
+        }
         if (!seg_start && __any_sync(0xffffffffu, aA != 1.0f || aB != 1.0f)) {
           ok = mbar_wait(bar(Cfg::kBarPDone + ((T - 1) & 1)), ((T - 1) >> 1) & 1, abort_flag, args.err, kDevTimeoutMma);
           ok = __all_sync(0xffffffffu, ok);

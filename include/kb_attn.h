@@ -393,9 +393,10 @@ kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, i
  * A row's result is the contract's walk over its listed blocks alone, with the
  * contract's segments, so it has the same bits in a chunk of any split and as
  * a new token, and equals the dense entry points' bits when its list holds
- * every block.  A row that lists nothing is zero (log-sum-exp -inf).  K and V
- * of the cache's visible rows must be finite: a neighbour's listed block is
- * multiplied by weights of exactly zero.
+ * every block.  A row that lists nothing is zero (log-sum-exp -inf), whatever
+ * its q holds.  In a chunk or a whole sequence V of the cache's visible rows must
+ * be finite: 32 neighbouring positions are computed together, and V of a block
+ * that only a neighbour listed is multiplied by weights of exactly zero.
  *
  * kb_attn_sparse_chunk: rows at start..start+L-1 of every sequence, or (starts
  * != NULL) at starts[b].., lens[b] of them (L when lens is NULL), against a
@@ -428,7 +429,8 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
  * Backward of kb_attn_sparse_prefill_lse: as kb_attn_backward, over the listed
  * keys (the lists themselves take no gradient).  o and lse from the forward
  * with the same q, k, v and blocks; delta [B, Hq, S] fp32 is an output.  A row
- * that lists nothing has dq = 0, a block that no row lists dk = dv = 0.
+ * that lists nothing has dq = 0 and no part in dk and dv, whatever its q and
+ * dout hold; a block that no row lists has dk = dv = 0.  K and V are finite.
  * Every sum has one order: repeated calls give identical bits, and a
  * sequence's gradients do not depend on the batch or on n_select.  workspace:
  * 256-byte aligned scratch of kb_attn_sparse_backward_workspace_bytes(B, Hkv,
