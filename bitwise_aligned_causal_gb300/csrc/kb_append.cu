@@ -25,8 +25,10 @@
 // holds eight planes of a row, so the table's 64 bytes are fetched once for
 // the five or six rows it turns.  Measured: the rotation of 32 heads x 16384
 // positions 43.9 us (6.3 TB/s of bytes read and written; HBM copies at 6.8);
-// an append of four ragged prompts of up to 4096, 39 to 50 us from GPU to GPU
-// (5.5 to 7.0 TB/s), of one token of 16 sequences 5.0 us, a launch's latency.
+// an append of four ragged prompts of up to 4096, 39 to 51 us from GPU to GPU
+// (274 MB read and written: 5.3 TB/s at 51; above the copy rate at 39, because
+// a good part of the writes is still in L2 when the kernel ends), of one token
+// of 16 sequences 5.0 us, a launch's latency.
 #include <algorithm>
 
 #include "kb_boxes.cuh"

@@ -75,7 +75,7 @@ __device__ __forceinline__ int row_position(const SelectArgs& a, int b, int i) {
   return i < len ? start + i : -1;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));       // NaN goes through
   return r;
@@ -106,10 +106,23 @@ __device__ __forceinline__ const __nv_bfloat16* box_of(const SelectArgs& a, int 
 // channels of both bounds each), so a warp has twelve blocks of 512 bytes
 // in flight, the first of them while the query is still on its way to whole
 // numbers.  For one token the boxes are read once and nothing else counts:
-// 16 sequences of 64K (33.6 MB) take 12.6 us, 128 CTAs whose loads, search and
-// start follow one another.
+// 16 sequences of 64K (33.6 MB) take 13.0 to 13.7 us, 128 CTAs whose loads,
+// search and start follow one another.
+//
+// It also runs for longer calls that the tile kernel does not take (more than
+// 256 blocks to choose from and more than 32 of them by score): there every row
+// reads its boxes again, 872 us for 2048 rows at 64K and 35 blocks a row, where
+// the tile kernel takes 136 us for 34.
 constexpr int kSelectRowThreads = 512;
-constexpr int kSelectRowMax = 16;               // query rows per sequence up to which this kernel runs
+// Query rows per sequence up to which this kernel runs, whatever the batch and
+// the number of blocks.  Measured at 16 blocks a row, this kernel against the
+// tile kernel (a replayed graph, L2 flushed): B = 1 and 64 blocks, 16 rows 13.5
+// us against 21.6, 64 rows 27.8 against 21.6; 512 blocks, 16 rows 15.5 against
+// 116, 64 rows 40 against 119; B = 16 and 64 blocks, 1 row 13.5 against 21.6, 4
+// rows 27.8 against 21.6, 16 rows 77 against 23.6; 512 blocks, 12 rows 95 against
+// 116, 16 rows 120 against 114.  One number meets the last of these; a batch of
+// short contexts pays from 4 rows on, one long context not before 64.
+constexpr int kSelectRowMax = 16;
 
 __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(const SelectArgs args) {
   extern __shared__ float sel_smem[];
@@ -291,7 +304,7 @@ __global__ void __launch_bounds__(kSelectRowThreads, 1) kb_select_row_kernel(con
 // shared memory.
 // Bound: q is read once (1 KB a row and KV head); 96 KB of shared memory and
 // half of TMEM let two CTAs share an SM, so one loads while the other
-// searches.  A 16K prompt (134 MB of q) takes 90 us, 1.6 TB/s: rounding q to
+// searches.  A 16K prompt (134 MB of q) takes 92 us, 1.5 TB/s: rounding q to
 // whole numbers and the search are instructions (56 % of issue slots), and a
 // tile's slowest row holds up its CTA.  Sixteen rows per warp with register
 // products of 16 x 8 in place of tcgen05, so that no warp waits for another,
@@ -425,7 +438,7 @@ __global__ void __launch_bounds__(SelectTileCfg::kThreads, 2) kb_select_tile_ker
         for (int h = 0; h < kGroup; ++h) {
           const uint32_t w[4] = {x[a][h].x, x[a][h].y, x[a][h].z, x[a][h].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = bf16x2_max(top, w[e] & 0x7FFF7FFFu);
+          for (int e = 0; e < 4; ++e) top = bf16x2_max_nan(top, w[e] & 0x7FFF7FFFu);
         }
         uint32_t top32 = max(top << 16, top & 0xFFFF0000u);  // as fp32 bits, whose order is that of the magnitudes
 #pragma unroll
@@ -764,9 +777,9 @@ cudaError_t launch_select(const SelectArgs& a, int device, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured[device] = true;
   }
-  // A CTA of 128 rows pays from about 16 rows per sequence on.  Its lists of
-  // earlier passes hold 32 winners, so longer ones stay with it only while
-  // all blocks fit one pass.
+  // A CTA of 128 rows pays from some number of rows per sequence on (measured
+  // at kSelectRowMax).  Its lists of earlier passes hold 32 winners, so longer
+  // ones stay with it only while all blocks fit one pass.
   const bool several = a.max_blocks - a.keep_last > Cfg::kPass;
   if (a.L > kSelectRowMax && (!several || a.n - a.keep_first - a.keep_last <= Cfg::kMaxListed)) {
     const int n_tiles = a.starts != nullptr ? (a.L + kTileKeys - 2) / kTileKeys + 1

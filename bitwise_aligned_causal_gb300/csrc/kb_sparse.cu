@@ -31,8 +31,8 @@
 // softmax warps read a tile's scores at once and release them before they
 // compute, so Q K^T of the next tile runs under the softmax of this one.
 //
-// Measured: 2048 rows at the end of 64K keys, 16 blocks a row (47 a unit) 234
-// us; 8192 rows, 16 a row (21 a unit) 334 us.  That is about 2,300 cycles a tile
+// Measured: 2048 rows at the end of 64K keys, 16 blocks a row (47 a unit) 235
+// us; 8192 rows, 16 a row (21 a unit) 337 us.  That is about 2,300 cycles a tile
 // and SM, against 1,750 of the dense kernel, whose segments are eight tiles
 // long: the softmax warps' chain is the bound (two warps per SM quarter, 47 %
 // of issue slots, tensor pipe 44 to 50 % busy).  Of the chunk with its plan (248

@@ -75,8 +75,9 @@ __device__ __forceinline__ const uint2* unit_walk(const SparseArgs& a, int u) {
 // and TMEM already set up, where that leaves SMs idle for at most 1/`part` of the
 // units' time; else one per unit, as SMs come free.  Forward (part 16): 13.5
 // units per SM 338 us against 352 with a CTA per unit, 9.9 117 against 135, 3.4
-// 250 against 234.  dq (part 32), whose start costs less, before dS went in two
-// parts: 479 against 461, 138 against 154.
+// 250 against 234.  dq (part 32), whose start costs less, by the whole gradient:
+// 13.5 units per SM (8192 rows) 1304 us against 1222, 9.9 (3 x 1999) 358 against
+// 379, 8.0 (4864) 582 against 579.
 inline int unit_grid(const SparseArgs& a, int sm_count, int part) {
   const long long idle = (static_cast<long long>(a.n_units) + sm_count - 1) / sm_count * sm_count - a.n_units;
   return a.n_units > sm_count && idle * part <= a.n_units ? sm_count : a.n_units;

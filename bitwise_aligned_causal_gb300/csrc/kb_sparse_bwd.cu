@@ -16,18 +16,23 @@
 // the second adds both halves; atomics count rows and draw tickets, no more.
 //
 // Roundings: P and dS go to the tensor core as bf16, with fp32 sums, but for dq
-// dS goes as two bf16 parts.  delta comes from the forward's bf16 o, and its
-// error is common to a row's keys: with dS's own rounding on top dq was 0.0027
-// to 0.0031 off the 64-bit formula (relative, root mean square), where rounding
-// the result to bf16 alone is 0.0017; with the second product it is 0.0022 to
-// 0.0026, for 7 % of the kernel's time (455 us without it).  dk, whose rows'
-// errors are independent, is there with one part.  The rest is delta's, and an
-// exact delta would take a pass over the tiles of its own.
+// dS goes as two bf16 parts, for 7 % of the kernel's time.  Relative errors
+// against the 64-bit formulas, root mean square, of 1999 rows with 7 blocks;
+// rounding the result to bf16 alone is 0.0017:
+//   dq 0.0023 (replayed in 64 bits with one part 0.0031).  What is left is
+//     delta's, which comes from the forward's bf16 o and whose error is common to
+//     a row's keys: 0.0020 with o in two bf16 parts (another tensor between
+//     forward and backward, not made), 0.0017 with an exact delta.
+//   dk 0.0024 to 0.0029.  What is left is the one rounding of its dS: replayed
+//     0.0024 to 0.0027, with an exact delta 0.0024 to 0.0025, with dS in two parts
+//     0.0018 (a second product a step, not made).
+//   dv 0.0023, the one rounding of P, as in the forward, whose bits are the
+//     dense contract's.
 //
-// Measured for 8192 rows of 32 heads, 16 blocks a row: delta 25 us, dq 488 us
-// (42,700 tiles: about 3,350 cycles a tile and SM; the dense kernel 3,200),
-// dk/dv 459 us (201 steps an SM: 4,400 cycles a step, the dense kernel's pace),
-// plan and order 15 us.
+// Measured for 8192 rows of 32 heads, 16 blocks a row, in the launch list of
+// one pass: delta 23 us, dq 502 us (42,700 tiles: about 3,400 cycles a tile and
+// SM; the dense kernel 3,200), dk/dv 452 us (201 steps an SM: 4,400 cycles a
+// step, the dense kernel's pace), plan and order 17 us.
 #include <type_traits>
 
 #include "kb_bwd.cuh"
@@ -378,7 +383,7 @@ kb_sparse_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
 // TMA box per position (four heads, 512 bytes) took 11,000 cycles a step, and
 // whole units (all 32 rows of a unit of which some listed the block) 1.5 times
 // the steps.  At S = 8192 with 16 blocks per row, without shared blocks and in
-// order of the blocks: 565 us, against 1127 and 688 us; with both 459 us.
+// order of the blocks: 565 us, against 1127 and 688 us; with both 452 us.
 //
 // Blocks differ in how many rows list them (the first block is kept by all),
 // and one CTA for the longest would hold up the launch.  So a block of

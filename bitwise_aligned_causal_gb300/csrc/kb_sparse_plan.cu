@@ -6,7 +6,7 @@
 // may come in any order and name a block twice; blocks past a row's own are
 // dropped, since none of their keys is visible to it.  The lists are read
 // once (4 bytes an entry) and the walk written once (8 bytes): 6.6 us for 512
-// units and 512 blocks, 10.8 us for 2048 units and 64, beside 234 and 334 us of
+// units and 512 blocks, 10.8 us for 2048 units and 64, beside 235 and 337 us of
 // attention; bound by the latency of its steps.
 #include "kb_sparse.cuh"
 

@@ -366,7 +366,9 @@ kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, 
  * block.  Score: t_h = rint(q_h 2^(15-E)) of the group's four heads with their
  * common E (as for a box), u = sum_h t_h, n = rint(u 2^(7-E')) with E' that of
  * u, score = sum_d max(n_d upper_d, n_d lower_d).  Every step is exact, so the
- * choice does not depend on the batch, the split or the kernel.  This holds for
+ * choice does not depend on the batch, the split or the kernel.  More than 32
+ * blocks by score out of more than 256 are chosen row by row, about six times
+ * slower than 32.  The choice is defined for
  * boxes from kb_attn_append and kb_attn_block_boxes; where `boxes` holds
  * anything else (infinities, NaN, memory that was never written) a row's list
  * is some n_select distinct blocks of its own, ascending, the kept ones among
@@ -434,8 +436,9 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
  * Every sum has one order: repeated calls give identical bits, and a
  * sequence's gradients do not depend on the batch or on n_select.  workspace:
  * 256-byte aligned scratch of kb_attn_sparse_backward_workspace_bytes(B, Hkv,
- * S, n_select), which from S = 4065 on includes 256 KB per KV head for every
- * block with 4065 positions or more from its first on.
+ * S, n_select).  Per KV head of a sequence that is S^2 / 1024 bytes of row masks
+ * and, from S = 4065 on, 256 KB for every block with 4065 positions or more from
+ * its first on: at S = 131072, B = 1 and 8 KV heads 0.13 GB and 2.1 GB.
  */
 size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select);
 kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
