@@ -34,71 +34,11 @@
 #include "kb_boxes.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
+#include "kb_turn.cuh"
 
 namespace kb {
 
 namespace {
-
-constexpr int kPlanesPerLane = 8;
-constexpr int kRowsPerWarp = 4;                 // eight lanes per row, two 16-byte chunks each
-
-struct Turn {
-  float2 cs[kPlanesPerLane];                    // (cos, sin) of the lane's planes
-};
-
-// The two 16-byte chunks of a row that lane u of its eight holds, and whether
-// they are turned: the pairs of planes 8u..8u+7, or (beyond rot_dim) two
-// chunks that pass unchanged.
-struct LaneChunks {
-  int c0, c1;
-  bool turns;
-};
-__device__ __forceinline__ LaneChunks lane_chunks(int u, int rot_dim, bool interleaved) {
-  const int m = rot_dim >> 4;                   // chunks of one half
-  if (interleaved || u >= m) return LaneChunks{2 * u, 2 * u + 1, u < m};
-  return LaneChunks{u, u + m, true};
-}
-
-__device__ __forceinline__ void load_turn(Turn& t, const float* table, long long pos, int rot_dim, int u, bool inverse) {
-  const float4* src = reinterpret_cast<const float4*>(table + pos * rot_dim) + 4 * u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(src + i);
-    t.cs[2 * i] = make_float2(v.x, inverse ? -v.y : v.y);
-    t.cs[2 * i + 1] = make_float2(v.z, inverse ? -v.w : v.w);
-  }
-}
-
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ float turn_a(float a, float b, float2 cs) {
-  return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-}
-__device__ __forceinline__ float turn_b(float a, float b, float2 cs) {
-  return __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
-}
-
-// Turn the lane's two chunks in place.
-__device__ __forceinline__ void turn_chunks(uint4& x, uint4& y, const Turn& t, bool interleaved) {
-  uint32_t* a = reinterpret_cast<uint32_t*>(&x);
-  uint32_t* b = reinterpret_cast<uint32_t*>(&y);
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = lo_of(a[i]), a1 = hi_of(a[i]), b0 = lo_of(b[i]), b1 = hi_of(b[i]);
-      a[i] = pack_bf16x2(turn_a(a0, a1, t.cs[i]), turn_b(a0, a1, t.cs[i]));
-      b[i] = pack_bf16x2(turn_a(b0, b1, t.cs[4 + i]), turn_b(b0, b1, t.cs[4 + i]));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = lo_of(a[i]), a1 = hi_of(a[i]), b0 = lo_of(b[i]), b1 = hi_of(b[i]);
-      a[i] = pack_bf16x2(turn_a(a0, b0, t.cs[2 * i]), turn_a(a1, b1, t.cs[2 * i + 1]));
-      b[i] = pack_bf16x2(turn_b(a0, b0, t.cs[2 * i]), turn_b(a1, b1, t.cs[2 * i + 1]));
-    }
-  }
-}
 
 __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -135,7 +75,10 @@ cudaError_t launch_rope_table(float* table, int n_pos, int rot_dim, const double
 
 // ---------------------------------------------------------------- rotation
 
-// A warp turns four heads of four consecutive positions.
+// A warp turns four heads of four consecutive rows.  kAxes: a row's planes
+// turn by the positions that the call gives on each axis; a row with a
+// position outside the table is recorded and left unwritten.
+template <bool kAxes>
 __global__ void __launch_bounds__(256) kb_rope_kernel(const RopeArgs args) {
   if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) return;
   const int lane = threadIdx.x & 31, u = lane & 7;
@@ -148,6 +91,20 @@ __global__ void __launch_bounds__(256) kb_rope_kernel(const RopeArgs args) {
   const int h0 = (rem % quads) * 4, i = (rem / quads) * kRowsPerWarp + (lane >> 3);
   if (i >= args.L) return;
   const LaneChunks lc = lane_chunks(u, args.rot_dim, args.interleaved);
+  int pos[kMaxAxes] = {0, 0, 0, 0};
+  if constexpr (kAxes) {
+    bool in_table = true;
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a)
+      if (a < args.n_axes) {
+        pos[a] = __ldg(args.positions + (static_cast<size_t>(a) * args.B + b) * args.L + i);
+        in_table = in_table && pos[a] >= 0 && pos[a] < args.n_pos;
+      }
+    if (!in_table) {
+      atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
+      return;
+    }
+  }
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(args.x) + b * args.sb + h0 * args.sh +
                                                     i * args.sl);
   const long long hstep = args.sh / 8;
@@ -161,7 +118,8 @@ __global__ void __launch_bounds__(256) kb_rope_kernel(const RopeArgs args) {
     }
   if (lc.turns) {
     Turn t;
-    load_turn(t, args.table, static_cast<long long>(args.start) + i, args.rot_dim, u, args.inverse);
+    if constexpr (kAxes) load_turn_axes(t, args.table, pos, args.plane_axes[u], args.rot_dim, u, args.inverse);
+    else load_turn(t, args.table, static_cast<long long>(args.start) + i, args.rot_dim, u, args.inverse);
 #pragma unroll
     for (int h = 0; h < 4; ++h)
       if (h < nh) turn_chunks(x[h], y[h], t, args.interleaved);
@@ -179,7 +137,9 @@ __global__ void __launch_bounds__(256) kb_rope_kernel(const RopeArgs args) {
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const long long warps = static_cast<long long>(a.B) * ((a.H + 3) / 4) * ((a.L + kRowsPerWarp - 1) / kRowsPerWarp);
-  kb_rope_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(a);
+  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
+  if (a.positions != nullptr) kb_rope_kernel<true><<<grid, 256, 0, s>>>(a);
+  else kb_rope_kernel<false><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -282,6 +282,13 @@ __device__ __forceinline__ void normalise32(const uint32_t (&o)[32], float inv_l
 
 __device__ __forceinline__ float row_inv_l(const RowState& st) { return __frcp_rn(st.l); }
 
+// Natural-log log-sum-exp of the row's scaled scores: the weights are
+// 2^(s c - mc), so log2 sum_j 2^(s_j c) = mc + log2(l).
+__device__ __forceinline__ float row_lse(const RowState& st) {
+  constexpr float kLn2 = 0.69314718055994531f;
+  return __fmul_rn(__fadd_rn(st.mc, log2f(st.l)), kLn2);
+}
+
 // C5 fold of a segment's (m, mc, l, O) into the accumulated (m, mc, l, O) of
 // the segments before it: both are brought to the larger reference max M,
 // the side already at M by exactly 1, the other by 2^(m c - M c):

@@ -48,6 +48,7 @@
 //    TMEM.
 //  - workspace mode (the *_seg entry points): one CTA per segment writes its
 //    partial to a caller workspace, which kb_seg_fold_kernel folds.
+#include "kb_cache8.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
 
@@ -55,16 +56,31 @@ namespace kb {
 
 // kSparse with one S buffer is the lean shape: half of TMEM and of shared
 // memory, so that two CTAs share an SM.
-template <bool kWide, int kNumSBufs, bool kSparse = false>
+// k8: the cache is held in 8 bits, and four warps per ring take the TMA
+// producer's place: they load a tile's bytes into registers (a tile ahead, so
+// that the loads of one are in flight while the last is written), turn them
+// into the bf16 values they stand for and write those to the ring in the
+// swizzled layout that TMA gives.  Staging the bytes in shared memory instead
+// would add their write and read to the 160 KB that a pair of tiles moves
+// through it (values in, MMA operands out) and make that the bound: 1750
+// cycles of 128 B against the 1390 in which HBM brings a pair to each SM.
+// The rest of the kernel is the same, and so are the bits.
+template <bool kWide, int kNumSBufs, bool kSparse = false, bool k8 = false>
 struct PackedCfg {
   static constexpr bool kLean = kSparse && kNumSBufs == 1;
   static constexpr int kSoftmaxWarps = kWide ? 4 : 1;
-  static constexpr int kKProdWarp = kWide ? 4 : 1;
-  static constexpr int kQkWarp = kWide ? 5 : 2;             // TMEM allocator + Q K^T issuer
-  static constexpr int kVProdWarp = kWide ? 6 : 3;
-  static constexpr int kPvWarp = kWide ? 7 : 5;
+  static constexpr int kProdWarps = k8 ? 4 : 1;             // per ring
+  static constexpr int kKProdWarp = k8 ? (kWide ? 8 : 4) : kWide ? 4 : 1;   // (8 bits, narrow: warps 3, 5, 6, 7)
+  static constexpr int kQkWarp = k8 ? (kWide ? 4 : 1) : kWide ? 5 : 2;      // TMEM allocator + Q K^T issuer
+  static constexpr int kVProdWarp = k8 ? kKProdWarp + 4 : kWide ? 6 : 3;
+  static constexpr int kPvWarp = k8 ? (kWide ? 5 : 2) : kWide ? 7 : 5;
   static constexpr int kFoldWarp = kWide ? -1 : 4;          // narrow: folds and epilogue
-  static constexpr int kThreads = (kWide ? 8 : 6) * 32;
+  static constexpr int kThreads = (k8 ? (kWide ? 16 : 12) : kWide ? 8 : 6) * 32;
+  static constexpr bool is_ring_warp(int w) { return k8 && (kWide ? w >= 8 : w == 3 || w >= 5); }
+  // wide, 8 bits: registers per thread after setmaxnreg, of a launch with 512
+  // x 128 (softmax, issuers and two idle warps, the two rings)
+  static constexpr uint32_t kSoftmaxRegs = 232, kIssuerRegs = 64, kRingRegs = 104;
+  static_assert(kSoftmaxRegs + kIssuerRegs + 2 * kRingRegs <= 512, "register split above the launch's registers");
   static constexpr int kKStages = kLean ? 2 : 3;
   static constexpr int kVStages = kLean ? 1 : 3;
   static constexpr int kQRows = kWide ? 128 : 8;
@@ -196,15 +212,81 @@ __device__ __forceinline__ int2 build_walk(const int* list, int n_select, int ow
   return make_int2(n, ns);
 }
 
+// The four warps of a ring (K or V) whose cache is held in 8 bits: key tiles
+// j0 .. j0 + nt - 1 of sequence b, KV head g.  Eight threads take a row (16
+// bytes each), sixteen rows a pass.  Rows from seq_kv on are not read and are
+// zero in the ring.  The upper half of a row goes out with its two chunks in
+// the other order: so the eight threads of a row write to all eight 16-byte
+// columns of the swizzle atom at once.
+template <typename Cfg>
+__device__ __forceinline__ void fill_ring8(const PackedArgs& args, bool is_v, uint8_t* ring, int b, int g, int j0, int nt,
+                                           int seq_kv, uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag) {
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  const int t = 32 * max(warp - (is_v ? Cfg::kVProdWarp : Cfg::kKProdWarp), 0) + static_cast<int>(threadIdx.x & 31);   // (warp 3: the first)
+  const int col = t & 7, row0 = t >> 3;
+  const uint8_t* bytes = is_v ? args.v8 : args.k8;
+  const int8_t* exps = is_v ? args.v_exp : args.k_exp;
+  const int blocks = (args.plane_rows + kTileKeys - 1) / kTileKeys;
+  const int stages = is_v ? Cfg::kVStages : Cfg::kKStages;
+  const uint32_t swap = col >= 4 ? 1u : 0u;
+  // chunks 2 col and 2 col + 1 of the bf16 row, in slab col / 4
+  uint8_t* dst0 = ring + (col >> 2) * kSlabBytes;
+  const uint32_t c0 = ((2 * (col & 3) + swap) ^ (row0 & 7)) << 4, c1 = ((2 * (col & 3) + (swap ^ 1u)) ^ (row0 & 7)) << 4;
+
+  struct Tile {
+    uint4 w[8];
+    int n, e;                                              // rows of the sequence, exponent
+  };
+  auto load = [&](int jj, Tile& x) {
+    int row = 0, plane = 0;
+    const bool in_pool = kv_tile_coords(args, b, g, j0 + jj, row, plane);
+    x.n = in_pool ? min(kTileKeys, seq_kv - (j0 + jj) * kTileKeys) : 0;
+    x.e = x.n > 0 ? exps[static_cast<size_t>(plane) * blocks + row / kTileKeys] : 0;
+    const uint8_t* src = bytes + (static_cast<size_t>(plane) * args.plane_rows + row + row0) * kHeadDim + col * 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (row0 + 16 * i < x.n) x.w[i] = ld_stream16(src + static_cast<size_t>(i) * 16 * kHeadDim);
+  };
+  auto store = [&](int jj, const Tile& x) {
+    const int slot = jj % stages;
+    if (jj >= stages) {
+      const bool ok = mbar_wait(empty0 + 8u * slot, (jj / stages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+    const Scale8 sc = scale8(x.e);
+    uint8_t* dst = dst0 + slot * kTileBytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+      if (row0 + 16 * i < x.n) values8x16(x.w[i], sc, lo, hi);
+      uint8_t* r = dst + ((row0 + 16 * i) >> 3) * 1024 + (row0 & 7) * 128;
+      *reinterpret_cast<uint4*>(r + c0) = swap ? hi : lo;
+      *reinterpret_cast<uint4*>(r + c1) = swap ? lo : hi;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(full0 + 8u * slot);
+    return true;
+  };
+  Tile x, y;
+  load(0, x);
+  if (!__all_sync(0xffffffffu, no_error(args.err, abort_flag))) return;
+  for (int jj = 0; jj < nt; jj += 2) {
+    if (jj + 1 < nt) load(jj + 1, y);
+    if (!store(jj, x)) return;
+    if (jj + 2 < nt) load(jj + 2, x);
+    if (jj + 1 < nt && !store(jj + 1, y)) return;
+  }
+}
+
 // kSparse (narrow, one query row per head): the row's key tiles are those of
 // its block list instead of 0..floor(p/128); its segments are the contract's
 // segments of which it lists a tile.
-template <bool kWide, int kNumSBufs, bool kSparse>
-__global__ void __launch_bounds__(PackedCfg<kWide, kNumSBufs, kSparse>::kThreads, 1)
+template <bool kWide, int kNumSBufs, bool kSparse, bool k8>
+__global__ void __launch_bounds__(PackedCfg<kWide, kNumSBufs, kSparse, k8>::kThreads, 1)
 kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const PackedArgs args) {
-  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse>;
-  static_assert(!kSparse || (!kWide && Cfg::kThreads > KB_MAX_SELECT), "sparse walks are narrow");
+  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse, k8>;
+  static_assert(!kSparse || (!kWide && !k8 && Cfg::kThreads > KB_MAX_SELECT), "sparse walks are narrow, over bf16 caches");
   static_assert(!Cfg::kLean || 2 * Cfg::kSmemBytes <= 226u * 1024u, "two lean CTAs share an SM");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -301,7 +383,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   // sparse: is step jj the first or the last of its segment?
   auto starts_seg = [&](int jj) { return jj == 0 || walk[j0 + jj - 1] / kSegTiles != walk[j0 + jj] / kSegTiles; };
   auto ends_seg = [&](int jj) { return jj == nt - 1 || walk[j0 + jj + 1] / kSegTiles != walk[j0 + jj] / kSegTiles; };
-  const bool zero_tail = (args.block_table != nullptr) || (args.ctx_lens != nullptr) || (args.starts != nullptr);
+  // (a ring filled from bytes has zeros behind the sequence already)
+  const bool zero_tail = !k8 && ((args.block_table != nullptr) || (args.ctx_lens != nullptr) || (args.starts != nullptr));
   const int tail_from = seq_kv - (n_kv - 1) * kTileKeys;   // first V row of the last tile past the sequence
   const uint32_t slot_bytes = static_cast<uint32_t>(n_rows) * kPartFloats * 4u;
   // fold mode, C > 1: the other CTAs' segments (from s_first on) reach the
@@ -329,6 +412,9 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       // (the others' bytes complete its transaction count)
       if (i == Cfg::kBarPart && C > 1) count = static_cast<uint32_t>(push ? 32 * C : 32);
       if (i == Cfg::kBarQReady) count = static_cast<uint32_t>(Cfg::kQLoaders);
+      if (k8 && ((i >= Cfg::kBarKFull && i < Cfg::kBarKFull + Cfg::kKStages) ||
+                 (i >= Cfg::kBarVFull && i < Cfg::kBarVFull + Cfg::kVStages)))
+        count = 32u * Cfg::kProdWarps;
       mbar_init(bar(i), count);
     }
     misc[1] = 0u;
@@ -377,7 +463,92 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     mbar_arrive(bar(Cfg::kBarQReady));
   }
 
-  if (warp == Cfg::kKProdWarp || warp == Cfg::kVProdWarp) {
+  auto issue_scores = [&]() {
+    // -------------------------------------------------------- Q K^T issuer
+    // S(j) goes to buffer j%n once K(j) has landed and P V(j-n) has read
+    // P(j-n) out of that buffer.
+    if (lane == 0 && run) {
+      const uint32_t q_saddr = sbase + Cfg::kQOff;
+      bool ok = no_error(args.err, abort_flag) &&
+                mbar_wait(bar(Cfg::kBarQReady), 0, abort_flag, args.err, kDevTimeoutTma);
+      for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
+        const int slot = j % Cfg::kKStages;
+        const int sb = j % Cfg::kSBufs;
+        ok = mbar_wait(bar(Cfg::kBarKFull + slot), (j / Cfg::kKStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+        if (ok && j >= Cfg::kSBufs)
+          ok = mbar_wait(bar(Cfg::kBarOFull + sb), ((j - Cfg::kSBufs) / Cfg::kSBufs) & 1, abort_flag, args.err,
+                         kDevTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+        issue_qk(tmem_base + sb * 128u, q_saddr, Cfg::kQSbo, Cfg::kQSlab, sbase + Cfg::kKOff + slot * kTileBytes);
+        tc_commit(bar(Cfg::kBarSFull + sb));
+        tc_commit(bar(Cfg::kBarKEmpty + slot));
+      }
+      if (!ok) {
+        tc_commit(bar(Cfg::kBarDrain));
+        packed_drain_wait(bar(Cfg::kBarDrain), 0);
+      }
+    }
+    __syncwarp();
+    if (C > 1) {
+      cluster_wait();
+      if (pull_sync) cluster_sync();
+    }
+  };
+  auto issue_outputs = [&]() {
+    // ---------------------------------------------------------- P V issuer
+    // The first P V of every segment clears O; after the CTA's first segment
+    // it waits until the previous segment's O has been read.
+    if (lane == 0 && run) {
+      int F = 0;                                            // segments started
+      int js = 0;                                           // tile index within its segment (j0 starts one)
+      bool ok = no_error(args.err, abort_flag);
+      for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
+        const int slot = j % Cfg::kVStages;
+        const int sb = j % Cfg::kSBufs;
+        if (zero_tail && has_last && j == nt - 1)
+          ok = mbar_wait(bar(Cfg::kBarVReady), 0, abort_flag, args.err, kDevTimeoutTma);
+        else
+          ok = mbar_wait(bar(Cfg::kBarVFull + slot), (j / Cfg::kVStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+        const bool first = kSparse ? starts_seg(j) : (js == 0);
+        if (++js == seg_len) js = 0;
+        if (ok && first && F > 0)
+          ok = mbar_wait(bar(Cfg::kBarORead), (F - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+        if (ok)
+          ok = mbar_wait_hint(bar(Cfg::kBarPFull + sb), (j / Cfg::kSBufs) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(tmem_base + Cfg::kOCol, tmem_base + sb * 128u, sbase + Cfg::kVOff + slot * kTileBytes, first);
+        tc_commit(bar(Cfg::kBarOFull + sb));
+        tc_commit(bar(Cfg::kBarVEmpty + slot));
+        if (first) ++F;
+      }
+      if (!ok) {
+        tc_commit(bar(Cfg::kBarDrain + 1));
+        packed_drain_wait(bar(Cfg::kBarDrain + 1), 0);
+      }
+    }
+    __syncwarp();
+    if (C > 1) {
+      cluster_wait();
+      if (pull_sync) cluster_sync();
+    }
+  };
+
+  if (Cfg::is_ring_warp(warp)) {
+    // ------------------------------------------------- producers from bytes
+    if constexpr (k8) {
+      if constexpr (kWide) regs_decrease<Cfg::kRingRegs>();
+      const bool is_v = warp >= Cfg::kVProdWarp;
+      if (run) fill_ring8<Cfg>(args, is_v, smem + (is_v ? Cfg::kVOff : Cfg::kKOff), b, g, j0, nt, seq_kv,
+                               bar(is_v ? Cfg::kBarVFull : Cfg::kBarKFull), bar(is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty),
+                               abort_flag);
+    }
+    if (C > 1) {
+      cluster_wait();
+      if (pull_sync) cluster_sync();
+    }
+  } else if (!k8 && (warp == Cfg::kKProdWarp || warp == Cfg::kVProdWarp)) {
     // ----------------------------------------------------------- producers
     // One warp per ring: a slot is refilled once its tile's product (Q K^T
     // for K, P V for V) has finished.
@@ -439,77 +610,24 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       cluster_wait();
       if (pull_sync) cluster_sync();
     }
+  } else if (k8 && kWide && warp >= 4) {
+    // ---------------------------------------- issuers, and two idle warps
+    if constexpr (k8 && kWide) regs_decrease<Cfg::kIssuerRegs>();
+    if (warp == Cfg::kQkWarp) {
+      issue_scores();
+    } else if (warp == Cfg::kPvWarp) {
+      issue_outputs();
+    } else if (C > 1) {
+      cluster_wait();
+      if (pull_sync) cluster_sync();
+    }
   } else if (warp == Cfg::kQkWarp) {
-    // -------------------------------------------------------- Q K^T issuer
-    // S(j) goes to buffer j%n once K(j) has landed and P V(j-n) has read
-    // P(j-n) out of that buffer.
-    if (lane == 0 && run) {
-      const uint32_t q_saddr = sbase + Cfg::kQOff;
-      bool ok = no_error(args.err, abort_flag) &&
-                mbar_wait(bar(Cfg::kBarQReady), 0, abort_flag, args.err, kDevTimeoutTma);
-      for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
-        const int slot = j % Cfg::kKStages;
-        const int sb = j % Cfg::kSBufs;
-        ok = mbar_wait(bar(Cfg::kBarKFull + slot), (j / Cfg::kKStages) & 1, abort_flag, args.err, kDevTimeoutTma);
-        if (ok && j >= Cfg::kSBufs)
-          ok = mbar_wait(bar(Cfg::kBarOFull + sb), ((j - Cfg::kSBufs) / Cfg::kSBufs) & 1, abort_flag, args.err,
-                         kDevTimeoutMma);
-        if (!ok) break;
-        tc_fence_after();
-        issue_qk(tmem_base + sb * 128u, q_saddr, Cfg::kQSbo, Cfg::kQSlab, sbase + Cfg::kKOff + slot * kTileBytes);
-        tc_commit(bar(Cfg::kBarSFull + sb));
-        tc_commit(bar(Cfg::kBarKEmpty + slot));
-      }
-      if (!ok) {
-        tc_commit(bar(Cfg::kBarDrain));
-        packed_drain_wait(bar(Cfg::kBarDrain), 0);
-      }
-    }
-    __syncwarp();
-    if (C > 1) {
-      cluster_wait();
-      if (pull_sync) cluster_sync();
-    }
+    issue_scores();
   } else if (warp == Cfg::kPvWarp) {
-    // ---------------------------------------------------------- P V issuer
-    // The first P V of every segment clears O; after the CTA's first segment
-    // it waits until the previous segment's O has been read.
-    if (lane == 0 && run) {
-      int F = 0;                                            // segments started
-      int js = 0;                                           // tile index within its segment (j0 starts one)
-      bool ok = no_error(args.err, abort_flag);
-      for (int j = 0; j < nt && ok; ++j) {                  // j: tile j0 + j
-        const int slot = j % Cfg::kVStages;
-        const int sb = j % Cfg::kSBufs;
-        if (zero_tail && has_last && j == nt - 1)
-          ok = mbar_wait(bar(Cfg::kBarVReady), 0, abort_flag, args.err, kDevTimeoutTma);
-        else
-          ok = mbar_wait(bar(Cfg::kBarVFull + slot), (j / Cfg::kVStages) & 1, abort_flag, args.err, kDevTimeoutTma);
-        const bool first = kSparse ? starts_seg(j) : (js == 0);
-        if (++js == seg_len) js = 0;
-        if (ok && first && F > 0)
-          ok = mbar_wait(bar(Cfg::kBarORead), (F - 1) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
-        if (ok)
-          ok = mbar_wait_hint(bar(Cfg::kBarPFull + sb), (j / Cfg::kSBufs) & 1, abort_flag, args.err, kDevTimeoutSoftmax);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(tmem_base + Cfg::kOCol, tmem_base + sb * 128u, sbase + Cfg::kVOff + slot * kTileBytes, first);
-        tc_commit(bar(Cfg::kBarOFull + sb));
-        tc_commit(bar(Cfg::kBarVEmpty + slot));
-        if (first) ++F;
-      }
-      if (!ok) {
-        tc_commit(bar(Cfg::kBarDrain + 1));
-        packed_drain_wait(bar(Cfg::kBarDrain + 1), 0);
-      }
-    }
-    __syncwarp();
-    if (C > 1) {
-      cluster_wait();
-      if (pull_sync) cluster_sync();
-    }
+    issue_outputs();
   } else if constexpr (kWide) {
     // ------------------------------------------------- softmax, row per thread
+    if constexpr (k8) regs_increase<Cfg::kSoftmaxRegs>();
     const int m = warp * 32 + lane;                    // packed row = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_tmem = tmem_base + Cfg::kOCol + lane_off;
@@ -637,6 +755,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       else f = fold_state(acc, st);
       const float inv_l = row_inv_l(acc);
       const bool store = m < n_rows;
+      if (store && args.lse != nullptr)
+        args.lse[(static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r] = row_lse(acc);
       uint4* dst = reinterpret_cast<uint4*>(
           static_cast<__nv_bfloat16*>(args.o) +
           ((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) * kHeadDim);
@@ -872,6 +992,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
       // C4 into the rows' outputs: thread (m, u) stores its 32 columns
       const float inv_l = row_inv_l(acc);
+      if (!kSparse && row_used && u == 0 && args.lse != nullptr)
+        args.lse[(static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r] = row_lse(acc);
       if (row_used) {
         uint32_t* dst = reinterpret_cast<uint32_t*>(
             static_cast<__nv_bfloat16*>(args.o) +
@@ -1020,6 +1142,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const float inv_l = row_inv_l(acc);
       const int head = r / Lc;
       const int rr = r0 + r % Lc;
+      if (!kSparse && cb == 0 && args.lse != nullptr)
+        args.lse[(static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + rr] = row_lse(acc);
       uint4 packed;
       packed.x = pack_bf16x2(__fmul_rn(o[0], inv_l), __fmul_rn(o[1], inv_l));
       packed.y = pack_bf16x2(__fmul_rn(o[2], inv_l), __fmul_rn(o[3], inv_l));
@@ -1042,17 +1166,17 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
 }
 
-template <bool kWide, int kNumSBufs, bool kSparse = false>
+template <bool kWide, int kNumSBufs, bool kSparse = false, bool k8 = false>
 static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub,
                                    cudaStream_t s) {
-  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse>;
+  using Cfg = PackedCfg<kWide, kNumSBufs, kSparse, k8>;
   static_assert(Cfg::kSmemBytes <= 227u * 1024u, "shared memory budget");
   static int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(kb_decode_kernel<kWide, kNumSBufs, kSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(kb_decode_kernel<kWide, kNumSBufs, kSparse, k8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Cfg::kSmemBytes));
     if (e != cudaSuccess) return e;
     configured_device = dev;
@@ -1061,7 +1185,7 @@ static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv,
   const int C = ws_mode ? 1 : a.cluster;
   const unsigned grid = static_cast<unsigned>((ws_mode ? a.n_seg : C) * n_sub * a.B * a.Hkv);
   if (C <= 1) {
-    kb_decode_kernel<kWide, kNumSBufs, kSparse><<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
+    kb_decode_kernel<kWide, kNumSBufs, kSparse, k8><<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
@@ -1076,7 +1200,7 @@ static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kb_decode_kernel<kWide, kNumSBufs, kSparse>, tk, tv, a);
+  e = cudaLaunchKernelEx(&cfg, kb_decode_kernel<kWide, kNumSBufs, kSparse, k8>, tk, tv, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -1093,6 +1217,9 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     if (a.lean) return launch_packed_t<false, 1, true>(tk, tv, a, n_sub, s);
     return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
   }
+  if (a.k8 != nullptr)
+    return a.L <= 2 ? launch_packed_t<false, 3, false, true>(tk, tv, a, n_sub, s)
+                    : launch_packed_t<true, 2, false, true>(tk, tv, a, n_sub, s);
   if (a.L <= 2) return launch_packed_t<false, 3>(tk, tv, a, n_sub, s);
   if (a.part != nullptr) return launch_packed_t<true, 3>(tk, tv, a, n_sub, s);
   return launch_packed_t<true, 2>(tk, tv, a, n_sub, s);
@@ -1105,7 +1232,7 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
 void packed_cluster_capacity(int (&active)[4]) {
   using Cfg = PackedCfg<false, 3>;
   for (int i = 0; i < 4; ++i) active[i] = 0;
-  if (cudaFuncSetAttribute(kb_decode_kernel<false, 3, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(kb_decode_kernel<false, 3, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(Cfg::kSmemBytes)) != cudaSuccess) {
     (void)cudaGetLastError();
     return;
@@ -1123,7 +1250,7 @@ void packed_cluster_capacity(int (&active)[4]) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kb_decode_kernel<false, 3, false>, &cfg) == cudaSuccess) active[i] = n;
+    if (cudaOccupancyMaxActiveClusters(&n, kb_decode_kernel<false, 3, false, false>, &cfg) == cudaSuccess) active[i] = n;
     else (void)cudaGetLastError();
   }
 }

@@ -165,25 +165,6 @@ struct Ragged {
   const int* lens = nullptr;
 };
 
-// CTAs per (sub-chunk, b, kv head) of the packed kernel's fold mode: the
-// largest cluster whose clusters all run at once (one wave), when the batch
-// alone would leave SMs idle.  Narrow rows only; the other CTAs of a cluster
-// keep their segments' partials in shared memory, so a CTA may own at most
-// as many segments as it has partial slots.
-int choose_cluster(const DeviceState& dst, int L, int n_sub, int B, int Hkv, int n_kv_max) {
-  if (L > 2) return 1;
-  const long long units = static_cast<long long>(n_sub) * B * Hkv;
-  if (2 * units > dst.sm_count) return 1;
-  const int ns = (n_kv_max + kb::kSegTiles - 1) / kb::kSegTiles;
-  const long long slots = kb::packed_partial_slots(kb::kGroup * L);
-  for (int i = 3, c = 8; i >= 1; --i, c /= 2) {
-    if (c > ns || units > dst.cluster_fit[i]) continue;
-    if ((ns + c - 1) / c > slots) continue;
-    return c;
-  }
-  return 1;
-}
-
 // seg_tiles: 0 for the default entry points (the contract's segment length,
 // folded in the kernels); > 0 for the *_seg entry points (that length; chunks
 // of at most 32 rows then leave per-segment partials in `workspace`, which a
@@ -205,7 +186,6 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
   const bool force_snake = (cta_shape == kb::kShapeSnake);
   const bool packed = (cta_shape == 0);
   if (packed && L > kb::kMaxPackedRows) return KB_ERR_INVALID_ARG;
-  if (lse != nullptr && packed) return KB_ERR_INVALID_ARG;
   if (seg_tiles < 0) return KB_ERR_INVALID_ARG;
   const bool explicit_seg = seg_tiles > 0;
   if (explicit_seg) {
@@ -259,7 +239,7 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
   if (packed) {
     // query rows packed by GQA group
     const int split = std::min(L, kb::kTileKeys - start % kb::kTileKeys);
-    const int n_sub = (ragged || split < L) ? 2 : 1;
+    const int n_sub = L > 1 && (ragged || split < L) ? 2 : 1;      // (one row never crosses a tile boundary)
     kb::PackedArgs a{};
     a.q = q;
     a.o = o;
@@ -279,6 +259,7 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
       a.page_size = paging->page_size;
       a.num_pages = paging->num_pages;
     }
+    a.lse = lse;
     a.err = dst->err;
     a.n_sub = n_sub;
     int n_seg = 0;
@@ -292,7 +273,7 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
     } else {
       const int n_kv_max = ragged ? (kv_cap - 1) / kb::kTileKeys + 1 : (start + L - 1) / kb::kTileKeys + 1;
       a.fold_seg = seg;
-      a.cluster = choose_cluster(*dst, L, n_sub, B, Hkv, n_kv_max);
+      a.cluster = kb::host_choose_cluster(dst->sm_count, dst->cluster_fit, L, n_sub, B, Hkv, n_kv_max);
     }
     cudaError_t e = kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess && explicit_seg)
@@ -412,6 +393,25 @@ kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64
   return r == CUDA_SUCCESS ? KB_OK : KB_ERR_CUDA;
 }
 
+// CTAs per (sub-chunk, b, kv head) of the packed kernel's fold mode: the
+// largest cluster whose clusters all run at once (one wave), when the batch
+// alone would leave SMs idle.  Narrow rows only; the other CTAs of a cluster
+// keep their segments' partials in shared memory, so a CTA may own at most
+// as many segments as it has partial slots.
+int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max) {
+  if (L > 2) return 1;
+  const long long units = static_cast<long long>(n_sub) * B * Hkv;
+  if (2 * units > sm_count) return 1;
+  const int ns = (n_kv_max + kSegTiles - 1) / kSegTiles;
+  const long long slots = packed_partial_slots(kGroup * L);
+  for (int i = 3, c = 8; i >= 1; --i, c /= 2) {
+    if (c > ns || units > cluster_fit[i]) continue;
+    if ((ns + c - 1) / c > slots) continue;
+    return c;
+  }
+  return 1;
+}
+
 kb_status host_check_heads(int B, int Hq, int Hkv) { return check_heads(B, Hq, Hkv); }
 
 kb_status host_check_paging(const int* block_table, int pages_per_seq, int page_size, int num_pages, int Hkv) {
@@ -495,6 +495,28 @@ kb_status kb_attn_prefill_lse(const void* q, const void* k, const void* v, void*
   if (S < 1 || lse == nullptr) return KB_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return KB_ERR_INVALID_ARG;
   return chunk_impl(q, k, v, o, B, Hq, Hkv, S, 0, S, kb::kShapeOneTilePerSm, stream, nullptr, nullptr, lse);
+}
+
+kb_status kb_attn_chunk_lse(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                            int L, int start, const int* starts, const int* lens, int kv_cap, const int* block_table,
+                            int pages_per_seq, int page_size, int num_pages, void* stream) {
+  if (lse == nullptr || !kb::host_aligned(lse, 4) || (starts == nullptr) != (lens == nullptr)) return KB_ERR_INVALID_ARG;
+  if (!kb::host_aligned(starts, 4) || !kb::host_aligned(lens, 4)) return KB_ERR_INVALID_ARG;
+  int cap = 0;
+  kb_status s = check_heads(B, Hq, Hkv);
+  if (s != KB_OK) return s;
+  if ((s = kb::host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
+  if (L < 1 || L > cap) return KB_ERR_INVALID_ARG;
+  Paging pg;
+  pg.block_table = block_table;
+  pg.pages_per_seq = pages_per_seq;
+  pg.page_size = page_size;
+  pg.num_pages = num_pages;
+  Ragged rg;
+  rg.starts = starts;
+  rg.lens = lens;
+  return chunk_impl(q, k, v, o, B, Hq, Hkv, L, starts ? 0 : start, cap, chunk_cta_shape(L), stream,
+                    block_table ? &pg : nullptr, starts ? &rg : nullptr, lse);
 }
 
 kb_status kb_attn_backward(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -634,7 +656,7 @@ kb_status kb_attn_decode_paged(const void* q, const void* k_pages, const void* v
   a.ctx_lens = ctx_lens;
   a.max_ctx = pages_per_seq * page_size;
   a.fold_seg = kb::kSegTiles;
-  a.cluster = choose_cluster(*dst, 1, 1, B, Hkv, (a.max_ctx - 1) / kb::kTileKeys + 1);
+  a.cluster = kb::host_choose_cluster(dst->sm_count, dst->cluster_fit, 1, 1, B, Hkv, (a.max_ctx - 1) / kb::kTileKeys + 1);
   a.block_table = block_table;
   a.pages_per_seq = pages_per_seq;
   a.page_size = page_size;

@@ -1,0 +1,362 @@
+// kb_host_cache.cu -- C entry points of smaller caches: a cache held in 8 bits
+// and the attention over it, rotation by positions of several axes.
+// Declarations and their contract are in include/kb_attn.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/kb_attn.h"
+#include "kb_contract.cuh"
+#include "kb_host.h"
+#include "kb_launch.h"
+
+namespace {
+
+using kb::host_aligned;
+using kb::host_cache_rows;
+using kb::host_check_ragged;
+using kb::host_check_strides;
+using kb::host_check_table;
+using kb::host_device_pointers;
+using kb::host_done;
+using kb::kMaxRows;
+
+long long blocks_of(long long rows) { return (rows + kb::kTileKeys - 1) / kb::kTileKeys; }
+
+long long align256(long long n) { return (n + 255) / 256 * 256; }
+
+// An attention call over a cache held in 8 bits.
+struct Call8 {
+  const void *q, *k, *v;
+  const int8_t *k_exp, *v_exp;
+  void* o;
+  int B, Hq, Hkv, L, start;
+  const int *starts, *lens, *ctx_lens;
+  int kv_cap;
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+};
+
+kb_status check_call(const Call8& c, int* cap, kb::HostDevice* dev) {
+  if (!c.q || !c.k || !c.v || !c.k_exp || !c.v_exp || !c.o) return KB_ERR_INVALID_ARG;
+  for (const void* p : {c.q, c.k, c.v, static_cast<const void*>(c.o)})
+    if (!host_aligned(p, 16)) return KB_ERR_INVALID_ARG;
+  if (!host_aligned(c.starts, 4) || !host_aligned(c.lens, 4) || !host_aligned(c.ctx_lens, 4)) return KB_ERR_INVALID_ARG;
+  if ((c.starts == nullptr) != (c.lens == nullptr)) return KB_ERR_INVALID_ARG;
+  kb_status s = kb::host_check_heads(c.B, c.Hq, c.Hkv);
+  if (s != KB_OK) return s;
+  if ((s = host_cache_rows(cap, c.kv_cap, c.block_table, c.pages_per_seq, c.page_size, c.num_pages, c.Hkv)) != KB_OK) return s;
+  if (c.L < 1 || c.L > *cap) return KB_ERR_INVALID_ARG;
+  if (c.starts == nullptr && c.ctx_lens == nullptr && (c.start < 0 || c.start > *cap - c.L)) return KB_ERR_INVALID_ARG;
+  if ((s = kb::host_device(dev)) != KB_OK) return s;
+  const void* p[] = {c.q, c.k, c.v, c.k_exp, c.v_exp, c.o, c.starts, c.lens, c.ctx_lens, c.block_table};
+  return host_device_pointers(p, 10);
+}
+
+// At most 32 rows: the packed kernel reads the bytes.
+kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* stream) {
+  const bool ragged = c.starts != nullptr;
+  const int split = std::min(c.L, kb::kTileKeys - c.start % kb::kTileKeys);
+  const int n_sub = c.L > 1 && (ragged || split < c.L) ? 2 : 1;       // (one row never crosses a tile boundary)
+  kb::PackedArgs a{};
+  a.q = c.q;
+  a.o = c.o;
+  a.B = c.B;
+  a.Hq = c.Hq;
+  a.Hkv = c.Hkv;
+  a.L = c.L;
+  a.start = c.start;
+  a.ctx_lens = c.ctx_lens;
+  a.max_ctx = cap;
+  a.block_table = c.block_table;
+  a.pages_per_seq = c.pages_per_seq;
+  a.page_size = c.page_size;
+  a.num_pages = c.num_pages;
+  a.starts = c.starts;
+  a.lens = c.lens;
+  a.n_sub = n_sub;
+  const long long keys = ragged || c.ctx_lens != nullptr ? cap : static_cast<long long>(c.start) + c.L;
+  a.fold_seg = kb::kSegTiles;
+  a.cluster = kb::host_choose_cluster(dev.sm_count, dev.cluster_fit, c.L, n_sub, c.B, c.Hkv, static_cast<int>(blocks_of(keys)));
+  a.k8 = static_cast<const uint8_t*>(c.k);
+  a.v8 = static_cast<const uint8_t*>(c.v);
+  a.k_exp = c.k_exp;
+  a.v_exp = c.v_exp;
+  a.plane_rows = c.block_table != nullptr ? c.page_size : c.kv_cap;
+  a.err = dev.err;
+  const CUtensorMap unused{};
+  return host_done(kb::launch_packed(unused, unused, a, n_sub, static_cast<cudaStream_t>(stream)));
+}
+
+// Bytes of one of the two bf16 caches that a longer chunk is computed from.
+long long gathered_bytes(int B, int Hkv, long long rows) { return align256(static_cast<long long>(B) * Hkv * rows * kb::kHeadDim * 2); }
+
+}  // namespace
+
+extern "C" {
+
+kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, const float* table, int n_pos, int rot_dim,
+                            int interleaved, int inverse, const int* positions, int n_axes, const unsigned char* plane_axes,
+                            int B, int H, int L, void* stream) {
+  if (!x || !out || !strides || !table || !positions || !plane_axes) return KB_ERR_INVALID_ARG;
+  if (!host_aligned(x, 16) || !host_aligned(out, 16) || !host_aligned(positions, 4)) return KB_ERR_INVALID_ARG;
+  kb_status s = host_check_table(table, n_pos, rot_dim);
+  if (s != KB_OK) return s;
+  if ((s = host_check_strides(strides)) != KB_OK) return s;
+  if (B < 1 || H < 1 || L < 1 || n_axes < 1) return KB_ERR_INVALID_ARG;
+  if (n_axes > kb::kMaxAxes) return KB_ERR_UNSUPPORTED;
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (plane_axes[i] >= n_axes) return KB_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * ((H + 3) / 4) * ((L + 3) / 4) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  kb::HostDevice dev;
+  if ((s = kb::host_device(&dev)) != KB_OK) return s;
+  const void* p[] = {x, out, table, positions};
+  if ((s = host_device_pointers(p, 4)) != KB_OK) return s;
+  kb::RopeArgs a{};
+  a.x = x;
+  a.sb = strides[0];
+  a.sh = strides[1];
+  a.sl = strides[2];
+  a.out = out;
+  a.table = table;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  a.B = B;
+  a.H = H;
+  a.L = L;
+  a.positions = positions;
+  a.n_axes = n_axes;
+  a.n_pos = n_pos;
+  for (int i = 0; i < rot_dim / 2; ++i)
+    a.plane_axes[i / kb::kPlanesPerLane] |= static_cast<uint64_t>(plane_axes[i]) << (8 * (i % kb::kPlanesPerLane));
+  a.err = dev.err;
+  return host_done(kb::launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
+                              void* k_cache, void* v_cache, signed char* k_exp, signed char* v_exp, const float* table,
+                              int n_pos, int rot_dim, int interleaved, int B, int Hq, int Hkv, int L, int start,
+                              const int* starts, const int* lens, int kv_cap, const int* block_table, int pages_per_seq,
+                              int page_size, int num_pages, void* stream) {
+  if (!k || !v || !strides || !k_cache || !v_cache || !k_exp || !v_exp || (q == nullptr) != (q_out == nullptr))
+    return KB_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
+    if (!host_aligned(p, 16)) return KB_ERR_INVALID_ARG;
+  kb_status s = kb::host_check_heads(B, Hq, Hkv);
+  if (s != KB_OK) return s;
+  if (table != nullptr && (s = host_check_table(table, n_pos, rot_dim)) != KB_OK) return s;
+  for (int i = 0; i < 3; ++i)
+    if ((s = host_check_strides(strides + 3 * i)) != KB_OK) return s;
+  if ((s = host_check_ragged(starts, lens)) != KB_OK) return s;
+  int cap = 0;
+  if ((s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
+  if (L < 1 || L > cap) return KB_ERR_INVALID_ARG;
+  if (starts == nullptr && (start < 0 || start > cap - L || (table != nullptr && start > n_pos - L))) return KB_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * Hkv * (blocks_of(L) + 1) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  kb::HostDevice dev;
+  if ((s = kb::host_device(&dev)) != KB_OK) return s;
+  const void* p[] = {q, k, v, q_out, k_cache, v_cache, k_exp, v_exp, table, starts, lens, block_table};
+  if ((s = host_device_pointers(p, 12)) != KB_OK) return s;
+  kb::Append8Args x{};
+  kb::AppendArgs& a = x.a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = strides[i];
+    a.ks[i] = strides[3 + i];
+    a.vs[i] = strides[6 + i];
+  }
+  a.q_out = q_out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = table;
+  a.n_pos = n_pos;
+  a.rot_dim = table != nullptr ? rot_dim : kb::kHeadDim;
+  a.interleaved = interleaved != 0;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.start = start;
+  a.starts = starts;
+  a.lens = lens;
+  a.kv_cap = cap;
+  a.block_table = block_table;
+  a.pages_per_seq = pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.err = dev.err;
+  x.k_exp = reinterpret_cast<int8_t*>(k_exp);
+  x.v_exp = reinterpret_cast<int8_t*>(v_exp);
+  return host_done(kb::launch_append8(x, static_cast<cudaStream_t>(stream)));
+}
+
+kb_status kb_attn_cache_values(const void* cache, const signed char* exps, void* out, long long planes, int rows, void* stream) {
+  if (!cache || !exps || !out || !host_aligned(cache, 16) || !host_aligned(out, 16)) return KB_ERR_INVALID_ARG;
+  if (planes < 1 || rows < 1) return KB_ERR_INVALID_ARG;
+  if (rows > kMaxRows || planes > 0x7FFFFFFFLL / blocks_of(rows)) return KB_ERR_UNSUPPORTED;
+  kb::HostDevice dev;
+  kb_status s = kb::host_device(&dev);
+  if (s != KB_OK) return s;
+  const void* p[] = {cache, exps, out};
+  if ((s = host_device_pointers(p, 3)) != KB_OK) return s;
+  kb::Values8Args a{};
+  a.cache = cache;
+  a.exps = reinterpret_cast<const int8_t*>(exps);
+  a.out = out;
+  a.planes = planes;
+  a.rows = rows;
+  a.blocks = static_cast<int>(blocks_of(rows));
+  a.err = dev.err;
+  return host_done(kb::launch_cache_values(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kb_attn_chunk_8bit_workspace_bytes(int B, int Hkv, int L, int rows) {
+  if (B < 1 || Hkv < 1 || L < 1 || rows < L || rows > kMaxRows || L <= kb::kMaxPackedRows) return 0;
+  return static_cast<size_t>(2 * gathered_bytes(B, Hkv, rows));
+}
+
+kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const signed char* k_exp, const signed char* v_exp,
+                             void* o, int B, int Hq, int Hkv, int L, int start, const int* starts, const int* lens,
+                             int kv_cap, const int* block_table, int pages_per_seq, int page_size, int num_pages,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  Call8 c{q, k, v, reinterpret_cast<const int8_t*>(k_exp), reinterpret_cast<const int8_t*>(v_exp), o, B, Hq, Hkv, L,
+          starts ? 0 : start, starts, lens, nullptr, kv_cap, block_table, pages_per_seq, page_size, num_pages};
+  int cap = 0;
+  kb::HostDevice dev;
+  kb_status s = check_call(c, &cap, &dev);
+  if (s != KB_OK) return s;
+  if (L <= kb::kMaxPackedRows) return packed8(c, cap, dev, stream);
+  const int rows = starts != nullptr ? cap : start + L;
+  const size_t need = kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows);
+  if (workspace == nullptr || !host_aligned(workspace, 256) || workspace_bytes < need) return KB_ERR_INVALID_ARG;
+  if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
+  if (static_cast<long long>(B) * Hkv * blocks_of(rows) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  kb::Gather8Args a{};
+  a.k = k;
+  a.v = v;
+  a.k_exp = c.k_exp;
+  a.v_exp = c.v_exp;
+  a.k_out = workspace;
+  a.v_out = static_cast<char*>(workspace) + gathered_bytes(B, Hkv, rows);
+  a.B = B;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.rows = rows;
+  a.blocks = static_cast<int>(blocks_of(rows));
+  a.starts = starts;
+  a.lens = lens;
+  a.kv_cap = kv_cap;
+  a.block_table = block_table;
+  a.pages_per_seq = pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.err = dev.err;
+  if ((s = host_done(kb::launch_cache_gather(a, static_cast<cudaStream_t>(stream)))) != KB_OK) return s;
+  if (starts != nullptr)
+    return kb_attn_chunk_varlen(q, a.k_out, a.v_out, o, B, Hq, Hkv, L, starts, lens, rows, nullptr, 0, 0, 0, stream);
+  return kb_attn_chunk(q, a.k_out, a.v_out, o, B, Hq, Hkv, L, start, rows, stream);
+}
+
+kb_status kb_attn_decode_8bit(const void* q, const void* k, const void* v, const signed char* k_exp, const signed char* v_exp,
+                              void* o, int B, int Hq, int Hkv, int ctx_len, const int* ctx_lens, int kv_cap,
+                              const int* block_table, int pages_per_seq, int page_size, int num_pages, void* stream) {
+  if (ctx_lens == nullptr && ctx_len < 1) return KB_ERR_INVALID_ARG;
+  Call8 c{q, k, v, reinterpret_cast<const int8_t*>(k_exp), reinterpret_cast<const int8_t*>(v_exp), o, B, Hq, Hkv, 1,
+          ctx_lens ? 0 : ctx_len - 1, nullptr, nullptr, ctx_lens, kv_cap, block_table, pages_per_seq, page_size, num_pages};
+  int cap = 0;
+  kb::HostDevice dev;
+  const kb_status s = check_call(c, &cap, &dev);
+  return s != KB_OK ? s : packed8(c, cap, dev, stream);
+}
+
+kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, float* weights, int B, int Hq, int Hkv, int L,
+                              int start, const int* starts, const int* lens, int kv_cap, const int* block_table,
+                              int pages_per_seq, int page_size, int num_pages, void* stream) {
+  if (!q || !k || !lse || !weights || !host_aligned(q, 16) || !host_aligned(k, 16)) return KB_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(lse), static_cast<const void*>(weights), static_cast<const void*>(starts),
+                        static_cast<const void*>(lens)})
+    if (!host_aligned(p, 4)) return KB_ERR_INVALID_ARG;
+  if ((starts == nullptr) != (lens == nullptr)) return KB_ERR_INVALID_ARG;
+  kb_status s = kb::host_check_heads(B, Hq, Hkv);
+  if (s != KB_OK) return s;
+  int cap = 0;
+  if ((s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
+  if (L < 1 || L > cap || (starts == nullptr && (start < 0 || start > cap - L))) return KB_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * Hkv * blocks_of(cap) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  kb::HostDevice dev;
+  if ((s = kb::host_device(&dev)) != KB_OK) return s;
+  const void* p[] = {q, k, lse, weights, starts, lens, block_table};
+  if ((s = host_device_pointers(p, 7)) != KB_OK) return s;
+  // K map as the attention's: a contiguous uniform cache ends at the call's last key
+  const uint64_t row_bytes = kb::kHeadDim * 2u;
+  const bool paged = block_table != nullptr;
+  const uint64_t stride_rows = static_cast<uint64_t>(paged ? page_size : kv_cap);
+  const uint64_t rows = paged || starts != nullptr ? stride_rows : static_cast<uint64_t>(start) + L;
+  CUtensorMap tq, tk;
+  if ((s = kb::host_rows_map(&tq, q, static_cast<uint64_t>(L), static_cast<uint64_t>(B) * Hq, static_cast<uint64_t>(L) * row_bytes)) != KB_OK)
+    return s;
+  if ((s = kb::host_rows_map(&tk, k, rows, static_cast<uint64_t>(paged ? num_pages : B) * Hkv, stride_rows * row_bytes)) != KB_OK)
+    return s;
+  kb::WeightsArgs a{};
+  a.q = q;
+  a.lse = lse;
+  a.weights = weights;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.start = start;
+  a.starts = starts;
+  a.lens = lens;
+  a.kv_cap = cap;
+  a.block_table = block_table;
+  a.pages_per_seq = pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.err = dev.err;
+  return host_done(kb::launch_weights(tq, tk, a, starts != nullptr ? cap : start + L, dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+kb_status kb_attn_evict(void* k, void* v, const float* weights, float* weights_out, int* kept, int B, int Hkv, const int* lens,
+                        int keep, int keep_first, int keep_last, int kv_cap, const int* block_table, int pages_per_seq,
+                        int page_size, int num_pages, void* stream) {
+  if (!k || !v || !weights || !weights_out || !kept || !lens || !host_aligned(k, 16) || !host_aligned(v, 16))
+    return KB_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(weights_out), static_cast<const void*>(kept),
+                        static_cast<const void*>(lens)})
+    if (!host_aligned(p, 4)) return KB_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1) return KB_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * Hkv > (1LL << 24)) return KB_ERR_UNSUPPORTED;
+  int cap = 0;
+  kb_status s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv);
+  if (s != KB_OK) return s;
+  if (keep < 1 || keep > cap || keep_first < 0 || keep_last < 0 || keep_first > keep - keep_last) return KB_ERR_INVALID_ARG;
+  kb::HostDevice dev;
+  if ((s = kb::host_device(&dev)) != KB_OK) return s;
+  const void* p[] = {k, v, weights, weights_out, kept, lens, block_table};
+  if ((s = host_device_pointers(p, 7)) != KB_OK) return s;
+  kb::EvictArgs a{};
+  a.k = k;
+  a.v = v;
+  a.weights = weights;
+  a.weights_out = weights_out;
+  a.kept = kept;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.lens = lens;
+  a.keep = keep;
+  a.keep_first = keep_first;
+  a.keep_last = keep_last;
+  a.kv_cap = cap;
+  a.block_table = block_table;
+  a.pages_per_seq = pages_per_seq;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.err = dev.err;
+  return host_done(kb::launch_evict(a, dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -16,54 +16,13 @@
 namespace {
 
 using kb::host_aligned;
+using kb::host_cache_rows;
+using kb::host_check_ragged;
+using kb::host_check_strides;
+using kb::host_check_table;
+using kb::host_device_pointers;
+using kb::host_done;
 using kb::kMaxRows;
-
-kb_status done(cudaError_t e) { return e == cudaSuccess ? KB_OK : kb::host_cuda_fail(e); }
-
-kb_status device_pointers(const void* const* p, int n) {
-  for (int i = 0; i < n; ++i)
-    if (p[i] != nullptr) {
-      const kb_status s = kb::host_device_pointer(p[i]);
-      if (s != KB_OK) return s;
-    }
-  return KB_OK;
-}
-
-kb_status check_table(const float* table, int n_pos, int rot_dim) {
-  if (!host_aligned(table, 16)) return KB_ERR_INVALID_ARG;
-  if (n_pos < 1 || rot_dim < 2) return KB_ERR_INVALID_ARG;
-  if (rot_dim % 16 != 0 || rot_dim > kb::kHeadDim || n_pos > kMaxRows) return KB_ERR_UNSUPPORTED;
-  return KB_OK;
-}
-
-// Batch, head and row strides of a [*, *, *, 128] view, in elements.
-kb_status check_strides(const long long* st) {
-  for (int i = 0; i < 3; ++i)
-    if (st[i] < 0 || st[i] % 8 != 0) return KB_ERR_INVALID_ARG;
-  return KB_OK;
-}
-
-// Per-sequence starts and lens (device int32 arrays; both null: `start` and L rows).
-kb_status check_ragged(const int* starts, const int* lens) {
-  if (lens != nullptr && starts == nullptr) return KB_ERR_INVALID_ARG;
-  if (!host_aligned(starts, 4) || !host_aligned(lens, 4)) return KB_ERR_INVALID_ARG;
-  return KB_OK;
-}
-
-// The cache's capacity in positions: kv_cap, or the page table's.
-kb_status cache_rows(int* cap, int kv_cap, const int* block_table, int pages_per_seq, int page_size, int num_pages,
-                     int Hkv) {
-  if (block_table != nullptr) {
-    const kb_status s = kb::host_check_paging(block_table, pages_per_seq, page_size, num_pages, Hkv);
-    if (s != KB_OK) return s;
-    *cap = pages_per_seq * page_size;
-    return KB_OK;
-  }
-  if (kv_cap < 1) return KB_ERR_INVALID_ARG;
-  if (kv_cap > kMaxRows) return KB_ERR_UNSUPPORTED;
-  *cap = kv_cap;
-  return KB_OK;
-}
 
 // Position tiles of 32 that L consecutive positions can touch.
 long long max_tiles32(long long L) { return (L + kb::kUnitRows - 2) / kb::kUnitRows + 1; }
@@ -128,15 +87,15 @@ kb_status check_sparse(const SparseCall& c, int* cap, kb::HostDevice* dev) {
   if (!host_aligned(c.blocks, 4) || !host_aligned(c.lse, 4)) return KB_ERR_INVALID_ARG;
   kb_status s = kb::host_check_heads(c.B, c.Hq, c.Hkv);
   if (s != KB_OK) return s;
-  if ((s = check_ragged(c.starts, c.lens)) != KB_OK) return s;
+  if ((s = host_check_ragged(c.starts, c.lens)) != KB_OK) return s;
   if (c.n_select < 1) return KB_ERR_INVALID_ARG;
   if (c.n_select > KB_MAX_SELECT) return KB_ERR_UNSUPPORTED;
-  if ((s = cache_rows(cap, c.kv_cap, c.block_table, c.pages_per_seq, c.page_size, c.num_pages, c.Hkv)) != KB_OK) return s;
+  if ((s = host_cache_rows(cap, c.kv_cap, c.block_table, c.pages_per_seq, c.page_size, c.num_pages, c.Hkv)) != KB_OK) return s;
   if (c.L < 1 || c.L > *cap || (c.starts == nullptr && (c.start < 0 || c.start > *cap - c.L))) return KB_ERR_INVALID_ARG;
   if (static_cast<long long>(c.B) * c.Hkv * max_tiles32(c.L) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   if ((s = kb::host_device(dev)) != KB_OK) return s;
   const void* p[] = {c.q, c.k, c.v, c.o, c.lse, c.blocks, c.starts, c.lens, c.block_table, c.workspace};
-  return device_pointers(p, 10);
+  return host_device_pointers(p, 10);
 }
 
 // K/V maps: a contiguous uniform cache ends at the call's last key (later rows
@@ -202,7 +161,7 @@ kb_status sparse_forward(const SparseCall& c, void* stream) {
   if ((s = cache_maps(c, &tk, &tv)) != KB_OK) return s;
   cudaError_t e = kb::launch_sparse_plan(a, dev.index, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = kb::launch_sparse_tile(tq, tk, tv, a, dev.index, dev.sm_count, static_cast<cudaStream_t>(stream));
-  return done(e);
+  return host_done(e);
 }
 
 // CTAs per (b, KV head) of a block-sparse token: the largest cluster whose
@@ -224,27 +183,27 @@ extern "C" {
 
 kb_status kb_attn_rope_table(float* table, int n_pos, int rot_dim, const double* inv_freq, void* stream) {
   if (!table || !inv_freq || !host_aligned(inv_freq, 8)) return KB_ERR_INVALID_ARG;
-  kb_status s = check_table(table, n_pos, rot_dim);
+  kb_status s = host_check_table(table, n_pos, rot_dim);
   if (s != KB_OK) return s;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
   const void* p[] = {table, inv_freq};
-  if ((s = device_pointers(p, 2)) != KB_OK) return s;
-  return done(kb::launch_rope_table(table, n_pos, rot_dim, inv_freq, static_cast<cudaStream_t>(stream)));
+  if ((s = host_device_pointers(p, 2)) != KB_OK) return s;
+  return host_done(kb::launch_rope_table(table, n_pos, rot_dim, inv_freq, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_rope(const void* x, const long long* strides, void* out, const float* table, int n_pos, int rot_dim,
                        int interleaved, int inverse, int B, int H, int L, int start, void* stream) {
   if (!x || !out || !strides || !table || !host_aligned(x, 16) || !host_aligned(out, 16)) return KB_ERR_INVALID_ARG;
-  kb_status s = check_table(table, n_pos, rot_dim);
+  kb_status s = host_check_table(table, n_pos, rot_dim);
   if (s != KB_OK) return s;
-  if ((s = check_strides(strides)) != KB_OK) return s;
+  if ((s = host_check_strides(strides)) != KB_OK) return s;
   if (B < 1 || H < 1 || L < 1 || start < 0 || start > n_pos - L) return KB_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * ((H + 3) / 4) * ((L + 3) / 4) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
   const void* p[] = {x, out, table};
-  if ((s = device_pointers(p, 3)) != KB_OK) return s;
+  if ((s = host_device_pointers(p, 3)) != KB_OK) return s;
   kb::RopeArgs a{};
   a.x = x;
   a.sb = strides[0];
@@ -260,7 +219,7 @@ kb_status kb_attn_rope(const void* x, const long long* strides, void* out, const
   a.L = L;
   a.start = start;
   a.err = dev.err;
-  return done(kb::launch_rope(a, static_cast<cudaStream_t>(stream)));
+  return host_done(kb::launch_rope(a, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_append(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
@@ -274,19 +233,19 @@ kb_status kb_attn_append(const void* q, const void* k, const void* v, const long
     if (!host_aligned(p[i], 16)) return KB_ERR_INVALID_ARG;
   kb_status s = kb::host_check_heads(B, Hq, Hkv);
   if (s != KB_OK) return s;
-  if (table != nullptr && (s = check_table(table, n_pos, rot_dim)) != KB_OK) return s;
+  if (table != nullptr && (s = host_check_table(table, n_pos, rot_dim)) != KB_OK) return s;
   for (int i = q == nullptr ? 1 : 0; i < 3; ++i)
-    if ((s = check_strides(strides + 3 * i)) != KB_OK) return s;
-  if ((s = check_ragged(starts, lens)) != KB_OK) return s;
+    if ((s = host_check_strides(strides + 3 * i)) != KB_OK) return s;
+  if ((s = host_check_ragged(starts, lens)) != KB_OK) return s;
   int cap = 0;
-  if ((s = cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
+  if ((s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
   if (L < 1 || L > cap) return KB_ERR_INVALID_ARG;
   if (starts == nullptr && (start < 0 || start > cap - L || (table != nullptr && start > n_pos - L)))
     return KB_ERR_INVALID_ARG;
   if ((static_cast<long long>(L) / kb::kTileKeys + 2) * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
-  if ((s = device_pointers(p, 11)) != KB_OK) return s;
+  if ((s = host_device_pointers(p, 11)) != KB_OK) return s;
   kb::AppendArgs a{};
   a.q = q;
   a.k = k;
@@ -316,7 +275,7 @@ kb_status kb_attn_append(const void* q, const void* k, const void* v, const long
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return done(kb::launch_append(a, false, dev.sm_count, static_cast<cudaStream_t>(stream)));
+  return host_done(kb::launch_append(a, false, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, int kv_len, const int* kv_lens,
@@ -327,13 +286,13 @@ kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, 
   kb_status s = kb::host_check_heads(B, kb::kGroup * Hkv, Hkv);
   if (s != KB_OK) return s;
   int cap = 0;
-  if ((s = cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
+  if ((s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
   if (kv_len < 1 || kv_len > cap) return KB_ERR_INVALID_ARG;
   if ((static_cast<long long>(kv_len) / kb::kTileKeys + 2) * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
   const void* p[] = {k_cache, boxes, kv_lens, block_table};
-  if ((s = device_pointers(p, 4)) != KB_OK) return s;
+  if ((s = host_device_pointers(p, 4)) != KB_OK) return s;
   kb::AppendArgs a{};
   a.k_cache = const_cast<void*>(k_cache);
   a.boxes = boxes;
@@ -348,7 +307,7 @@ kb_status kb_attn_block_boxes(const void* k_cache, void* boxes, int B, int Hkv, 
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return done(kb::launch_append(a, true, dev.sm_count, static_cast<cudaStream_t>(stream)));
+  return host_done(kb::launch_append(a, true, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, int B, int Hq, int Hkv, int L,
@@ -359,21 +318,21 @@ kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, i
     return KB_ERR_INVALID_ARG;
   kb_status s = kb::host_check_heads(B, Hq, Hkv);
   if (s != KB_OK) return s;
-  if ((s = check_ragged(starts, lens)) != KB_OK) return s;
+  if ((s = host_check_ragged(starts, lens)) != KB_OK) return s;
   if (n_select < 1 || keep_first < 0 || keep_last < 1 || keep_first > n_select || keep_last > n_select - keep_first)
     return KB_ERR_INVALID_ARG;
   if (n_select > KB_MAX_SELECT) return KB_ERR_UNSUPPORTED;
   if (block_table == nullptr && (n_blocks < 1 || n_blocks > kMaxRows / kb::kTileKeys))
     return n_blocks < 1 ? KB_ERR_INVALID_ARG : KB_ERR_UNSUPPORTED;
   int cap = 0;
-  if ((s = cache_rows(&cap, n_blocks * kb::kTileKeys, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK)
+  if ((s = host_cache_rows(&cap, n_blocks * kb::kTileKeys, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK)
     return s;
   if (L < 1 || L > cap || (starts == nullptr && (start < 0 || start > cap - L))) return KB_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * Hkv * L > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
   const void* p[] = {q, boxes, blocks, starts, lens, block_table};
-  if ((s = device_pointers(p, 6)) != KB_OK) return s;
+  if ((s = host_device_pointers(p, 6)) != KB_OK) return s;
   kb::SelectArgs a{};
   a.q = q;
   a.boxes = boxes;
@@ -394,7 +353,7 @@ kb_status kb_attn_select_blocks(const void* q, const void* boxes, int* blocks, i
   a.pages_per_seq = pages_per_seq;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return done(kb::launch_select(a, dev.index, static_cast<cudaStream_t>(stream)));
+  return host_done(kb::launch_select(a, dev.index, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kb_attn_sparse_workspace_bytes(int B, int Hkv, int L, int n_select, int kv_cap) {
@@ -455,7 +414,7 @@ kb_status kb_attn_sparse_decode(const void* q, const void* k, const void* v, voi
   a.cluster = sparse_cluster(dev, B, Hkv, n_select, max_blocks);
   a.lean = a.cluster == 1 && static_cast<long long>(B) * Hkv > dev.sm_count;
   a.err = dev.err;
-  return done(kb::launch_packed(tk, tv, a, 1, static_cast<cudaStream_t>(stream)));
+  return host_done(kb::launch_packed(tk, tv, a, 1, static_cast<cudaStream_t>(stream)));
 }
 
 size_t kb_attn_sparse_backward_workspace_bytes(int B, int Hkv, int S, int n_select) {
@@ -478,7 +437,7 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   kb::HostDevice dev;
   kb_status s = check_sparse(c, &cap, &dev);
   if (s != KB_OK) return s;
-  if ((s = device_pointers(outs, 6)) != KB_OK) return s;
+  if ((s = host_device_pointers(outs, 6)) != KB_OK) return s;
   kb::SparseBwdArgs a{};
   if ((s = fill_plan(c, cap, dev.err, true, &a.plan)) != KB_OK) return s;
   if (2LL * a.plan.max_blocks * B * Hkv > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
@@ -506,7 +465,7 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
   if (e == cudaSuccess) e = kb::launch_sparse_plan(a.plan, dev.index, st);
   if (e == cudaSuccess) e = kb::launch_bwd_delta(o, dout, delta, static_cast<long long>(B) * Hq * S, st);
   if (e == cudaSuccess) e = kb::launch_sparse_backward(tq, tk, tv, tdo, a, dev.index, dev.sm_count, st);
-  return done(e);
+  return host_done(e);
 }
 
 }  // extern "C"

@@ -57,6 +57,12 @@ struct PackedArgs {
   const int* blocks;
   int n_select;
   bool lean;               // more units than SMs (cluster 1): the shape of which two CTAs share an SM
+  // cache held in 8 bits (kb_cache8.cuh; fold mode): bytes laid out as the bf16
+  // caches, exponents [planes, blocks of a plane]; the tensor maps are unused
+  const uint8_t *k8, *v8;
+  const int8_t *k_exp, *v_exp;
+  int plane_rows;          // rows of a plane: the cache's capacity or the page size
+  float* lse;              // optional [B, Hq, L] fp32 (fold mode): natural-log log-sum-exp of each row's scaled scores
   uint32_t* err;
 };
 
@@ -112,8 +118,12 @@ cudaError_t launch_bwd_delta(const void* o, const void* dout, float* delta, long
 cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
                             cudaStream_t s);
 
+constexpr int kMaxAxes = 4;          // positions a row can have in rope_axes
+constexpr int kPlanesPerLane = 8;    // planes of a row that one lane turns
+
 // Rotation of rows x[b, h, i] (strides in elements, last dimension contiguous)
-// at positions start + i into contiguous out [B, H, L, 128] (kb_append.cu).
+// at positions start + i, or by positions of several axes, into contiguous
+// out [B, H, L, 128] (kb_append.cu).
 struct RopeArgs {
   const void* x;
   long long sb, sh, sl;
@@ -123,6 +133,9 @@ struct RopeArgs {
   bool interleaved, inverse;
   int B, H, L;
   int start;
+  const int* positions;    // optional device [n_axes, B, L], each below n_pos
+  int n_axes, n_pos;
+  uint64_t plane_axes[8];  // axis of planes 8u .. 8u+7, one byte each
   uint32_t* err;
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
@@ -151,6 +164,78 @@ struct AppendArgs {
 // only_boxes: read the cache's keys at the rows' positions and make their
 // blocks' boxes anew (q, k, v unused).
 cudaError_t launch_append(const AppendArgs& a, bool only_boxes, int sm_count, cudaStream_t s);
+
+// Append to a cache held in 8 bits (kb_cache8.cu): a.k_cache and a.v_cache are
+// bytes, a.boxes is unused.
+struct Append8Args {
+  AppendArgs a;
+  int8_t *k_exp, *v_exp;       // [planes, ceil(rows of a plane / 128)]
+};
+cudaError_t launch_append8(const Append8Args& a, cudaStream_t s);
+
+// What a whole 8-bit cache or pool [planes, rows, 128] stands for, as bf16.
+struct Values8Args {
+  const void* cache;
+  const int8_t* exps;          // [planes, blocks]
+  void* out;
+  long long planes;
+  int rows, blocks;            // of a plane; blocks = ceil(rows / 128)
+  uint32_t* err;
+};
+cudaError_t launch_cache_values(const Values8Args& a, cudaStream_t s);
+
+// What a call's visible keys and values stand for, as contiguous bf16 caches
+// [B, Hkv, rows, 128].
+struct Gather8Args {
+  const void *k, *v;
+  const int8_t *k_exp, *v_exp;
+  void *k_out, *v_out;
+  int B, Hkv, L;
+  int rows;                    // positions per sequence of the outputs: start + L, or the capacity (starts given)
+  int blocks;                  // ceil(rows / 128)
+  const int* starts;           // optional device [B] ...
+  const int* lens;             // ... and row counts (else L)
+  int kv_cap;                  // rows of a contiguous cache's plane
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  uint32_t* err;
+};
+cudaError_t launch_cache_gather(const Gather8Args& a, cudaStream_t s);
+
+// Attention weight that each cached key gets from a call's rows (kb_weights.cu).
+struct WeightsArgs {
+  const void* q;               // [B, Hq, L, 128] bf16
+  const float* lse;            // [B, Hq, L]
+  float* weights;              // [B, Hkv, kv_cap], added to
+  int B, Hkv, L;
+  int start;
+  const int* starts;           // optional device [B] ...
+  const int* lens;             // ... and row counts
+  int kv_cap;                  // positions per sequence the cache can hold
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  int splits;                  // CTAs per (batch, KV head)
+  uint32_t* err;
+};
+// tq, tk: host_rows_map of q and of the cache; max_keys: keys of the longest sequence the call can have.
+cudaError_t launch_weights(const CUtensorMap& tq, const CUtensorMap& tk, WeightsArgs a, int max_keys, int sm_count,
+                           cudaStream_t s);
+
+// Eviction of a cache's lightest keys (kb_evict.cu).
+struct EvictArgs {
+  void *k, *v;                 // bf16 caches or pools
+  const float* weights;        // [B, Hkv, kv_cap]
+  float* weights_out;          // the same shape; may be weights
+  int* kept;                   // [B, Hkv, keep]
+  int B, Hkv;
+  const int* lens;             // device [B]
+  int keep, keep_first, keep_last;
+  int kv_cap;                  // positions per sequence the cache can hold
+  const int* block_table;
+  int pages_per_seq, page_size, num_pages;
+  uint32_t* err;
+};
+cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s);
 
 // Choice of key blocks per query row (kb_select.cu).
 struct SelectArgs {

@@ -287,13 +287,8 @@ kb_prefill_kernel_s2(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
       const int i = w.t * kTileRows + row - w.start;                 // query row index in q / o
       if (i >= 0 && i < w.L) {
         const float inv_l = row_inv_l(acc);
-        if (args.lse != nullptr) {
-          // natural-log log-sum-exp of the row's scaled scores: the weights are
-          // 2^(s c - mc), so log2 sum_j 2^(s_j c) = mc + log2(l)
-          constexpr float kLn2 = 0.69314718055994531f;
-          args.lse[(static_cast<size_t>(w.b) * args.Hq + w.h) * static_cast<size_t>(args.L) + i] =
-              __fmul_rn(__fadd_rn(acc.mc, log2f(acc.l)), kLn2);
-        }
+        if (args.lse != nullptr)
+          args.lse[(static_cast<size_t>(w.b) * args.Hq + w.h) * static_cast<size_t>(args.L) + i] = row_lse(acc);
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.o) +
                                               ((static_cast<size_t>(w.b) * args.Hq + w.h) * args.L + i) * kHeadDim);
 #pragma unroll

@@ -64,6 +64,17 @@ _SIGS = {
     "kb_attn_sparse_backward_workspace_bytes": [_I, _I, _I, _I],
     "kb_attn_sparse_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t,
                                 _P],
+    "kb_attn_rope_axes": [_P, _N, _P, _P, _I, _I, _I, _I, _P, _I, ctypes.c_char_p, _I, _I, _I, _P],
+    "kb_attn_append_8bit": [_P, _P, _P, _N, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I,
+                            _I, _P],
+    "kb_attn_cache_values": [_P, _P, _P, ctypes.c_longlong, _I, _P],
+    "kb_attn_chunk_8bit_workspace_bytes": [_I, _I, _I, _I],
+    "kb_attn_chunk_8bit": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P, ctypes.c_size_t,
+                           _P],
+    "kb_attn_decode_8bit": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_chunk_lse": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_key_weights": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_evict": [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _P],
     "kb_status_string": [_I],
     "kb_contract_version": [],
     "kb_attn_last_cuda_error": [],
@@ -229,6 +240,58 @@ def kb_attn_sparse_backward(q, k, v, o, dout, lse, delta, blocks, n_select, dq, 
                             workspace_bytes, stream=None) -> int:
     return _lib.kb_attn_sparse_backward(q, k, v, o, dout, lse, delta, blocks, n_select, dq, dk, dv, B, Hq, Hkv, S,
                                         workspace, workspace_bytes, stream)
+
+
+def kb_attn_rope_axes(x, strides, out, table, n_pos, rot_dim, interleaved, inverse, positions, n_axes, plane_axes, B, H,
+                      L, stream=None) -> int:
+    return _lib.kb_attn_rope_axes(x, strides, out, table, n_pos, rot_dim, interleaved, inverse, positions, n_axes,
+                                  plane_axes, B, H, L, stream)
+
+
+def kb_attn_append_8bit(q, k, v, strides, q_out, k_cache, v_cache, k_exp, v_exp, table, n_pos, rot_dim, interleaved, B,
+                        Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq, page_size, num_pages,
+                        stream=None) -> int:
+    return _lib.kb_attn_append_8bit(q, k, v, strides, q_out, k_cache, v_cache, k_exp, v_exp, table, n_pos, rot_dim,
+                                    interleaved, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq,
+                                    page_size, num_pages, stream)
+
+
+def kb_attn_cache_values(cache, exps, out, planes, rows, stream=None) -> int:
+    return _lib.kb_attn_cache_values(cache, exps, out, planes, rows, stream)
+
+
+def kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows) -> int:
+    return int(_lib.kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows))
+
+
+def kb_attn_chunk_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq,
+                       page_size, num_pages, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.kb_attn_chunk_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table,
+                                   pages_per_seq, page_size, num_pages, workspace, workspace_bytes, stream)
+
+
+def kb_attn_decode_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table, pages_per_seq,
+                        page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_decode_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table,
+                                    pages_per_seq, page_size, num_pages, stream)
+
+
+def kb_attn_chunk_lse(q, k, v, o, lse, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq, page_size,
+                      num_pages, stream=None) -> int:
+    return _lib.kb_attn_chunk_lse(q, k, v, o, lse, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table,
+                                  pages_per_seq, page_size, num_pages, stream)
+
+
+def kb_attn_key_weights(q, k, lse, weights, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq,
+                        page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_key_weights(q, k, lse, weights, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table,
+                                    pages_per_seq, page_size, num_pages, stream)
+
+
+def kb_attn_evict(k, v, weights, weights_out, kept, B, Hkv, lens, keep, keep_first, keep_last, kv_cap, block_table,
+                  pages_per_seq, page_size, num_pages, stream=None) -> int:
+    return _lib.kb_attn_evict(k, v, weights, weights_out, kept, B, Hkv, lens, keep, keep_first, keep_last, kv_cap,
+                              block_table, pages_per_seq, page_size, num_pages, stream)
 
 
 def kb_attn_check_device_status(stream=None) -> int:
@@ -921,3 +984,314 @@ def sparse_backward(q, k, v, o, dout, lse, blocks, delta=None, dq=None, dk=None,
                                     ws.numel() * ws.element_size(), _handle(stream, device)),
             "kb_attn_sparse_backward", check, stream)
     return dq, dk, dv, delta
+
+
+# ------------------------------------------- caches in 8 bits, key weights, eviction, several axes
+
+def _check_type(t, name, dtype, what, ndim):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {what} CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    _on_current_device(t, name)
+
+
+def _need_8bit(t, name, device):
+    if not _plain(t, _torch().float8_e4m3fn, device) or t.dim() != 4:
+        _check_type(t, name, _torch().float8_e4m3fn, "float8_e4m3fn", 4)
+
+
+def _need_exp(t, name, device):
+    if not _plain(t, _torch().int8, device) or t.dim() != 3:
+        _check_type(t, name, _torch().int8, "int8", 3)
+
+
+_shapes_append_8bit = functools.lru_cache(maxsize=1024)(shapes.append_8bit)
+_shapes_cache_values = functools.lru_cache(maxsize=1024)(shapes.cache_values)
+_shapes_attend_8bit = functools.lru_cache(maxsize=1024)(shapes.attend_8bit)
+_shapes_chunk_lse = functools.lru_cache(maxsize=1024)(shapes.chunk_lse)
+_shapes_key_weights = functools.lru_cache(maxsize=1024)(shapes.key_weights)
+_shapes_evict = functools.lru_cache(maxsize=1024)(shapes.evict)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shapes_rope_axes(x, table, positions, planes, out):
+    return (*shapes.rope_axes(x, table, positions, planes, out), bytes(planes))
+
+
+def _need_rows(start, L, cap, n_pos=None):
+    if not 0 <= start <= cap - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the cache's 0..{cap - 1}")
+    if n_pos is not None and start > n_pos - L:
+        raise ValueError(f"positions {start}..{start + L - 1} must lie in the table's 0..{n_pos - 1}")
+
+
+def _ragged(B, starts, lens, device, both=True):
+    if starts is None or (both and lens is None):
+        raise TypeError("starts and lens must be contiguous int32 CUDA tensors" if both else
+                        "starts must be a contiguous int32 CUDA tensor")
+    for t, name in ((starts, "starts"), (lens, "lens")):
+        _need_i32(t, name, device)
+        _per_sequence(B, t, name)
+
+
+def rope_axes(x, table, positions, planes, inverse=False, interleaved=False, out=None, stream=None, check=False):
+    """Rotate x [B,H,L,128] (any strides, last dimension contiguous) by positions int32 [axes,B,L] of one to four axes:
+    plane i of the table's rot_dim/2 turns by its angle at positions[planes[i]].  `planes` lists an axis per plane
+    (three axes in sections of 16, 24 and 24 planes: [0] * 16 + [1] * 24 + [2] * 24).  inverse=True rotates by the
+    negative angle: the gradient of x from that of the result."""
+    device = _device()
+    _check_view(x, "x", device)
+    if not _plain(table, _torch().float32, device):
+        _check_f32(table, "table")
+    if not _plain(positions, _torch().int32, device):
+        _check_i32(positions, "positions")
+    if out is not None:
+        _need_bf16(out, "out", device)
+    B, H, L, n_pos, rot_dim, axes, plane_axes = _shapes_rope_axes(x.shape, table.shape, positions.shape, tuple(planes),
+                                                                  _shape(out))
+    o = _empty((B, H, L, 128), x.dtype, x.device, stream) if out is None else out
+    _finish(kb_attn_rope_axes(x.data_ptr(), _stride_array(*x.stride()[:3]), o.data_ptr(), table.data_ptr(), n_pos,
+                              rot_dim, bool(interleaved), bool(inverse), positions.data_ptr(), axes, plane_axes, B, H, L,
+                              _handle(stream, device)), "kb_attn_rope_axes", check, stream)
+    return o
+
+
+def _append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, start, starts, lens, block_table, interleaved, out,
+                 stream, check):
+    device = _device()
+    if q is not None:
+        _check_view(q, "q", device)
+    _check_view(k, "k", device)
+    _check_view(v, "v", device)
+    _need_8bit(k_cache, "k_cache", device)
+    _need_8bit(v_cache, "v_cache", device)
+    _need_exp(k_exp, "k_exp", device)
+    _need_exp(v_exp, "v_exp", device)
+    _need_f32(table, "table", device)
+    _need_i32(block_table, "block_table", device)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    B, Hq, Hkv, L, cap, num_pages, page, pps, n_pos, rot_dim = _shapes_append_8bit(
+        _shape(q), k.shape, v.shape, k_cache.shape, v_cache.shape, k_exp.shape, v_exp.shape, _shape(table),
+        _shape(block_table), _shape(out))
+    if start is None:
+        _ragged(B, starts, lens, device, both=False)
+        start = 0
+    else:
+        _need_rows(start, L, cap, None if table is None else n_pos)
+    if q is not None and out is None:
+        out = _empty((B, Hq, L, 128), q.dtype, q.device, stream)
+    _finish(kb_attn_append_8bit(_ptr(q), k.data_ptr(), v.data_ptr(),
+                                _stride_array(*_stride3(q), *_stride3(k), *_stride3(v)), _ptr(out), k_cache.data_ptr(),
+                                v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _ptr(table), n_pos, rot_dim,
+                                bool(interleaved), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap,
+                                _ptr(block_table), pps, page, num_pages, _handle(stream, device)),
+            "kb_attn_append_8bit", check, stream)
+    return out
+
+
+def append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, start, interleaved=False, out=None, stream=None,
+                check=False):
+    """append to a cache held in 8 bits: k_cache, v_cache float8_e4m3fn [B,Hkv,cap,128], k_exp, v_exp int8
+    [B,Hkv,ceil(cap/128)], the exponent of two of each block of 128 keys.  Keys are rounded from the fp32 rotation to
+    their bytes at once; a block's bytes are the same for any split of its keys into appends.  Returns the rotated q,
+    contiguous (None without q)."""
+    return _append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, int(start), None, None, None, interleaved, out,
+                        stream, check)
+
+
+def append_8bit_varlen(q, k, v, k_cache, v_cache, k_exp, v_exp, table, starts, lens=None, block_table=None,
+                       interleaved=False, out=None, stream=None, check=False):
+    """append_8bit with a start (and row count, default all rows) per sequence, int32 [B] on the device; with
+    block_table [B,pages_per_seq] the caches are pools [num_pages,Hkv,page_size,128] with exponents
+    [num_pages,Hkv,page_size/128].  Rows of the result from lens[b] on are left as they were."""
+    return _append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, None, starts, lens, block_table, interleaved,
+                        out, stream, check)
+
+
+def cache_values(cache, exps, out=None, stream=None, check=False):
+    """What an 8-bit cache or pool [n,Hkv,rows,128] with exponents [n,Hkv,ceil(rows/128)] stands for, in bfloat16
+    (exactly).  A block with exponent 127 reads as NaN."""
+    device = _device()
+    _need_8bit(cache, "cache", device)
+    _need_exp(exps, "exps", device)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    n, Hkv, rows = _shapes_cache_values(cache.shape, exps.shape, _shape(out))
+    out = _empty(cache.shape, _torch().bfloat16, cache.device, stream) if out is None else out
+    _finish(kb_attn_cache_values(cache.data_ptr(), exps.data_ptr(), out.data_ptr(), n * Hkv, rows,
+                                 _handle(stream, device)), "kb_attn_cache_values", check, stream)
+    return out
+
+
+def _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device):
+    _need_bf16(q, "q", device)
+    _need_8bit(k, "k_cache", device)
+    _need_8bit(v, "v_cache", device)
+    _need_exp(k_exp, "k_exp", device)
+    _need_exp(v_exp, "v_exp", device)
+    _need_i32(block_table, "block_table", device)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    sz = _shapes_attend_8bit(q.shape, k.shape, v.shape, k_exp.shape, v_exp.shape, _shape(block_table), _shape(out))
+    return _empty(q.shape, q.dtype, q.device, stream) if out is None else out, sz
+
+
+def _decode_8bit(q, k, v, k_exp, v_exp, ctx_len, ctx_lens, block_table, out, stream, check):
+    device = _device()
+    o, (B, Hq, Hkv, L, cap, num_pages, page, pps) = _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device)
+    if L != 1:
+        raise ValueError(f"decode takes one query row per (batch, head), got {L}")
+    _need_i32(ctx_lens, "ctx_lens", device)
+    _per_sequence(B, ctx_lens, "ctx_lens")
+    if ctx_lens is None and not 1 <= ctx_len <= cap:
+        raise ValueError(f"ctx_len must lie in 1..{cap} (the cache capacity), got {ctx_len}")
+    _finish(kb_attn_decode_8bit(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
+                                o.data_ptr(), B, Hq, Hkv, ctx_len, _ptr(ctx_lens), cap, _ptr(block_table), pps, page,
+                                num_pages, _handle(stream, device)), "kb_attn_decode_8bit", check, stream)
+    return o
+
+
+def decode_8bit(q, k_cache, v_cache, k_exp, v_exp, ctx_len, out=None, stream=None, check=False):
+    """decode over a cache held in 8 bits (append_8bit): q [B,Hq,1,128] at position ctx_len-1.  The bits are decode's on
+    the bf16 caches that cache_values gives."""
+    return _decode_8bit(q, k_cache, v_cache, k_exp, v_exp, int(ctx_len), None, None, out, stream, check)
+
+
+def decode_8bit_paged(q, k_pages, v_pages, k_exp, v_exp, block_table, ctx_lens, out=None, stream=None, check=False):
+    """decode_paged over pools held in 8 bits."""
+    for t, n in ((block_table, "block_table"), (ctx_lens, "ctx_lens")):
+        _check_i32(t, n)
+    return _decode_8bit(q, k_pages, v_pages, k_exp, v_exp, 0, ctx_lens, block_table, out, stream, check)
+
+
+def _chunk_8bit(q, k, v, k_exp, v_exp, start, starts, lens, block_table, out, workspace, stream, check):
+    device = _device()
+    o, (B, Hq, Hkv, L, cap, num_pages, page, pps) = _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device)
+    if start is None:
+        _ragged(B, starts, lens, device)
+        start, rows = 0, cap
+    else:
+        _need_rows(start, L, cap)
+        rows = start + L
+    nbytes = kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows)
+    ws = _stream_workspace(nbytes, q.device, workspace, stream) if nbytes else None
+    _finish(kb_attn_chunk_8bit(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
+                               o.data_ptr(), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps,
+                               page, num_pages, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _handle(stream, device)), "kb_attn_chunk_8bit", check, stream)
+    return o
+
+
+def chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, start, out=None, workspace=None, stream=None, check=False):
+    """chunk over a cache held in 8 bits (append_8bit): q [B,Hq,L,128] at positions start.. .  The bits are chunk's on the
+    bf16 caches that cache_values gives.  Up to 32 rows read the bytes; a longer chunk turns the visible keys and
+    values into bf16 in a workspace (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
+    return _chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, int(start), None, None, None, out, workspace, stream, check)
+
+
+def chunk_8bit_varlen(q, k, v, k_exp, v_exp, starts, lens, block_table=None, out=None, workspace=None, stream=None,
+                      check=False):
+    """chunk_8bit with a start and row count per sequence, int32 [B] on the device, and optionally pools with
+    block_table [B,pages_per_seq].  Rows from lens[b] on are left as they were."""
+    return _chunk_8bit(q, k, v, k_exp, v_exp, None, starts, lens, block_table, out, workspace, stream, check)
+
+
+def _chunk_lse(q, k, v, start, starts, lens, block_table, out, lse, stream, check):
+    device = _device()
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need_bf16(t, n, device)
+    if out is not None:
+        _need_bf16(out, "out", device)
+    _need_f32(lse, "lse", device)
+    _need_i32(block_table, "block_table", device)
+    B, Hq, Hkv, L, cap, num_pages, page, pps = _shapes_chunk_lse(q.shape, k.shape, v.shape, _shape(block_table),
+                                                                 _shape(out), _shape(lse))
+    if start is None:
+        _ragged(B, starts, lens, device)
+        start = 0
+    else:
+        _need_rows(start, L, cap)
+    o = _empty(q.shape, q.dtype, q.device, stream) if out is None else out
+    lse = _empty((B, Hq, L), _torch().float32, q.device, stream) if lse is None else lse
+    _finish(kb_attn_chunk_lse(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, L,
+                              start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
+                              _handle(stream, device)), "kb_attn_chunk_lse", check, stream)
+    return o, lse
+
+
+def chunk_lse(q, k, v, start, out=None, lse=None, stream=None, check=False):
+    """(o, lse): chunk (decode for one row) with the same bits, and lse [B,Hq,L] float32, the natural-log log-sum-exp
+    of each row's scaled scores."""
+    return _chunk_lse(q, k, v, int(start), None, None, None, out, lse, stream, check)
+
+
+def chunk_lse_varlen(q, k, v, starts, lens, block_table=None, out=None, lse=None, stream=None, check=False):
+    """chunk_varlen with the log-sum-exp of chunk_lse.  Rows of both results from lens[b] on are left as they were."""
+    return _chunk_lse(q, k, v, None, starts, lens, block_table, out, lse, stream, check)
+
+
+def _key_weights(q, k, lse, weights, start, starts, lens, block_table, stream, check):
+    device = _device()
+    _need_bf16(q, "q", device)
+    _need_bf16(k, "k", device)
+    for t, n in ((lse, "lse"), (weights, "weights")):
+        if not _plain(t, _torch().float32, device):
+            _check_f32(t, n)
+    _need_i32(block_table, "block_table", device)
+    B, Hq, Hkv, L, cap, num_pages, page, pps = _shapes_key_weights(q.shape, k.shape, lse.shape, weights.shape,
+                                                                   _shape(block_table))
+    if start is None:
+        _ragged(B, starts, lens, device)
+        start = 0
+    else:
+        _need_rows(start, L, cap)
+    _finish(kb_attn_key_weights(q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), B, Hq, Hkv, L, start,
+                                _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps, page, num_pages,
+                                _handle(stream, device)), "kb_attn_key_weights", check, stream)
+    return weights
+
+
+def key_weights(q, k, lse, weights, start, stream=None, check=False):
+    """Add to weights [B,Hkv,cap] float32 (in place) what each cached key gets from the rows of q [B,Hq,L,128] at
+    positions start..: the sum, over the rows that see it and the four heads of its group, of their softmax weights.
+    lse [B,Hq,L] from chunk_lse or prefill_lse of the same rows; k [B,Hkv,cap,128].  Returns weights."""
+    return _key_weights(q, k, lse, weights, int(start), None, None, None, stream, check)
+
+
+def key_weights_varlen(q, k, lse, weights, starts, lens, block_table=None, stream=None, check=False):
+    """key_weights with a start and row count per sequence, int32 [B] on the device, and optionally pools with
+    block_table [B,pages_per_seq]; weights [B,Hkv,pages_per_seq * page_size] go by position whatever the pages."""
+    return _key_weights(q, k, lse, weights, None, starts, lens, block_table, stream, check)
+
+
+def evict(k_cache, v_cache, weights, lens, keep, keep_first=4, keep_last=64, block_table=None, weights_out=None,
+          kept=None, stream=None, check=False):
+    """Cut each sequence's caches [B,Hkv,cap,128] (or pools with block_table) from lens[b] keys (int32 [B] on the device)
+    to at most `keep` per KV head, in place: the first keep_first, the last keep_last and the heaviest of the others by
+    weights [B,Hkv,cap] float32 stay and move to the front in their old order, ties to the lowest row.  weights_out
+    (default: weights itself) gets the kept keys' weights, zero behind.  Returns kept int32 [B,Hkv,keep]: the old rows,
+    -1 behind the last.  A sequence has min(lens[b], keep) keys afterwards."""
+    torch = _torch()
+    device = _device()
+    _need_bf16(k_cache, "k_cache", device)
+    _need_bf16(v_cache, "v_cache", device)
+    if not _plain(weights, torch.float32, device):
+        _check_f32(weights, "weights")
+    _need_f32(weights_out, "weights_out", device)
+    if not _plain(lens, torch.int32, device):
+        _check_i32(lens, "lens")
+    _need_i32(block_table, "block_table", device)
+    _need_i32(kept, "kept", device)
+    keep, keep_first, keep_last = int(keep), int(keep_first), int(keep_last)
+    B, Hkv, cap, num_pages, page, pps = _shapes_evict(k_cache.shape, v_cache.shape, weights.shape, lens.shape, keep,
+                                                      keep_first, keep_last, _shape(block_table), _shape(weights_out),
+                                                      _shape(kept))
+    weights_out = weights if weights_out is None else weights_out
+    kept = _empty((B, Hkv, keep), torch.int32, weights.device, stream) if kept is None else kept
+    _finish(kb_attn_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), weights_out.data_ptr(),
+                          kept.data_ptr(), B, Hkv, lens.data_ptr(), keep, keep_first, keep_last, cap, _ptr(block_table),
+                          pps, page, num_pages, _handle(stream, device)), "kb_attn_evict", check, stream)
+    return kept

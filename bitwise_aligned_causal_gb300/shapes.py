@@ -253,3 +253,107 @@ def sparse(q, k, v, blocks, block_table=None, out=None) -> tuple:
     _need(len(bl) == 4 and bl[:3] == (B, Hkv, L), f"blocks must have shape [{B}, {Hkv}, {L}, n], got {bl}")
     _need(1 <= bl[3] <= MAX_SELECT, f"blocks must list 1..{MAX_SELECT} per row, got {bl[3]}")
     return B, Hq, Hkv, L, bl[3], cap, num_pages, page, pps
+
+
+# ------------------------------------------- caches in 8 bits, key weights, eviction, several axes
+
+MAX_AXES = 4
+
+
+def exponents(cache, k_exp, v_exp=None) -> None:
+    """Exponents of a cache or pool [planes, Hkv, rows, 128]: one per block of 128 rows."""
+    c = _shape(cache)
+    want = (c[0], c[1], (c[2] + BLOCK - 1) // BLOCK)
+    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+        _need(t is None or _shape(t) == want, f"{name} must have shape {want} (one per block of the cache), got "
+              f"{None if t is None else _shape(t)}")
+
+
+def append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table=None, block_table=None, out=None) -> tuple:
+    """append to a cache held in 8 bits; the result is append's."""
+    sz = append(q, k, v, k_cache, v_cache, table, None, block_table, out)
+    exponents(k_cache, k_exp, v_exp)
+    return sz
+
+
+def cache_values(cache, exps, out=None) -> tuple[int, int, int]:
+    """cache [planes, Hkv, rows, 128], exps [planes, Hkv, blocks].  Returns (planes, Hkv, rows)."""
+    c = _shape(cache)
+    _rows("cache", c)
+    want = (c[0], c[1], (c[2] + BLOCK - 1) // BLOCK)
+    _need(_shape(exps) == want, f"exps must have shape {want} (one per block of the cache), got {_shape(exps)}")
+    if out is not None:
+        _same("out", _shape(out), "cache", c)
+    return c[0], c[1], c[2]
+
+
+def cached(q, k, v, block_table=None, out=None) -> tuple:
+    """q [B,Hq,L,128]; caches [B,Hkv,cap,128], or pools with block_table.
+    Returns (B, Hq, Hkv, L, cap, num_pages, page_size, pages_per_seq)."""
+    if block_table is None:
+        B, Hq, Hkv, L, cap = query_and_cache(q, k, v, out)
+        return B, Hq, Hkv, L, cap, 0, 0, 0
+    B, Hq, Hkv, L, num_pages, page, pps = pools(q, k, v, block_table, out)
+    _need(page % BLOCK == 0, f"page_size must be a multiple of {BLOCK}, got {page}")
+    return B, Hq, Hkv, L, pps * page, num_pages, page, pps
+
+
+def attend_8bit(q, k, v, k_exp, v_exp, block_table=None, out=None) -> tuple:
+    """cached, over a cache held in 8 bits."""
+    sz = cached(q, k, v, block_table, out)
+    _need(sz[3] <= sz[4], f"{sz[3]} query rows exceed the cache's {sz[4]} positions")
+    exponents(k, k_exp, v_exp)
+    return sz
+
+
+def chunk_lse(q, k, v, block_table=None, out=None, lse=None) -> tuple:
+    """cached, with lse [B,Hq,L]."""
+    sz = cached(q, k, v, block_table, out)
+    _need(sz[3] <= sz[4], f"{sz[3]} query rows exceed the cache's {sz[4]} positions")
+    if lse is not None:
+        vector_f32("lse", lse, sz[0], sz[1], sz[3])
+    return sz
+
+
+def key_weights(q, k, lse, weights, block_table=None) -> tuple:
+    """cached, with lse [B,Hq,L] and weights [B,Hkv,cap]."""
+    sz = cached(q, k, k, block_table)
+    _need(sz[3] <= sz[4], f"{sz[3]} query rows exceed the cache's {sz[4]} positions")
+    vector_f32("lse", lse, sz[0], sz[1], sz[3])
+    want = (sz[0], sz[2], sz[4])
+    _need(_shape(weights) == want, f"weights must have shape {want}, got {_shape(weights)}")
+    return sz
+
+
+def evict(k, v, weights, lens, keep: int, keep_first: int, keep_last: int, block_table=None, weights_out=None,
+          kept=None) -> tuple:
+    """Caches as in block_boxes, weights [B,Hkv,cap], lens [B].
+    Returns (B, Hkv, cap, num_pages, page_size, pages_per_seq)."""
+    B, Hkv, cap, num_pages, page, pps, _ = block_boxes(k, block_table)
+    _same("v", _shape(v), "k", _shape(k))
+    want = (B, Hkv, cap)
+    for name, t in (("weights", weights), ("weights_out", weights_out)):
+        _need(t is None or _shape(t) == want, f"{name} must have shape {want}, got {None if t is None else _shape(t)}")
+    per_sequence(B, lens=lens)
+    _need(1 <= keep <= cap, f"keep must lie in 1..{cap} (the cache's positions), got {keep}")
+    _need(keep_first >= 0 and keep_last >= 0 and keep_first + keep_last <= keep,
+          f"keep_first and keep_last must not be negative and add up to at most keep = {keep}, got {keep_first} and "
+          f"{keep_last}")
+    _need(kept is None or _shape(kept) == (B, Hkv, keep), f"kept must have shape {(B, Hkv, keep)}, got "
+          f"{None if kept is None else _shape(kept)}")
+    return B, Hkv, cap, num_pages, page, pps
+
+
+def rope_axes(x, table, positions, planes, out=None) -> tuple[int, int, int, int, int, int]:
+    """x [B,H,L,128], positions [axes,B,L], planes: the axis of each of the table's rot_dim/2 planes.
+    Returns (B, H, L, n_pos, rot_dim, axes)."""
+    x, p = _shape(x), _shape(positions)
+    _rows("x", x)
+    n_pos, rot_dim = rope_table(table)
+    _need(len(p) == 3 and p[1:] == (x[0], x[2]) and 1 <= p[0] <= MAX_AXES,
+          f"positions must be [1..{MAX_AXES} axes, {x[0]}, {x[2]}], got {p}")
+    _need(len(planes) == rot_dim // 2, f"planes must name an axis for each of {rot_dim // 2} planes, got {len(planes)}")
+    _need(min(planes) >= 0 and max(planes) < p[0], f"planes must name axes below {p[0]}, got {min(planes)}..{max(planes)}")
+    if out is not None:
+        _same("out", _shape(out), "x", x)
+    return x[0], x[1], x[2], n_pos, rot_dim, p[0]

@@ -447,6 +447,139 @@ kb_status kb_attn_sparse_backward(const void* q, const void* k, const void* v, c
                                   size_t workspace_bytes, void* stream);
 
 /*
+ * Rotation by positions of several axes (time, height and width of a patch; or
+ * one axis: a position per token, as a cache needs whose rows are no longer
+ * the positions).  As kb_attn_rope, with plane i of row (b, l) turned by
+ * p * inv_freq[i], p = positions[plane_axes[i]][b][l].
+ *   positions  : device int32 [n_axes, B, L], 1 <= n_axes <= 4
+ *   plane_axes : host array of rot_dim/2 axis numbers below n_axes
+ * out may be x itself when x is contiguous, and must not overlap it otherwise.
+ * A position outside 0 .. n_pos-1 is found on the device: that row is not
+ * written, others may not be, and the next kb_attn_check_device_status returns
+ * KB_ERR_INVALID_ARG.
+ */
+kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, const float* table, int n_pos,
+                            int rot_dim, int interleaved, int inverse, const int* positions, int n_axes,
+                            const unsigned char* plane_axes, int B, int H, int L, void* stream);
+
+/*
+ * A KV cache held in 8 bits: e4m3 bytes laid out as the bf16 caches, [B, Hkv,
+ * kv_cap, 128] or pools [num_pages, Hkv, page_size, 128] (16-byte aligned), and
+ * for each block of 128 rows an exponent, int8 [B, Hkv, ceil(kv_cap/128)] or
+ * [num_pages, Hkv, page_size/128], of K and V each.  A byte stands for its
+ * e4m3 value times 2^E, which bf16 holds exactly.
+ * How values get there: E is the smallest integer in -100..100 for which the
+ * block's largest magnitude is at most 448 * 2^E; a value is rounded to four
+ * significant bits (ties to even), and to zero (of its sign) where the rounded
+ * magnitude lies below 2^(E-6); beyond 448 * 2^100 values saturate.  A value
+ * that is not finite makes E 127 and all bytes of the block's keys so far 0x7F:
+ * a block with exponent 127 reads as NaN throughout, until its first row is
+ * written anew.  Exponents below -100 or in 101..126 are read as the nearer of
+ * -100 and 100.
+ *
+ * kb_attn_append_8bit: as kb_attn_append (without boxes).  Keys are rounded
+ * from the fp32 rotation to bytes at once.  Where later keys enlarge a block's
+ * E, its earlier bytes are brought to it; a block has the same bytes and E for
+ * any split of its keys into appends.  Keys overwritten inside a block leave
+ * their E, until the block's first row is written anew.
+ *
+ * kb_attn_cache_values: out [planes, rows, 128] bf16 = what a whole cache or
+ * pool (planes = B * Hkv or num_pages * Hkv, rows = kv_cap or page_size)
+ * stands for.  Rows that were never written give whatever their bytes say.
+ *
+ * kb_attn_chunk_8bit, kb_attn_decode_8bit: rows at start .. start+L-1 of every
+ * sequence, or (starts and lens != NULL, device int32 [B]) lens[b] rows at
+ * starts[b]..; one token at ctx_len - 1, or (ctx_lens != NULL) at ctx_lens[b] -
+ * 1.  Contiguous caches, or pools where block_table != NULL.  The result has
+ * the bits of kb_attn_chunk, _paged, _varlen and kb_attn_decode on a bf16 cache
+ * that holds the same values, so a row has the same bits in any split over the
+ * same cache; a later append that enlarges a block's E can change its smallest
+ * values (those below 2^(E-6)) for rows computed after it.
+ * L <= 32 reads the bytes and needs no workspace.  A longer chunk is computed
+ * from the visible values in bf16, in a device workspace (256-byte aligned,
+ * caller-owned, contents scratch) of kb_attn_chunk_8bit_workspace_bytes(B, Hkv,
+ * L, rows) bytes, rows being start + L, or the cache's positions per sequence
+ * when starts is given; calls that can overlap on the GPU need one each.
+ */
+kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
+                              void* k_cache, void* v_cache, signed char* k_exp, signed char* v_exp,
+                              const float* table, int n_pos, int rot_dim, int interleaved, int B, int Hq, int Hkv,
+                              int L, int start, const int* starts, const int* lens, int kv_cap,
+                              const int* block_table, int pages_per_seq, int page_size, int num_pages,
+                              void* stream);
+kb_status kb_attn_cache_values(const void* cache, const signed char* exps, void* out, long long planes, int rows,
+                               void* stream);
+size_t kb_attn_chunk_8bit_workspace_bytes(int B, int Hkv, int L, int rows);
+kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const signed char* k_exp,
+                             const signed char* v_exp, void* o, int B, int Hq, int Hkv, int L, int start,
+                             const int* starts, const int* lens, int kv_cap, const int* block_table,
+                             int pages_per_seq, int page_size, int num_pages, void* workspace,
+                             size_t workspace_bytes, void* stream);
+kb_status kb_attn_decode_8bit(const void* q, const void* k, const void* v, const signed char* k_exp,
+                              const signed char* v_exp, void* o, int B, int Hq, int Hkv, int ctx_len,
+                              const int* ctx_lens, int kv_cap, const int* block_table, int pages_per_seq,
+                              int page_size, int num_pages, void* stream);
+
+/*
+ * kb_attn_chunk (starts and lens NULL) or kb_attn_chunk_varlen, contiguous or
+ * paged, plus each row's log-sum-exp as kb_attn_prefill_lse gives it: lse
+ * [B, Hq, L] fp32, rows from lens[b] on left as they were.  o has the same bits
+ * as without; L = 1 is a decode.
+ */
+kb_status kb_attn_chunk_lse(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                            int Hkv, int L, int start, const int* starts, const int* lens, int kv_cap,
+                            const int* block_table, int pages_per_seq, int page_size, int num_pages, void* stream);
+
+/*
+ * Add the attention weight that each cached key gets from a call's rows:
+ *   weights[b, g, j] += sum over rows i with j <= p_i, and heads h of group g,
+ *                       of exp(q_i . k_j / sqrt(128) - lse[b, h, i])
+ * with p_i = start + i, or starts[b] + i for i < lens[b] (both device int32
+ * [B], or both NULL).
+ *   q       : [B, Hq, L, 128] bf16, k: a contiguous cache or pools, as in
+ *             kb_attn_chunk_varlen; lse: [B, Hq, L] fp32 from kb_attn_chunk_lse
+ *             or kb_attn_prefill_lse of the same rows
+ *   weights : [B, Hkv, kv_cap] fp32 (pages_per_seq * page_size of a paged
+ *             cache), by position whatever the pages; entries of keys that no
+ *             row sees are left as they were
+ * A row whose lse is -inf (it saw nothing) or +inf adds nothing.  Every sum has
+ * one order that depends on the call's sizes and lengths alone: repeated calls
+ * give identical bits.  Out-of-range starts, lens or page indices are found on
+ * the device (the sequence's, or that key block's, weights stay) and reported
+ * by the next kb_attn_check_device_status as KB_ERR_INVALID_ARG.
+ */
+kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, float* weights, int B, int Hq,
+                              int Hkv, int L, int start, const int* starts, const int* lens, int kv_cap,
+                              const int* block_table, int pages_per_seq, int page_size, int num_pages,
+                              void* stream);
+
+/*
+ * Cut each sequence's cache to at most `keep` keys per KV head.  Of the n =
+ * lens[b] keys (device int32 [B], 0..capacity) of every KV head the first
+ * keep_first and the last keep_last stay, and of the others those of the
+ * largest weights until `keep` are kept, ties to the lowest row; a NaN counts
+ * as larger than any number.  The kept rows of K and V move to rows 0 ..
+ * min(n, keep)-1 in their old order, in place; rows behind are left as they
+ * were.  A sequence of at most `keep` keys stays as it is.
+ *   k, v        : bf16 contiguous caches [B, Hkv, kv_cap, 128] or pools, in
+ *                 which no two sequences share a page
+ *   weights     : [B, Hkv, kv_cap] fp32 (positions per sequence of a paged
+ *                 cache) as kb_attn_key_weights adds them
+ *   weights_out : the same shape: the kept keys' weights, zero behind; may be
+ *                 weights itself, and must not overlap it otherwise
+ *   kept        : int32 [B, Hkv, keep] (output): the old rows of the kept keys,
+ *                 ascending, -1 behind the last
+ * keep_first + keep_last <= keep <= capacity.  New keys go to row min(n, keep)
+ * on; their positions are no longer their rows (kb_attn_rope_axes).  Boxes of
+ * the cache's blocks must be made anew (kb_attn_block_boxes).  An out-of-range
+ * lens or page index is found on the device (nothing of that sequence moves)
+ * and reported by the next kb_attn_check_device_status as KB_ERR_INVALID_ARG.
+ */
+kb_status kb_attn_evict(void* k, void* v, const float* weights, float* weights_out, int* kept, int B, int Hkv,
+                        const int* lens, int keep, int keep_first, int keep_last, int kv_cap,
+                        const int* block_table, int pages_per_seq, int page_size, int num_pages, void* stream);
+
+/*
  * Prefill/chunk with an explicit kernel shape, for tests of the contract:
  * q_tiles_per_cta = 3 runs the tile kernel (one 128-row query tile per CTA,
  * one CTA per SM, three score buffers, so Q K^T of later key tiles overlaps
