@@ -74,24 +74,33 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 // Four bytes as two bf16 pairs.  A byte's exponent and mantissa moved to the
 // bf16 places give its value times 2^-120 (the biases differ by 120, and the
-// product is exact for e4m3's own subnormals too).
-__device__ __forceinline__ uint2 values8(uint32_t w, const Scale8& s) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);   // bytes in the upper halves
-  uint2 r;
-  r.x = mul_bf16x2(((a & 0x7F007F00u) >> 4) | (a & 0x80008000u), s.first);
-  r.y = mul_bf16x2(((b & 0x7F007F00u) >> 4) | (b & 0x80008000u), s.first);
-  if (s.two) {                                     // one decision per block
-    r.x = mul_bf16x2(r.x, s.second);
-    r.y = mul_bf16x2(r.y, s.second);
-  }
-  return r;
+// product is exact for e4m3's own subnormals too).  The permutation puts eight
+// copies of a byte's sign above it, so one shift and one mask place all three
+// fields.
+__device__ __forceinline__ uint2 values8(uint32_t w, uint32_t first) {
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));         // sign byte 1 | byte 1 | sign byte 0 | byte 0
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(w));
+  return make_uint2(mul_bf16x2((a << 4) & 0x87F087F0u, first), mul_bf16x2((b << 4) & 0x87F087F0u, first));
 }
 
 // Sixteen bytes as sixteen bf16 values.
-__device__ __forceinline__ void values8x16(const uint4& w, const Scale8& s, uint4& lo, uint4& hi) {
-  const uint2 a = values8(w.x, s), b = values8(w.y, s), c = values8(w.z, s), d = values8(w.w, s);
+__device__ __forceinline__ void values8x16(const uint4& w, uint32_t first, uint4& lo, uint4& hi) {
+  const uint2 a = values8(w.x, first), b = values8(w.y, first), c = values8(w.z, first), d = values8(w.w, first);
   lo = make_uint4(a.x, a.y, b.x, b.y);
   hi = make_uint4(c.x, c.y, d.x, d.y);
+}
+
+// The same for any exponent: a second factor where one does not reach.
+__device__ __forceinline__ uint4 scaled_again(const uint4& v, uint32_t second) {
+  return make_uint4(mul_bf16x2(v.x, second), mul_bf16x2(v.y, second), mul_bf16x2(v.z, second), mul_bf16x2(v.w, second));
+}
+__device__ __forceinline__ void values8x16(const uint4& w, const Scale8& s, uint4& lo, uint4& hi) {
+  values8x16(w, s.first, lo, hi);
+  if (s.two) {                                     // one decision per block
+    lo = scaled_again(lo, s.second);
+    hi = scaled_again(hi, s.second);
+  }
 }
 
 }  // namespace kb

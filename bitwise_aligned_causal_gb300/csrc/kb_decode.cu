@@ -57,14 +57,13 @@ namespace kb {
 // kSparse with one S buffer is the lean shape: half of TMEM and of shared
 // memory, so that two CTAs share an SM.
 // k8: the cache is held in 8 bits, and four warps per ring take the TMA
-// producer's place: they load a tile's bytes into registers (a tile ahead, so
-// that the loads of one are in flight while the last is written), turn them
-// into the bf16 values they stand for and write those to the ring in the
-// swizzled layout that TMA gives.  Staging the bytes in shared memory instead
-// would add their write and read to the 160 KB that a pair of tiles moves
-// through it (values in, MMA operands out) and make that the bound: 1750
-// cycles of 128 B against the 1390 in which HBM brings a pair to each SM.
-// The rest of the kernel is the same, and so are the bits.
+// producer's place: one of their threads has TMA bring a tile's bytes to a
+// staging ring, all of them read it, turn the bytes into the bf16 values they
+// stand for and write those to the K or V ring in the swizzled layout that TMA
+// gives the others.  The rest of the kernel is the same, and so are the bits.
+// Staging by TMA, not in registers: with four half tiles in registers the
+// loads' latency came through on every half (the few scoreboards of a warp do
+// not tell them apart), 2.2 us a pair of tiles against 1.1 without the loads.
 template <bool kWide, int kNumSBufs, bool kSparse = false, bool k8 = false>
 struct PackedCfg {
   static constexpr bool kLean = kSparse && kNumSBufs == 1;
@@ -81,8 +80,9 @@ struct PackedCfg {
   // x 128 (softmax, issuers and two idle warps, the two rings)
   static constexpr uint32_t kSoftmaxRegs = 232, kIssuerRegs = 64, kRingRegs = 104;
   static_assert(kSoftmaxRegs + kIssuerRegs + 2 * kRingRegs <= 512, "register split above the launch's registers");
-  static constexpr int kKStages = kLean ? 2 : 3;
-  static constexpr int kVStages = kLean ? 1 : 3;
+  static constexpr int kKStages = kLean || k8 ? 2 : 3;
+  static constexpr int kVStages = kLean ? 1 : k8 ? 2 : 3;
+  static constexpr int kByteStages = k8 ? 2 : 0;            // staged tiles of bytes, per ring
   static constexpr int kQRows = kWide ? 128 : 8;
   static constexpr int kSBufs = kNumSBufs;
   static constexpr bool kFoldTmem = kWide && kNumSBufs == 2;  // wide fold mode: folded O in TMEM
@@ -94,7 +94,9 @@ struct PackedCfg {
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kKOff = 2 * kQSlab;
   static constexpr uint32_t kVOff = kKOff + kKStages * kTileBytes;
-  static constexpr uint32_t kBarOff = kVOff + kVStages * kTileBytes;
+  static constexpr uint32_t kByteOff = kVOff + kVStages * kTileBytes;       // K's staged tiles, then V's
+  static constexpr uint32_t kByteTile = kTileBytes / 2;
+  static constexpr uint32_t kBarOff = kByteOff + 2 * kByteStages * kByteTile;
   static constexpr int kBarKFull = 0;
   static constexpr int kBarKEmpty = kBarKFull + kKStages;
   static constexpr int kBarVFull = kBarKEmpty + kKStages;
@@ -110,7 +112,8 @@ struct PackedCfg {
   static constexpr int kBarDrain = kBarPart + 1;           // 2: one per MMA issuer
   static constexpr int kBarQReady = kBarDrain + 2;         // Q written to shared memory by its loaders
   static constexpr int kBarGo = kBarQReady + 1;            // gather: the first CTA's K/V rings are free
-  static constexpr int kNumBars = kBarGo + 1;
+  static constexpr int kBarBytes = kBarGo + 1;             // 8 bits: a staged tile has landed (K's stages, then V's)
+  static constexpr int kNumBars = kBarBytes + 2 * kByteStages;
   // Q is loaded by the softmax warps (and the fold warp when narrow) while
   // the producers' first K/V loads are already in flight
   static constexpr int kQLoaders = 32 * (kSoftmaxWarps + (kWide ? 0 : 1));
@@ -130,8 +133,10 @@ struct PackedCfg {
 };
 
 // Partials a narrow CTA can hold in shared memory, for n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows, bool sparse) {
-  return (sparse ? PackedCfg<false, 3, true>::kPartBytes : PackedCfg<false, 3>::kPartBytes) /
+uint32_t packed_partial_slots(int n_rows, bool sparse, bool bytes) {
+  return (sparse  ? PackedCfg<false, 3, true>::kPartBytes
+          : bytes ? PackedCfg<false, 3, false, true>::kPartBytes
+                  : PackedCfg<false, 3>::kPartBytes) /
          (static_cast<uint32_t>(n_rows) * kPartFloats * 4u);
 }
 
@@ -213,69 +218,103 @@ __device__ __forceinline__ int2 build_walk(const int* list, int n_select, int ow
 }
 
 // The four warps of a ring (K or V) whose cache is held in 8 bits: key tiles
-// j0 .. j0 + nt - 1 of sequence b, KV head g.  Eight threads take a row (16
-// bytes each), sixteen rows a pass.  Rows from seq_kv on are not read and are
-// zero in the ring.  The upper half of a row goes out with its two chunks in
-// the other order: so the eight threads of a row write to all eight 16-byte
-// columns of the swizzle atom at once.
+// j0 .. j0 + nt - 1 of sequence b, KV head g.  A staged tile has rows of 128
+// bytes, its eight 16-byte columns swizzled as TMA does (column c of row r at c
+// ^ (r % 8)).  A thread takes one column of eight rows.  Lanes 8i .. 8i+3 hold
+// four neighbouring columns of a row, lanes 8i+4 .. 8i+7 the same of the row
+// whose number differs in bits 0 and 2: so the eight read from all eight
+// swizzled columns of the staged tile, and write to all eight of the bf16
+// tile.  Rows from seq_kv on are zero in the ring, whatever the cache holds.
 template <typename Cfg>
-__device__ __forceinline__ void fill_ring8(const PackedArgs& args, bool is_v, uint8_t* ring, int b, int g, int j0, int nt,
-                                           int seq_kv, uint32_t full0, uint32_t empty0, volatile uint32_t* abort_flag) {
+__device__ __forceinline__ void fill_ring8(const CUtensorMap* tmap, const PackedArgs& args, bool is_v, uint8_t* ring,
+                                           uint8_t* staged, int b, int g, int j0, int nt, int seq_kv, uint32_t full0,
+                                           uint32_t empty0, uint32_t bytes0, volatile uint32_t* abort_flag) {
   const int warp = static_cast<int>(threadIdx.x >> 5);
   const int t = 32 * max(warp - (is_v ? Cfg::kVProdWarp : Cfg::kKProdWarp), 0) + static_cast<int>(threadIdx.x & 31);   // (warp 3: the first)
-  const int col = t & 7, row0 = t >> 3;
-  const uint8_t* bytes = is_v ? args.v8 : args.k8;
+  const int col = (t & 3) | ((t >> 1) & 4);
+  const int low = ((t >> 4) & 3) ^ ((t & 4) ? 5 : 0);      // row % 8
+  const int row0 = low + 8 * (t >> 6);                     // rows row0 + 16 i
+  const uint8_t* src0 = staged + row0 * 128 + ((col ^ low) << 4);
+  // chunks 2 col and 2 col + 1 of the bf16 row, in slab col / 4
+  uint8_t* dst0 = ring + (col >> 2) * kSlabBytes + (row0 >> 3) * 1024 + low * 128 + (((2 * (col & 3)) ^ low) << 4);
+  const int next_chunk = (low & 1) ? -16 : 16;
   const int8_t* exps = is_v ? args.v_exp : args.k_exp;
   const int blocks = (args.plane_rows + kTileKeys - 1) / kTileKeys;
-  const int stages = is_v ? Cfg::kVStages : Cfg::kKStages;
-  const uint32_t swap = col >= 4 ? 1u : 0u;
-  // chunks 2 col and 2 col + 1 of the bf16 row, in slab col / 4
-  uint8_t* dst0 = ring + (col >> 2) * kSlabBytes;
-  const uint32_t c0 = ((2 * (col & 3) + swap) ^ (row0 & 7)) << 4, c1 = ((2 * (col & 3) + (swap ^ 1u)) ^ (row0 & 7)) << 4;
-
-  struct Tile {
-    uint4 w[8];
-    int n, e;                                              // rows of the sequence, exponent
-  };
-  auto load = [&](int jj, Tile& x) {
+  constexpr int kStages = Cfg::kKStages, kByteStages = Cfg::kByteStages;
+  static_assert(Cfg::kKStages == Cfg::kVStages, "one walk for both rings");
+  const uint64_t stream_once = l2_policy_evict_first();
+  int issued = 0;
+  auto issue = [&](int jj) {                               // thread 0
     int row = 0, plane = 0;
-    const bool in_pool = kv_tile_coords(args, b, g, j0 + jj, row, plane);
-    x.n = in_pool ? min(kTileKeys, seq_kv - (j0 + jj) * kTileKeys) : 0;
-    x.e = x.n > 0 ? exps[static_cast<size_t>(plane) * blocks + row / kTileKeys] : 0;
-    const uint8_t* src = bytes + (static_cast<size_t>(plane) * args.plane_rows + row + row0) * kHeadDim + col * 16;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (row0 + 16 * i < x.n) x.w[i] = ld_stream16(src + static_cast<size_t>(i) * 16 * kHeadDim);
+    kv_tile_coords(args, b, g, j0 + jj, row, plane);
+    const int st = jj % kByteStages;
+    mbar_arrive_expect_tx(bytes0 + 8u * st, Cfg::kByteTile);
+    tma_load_3d_hint(smem_addr(staged) + st * Cfg::kByteTile, tmap, 0, row, plane, bytes0 + 8u * st, stream_once);
+    issued = jj + 1;
   };
-  auto store = [&](int jj, const Tile& x) {
-    const int slot = jj % stages;
-    if (jj >= stages) {
-      const bool ok = mbar_wait(empty0 + 8u * slot, (jj / stages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
-      if (!__all_sync(0xffffffffu, ok)) return false;
+  // the exponent of tile jj (any number for a page out of range)
+  auto exponent_of = [&](int jj) {
+    if (jj >= nt) return 0;
+    const int key = (j0 + jj) * kTileKeys;
+    size_t at = (static_cast<size_t>(b) * args.Hkv + g) * blocks + key / kTileKeys;
+    if (args.block_table != nullptr) {
+      const int pg = __ldg(args.block_table + static_cast<size_t>(b) * args.pages_per_seq + key / args.page_size);
+      if (pg < 0 || pg >= args.num_pages) return 0;
+      at = (static_cast<size_t>(pg) * args.Hkv + g) * blocks + key % args.page_size / kTileKeys;
     }
-    const Scale8 sc = scale8(x.e);
-    uint8_t* dst = dst0 + slot * kTileBytes;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-      if (row0 + 16 * i < x.n) values8x16(x.w[i], sc, lo, hi);
-      uint8_t* r = dst + ((row0 + 16 * i) >> 3) * 1024 + (row0 & 7) * 128;
-      *reinterpret_cast<uint4*>(r + c0) = swap ? hi : lo;
-      *reinterpret_cast<uint4*>(r + c1) = swap ? lo : hi;
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(full0 + 8u * slot);
-    return true;
+    return static_cast<int>(exps[at]);
   };
-  Tile x, y;
-  load(0, x);
-  if (!__all_sync(0xffffffffu, no_error(args.err, abort_flag))) return;
-  for (int jj = 0; jj < nt; jj += 2) {
-    if (jj + 1 < nt) load(jj + 1, y);
-    if (!store(jj, x)) return;
-    if (jj + 2 < nt) load(jj + 2, x);
-    if (jj + 1 < nt && !store(jj + 1, y)) return;
+  if (t == 0) {
+    tma_prefetch_desc(tmap);
+    for (int jj = 0; jj < min(nt, kByteStages); ++jj) issue(jj);
   }
+  int e = exponent_of(0);
+  bool ok = no_error(args.err, abort_flag);
+#pragma unroll 1
+  for (int jj = 0; jj < nt; ++jj) {
+    const int st = jj % kByteStages, slot = jj % kStages;
+    ok = ok && mbar_wait(bytes0 + 8u * st, (jj / kByteStages) & 1, abort_flag, args.err, kDevTimeoutTma);
+    uint4 w[8];
+    const uint8_t* src = src0 + st * Cfg::kByteTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
+    // the stage is read; one decision for the four warps: all go on, or none does
+    if (named_bar_or(is_v ? 3u : 2u, 128u, !ok)) {
+      if (t == 0)
+        for (int x = max(0, issued - kByteStages); x < issued; ++x) packed_drain_wait(bytes0 + 8u * (x % kByteStages), (x / kByteStages) & 1);
+      return;
+    }
+    if (t == 0 && jj + kByteStages < nt) issue(jj + kByteStages);
+    const Scale8 sc = scale8(e);
+    e = exponent_of(jj + 1);
+    if (jj >= kStages) ok = mbar_wait(empty0 + 8u * slot, (jj / kStages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
+    if (ok) {
+      uint8_t* dst = dst0 + slot * kTileBytes;
+      const int n = seq_kv - (j0 + jj) * kTileKeys;        // rows of the sequence in the tile
+      if (n >= kTileKeys && !sc.two) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 lo, hi;
+          values8x16(w[i], sc.first, lo, hi);
+          *reinterpret_cast<uint4*>(dst + i * 2048) = lo;
+          *reinterpret_cast<uint4*>(dst + i * 2048 + next_chunk) = hi;
+        }
+      } else {
+        // the sequence's last tile, or values beyond 448 * 2^7
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 lo, hi;
+          values8x16(w[i], sc, lo, hi);
+          if (row0 + 16 * i >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);    // (a marked block's factor is NaN)
+          *reinterpret_cast<uint4*>(dst + i * 2048) = lo;
+          *reinterpret_cast<uint4*>(dst + i * 2048 + next_chunk) = hi;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(full0 + 8u * slot);
+    }
+  }
+  // a wait that failed on the last tile leaves nothing in flight: every staged tile has been waited for
 }
 
 // kSparse (narrow, one query row per head): the row's key tiles are those of
@@ -540,9 +579,11 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     if constexpr (k8) {
       if constexpr (kWide) regs_decrease<Cfg::kRingRegs>();
       const bool is_v = warp >= Cfg::kVProdWarp;
-      if (run) fill_ring8<Cfg>(args, is_v, smem + (is_v ? Cfg::kVOff : Cfg::kKOff), b, g, j0, nt, seq_kv,
-                               bar(is_v ? Cfg::kBarVFull : Cfg::kBarKFull), bar(is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty),
-                               abort_flag);
+      if (run)
+        fill_ring8<Cfg>(is_v ? &tmap_v : &tmap_k, args, is_v, smem + (is_v ? Cfg::kVOff : Cfg::kKOff),
+                        smem + Cfg::kByteOff + (is_v ? Cfg::kByteStages * Cfg::kByteTile : 0u), b, g, j0, nt, seq_kv,
+                        bar(is_v ? Cfg::kBarVFull : Cfg::kBarKFull), bar(is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty),
+                        bar(Cfg::kBarBytes + (is_v ? Cfg::kByteStages : 0)), abort_flag);
     }
     if (C > 1) {
       cluster_wait();
@@ -1217,7 +1258,7 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     if (a.lean) return launch_packed_t<false, 1, true>(tk, tv, a, n_sub, s);
     return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
   }
-  if (a.k8 != nullptr)
+  if (a.k_exp != nullptr)
     return a.L <= 2 ? launch_packed_t<false, 3, false, true>(tk, tv, a, n_sub, s)
                     : launch_packed_t<true, 2, false, true>(tk, tv, a, n_sub, s);
   if (a.L <= 2) return launch_packed_t<false, 3>(tk, tv, a, n_sub, s);

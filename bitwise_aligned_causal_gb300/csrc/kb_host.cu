@@ -381,6 +381,17 @@ kb_status host_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_
   return encode_rows_map(m, base, rows, planes, plane_stride);
 }
 
+kb_status host_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), rows, planes};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim), plane_stride};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(kHeadDim), static_cast<cuuint32_t>(kTileKeys), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KB_OK : KB_ERR_CUDA;
+}
+
 kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t groups) {
   const cuuint64_t head_stride = rows * kHeadDim * 2u;
   cuuint64_t dims[5] = {64u, rows, static_cast<cuuint64_t>(kGroup), 2u, groups};
@@ -398,12 +409,12 @@ kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64
 // alone would leave SMs idle.  Narrow rows only; the other CTAs of a cluster
 // keep their segments' partials in shared memory, so a CTA may own at most
 // as many segments as it has partial slots.
-int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max) {
+int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max, bool bytes) {
   if (L > 2) return 1;
   const long long units = static_cast<long long>(n_sub) * B * Hkv;
   if (2 * units > sm_count) return 1;
   const int ns = (n_kv_max + kSegTiles - 1) / kSegTiles;
-  const long long slots = packed_partial_slots(kGroup * L);
+  const long long slots = packed_partial_slots(kGroup * L, false, bytes);
   for (int i = 3, c = 8; i >= 1; --i, c /= 2) {
     if (c > ns || units > cluster_fit[i]) continue;
     if ((ns + c - 1) / c > slots) continue;

@@ -30,13 +30,17 @@ kb_status host_device_pointer(const void* p);
 // Tensor map of whole 128-row tiles: box {64 columns, 128 rows, 2 halves} of
 // a [planes, rows, 128] bf16 tensor (kb_host.cu).
 kb_status host_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride);
+// Tensor map of whole 128-row tiles of a cache held in 8 bits: box {128 bytes,
+// 128 rows} of a [planes, rows, 128] byte tensor, 128-byte swizzle.
+kb_status host_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride);
 // Tensor map of query rows packed by GQA group: box {64 columns, 32 rows,
 // 4 heads, 2 halves} of a [planes * 4 heads, rows, 128] bf16 tensor, so one
 // load brings the 32 rows of a KV head's four query heads as one 128-row tile
 // (row 32 * head + r) in two swizzled slabs.
 kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t groups);
 // CTAs per (sub-chunk, batch, KV head) of the packed kernel's fold mode.
-int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max);
+int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max,
+                        bool bytes = false);
 kb_status host_check_heads(int B, int Hq, int Hkv);
 // A page table: pages_per_seq * page_size positions per sequence, page_size a
 // multiple of 128.

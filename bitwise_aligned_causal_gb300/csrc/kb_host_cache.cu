@@ -79,15 +79,21 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* stre
   a.n_sub = n_sub;
   const long long keys = ragged || c.ctx_lens != nullptr ? cap : static_cast<long long>(c.start) + c.L;
   a.fold_seg = kb::kSegTiles;
-  a.cluster = kb::host_choose_cluster(dev.sm_count, dev.cluster_fit, c.L, n_sub, c.B, c.Hkv, static_cast<int>(blocks_of(keys)));
-  a.k8 = static_cast<const uint8_t*>(c.k);
-  a.v8 = static_cast<const uint8_t*>(c.v);
+  a.cluster = kb::host_choose_cluster(dev.sm_count, dev.cluster_fit, c.L, n_sub, c.B, c.Hkv, static_cast<int>(blocks_of(keys)), true);
   a.k_exp = c.k_exp;
   a.v_exp = c.v_exp;
   a.plane_rows = c.block_table != nullptr ? c.page_size : c.kv_cap;
   a.err = dev.err;
-  const CUtensorMap unused{};
-  return host_done(kb::launch_packed(unused, unused, a, n_sub, static_cast<cudaStream_t>(stream)));
+  // the maps end where the attention's do: a contiguous uniform cache at the call's last key
+  const bool paged = c.block_table != nullptr;
+  const uint64_t rows = paged || ragged || c.ctx_lens != nullptr ? static_cast<uint64_t>(a.plane_rows) : static_cast<uint64_t>(keys);
+  const uint64_t planes = static_cast<uint64_t>(paged ? c.num_pages : c.B) * c.Hkv;
+  const uint64_t stride = static_cast<uint64_t>(a.plane_rows) * kb::kHeadDim;
+  CUtensorMap tk, tv;
+  kb_status s = kb::host_bytes_map(&tk, c.k, rows, planes, stride);
+  if (s != KB_OK) return s;
+  if ((s = kb::host_bytes_map(&tv, c.v, rows, planes, stride)) != KB_OK) return s;
+  return host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
 }
 
 // Bytes of one of the two bf16 caches that a longer chunk is computed from.

@@ -58,8 +58,8 @@ struct PackedArgs {
   int n_select;
   bool lean;               // more units than SMs (cluster 1): the shape of which two CTAs share an SM
   // cache held in 8 bits (kb_cache8.cuh; fold mode): bytes laid out as the bf16
-  // caches, exponents [planes, blocks of a plane]; the tensor maps are unused
-  const uint8_t *k8, *v8;
+  // caches and brought by the tensor maps (host_bytes_map), exponents [planes,
+  // blocks of a plane] (null: a bf16 cache)
   const int8_t *k_exp, *v_exp;
   int plane_rows;          // rows of a plane: the cache's capacity or the page size
   float* lse;              // optional [B, Hq, L] fp32 (fold mode): natural-log log-sum-exp of each row's scaled scores
@@ -89,7 +89,7 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
                           cudaStream_t s);
 // Partials a CTA of the narrow packed kernel can keep in shared memory for
 // the cluster's first CTA, with n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows, bool sparse = false);
+uint32_t packed_partial_slots(int n_rows, bool sparse = false, bool bytes = false);
 // Clusters of 2, 4 and 8 CTAs (entries 1, 2, 3) of the narrow packed kernel
 // the current device runs at once; entry 0 is unused.
 void packed_cluster_capacity(int (&active)[4]);
