@@ -47,7 +47,10 @@
 //    Narrow rows only take C > 1; wide chunks run C = 1 with the folded O in
 //    TMEM.
 //  - workspace mode (the *_seg entry points): one CTA per segment writes its
-//    partial to a caller workspace, which kb_seg_fold_kernel folds.
+//    partial to a caller workspace, which kb_seg_fold_kernel folds.  Over a
+//    cache held in 8 bits a CTA takes a contiguous block of segments, as many
+//    CTAs per (sub-chunk, batch, KV head) as fill the SMs, and leaves each
+//    segment's partial there (kb_rows_fold_kernel).
 #include "kb_cache8.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
@@ -339,10 +342,14 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const int lane = threadIdx.x & 31;
   const int bh = args.B * args.Hkv;
   const bool ws_mode = args.part != nullptr;                 // one segment per CTA, partials to a workspace
-  const int C = ws_mode ? 1 : args.cluster;                  // CTAs per (sub-chunk, b, kv head)
-  const int rank = ws_mode ? 0 : static_cast<int>(blockIdx.x) % C;
-  const int seg_ws = ws_mode ? static_cast<int>(blockIdx.x) / (args.n_sub * bh) : 0;
-  const int cta = ws_mode ? static_cast<int>(blockIdx.x) % (args.n_sub * bh) : static_cast<int>(blockIdx.x) / C;
+  const bool ws_block = k8 && ws_mode;                       // ... or a block of segments per CTA
+  const int C = ws_mode ? 1 : args.cluster;                  // CTAs per (sub-chunk, b, kv head) in a cluster
+  const int parts = ws_block ? args.split : C;               // ... that share its segments
+  const int rank = ws_block ? static_cast<int>(blockIdx.x) / bh % parts : ws_mode ? 0 : static_cast<int>(blockIdx.x) % C;
+  const int seg_ws = ws_mode && !ws_block ? static_cast<int>(blockIdx.x) / (args.n_sub * bh) : 0;
+  const int cta = ws_block  ? static_cast<int>(blockIdx.x) / (bh * parts) * bh + static_cast<int>(blockIdx.x) % bh   // sub-chunk 0 first
+                  : ws_mode ? static_cast<int>(blockIdx.x) % (args.n_sub * bh)
+                            : static_cast<int>(blockIdx.x) / C;
   const int sub = cta / bh;
   const int b = (cta % bh) / args.Hkv;
   const int g = cta % args.Hkv;
@@ -401,18 +408,18 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   // the tiles this CTA runs: one C5 segment (workspace mode) or a contiguous
   // block of segments (fold mode)
-  const int seg_len = ws_mode ? args.seg_tiles : args.fold_seg;
+  const int seg_len = ws_mode && !ws_block ? args.seg_tiles : args.fold_seg;
   const int ns = kSparse ? walked.y : (n_kv + seg_len - 1) / seg_len;   // segments of the sub-chunk's rows
   int j0, j1;                                           // tiles, or (sparse) entries of the walk
   if constexpr (kSparse) {
     j0 = active ? seg_first[seg_block_start(rank, ns, C)] : 0;
     j1 = active ? seg_first[seg_block_start(rank + 1, ns, C)] : 0;
-  } else if (ws_mode) {
+  } else if (ws_mode && !ws_block) {
     j0 = seg_ws * seg_len;
     j1 = min(n_kv, j0 + seg_len);
   } else {
-    j0 = seg_block_start(rank, ns, C) * seg_len;
-    j1 = min(n_kv, seg_block_start(rank + 1, ns, C) * seg_len);
+    j0 = seg_block_start(rank, ns, parts) * seg_len;
+    j1 = min(n_kv, seg_block_start(rank + 1, ns, parts) * seg_len);
   }
   if (j0 >= j1) active = false;
   const int nt = active ? j1 - j0 : 0;
@@ -678,6 +685,25 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const int pos = pos0 + r;
     RowState st = row_state_init(), prev = st, acc = st;
     int nfin = 0;                                      // segments finished (and folded into O_acc)
+    // C5: a finished segment's partial (O unnormalised, m, mc, l) for the fold
+    auto store_partial = [&](const RowState& sg, int seg) {
+      const bool store = m < n_rows;
+      float* dst = args.part + ((((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) * args.n_seg + seg) *
+                                kPartFloats);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32_wait(o_tmem + c * 32u, o);                // collective: every lane loads
+        if (store) {
+#pragma unroll
+          for (int v4 = 0; v4 < 8; ++v4)
+            reinterpret_cast<float4*>(dst + 32 * c)[v4] =
+                make_float4(__uint_as_float(o[4 * v4]), __uint_as_float(o[4 * v4 + 1]),
+                            __uint_as_float(o[4 * v4 + 2]), __uint_as_float(o[4 * v4 + 3]));
+        }
+      }
+      if (store) reinterpret_cast<float4*>(dst + 128)[0] = make_float4(sg.m, sg.mc, sg.l, 0.0f);
+    };
     int js = 0;                                        // tile index within its segment (j0 starts one)
     bool ok = run && no_error(args.err, abort_flag);
     for (int j = 0; j < nt && ok; ++j) {               // j: tile j0 + j
@@ -737,10 +763,11 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           if (!ok) break;
           tc_fence_after();
           FoldScale f{1.0f, 1.0f};
-          if (nfin == 0) acc = prev;
+          if (ws_block) store_partial(prev, seg_block_start(rank, ns, parts) + nfin);
+          else if (nfin == 0) acc = prev;
           else f = fold_state(acc, prev);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = ws_block ? 4 : 0; c < 4; ++c) {
             uint32_t os[32], oa[32];
             tmem_ld32_wait(o_tmem + c * 32u, os);
             if (nfin == 0) {
@@ -770,24 +797,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                      args.err, kDevTimeoutMma);
     ok = __all_sync(0xffffffffu, ok) && nt > 0;
     if (ok && ws_mode) {
-      // C5: this segment's partial (O unnormalised, m, mc, l) for the fold
       tc_fence_after();
-      const bool store = m < n_rows;
-      float* dst = args.part + ((((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) * args.n_seg +
-                                 seg_ws) * kPartFloats);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32_wait(o_tmem + c * 32u, o);                // collective: every lane loads
-        if (store) {
-#pragma unroll
-          for (int v4 = 0; v4 < 8; ++v4)
-            reinterpret_cast<float4*>(dst + 32 * c)[v4] =
-                make_float4(__uint_as_float(o[4 * v4]), __uint_as_float(o[4 * v4 + 1]),
-                            __uint_as_float(o[4 * v4 + 2]), __uint_as_float(o[4 * v4 + 3]));
-        }
-      }
-      if (store) reinterpret_cast<float4*>(dst + 128)[0] = make_float4(st.m, st.mc, st.l, 0.0f);
+      store_partial(st, ws_block ? seg_block_start(rank, ns, parts) + nfin : seg_ws);
     } else if (ok) {
       // the last segment, folded with the ones before it (C5), then C4
       tc_fence_after();
@@ -851,14 +862,14 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const bool pushing = push && rank > 0;
     // the first CTA's partial slots and barrier, as addresses of the cluster
     const uint32_t lead_slots = pushing ? smem_addr_in_cta(sbase + Cfg::kPartOff, 0u) : 0u;
-    const int my_first = seg_block_start(rank, ns, C);  // this CTA's first segment
+    const int my_first = seg_block_start(rank, ns, parts);  // this CTA's first segment
     if (pushing) cluster_wait();                       // the first CTA's barriers are initialised
 
     auto finish_segment = [&](const RowState& sg, const uint32_t (&o0)[32], const uint32_t (&o1)[32]) {
       if (ws_mode) {
         if (row_used) {
           float* dst = args.part + ((((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) *
-                                     args.n_seg + seg_ws) * kPartFloats);
+                                     args.n_seg + (ws_block ? my_first + nfin : seg_ws)) * kPartFloats);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             *reinterpret_cast<float2*>(dst + 8 * q + 2 * u) =
@@ -1224,7 +1235,7 @@ static cudaError_t launch_packed_t(const CUtensorMap& tk, const CUtensorMap& tv,
   }
   const bool ws_mode = a.part != nullptr;
   const int C = ws_mode ? 1 : a.cluster;
-  const unsigned grid = static_cast<unsigned>((ws_mode ? a.n_seg : C) * n_sub * a.B * a.Hkv);
+  const unsigned grid = static_cast<unsigned>((!ws_mode ? C : k8 ? a.split : a.n_seg) * n_sub * a.B * a.Hkv);
   if (C <= 1) {
     kb_decode_kernel<kWide, kNumSBufs, kSparse, k8><<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
     return cudaGetLastError();

@@ -55,8 +55,40 @@ kb_status check_call(const Call8& c, int* cap, kb::HostDevice* dev) {
   return host_device_pointers(p, 10);
 }
 
+// Segments of 1024 keys of the longest sequence a call over `rows` positions can have.
+long long segments_of(long long rows) { return (blocks_of(rows) + kb::kSegTiles - 1) / kb::kSegTiles; }
+
+// Bytes of the segments' partials of a call of at most 32 rows, where CTAs
+// can share a KV head's segments: 0 for batches that fill the SMs without, and
+// where the partials would pass 1 GB.
+constexpr long long kMaxSplitUnits = 304;
+long long partial_bytes(int B, int Hkv, int L, long long rows) {
+  if (static_cast<long long>(B) * Hkv >= kMaxSplitUnits || segments_of(rows) < 2) return 0;
+  const long long n = static_cast<long long>(B) * Hkv * kb::kGroup * L * segments_of(rows) * kb::kPartFloats * 4;
+  return n <= (1LL << 30) ? align256(n) : 0;
+}
+
+// CTAs that share a (batch, KV head)'s segments: the number for which the
+// waves of CTAs take the least time, a segment counted as 9 us, a CTA's start
+// as 3 and the fold of the partials as 5 (fitted to timings at 16K and 64K);
+// 1 where a cluster of `cluster` CTAs, which needs no fold, does as well.
+int choose_split(int sm_count, long long units, long long segments, int cluster) {
+  auto cost = [&](long long split) {
+    const long long waves = (units * split + sm_count - 1) / sm_count;
+    return waves * (static_cast<double>((segments + split - 1) / split) * 9.0 + 3.0);
+  };
+  double best = (units * cluster + sm_count - 1) / sm_count * (static_cast<double>((segments + cluster - 1) / cluster) * 9.0 + 3.0);
+  int split = 1;
+  for (int n = 2; n <= segments && n <= sm_count; ++n)
+    if (cost(n) + 5.0 < best) {
+      best = cost(n) + 5.0;
+      split = n;
+    }
+  return split;
+}
+
 // At most 32 rows: the packed kernel reads the bytes.
-kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* stream) {
+kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* workspace, size_t workspace_bytes, void* stream) {
   const bool ragged = c.starts != nullptr;
   const int split = std::min(c.L, kb::kTileKeys - c.start % kb::kTileKeys);
   const int n_sub = c.L > 1 && (ragged || split < c.L) ? 2 : 1;       // (one row never crosses a tile boundary)
@@ -93,7 +125,32 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* stre
   kb_status s = kb::host_bytes_map(&tk, c.k, rows, planes, stride);
   if (s != KB_OK) return s;
   if ((s = kb::host_bytes_map(&tv, c.v, rows, planes, stride)) != KB_OK) return s;
-  return host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
+  const long long part = partial_bytes(c.B, c.Hkv, c.L, keys);
+  int share = 1;
+  if (workspace != nullptr) {
+    if (!host_aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(part)) return KB_ERR_INVALID_ARG;
+    if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
+    if (part > 0) share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv, segments_of(keys), a.cluster);
+  }
+  if (share == 1) return host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
+  a.cluster = 1;
+  a.part = static_cast<float*>(workspace);
+  a.n_seg = static_cast<int>(segments_of(keys));
+  a.split = share;
+  if ((s = host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)))) != KB_OK) return s;
+  kb::RowsFoldArgs f{};
+  f.part = a.part;
+  f.o = c.o;
+  f.B = c.B;
+  f.Hq = c.Hq;
+  f.L = c.L;
+  f.n_seg = a.n_seg;
+  f.start = c.start;
+  f.starts = c.starts;
+  f.lens = c.lens;
+  f.ctx_lens = c.ctx_lens;
+  f.err = dev.err;
+  return host_done(kb::launch_rows_fold(f, static_cast<cudaStream_t>(stream)));
 }
 
 // Bytes of one of the two bf16 caches that a longer chunk is computed from.
@@ -221,7 +278,8 @@ kb_status kb_attn_cache_values(const void* cache, const signed char* exps, void*
 }
 
 size_t kb_attn_chunk_8bit_workspace_bytes(int B, int Hkv, int L, int rows) {
-  if (B < 1 || Hkv < 1 || L < 1 || rows < L || rows > kMaxRows || L <= kb::kMaxPackedRows) return 0;
+  if (B < 1 || Hkv < 1 || L < 1 || rows < L || rows > kMaxRows) return 0;
+  if (L <= kb::kMaxPackedRows) return static_cast<size_t>(partial_bytes(B, Hkv, L, rows));
   return static_cast<size_t>(2 * gathered_bytes(B, Hkv, rows));
 }
 
@@ -235,7 +293,7 @@ kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const 
   kb::HostDevice dev;
   kb_status s = check_call(c, &cap, &dev);
   if (s != KB_OK) return s;
-  if (L <= kb::kMaxPackedRows) return packed8(c, cap, dev, stream);
+  if (L <= kb::kMaxPackedRows) return packed8(c, cap, dev, workspace, workspace_bytes, stream);
   const int rows = starts != nullptr ? cap : start + L;
   const size_t need = kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows);
   if (workspace == nullptr || !host_aligned(workspace, 256) || workspace_bytes < need) return KB_ERR_INVALID_ARG;
@@ -269,14 +327,15 @@ kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const 
 
 kb_status kb_attn_decode_8bit(const void* q, const void* k, const void* v, const signed char* k_exp, const signed char* v_exp,
                               void* o, int B, int Hq, int Hkv, int ctx_len, const int* ctx_lens, int kv_cap,
-                              const int* block_table, int pages_per_seq, int page_size, int num_pages, void* stream) {
+                              const int* block_table, int pages_per_seq, int page_size, int num_pages, void* workspace,
+                              size_t workspace_bytes, void* stream) {
   if (ctx_lens == nullptr && ctx_len < 1) return KB_ERR_INVALID_ARG;
   Call8 c{q, k, v, reinterpret_cast<const int8_t*>(k_exp), reinterpret_cast<const int8_t*>(v_exp), o, B, Hq, Hkv, 1,
           ctx_lens ? 0 : ctx_len - 1, nullptr, nullptr, ctx_lens, kv_cap, block_table, pages_per_seq, page_size, num_pages};
   int cap = 0;
   kb::HostDevice dev;
   const kb_status s = check_call(c, &cap, &dev);
-  return s != KB_OK ? s : packed8(c, cap, dev, stream);
+  return s != KB_OK ? s : packed8(c, cap, dev, workspace, workspace_bytes, stream);
 }
 
 kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, float* weights, int B, int Hq, int Hkv, int L,

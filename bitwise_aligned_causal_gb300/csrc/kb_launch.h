@@ -62,6 +62,7 @@ struct PackedArgs {
   // blocks of a plane] (null: a bf16 cache)
   const int8_t *k_exp, *v_exp;
   int plane_rows;          // rows of a plane: the cache's capacity or the page size
+  int split;               // with part: CTAs that share the segments of a (sub-chunk, batch, KV head)
   float* lse;              // optional [B, Hq, L] fp32 (fold mode): natural-log log-sum-exp of each row's scaled scores
   uint32_t* err;
 };
@@ -115,6 +116,17 @@ cudaError_t launch_backward(const CUtensorMap& tq, const CUtensorMap& tk, const 
 cudaError_t launch_bwd_delta(const void* o, const void* dout, float* delta, long long rows, cudaStream_t s);
 // C5 fold of the packed kernel's per-segment partials, one warp per row
 // (rows = B*Hq*L, row r of a (b, h) at position start + r), then C4 into o.
+// The same for the partials of 8-bit calls, whose rows' positions may be given per sequence: one CTA per row.
+struct RowsFoldArgs {
+  const float* part;       // [B, Hq, L, n_seg][132]
+  void* o;                 // [B, Hq, L, 128] bf16
+  int B, Hq, L, n_seg;
+  int start;
+  const int *starts, *lens, *ctx_lens;   // as PackedArgs
+  int max_ctx;
+  const uint32_t* err;
+};
+cudaError_t launch_rows_fold(const RowsFoldArgs& a, cudaStream_t s);
 cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
                             cudaStream_t s);
 

@@ -52,4 +52,58 @@ cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, i
   return cudaGetLastError();
 }
 
+// One CTA per output row, thread t owns column t: the loads of the next eight
+// segments are in flight while eight are folded, left to right.
+__global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldArgs args) {
+  if (*reinterpret_cast<const volatile uint32_t*>(args.err) != 0) return;    // the partials are not there
+  const int row = static_cast<int>(blockIdx.x);
+  const int r = row % args.L, b = row / args.L / args.Hq;
+  int start = args.start, rows = args.L;
+  if (args.ctx_lens != nullptr) start = args.ctx_lens[b] - args.L;
+  if (args.starts != nullptr) {
+    start = args.starts[b];
+    rows = args.lens[b];
+  }
+  if (r >= rows) return;
+  const int n_kv = (start + r) / kTileKeys + 1;                   // C1: tiles 0..floor(p / 128)
+  const int ns = min((n_kv + kSegTiles - 1) / kSegTiles, args.n_seg);
+  const int t = static_cast<int>(threadIdx.x);
+  const float* p = args.part + static_cast<size_t>(row) * args.n_seg * kPartFloats;
+  constexpr int kAhead = 8;
+  float o[kAhead];
+  float4 st[kAhead];
+  auto load = [&](int sg, int i) {
+    const int at = min(sg, ns - 1);
+    o[i] = __ldg(p + static_cast<size_t>(at) * kPartFloats + t);
+    st[i] = __ldg(reinterpret_cast<const float4*>(p + static_cast<size_t>(at) * kPartFloats + kHeadDim));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, i);
+  RowState acc = row_state_init();
+  float acc_o = 0.0f;
+  for (int s0 = 0; s0 < ns; s0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float os = o[i];
+      const RowState seg{st[i].x, st[i].y, st[i].z};
+      if (s0 + kAhead < ns) load(s0 + kAhead + i, i);
+      if (s0 + i >= ns) continue;
+      if (s0 + i == 0) {                                          // segment 0 as it is
+        acc = seg;
+        acc_o = os;
+      } else {
+        const FoldScale f = fold_state(acc, seg);
+        acc_o = fold_o(acc_o, os, f);
+      }
+    }
+  }
+  static_cast<__nv_bfloat16*>(args.o)[static_cast<size_t>(row) * kHeadDim + t] =
+      __float2bfloat16_rn(__fmul_rn(acc_o, row_inv_l(acc)));
+}
+
+cudaError_t launch_rows_fold(const RowsFoldArgs& a, cudaStream_t s) {
+  kb_rows_fold_kernel<<<static_cast<unsigned>(static_cast<long long>(a.B) * a.Hq * a.L), kHeadDim, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace kb

@@ -71,7 +71,7 @@ _SIGS = {
     "kb_attn_chunk_8bit_workspace_bytes": [_I, _I, _I, _I],
     "kb_attn_chunk_8bit": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P, ctypes.c_size_t,
                            _P],
-    "kb_attn_decode_8bit": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P],
+    "kb_attn_decode_8bit": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I, _P, ctypes.c_size_t, _P],
     "kb_attn_chunk_lse": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
     "kb_attn_key_weights": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _P],
     "kb_attn_evict": [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _P, _I, _I, _I, _P],
@@ -271,9 +271,9 @@ def kb_attn_chunk_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, L, start, starts, l
 
 
 def kb_attn_decode_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table, pages_per_seq,
-                        page_size, num_pages, stream=None) -> int:
+                        page_size, num_pages, workspace, workspace_bytes, stream=None) -> int:
     return _lib.kb_attn_decode_8bit(q, k, v, k_exp, v_exp, o, B, Hq, Hkv, ctx_len, ctx_lens, kv_cap, block_table,
-                                    pages_per_seq, page_size, num_pages, stream)
+                                    pages_per_seq, page_size, num_pages, workspace, workspace_bytes, stream)
 
 
 def kb_attn_chunk_lse(q, k, v, o, lse, B, Hq, Hkv, L, start, starts, lens, kv_cap, block_table, pages_per_seq, page_size,
@@ -1139,7 +1139,16 @@ def _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device):
     return _empty(q.shape, q.dtype, q.device, stream) if out is None else out, sz
 
 
-def _decode_8bit(q, k, v, k_exp, v_exp, ctx_len, ctx_lens, block_table, out, stream, check):
+def _workspace_8bit(B, Hkv, L, rows, device, workspace, stream):
+    """(pointer, bytes) of the call's workspace; (None, 0) where it needs none."""
+    nbytes = kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows)
+    if not nbytes:
+        return None, 0, None
+    ws = _stream_workspace(nbytes, device, workspace, stream)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _decode_8bit(q, k, v, k_exp, v_exp, ctx_len, ctx_lens, block_table, out, workspace, stream, check):
     device = _device()
     o, (B, Hq, Hkv, L, cap, num_pages, page, pps) = _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device)
     if L != 1:
@@ -1148,23 +1157,26 @@ def _decode_8bit(q, k, v, k_exp, v_exp, ctx_len, ctx_lens, block_table, out, str
     _per_sequence(B, ctx_lens, "ctx_lens")
     if ctx_lens is None and not 1 <= ctx_len <= cap:
         raise ValueError(f"ctx_len must lie in 1..{cap} (the cache capacity), got {ctx_len}")
+    ws, nbytes, _hold = _workspace_8bit(B, Hkv, 1, ctx_len if ctx_lens is None else cap, q.device, workspace, stream)
     _finish(kb_attn_decode_8bit(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
                                 o.data_ptr(), B, Hq, Hkv, ctx_len, _ptr(ctx_lens), cap, _ptr(block_table), pps, page,
-                                num_pages, _handle(stream, device)), "kb_attn_decode_8bit", check, stream)
+                                num_pages, ws, nbytes, _handle(stream, device)), "kb_attn_decode_8bit", check, stream)
     return o
 
 
-def decode_8bit(q, k_cache, v_cache, k_exp, v_exp, ctx_len, out=None, stream=None, check=False):
+def decode_8bit(q, k_cache, v_cache, k_exp, v_exp, ctx_len, out=None, workspace=None, stream=None, check=False):
     """decode over a cache held in 8 bits (append_8bit): q [B,Hq,1,128] at position ctx_len-1.  The bits are decode's on
-    the bf16 caches that cache_values gives."""
-    return _decode_8bit(q, k_cache, v_cache, k_exp, v_exp, int(ctx_len), None, None, out, stream, check)
+    the bf16 caches that cache_values gives.  Long contexts of small batches use a workspace
+    (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
+    return _decode_8bit(q, k_cache, v_cache, k_exp, v_exp, int(ctx_len), None, None, out, workspace, stream, check)
 
 
-def decode_8bit_paged(q, k_pages, v_pages, k_exp, v_exp, block_table, ctx_lens, out=None, stream=None, check=False):
-    """decode_paged over pools held in 8 bits."""
+def decode_8bit_paged(q, k_pages, v_pages, k_exp, v_exp, block_table, ctx_lens, out=None, workspace=None, stream=None,
+                      check=False):
+    """decode_paged over pools held in 8 bits; workspace as in decode_8bit."""
     for t, n in ((block_table, "block_table"), (ctx_lens, "ctx_lens")):
         _check_i32(t, n)
-    return _decode_8bit(q, k_pages, v_pages, k_exp, v_exp, 0, ctx_lens, block_table, out, stream, check)
+    return _decode_8bit(q, k_pages, v_pages, k_exp, v_exp, 0, ctx_lens, block_table, out, workspace, stream, check)
 
 
 def _chunk_8bit(q, k, v, k_exp, v_exp, start, starts, lens, block_table, out, workspace, stream, check):
@@ -1176,19 +1188,18 @@ def _chunk_8bit(q, k, v, k_exp, v_exp, start, starts, lens, block_table, out, wo
     else:
         _need_rows(start, L, cap)
         rows = start + L
-    nbytes = kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows)
-    ws = _stream_workspace(nbytes, q.device, workspace, stream) if nbytes else None
+    ws, nbytes, _hold = _workspace_8bit(B, Hkv, L, rows, q.device, workspace, stream)
     _finish(kb_attn_chunk_8bit(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
                                o.data_ptr(), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap, _ptr(block_table), pps,
-                               page, num_pages, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                               _handle(stream, device)), "kb_attn_chunk_8bit", check, stream)
+                               page, num_pages, ws, nbytes, _handle(stream, device)), "kb_attn_chunk_8bit", check,
+            stream)
     return o
 
 
 def chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, start, out=None, workspace=None, stream=None, check=False):
     """chunk over a cache held in 8 bits (append_8bit): q [B,Hq,L,128] at positions start.. .  The bits are chunk's on the
     bf16 caches that cache_values gives.  Up to 32 rows read the bytes; a longer chunk turns the visible keys and
-    values into bf16 in a workspace (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
+    values into bf16 in the workspace (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
     return _chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, int(start), None, None, None, out, workspace, stream, check)
 
 

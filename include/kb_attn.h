@@ -495,11 +495,14 @@ kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, 
  * that holds the same values, so a row has the same bits in any split over the
  * same cache; a later append that enlarges a block's E can change its smallest
  * values (those below 2^(E-6)) for rows computed after it.
- * L <= 32 reads the bytes and needs no workspace.  A longer chunk is computed
- * from the visible values in bf16, in a device workspace (256-byte aligned,
- * caller-owned, contents scratch) of kb_attn_chunk_8bit_workspace_bytes(B, Hkv,
- * L, rows) bytes, rows being start + L, or the cache's positions per sequence
- * when starts is given; calls that can overlap on the GPU need one each.
+ * workspace: device scratch (256-byte aligned, caller-owned) of
+ * kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows) bytes (L = 1 for a
+ * decode), rows being start + L, or the cache's positions per sequence when
+ * starts or ctx_lens is given; calls that can overlap on the GPU need one each.
+ * L <= 32 reads the bytes; with a workspace several CTAs share the keys of a KV
+ * head where the batch leaves SMs idle, and with NULL it runs without, slower
+ * there, with the same bits.  A longer chunk is computed from the visible
+ * values in bf16, in the workspace, which it needs.
  */
 kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
                               void* k_cache, void* v_cache, signed char* k_exp, signed char* v_exp,
@@ -518,7 +521,8 @@ kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const 
 kb_status kb_attn_decode_8bit(const void* q, const void* k, const void* v, const signed char* k_exp,
                               const signed char* v_exp, void* o, int B, int Hq, int Hkv, int ctx_len,
                               const int* ctx_lens, int kv_cap, const int* block_table, int pages_per_seq,
-                              int page_size, int num_pages, void* stream);
+                              int page_size, int num_pages, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /*
  * kb_attn_chunk (starts and lens NULL) or kb_attn_chunk_varlen, contiguous or

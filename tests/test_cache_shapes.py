@@ -124,10 +124,13 @@ def test_attend_8bit_abi(kb):
         assert kb.kb_attn_chunk_8bit(*changed(ok, **new)) == kb.KB_ERR_INVALID_ARG, new
     assert kb.kb_attn_chunk_8bit(*changed(ok, Hq=8)) == kb.KB_ERR_UNSUPPORTED
     dec = dict(q=FAKE, k=FAKE, v=FAKE, ke=FAKE, ve=FAKE, o=FAKE, B=1, Hq=32, Hkv=8, ctx=4, lens=None, cap=100, bt=None, pps=0, page=0,
-               pages=0)
+               pages=0, ws=None, nbytes=0)
     for new in (dict(ctx=0), dict(ctx=101), dict(ke=None), dict(lens=FAKE + 1)):
         assert kb.kb_attn_decode_8bit(*changed(dec, **new)) == kb.KB_ERR_INVALID_ARG, new
-    assert kb.kb_attn_chunk_8bit_workspace_bytes(1, 8, 32, 1000) == 0
+    assert kb.kb_attn_chunk_8bit_workspace_bytes(1, 8, 32, 1000) == 0                # one segment: nothing to share
+    assert kb.kb_attn_chunk_8bit_workspace_bytes(3, 8, 5, 2049) == 3 * 32 * 5 * 3 * 528
+    assert kb.kb_attn_chunk_8bit_workspace_bytes(64, 8, 1, 100000) == 0              # enough KV heads for every SM
+    assert kb.kb_attn_chunk_8bit_workspace_bytes(30, 8, 32, 1 << 22) == 0            # too large
     assert kb.kb_attn_chunk_8bit_workspace_bytes(2, 8, 33, 1000) == 2 * 2 * 8 * 1000 * 256
     assert kb.kb_attn_chunk_8bit_workspace_bytes(1, 8, 33, 32) == 0
     val = (FAKE, FAKE, FAKE, 8, 100)

@@ -242,7 +242,7 @@ def test_decode_has_the_bits_of_the_bf16_cache(kb, page, B, ctx):
 
 @pytest.mark.parametrize("page", [0, 256])
 @pytest.mark.parametrize("B,L,start", [(1, 2, 126), (2, 2, 127), (1, 3, 0), (2, 7, 1500), (1, 32, 1000), (3, 32, 112), (1, 33, 500),
-                                       (2, 130, 60), (1, 700, 0), (1, 257, 2047)])
+                                       (2, 130, 60), (1, 700, 0), (1, 257, 2047), (1, 5, 9000), (2, 32, 4090), (1, 2, 20479)])
 def test_chunks_have_the_bits_of_the_bf16_cache(kb, page, B, L, start):
     import torch
 
@@ -278,6 +278,33 @@ def test_ragged_chunks(kb, page, L, starts, lens):
     assert torch.equal(bits(out), bits(want))
     for b in range(B):
         assert bool((out[b, :, lens[b]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("B,L,start", [(1, 1, 9000), (2, 1, 70000), (1, 20, 9000)])
+def test_without_a_workspace_and_with_one_of_its_own(kb, B, L, start):
+    """Long contexts of small batches: CTAs that share a KV head's keys through the workspace, and the way without."""
+    import torch
+
+    ctx = start + L
+    cache, _, _ = filled(kb, B, ctx)
+    q = randn(86, B, 32, L, 128)
+    want = kb.chunk_8bit(q, *cache, start, check=True)
+    nbytes = kb.kb_attn_chunk_8bit_workspace_bytes(B, 8, L, ctx)
+    assert nbytes > 0
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert torch.equal(bits(kb.chunk_8bit(q, *cache, start, workspace=ws, check=True)), bits(want))
+    with pytest.raises(kb.KBError):
+        kb.chunk_8bit(q, *cache, start, workspace=ws[:-256])
+    ptrs = [t.data_ptr() for t in (q, *cache)]
+    o = torch.zeros_like(q)
+    s = torch.cuda.current_stream().cuda_stream
+    assert kb.kb_attn_chunk_8bit(*ptrs, o.data_ptr(), B, 32, 8, L, start, None, None, ctx, None, 0, 0, 0, None, 0, s) == kb.KB_OK
+    kb.check_device_status()
+    assert torch.equal(bits(o), bits(want))
+    if L == 1:
+        assert kb.kb_attn_decode_8bit(*ptrs, o.zero_().data_ptr(), B, 32, 8, ctx, None, ctx, None, 0, 0, 0, None, 0, s) == kb.KB_OK
+        kb.check_device_status()
+        assert torch.equal(bits(o), bits(want))
 
 
 def test_against_64_bits(kb):
