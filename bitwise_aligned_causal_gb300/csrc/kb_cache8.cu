@@ -13,7 +13,7 @@ namespace kb {
 
 namespace {
 
-constexpr int kRowsPerPass = 4;                 // rows of a thread's place: 8 warps x 4 rows x 4 = a block
+constexpr int kPasses = 2;                      // rows of a thread: 16 warps x 4 rows x 2 = a block
 
 // fp32 values of a lane's two chunks, turned where they are.
 __device__ __forceinline__ void turned_values(const uint4& x, const uint4& y, const Turn& t, bool turns, bool interleaved,
@@ -100,12 +100,13 @@ __device__ __forceinline__ void regrid(uint8_t* base, int n16, int d, int E) {
 
 // One CTA per (batch, KV head, key block that the call's rows touch), as
 // kb_append_kernel.  A block's exponent needs all of the block's new keys
-// before the first byte is written, so a thread keeps its rows (at most four)
+// before the first byte is written, so a thread keeps its rows (at most two)
 // in registers, turns its keys once for the largest magnitude and once more
-// for the bytes.  Where the exponent has grown, the block's earlier keys are
+// for the bytes; the queries pass two heads at a time.  That keeps to 64
+// registers, so that two CTAs of 16 warps share an SM.  Where the exponent has grown, the block's earlier keys are
 // brought to it: a CTA has the block to itself.
-__global__ void __launch_bounds__(256) kb_append8_kernel(const Append8Args args) {
-  __shared__ uint32_t amax[2][8];
+__global__ void __launch_bounds__(512, 2) kb_append8_kernel(const Append8Args args) {
+  __shared__ uint32_t amax[2][16];
   // one decision for the CTA: the word may change while its threads read it
   if (__syncthreads_or(*reinterpret_cast<volatile uint32_t*>(args.a.err) != 0)) return;
   const AppendArgs& a = args.a;
@@ -155,11 +156,11 @@ __global__ void __launch_bounds__(256) kb_append8_kernel(const Append8Args args)
   const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k) + b * a.ks[0] + g * a.ks[1];
   const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + b * a.vs[0] + g * a.vs[1];
   const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qs[0] + (g * kGroup) * a.qs[1];
-  uint4 kx[kRowsPerPass], ky[kRowsPerPass], vx[kRowsPerPass], vy[kRowsPerPass];
+  uint4 kx[kPasses], ky[kPasses], vx[kPasses], vy[kPasses];
   uint32_t k_max = 0, v_max = 0;
 #pragma unroll
-  for (int it = 0; it < kRowsPerPass; ++it) {
-    const int p = p0 + (it * n_warps + warp) * kRowsPerPass + r4;
+  for (int it = 0; it < kPasses; ++it) {
+    const int p = p0 + (it * n_warps + warp) * kRowsPerWarp + r4;
     if (p >= p1) continue;
     const long long i = p - start;                                     // row of the call's tensors
     const uint4* ksrc = reinterpret_cast<const uint4*>(kp + i * a.ks[2]);
@@ -171,20 +172,24 @@ __global__ void __launch_bounds__(256) kb_append8_kernel(const Append8Args args)
     Turn t;
     if (turns) load_turn(t, a.table, p, a.rot_dim, u, false);
     if (a.q != nullptr) {
-      uint4 qx[kGroup], qy[kGroup];
 #pragma unroll
-      for (int h = 0; h < kGroup; ++h) {
-        const uint4* qsrc = reinterpret_cast<const uint4*>(qp + h * a.qs[1] + i * a.qs[2]);
-        qx[h] = qsrc[lc.c0];
-        qy[h] = qsrc[lc.c1];
-      }
+      for (int h0 = 0; h0 < kGroup; h0 += 2) {
+        uint4 qx[2], qy[2];
 #pragma unroll
-      for (int h = 0; h < kGroup; ++h) {
-        if (turns) turn_chunks(qx[h], qy[h], t, a.interleaved);
-        uint4* qdst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
-                                               ((static_cast<size_t>(b) * a.Hkv * kGroup + g * kGroup + h) * a.L + i) * kHeadDim);
-        qdst[lc.c0] = qx[h];
-        qdst[lc.c1] = qy[h];
+        for (int h = 0; h < 2; ++h) {
+          const uint4* qsrc = reinterpret_cast<const uint4*>(qp + (h0 + h) * a.qs[1] + i * a.qs[2]);
+          qx[h] = qsrc[lc.c0];
+          qy[h] = qsrc[lc.c1];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (turns) turn_chunks(qx[h], qy[h], t, a.interleaved);
+          uint4* qdst = reinterpret_cast<uint4*>(
+              static_cast<__nv_bfloat16*>(a.q_out) +
+              ((static_cast<size_t>(b) * a.Hkv * kGroup + g * kGroup + h0 + h) * a.L + i) * kHeadDim);
+          qdst[lc.c0] = qx[h];
+          qdst[lc.c1] = qy[h];
+        }
       }
     }
     float fx[8], fy[8];
@@ -215,8 +220,8 @@ __global__ void __launch_bounds__(256) kb_append8_kernel(const Append8Args args)
     args.v_exp[e_at] = static_cast<int8_t>(v_e);
   }
 #pragma unroll
-  for (int it = 0; it < kRowsPerPass; ++it) {
-    const int p = p0 + (it * n_warps + warp) * kRowsPerPass + r4;
+  for (int it = 0; it < kPasses; ++it) {
+    const int p = p0 + (it * n_warps + warp) * kRowsPerWarp + r4;
     if (p >= p1) continue;
     const size_t r = static_cast<size_t>(p - block * kTileKeys) * kHeadDim;
     Turn t;
@@ -239,12 +244,32 @@ cudaError_t launch_append8(const Append8Args& args, cudaStream_t s) {
   const long long grid = touched * a.B * a.Hkv;
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int rows = a.L < kTileKeys ? a.L : kTileKeys;
-  const int warps = std::min((rows + kRowsPerPass - 1) / kRowsPerPass, 8);
+  const int warps = std::min((rows + kRowsPerWarp - 1) / kRowsPerWarp, 16);
   kb_append8_kernel<<<static_cast<unsigned>(grid), warps * 32, 0, s>>>(args);
   return cudaGetLastError();
 }
 
 // ------------------------------------------------------------ what it stands for
+
+// n chunks of 8 bytes of one block into 16-byte chunks, by 256 threads: eight
+// bytes per load, so that a warp's stores cover whole lines.
+__device__ __forceinline__ void values_of_block(const uint2* src, uint4* dst, int n, const Scale8& s) {
+  uint2 w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = threadIdx.x + 256 * i;
+    if (c < n) w[i] = __ldg(src + c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = threadIdx.x + 256 * i;
+    if (c < n) {
+      const uint2 a = values8(w[i].x, s.first), b = values8(w[i].y, s.first);
+      const uint4 v = make_uint4(a.x, a.y, b.x, b.y);
+      dst[c] = s.two ? scaled_again(v, s.second) : v;
+    }
+  }
+}
 
 // A CTA per block of 128 rows: 128 bytes of a row become 256.
 __global__ void __launch_bounds__(256) kb_cache_values_kernel(const Values8Args args) {
@@ -254,24 +279,9 @@ __global__ void __launch_bounds__(256) kb_cache_values_kernel(const Values8Args 
   const int rows = min(kTileKeys, args.rows - block * kTileKeys);
   const size_t row0 = static_cast<size_t>(plane) * args.rows + static_cast<size_t>(block) * kTileKeys;
   const Scale8 s = scale8(args.exps[blockIdx.x]);
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(args.cache) + row0 * kHeadDim);
+  const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(args.cache) + row0 * kHeadDim);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.out) + row0 * kHeadDim);
-  uint4 w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = threadIdx.x + 256 * i;
-    if (c < rows * 8) w[i] = __ldg(src + c);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = threadIdx.x + 256 * i;
-    if (c < rows * 8) {
-      uint4 lo, hi;
-      values8x16(w[i], s, lo, hi);
-      dst[2 * c] = lo;
-      dst[2 * c + 1] = hi;
-    }
-  }
+  values_of_block(src, dst, rows * 16, s);
 }
 
 cudaError_t launch_cache_values(const Values8Args& a, cudaStream_t s) {
@@ -311,25 +321,10 @@ __global__ void __launch_bounds__(256) kb_cache_gather_kernel(const Gather8Args 
     e_at = plane * (args.page_size / kTileKeys) + key % args.page_size / kTileKeys;
   }
   const Scale8 s = scale8((is_v ? args.v_exp : args.k_exp)[e_at]);
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_v ? args.v : args.k) + row0 * kHeadDim);
+  const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? args.v : args.k) + row0 * kHeadDim);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? args.v_out : args.k_out) +
                                         (static_cast<size_t>(bg) * args.rows + static_cast<size_t>(block) * kTileKeys) * kHeadDim);
-  uint4 w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = threadIdx.x + 256 * i;
-    if (c < rows * 8) w[i] = __ldg(src + c);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = threadIdx.x + 256 * i;
-    if (c < rows * 8) {
-      uint4 lo, hi;
-      values8x16(w[i], s, lo, hi);
-      dst[2 * c] = lo;
-      dst[2 * c + 1] = hi;
-    }
-  }
+  values_of_block(src, dst, rows * 16, s);
 }
 
 cudaError_t launch_cache_gather(const Gather8Args& a, cudaStream_t s) {
