@@ -47,7 +47,7 @@ struct WeightsCfg {
   static constexpr int kBarDrain = 14;
   static constexpr int kNumBars = 15;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8 + 8;
-  static constexpr uint32_t kColOff = kMiscOff + 16;      // float2 (-lse log2 e, position) x 128 x 2 buffers
+  static constexpr uint32_t kColOff = kMiscOff + 16;      // float -lse log2 e x 128 x 2 buffers, then int position the same
   static constexpr uint32_t kPartOff = kColOff + 2 * 128 * 8;   // float x 128 x 2: the upper half's sums of a key tile
   static constexpr uint32_t kSmemUsed = kPartOff + 2 * 128 * 4;
   static constexpr uint32_t kSmemBytes = kSmemUsed + 1024;
@@ -61,26 +61,28 @@ __device__ __forceinline__ void weights_drain_wait(uint32_t bar, uint32_t parity
     if (global_timer_ns() - t0 > 50000000ull) break;
 }
 
-// Weights of one key for 16 columns of a step: x scores, col their (-lse log2
-// e, position) in shared memory.
+// Weights of one key for 16 columns of a step: x scores, off -lse log2 e of the
+// columns, pos their positions (kMasked: a column gives nothing to a key behind it).
 template <bool kMasked>
-__device__ __forceinline__ float2 sum16(const uint32_t (&x)[16], const float4* col, int key) {
+__device__ __forceinline__ void sum16(const uint32_t (&x)[16], const float* off, const int* pos, int key, float2 (&sum)[2]) {
   const float c = score_scale_log2();
   const float2 c2 = make_float2(c, c);
-  float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 v = col[i];                              // two columns
-    const float2 arg = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2,
-                                  make_float2(v.x, v.z));
-    float2 w = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(off)[i];
+    const float2 a0 = __ffma2_rn(make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), c2, make_float2(v.x, v.y));
+    const float2 a1 = __ffma2_rn(make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), c2, make_float2(v.z, v.w));
+    float2 w0 = make_float2(ex2_approx(a0.x), ex2_approx(a0.y)), w1 = make_float2(ex2_approx(a1.x), ex2_approx(a1.y));
     if (kMasked) {
-      if (key > __float_as_int(v.y)) w.x = 0.0f;
-      if (key > __float_as_int(v.w)) w.y = 0.0f;
+      const int4 p = reinterpret_cast<const int4*>(pos)[i];
+      if (key > p.x) w0.x = 0.0f;
+      if (key > p.y) w0.y = 0.0f;
+      if (key > p.z) w1.x = 0.0f;
+      if (key > p.w) w1.y = 0.0f;
     }
-    s = __fadd2_rn(s, w);
+    sum[0] = __fadd2_rn(sum[0], w0);
+    sum[1] = __fadd2_rn(sum[1], w1);
   }
-  return s;
 }
 
 }  // namespace
@@ -246,10 +248,13 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          float2* cols = reinterpret_cast<float2*>(smem + Cfg::kColOff) + db * 128;
+          float* off = reinterpret_cast<float*>(smem + Cfg::kColOff) + db * 128;
+          int* pos = reinterpret_cast<int*>(smem + Cfg::kColOff + 1024) + db * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)      // a row that saw nothing (-inf) has no weights to give
-            cols[32 * i + lane] = make_float2(l[i] == -INFINITY ? -INFINITY : __fmul_rn(-l[i], kLog2e), __int_as_float(p[i]));
+          for (int i = 0; i < 4; ++i) {    // a row that saw nothing (-inf) has no weights to give
+            off[32 * i + lane] = l[i] == -INFINITY ? -INFINITY : __fmul_rn(-l[i], kLog2e);
+            pos[32 * i + lane] = p[i];
+          }
           mbar_arrive(bar(Cfg::kBarLFull + db));
         }
       }
@@ -274,7 +279,8 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     const int half = (warp - Cfg::kSumWarp0) >> 2;
     const int key = 32 * (warp & 3) + lane;               // TMEM lane = key of the tile
     const uint32_t d_tmem = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const float4* cols = reinterpret_cast<const float4*>(smem + Cfg::kColOff);
+    const float* col_off = reinterpret_cast<const float*>(smem + Cfg::kColOff);
+    const int* col_pos = reinterpret_cast<const int*>(smem + Cfg::kColOff + 1024);
     float* part = reinterpret_cast<float*>(smem + Cfg::kPartOff);
     int T = 0, K = 0;
     bool ok = !skip;
@@ -291,18 +297,38 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         // does some row of the step not see some key of the tile, or has a column no row?
         const int r0 = kPacked ? 0 : (t0 + s / kGroup) * kTileRows;
         const bool masked = pos0 + r0 < j * kTileKeys + kTileKeys - 1 || (!kPacked && r0 + kTileRows > rows);
-        float2 sum = make_float2(0.0f, 0.0f);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const int pkey = j * kTileKeys + key;
+        const uint32_t d = d_tmem + db * 128u + 64u * half;
+        const float* off = col_off + db * 128 + 64 * half;
+        const int* pos = col_pos + db * 128 + 64 * half;
+        if constexpr (kPacked) {
 #pragma unroll 1
-        for (int c = 64 * half; c < min(64 * half + 64, n_cols); c += 16) {
-          uint32_t x[16];
-          tmem_ld16_wait(d_tmem + db * 128u + c, x);
-          const float4* cp = cols + db * 64 + c / 2;
-          sum = __fadd2_rn(sum, masked ? sum16<true>(x, cp, pkey) : sum16<false>(x, cp, pkey));
+          for (int c = 0; c < n_cols - 64 * half && c < 64; c += 16) {
+            uint32_t x[16];
+            tmem_ld16_wait(d + c, x);
+            if (masked) sum16<true>(x, off + c, pos + c, pkey, sum);
+            else sum16<false>(x, off + c, pos + c, pkey, sum);
+          }
+        } else {
+          // the load of the next 16 columns is in flight while 16 are summed
+          uint32_t x[16], y[16];
+          tmem_ld16_issue(d, x);
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            tmem_ld16_wait_for(x);
+            tmem_ld16_issue(d + c + 16, y);
+            if (masked) sum16<true>(x, off + c, pos + c, pkey, sum);
+            else sum16<false>(x, off + c, pos + c, pkey, sum);
+            tmem_ld16_wait_for(y);
+            if (c + 32 < 64) tmem_ld16_issue(d + c + 32, x);
+            if (masked) sum16<true>(y, off + c + 16, pos + c + 16, pkey, sum);
+            else sum16<false>(y, off + c + 16, pos + c + 16, pkey, sum);
+          }
         }
         tc_fence_before();
         mbar_arrive(bar(Cfg::kBarDEmpty + db));
-        total = __fadd_rn(total, __fadd_rn(sum.x, sum.y));
+        total = __fadd_rn(total, __fadd_rn(__fadd_rn(sum[0].x, sum[0].y), __fadd_rn(sum[1].x, sum[1].y)));
       }
       if (half == 1) part[(K & 1) * 128 + key] = total;
       // one decision for the eight warps: all go on, or none does
