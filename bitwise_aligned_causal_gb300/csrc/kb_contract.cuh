@@ -262,6 +262,53 @@ __device__ __forceinline__ float row_softmax_tile_quad(float (&x)[32], int u, in
   return alpha;
 }
 
+// The same step for one or two tiles in turn (kTwo), with a row spread over
+// eight threads (lanes 8i .. 8i+7, thread u = lane % 8): x[t][r] is the score of
+// key 8r + u of tile t, so a thread holds one of the eight partial sums above.
+// Same operations in the same order per row, so the same bits; two tiles run
+// interleaved, since one warp alone mostly waits for its own results.  Masked
+// keys come as -inf.  x becomes the fp32 weights; alpha[t] as above.
+template <bool kTwo>
+__device__ __forceinline__ void row_softmax_tiles_oct(float (&x)[2][16], RowState& st, float (&alpha)[2]) {
+  constexpr int kTiles = kTwo ? 2 : 1;
+  const float c = score_scale_log2();
+  float top[2];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const float* y = x[t];
+    top[t] = fmaxf(max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[8])),
+                   fmaxf(max3(y[9], y[10], y[11]), max3(y[12], y[13], fmaxf(y[14], y[15]))));
+  }
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], d));
+  float mc[2];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const bool moves = __fsub_rn(top[t], st.m) > kRescaleThresholdRaw;
+    const float mc_new = __fmul_rn(top[t], c);
+    alpha[t] = moves ? ex2_approx(__fmaf_rn(st.m, c, -mc_new)) : 1.0f;
+    st.m = moves ? top[t] : st.m;
+    st.mc = moves ? mc_new : st.mc;
+    mc[t] = st.mc;
+  }
+  float acc[2];
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      x[t][r] = ex2_approx(__fmaf_rn(x[t][r], c, -mc[t]));
+      acc[t] = r == 0 ? x[t][r] : __fadd_rn(acc[t], x[t][r]);
+    }
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) acc[t] = __fadd_rn(acc[t], __shfl_xor_sync(0xffffffffu, acc[t], d));
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) st.l = __fmaf_rn(st.l, alpha[t], acc[t]);
+}
+
 // Scale 32 accumulator columns by alpha (bit-neutral when alpha == 1).
 __device__ __forceinline__ void rescale32(uint32_t (&o)[32], float alpha) {
   const float2 a2 = make_float2(alpha, alpha);

@@ -51,6 +51,7 @@
 //    cache held in 8 bits a CTA takes a contiguous block of segments, as many
 //    CTAs per (sub-chunk, batch, KV head) as fill the SMs, and leaves each
 //    segment's partial there (kb_rows_fold_kernel).
+#include "kb_bytes.cuh"
 #include "kb_cache8.cuh"
 #include "kb_contract.cuh"
 #include "kb_launch.h"
@@ -59,27 +60,28 @@ namespace kb {
 
 // kSparse with one S buffer is the lean shape: half of TMEM and of shared
 // memory, so that two CTAs share an SM.
-// k8: the cache is held in 8 bits, and four warps per ring take the TMA
-// producer's place: one of their threads has TMA bring a tile's bytes to a
-// staging ring, all of them read it, turn the bytes into the bf16 values they
-// stand for and write those to the K or V ring in the swizzled layout that TMA
-// gives the others.  The rest of the kernel is the same, and so are the bits.
-// Staging by TMA, not in registers: with four half tiles in registers the
-// loads' latency came through on every half (the few scoreboards of a warp do
-// not tell them apart), 2.2 us a pair of tiles against 1.1 without the loads.
+// k8 (wide): the cache is held in 8 bits.  A warp of its own has TMA bring the
+// tiles' bytes to staging rings, and four warps per ring turn them into the bf16
+// values they stand for and write those to the K or V ring in the swizzled
+// layout that TMA gives the others.  The rest of the kernel is the same, and so
+// are the bits.  Staged by TMA, not in registers: with four half tiles in
+// registers the loads' latency came through on every half (the few scoreboards
+// of a warp do not tell them apart), 2.2 us a pair of tiles against 1.1 without
+// the loads.
 template <bool kWide, int kNumSBufs, bool kSparse = false, bool k8 = false>
 struct PackedCfg {
   static constexpr bool kLean = kSparse && kNumSBufs == 1;
   static constexpr int kSoftmaxWarps = kWide ? 4 : 1;
   static constexpr int kProdWarps = k8 ? 4 : 1;             // per ring
-  static constexpr int kKProdWarp = k8 ? (kWide ? 8 : 4) : kWide ? 4 : 1;   // (8 bits, narrow: warps 3, 5, 6, 7)
-  static constexpr int kQkWarp = k8 ? (kWide ? 4 : 1) : kWide ? 5 : 2;      // TMEM allocator + Q K^T issuer
-  static constexpr int kVProdWarp = k8 ? kKProdWarp + 4 : kWide ? 6 : 3;
-  static constexpr int kPvWarp = k8 ? (kWide ? 5 : 2) : kWide ? 7 : 5;
+  static constexpr int kKProdWarp = k8 ? 8 : kWide ? 4 : 1;
+  static constexpr int kQkWarp = k8 ? 4 : kWide ? 5 : 2;    // TMEM allocator + Q K^T issuer
+  static constexpr int kVProdWarp = k8 ? 12 : kWide ? 6 : 3;
+  static constexpr int kPvWarp = k8 ? 5 : kWide ? 7 : 5;
   static constexpr int kFoldWarp = kWide ? -1 : 4;          // narrow: folds and epilogue
-  static constexpr int kThreads = (k8 ? (kWide ? 16 : 12) : kWide ? 8 : 6) * 32;
-  static constexpr bool is_ring_warp(int w) { return k8 && (kWide ? w >= 8 : w == 3 || w >= 5); }
-  // wide, 8 bits: registers per thread after setmaxnreg, of a launch with 512
+  static constexpr int kThreads = (k8 ? 16 : kWide ? 8 : 6) * 32;
+  static_assert(!k8 || (kWide && !kSparse), "chunks alone; tokens over bytes have a kernel of their own");
+  static constexpr bool is_ring_warp(int w) { return k8 && w >= 8; }
+  // 8 bits: registers per thread after setmaxnreg, of a launch with 512
   // x 128 (softmax, issuers and two idle warps, the two rings)
   static constexpr uint32_t kSoftmaxRegs = 232, kIssuerRegs = 64, kRingRegs = 104;
   static_assert(kSoftmaxRegs + kIssuerRegs + 2 * kRingRegs <= 512, "register split above the launch's registers");
@@ -116,12 +118,14 @@ struct PackedCfg {
   static constexpr int kBarQReady = kBarDrain + 2;         // Q written to shared memory by its loaders
   static constexpr int kBarGo = kBarQReady + 1;            // gather: the first CTA's K/V rings are free
   static constexpr int kBarBytes = kBarGo + 1;             // 8 bits: a staged tile has landed (K's stages, then V's)
-  static constexpr int kNumBars = kBarBytes + 2 * kByteStages;
+  static constexpr int kBarByteRead = kBarBytes + 2 * kByteStages;   // ... and has been read (a warp each)
+  static constexpr int kNumBars = kBarByteRead + 2 * kByteStages;
   // Q is loaded by the softmax warps (and the fold warp when narrow) while
   // the producers' first K/V loads are already in flight
   static constexpr int kQLoaders = 32 * (kSoftmaxWarps + (kWide ? 0 : 1));
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kStatsOff = kMiscOff + 16u;      // narrow: float2 (m, l) of rows 0..7
+  static constexpr uint32_t kStatsOff = kMiscOff + 16u;      // narrow: float2 (m, l) of rows 0..7; 8 bits: staged tiles' exponents
+  static constexpr int kByteProdWarp = 6;                    // 8 bits
   // narrow: the rest of shared memory holds the segment partials a
   // non-first CTA of a cluster leaves for the first one
   // sparse: before them the row's walk (listed key blocks, ascending) and the
@@ -136,10 +140,8 @@ struct PackedCfg {
 };
 
 // Partials a narrow CTA can hold in shared memory, for n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows, bool sparse, bool bytes) {
-  return (sparse  ? PackedCfg<false, 3, true>::kPartBytes
-          : bytes ? PackedCfg<false, 3, false, true>::kPartBytes
-                  : PackedCfg<false, 3>::kPartBytes) /
+uint32_t packed_partial_slots(int n_rows, bool sparse) {
+  return (sparse ? PackedCfg<false, 3, true>::kPartBytes : PackedCfg<false, 3>::kPartBytes) /
          (static_cast<uint32_t>(n_rows) * kPartFloats * 4u);
 }
 
@@ -220,8 +222,8 @@ __device__ __forceinline__ int2 build_walk(const int* list, int n_select, int ow
   return make_int2(n, ns);
 }
 
-// The four warps of a ring (K or V) whose cache is held in 8 bits: key tiles
-// j0 .. j0 + nt - 1 of sequence b, KV head g.  A staged tile has rows of 128
+// The four warps of a ring (K or V) whose cache is held in 8 bits: the nt key
+// tiles from j0 on, as produce_bytes stages them.  A staged tile has rows of 128
 // bytes, its eight 16-byte columns swizzled as TMA does (column c of row r at c
 // ^ (r % 8)).  A thread takes one column of eight rows.  Lanes 8i .. 8i+3 hold
 // four neighbouring columns of a row, lanes 8i+4 .. 8i+7 the same of the row
@@ -229,11 +231,10 @@ __device__ __forceinline__ int2 build_walk(const int* list, int n_select, int ow
 // swizzled columns of the staged tile, and write to all eight of the bf16
 // tile.  Rows from seq_kv on are zero in the ring, whatever the cache holds.
 template <typename Cfg>
-__device__ __forceinline__ void fill_ring8(const CUtensorMap* tmap, const PackedArgs& args, bool is_v, uint8_t* ring,
-                                           uint8_t* staged, int b, int g, int j0, int nt, int seq_kv, uint32_t full0,
-                                           uint32_t empty0, uint32_t bytes0, volatile uint32_t* abort_flag) {
-  const int warp = static_cast<int>(threadIdx.x >> 5);
-  const int t = 32 * max(warp - (is_v ? Cfg::kVProdWarp : Cfg::kKProdWarp), 0) + static_cast<int>(threadIdx.x & 31);   // (warp 3: the first)
+__device__ __forceinline__ void fill_ring8(bool is_v, uint8_t* ring, const uint8_t* staged, const int* held, int j0, int nt,
+                                           int seq_kv, uint32_t full0, uint32_t empty0, uint32_t bytes0, uint32_t read0,
+                                           volatile uint32_t* abort_flag, uint32_t* err) {
+  const int t = static_cast<int>(threadIdx.x) - 32 * (is_v ? Cfg::kVProdWarp : Cfg::kKProdWarp);
   const int col = (t & 3) | ((t >> 1) & 4);
   const int low = ((t >> 4) & 3) ^ ((t & 4) ? 5 : 0);      // row % 8
   const int row0 = low + 8 * (t >> 6);                     // rows row0 + 16 i
@@ -241,83 +242,42 @@ __device__ __forceinline__ void fill_ring8(const CUtensorMap* tmap, const Packed
   // chunks 2 col and 2 col + 1 of the bf16 row, in slab col / 4
   uint8_t* dst0 = ring + (col >> 2) * kSlabBytes + (row0 >> 3) * 1024 + low * 128 + (((2 * (col & 3)) ^ low) << 4);
   const int next_chunk = (low & 1) ? -16 : 16;
-  const int8_t* exps = is_v ? args.v_exp : args.k_exp;
-  const int blocks = (args.plane_rows + kTileKeys - 1) / kTileKeys;
   constexpr int kStages = Cfg::kKStages, kByteStages = Cfg::kByteStages;
   static_assert(Cfg::kKStages == Cfg::kVStages, "one walk for both rings");
-  const uint64_t stream_once = l2_policy_evict_first();
-  int issued = 0;
-  auto issue = [&](int jj) {                               // thread 0
-    int row = 0, plane = 0;
-    kv_tile_coords(args, b, g, j0 + jj, row, plane);
-    const int st = jj % kByteStages;
-    mbar_arrive_expect_tx(bytes0 + 8u * st, Cfg::kByteTile);
-    tma_load_3d_hint(smem_addr(staged) + st * Cfg::kByteTile, tmap, 0, row, plane, bytes0 + 8u * st, stream_once);
-    issued = jj + 1;
-  };
-  // the exponent of tile jj (any number for a page out of range)
-  auto exponent_of = [&](int jj) {
-    if (jj >= nt) return 0;
-    const int key = (j0 + jj) * kTileKeys;
-    size_t at = (static_cast<size_t>(b) * args.Hkv + g) * blocks + key / kTileKeys;
-    if (args.block_table != nullptr) {
-      const int pg = __ldg(args.block_table + static_cast<size_t>(b) * args.pages_per_seq + key / args.page_size);
-      if (pg < 0 || pg >= args.num_pages) return 0;
-      at = (static_cast<size_t>(pg) * args.Hkv + g) * blocks + key % args.page_size / kTileKeys;
-    }
-    return static_cast<int>(exps[at]);
-  };
-  if (t == 0) {
-    tma_prefetch_desc(tmap);
-    for (int jj = 0; jj < min(nt, kByteStages); ++jj) issue(jj);
-  }
-  int e = exponent_of(0);
-  bool ok = no_error(args.err, abort_flag);
 #pragma unroll 1
   for (int jj = 0; jj < nt; ++jj) {
     const int st = jj % kByteStages, slot = jj % kStages;
-    ok = ok && mbar_wait(bytes0 + 8u * st, (jj / kByteStages) & 1, abort_flag, args.err, kDevTimeoutTma);
-    uint4 w[8];
+    bool ok = mbar_wait(bytes0 + 8u * st, (jj / kByteStages) & 1, abort_flag, err, kDevTimeoutTma);
+    if (ok && jj >= kStages) ok = mbar_wait(empty0 + 8u * slot, (jj / kStages - 1) & 1, abort_flag, err, kDevTimeoutSlot);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    const Scale8 sc = scale8(held[st]);
     const uint8_t* src = src0 + st * Cfg::kByteTile;
+    uint8_t* dst = dst0 + slot * kTileBytes;
+    const int n = seq_kv - (j0 + jj) * kTileKeys;          // rows of the sequence in the tile
+    const bool whole = n >= kTileKeys && !sc.two;          // else: the sequence's last tile, or values beyond 448 * 2^7
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+      uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
-    // the stage is read; one decision for the four warps: all go on, or none does
-    if (named_bar_or(is_v ? 3u : 2u, 128u, !ok)) {
-      if (t == 0)
-        for (int x = max(0, issued - kByteStages); x < issued; ++x) packed_drain_wait(bytes0 + 8u * (x % kByteStages), (x / kByteStages) & 1);
-      return;
-    }
-    if (t == 0 && jj + kByteStages < nt) issue(jj + kByteStages);
-    const Scale8 sc = scale8(e);
-    e = exponent_of(jj + 1);
-    if (jj >= kStages) ok = mbar_wait(empty0 + 8u * slot, (jj / kStages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
-    if (ok) {
-      uint8_t* dst = dst0 + slot * kTileBytes;
-      const int n = seq_kv - (j0 + jj) * kTileKeys;        // rows of the sequence in the tile
-      if (n >= kTileKeys && !sc.two) {
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 2048);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 lo, hi;
-          values8x16(w[i], sc.first, lo, hi);
-          *reinterpret_cast<uint4*>(dst + i * 2048) = lo;
-          *reinterpret_cast<uint4*>(dst + i * 2048 + next_chunk) = hi;
+      for (int i = 0; i < 4; ++i) {
+        uint4 lo, hi;
+        values8x16(w[i], sc.first, lo, hi);
+        if (!whole) {
+          lo = scaled_again(lo, sc.second);
+          hi = scaled_again(hi, sc.second);
+          if (row0 + 16 * (i0 + i) >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);    // (a marked block's factor is NaN)
         }
-      } else {
-        // the sequence's last tile, or values beyond 448 * 2^7
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 lo, hi;
-          values8x16(w[i], sc, lo, hi);
-          if (row0 + 16 * i >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);    // (a marked block's factor is NaN)
-          *reinterpret_cast<uint4*>(dst + i * 2048) = lo;
-          *reinterpret_cast<uint4*>(dst + i * 2048 + next_chunk) = hi;
-        }
+        *reinterpret_cast<uint4*>(dst + (i0 + i) * 2048) = lo;
+        *reinterpret_cast<uint4*>(dst + (i0 + i) * 2048 + next_chunk) = hi;
       }
-      fence_proxy_async_smem();
-      mbar_arrive(full0 + 8u * slot);
     }
+    fence_proxy_async_smem();
+    mbar_arrive(full0 + 8u * slot);
+    __syncwarp();                                          // (the stage is read)
+    if ((threadIdx.x & 31u) == 0) mbar_arrive(read0 + 8u * st);
   }
-  // a wait that failed on the last tile leaves nothing in flight: every staged tile has been waited for
 }
 
 // kSparse (narrow, one query row per head): the row's key tiles are those of
@@ -458,6 +418,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       // (the others' bytes complete its transaction count)
       if (i == Cfg::kBarPart && C > 1) count = static_cast<uint32_t>(push ? 32 * C : 32);
       if (i == Cfg::kBarQReady) count = static_cast<uint32_t>(Cfg::kQLoaders);
+      if (k8 && i >= Cfg::kBarByteRead) count = static_cast<uint32_t>(Cfg::kProdWarps);
       if (k8 && ((i >= Cfg::kBarKFull && i < Cfg::kBarKFull + Cfg::kKStages) ||
                  (i >= Cfg::kBarVFull && i < Cfg::kBarVFull + Cfg::kVStages)))
         count = 32u * Cfg::kProdWarps;
@@ -584,13 +545,14 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   if (Cfg::is_ring_warp(warp)) {
     // ------------------------------------------------- producers from bytes
     if constexpr (k8) {
-      if constexpr (kWide) regs_decrease<Cfg::kRingRegs>();
+      regs_decrease<Cfg::kRingRegs>();
       const bool is_v = warp >= Cfg::kVProdWarp;
-      if (run)
-        fill_ring8<Cfg>(is_v ? &tmap_v : &tmap_k, args, is_v, smem + (is_v ? Cfg::kVOff : Cfg::kKOff),
-                        smem + Cfg::kByteOff + (is_v ? Cfg::kByteStages * Cfg::kByteTile : 0u), b, g, j0, nt, seq_kv,
+      const int first = is_v ? Cfg::kByteStages : 0;
+      if (run && no_error(args.err, abort_flag))
+        fill_ring8<Cfg>(is_v, smem + (is_v ? Cfg::kVOff : Cfg::kKOff), smem + Cfg::kByteOff + first * Cfg::kByteTile,
+                        reinterpret_cast<const int*>(smem + Cfg::kStatsOff) + first, j0, nt, seq_kv,
                         bar(is_v ? Cfg::kBarVFull : Cfg::kBarKFull), bar(is_v ? Cfg::kBarVEmpty : Cfg::kBarKEmpty),
-                        bar(Cfg::kBarBytes + (is_v ? Cfg::kByteStages : 0)), abort_flag);
+                        bar(Cfg::kBarBytes + first), bar(Cfg::kBarByteRead + first), abort_flag, args.err);
     }
     if (C > 1) {
       cluster_wait();
@@ -658,16 +620,25 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       cluster_wait();
       if (pull_sync) cluster_sync();
     }
-  } else if (k8 && kWide && warp >= 4) {
-    // ---------------------------------------- issuers, and two idle warps
-    if constexpr (k8 && kWide) regs_decrease<Cfg::kIssuerRegs>();
+  } else if (k8 && warp >= 4) {
+    // -------------------------- issuers, the bytes' producer, an idle warp
+    if constexpr (k8) regs_decrease<Cfg::kIssuerRegs>();
     if (warp == Cfg::kQkWarp) {
       issue_scores();
     } else if (warp == Cfg::kPvWarp) {
       issue_outputs();
-    } else if (C > 1) {
-      cluster_wait();
-      if (pull_sync) cluster_sync();
+    } else {
+      if constexpr (k8) {
+        if (warp == Cfg::kByteProdWarp && run)
+          produce_bytes<Cfg::kByteStages, false>(tmap_k, tmap_v, args, b, g, j0, nt, sbase + Cfg::kByteOff,
+                                          sbase + Cfg::kByteOff + Cfg::kByteStages * Cfg::kByteTile,
+                                          reinterpret_cast<int*>(smem + Cfg::kStatsOff), bar(Cfg::kBarBytes), bar(Cfg::kBarByteRead),
+                                          abort_flag);
+      }
+      if (C > 1) {
+        cluster_wait();
+        if (pull_sync) cluster_sync();
+      }
     }
   } else if (warp == Cfg::kQkWarp) {
     issue_scores();
@@ -862,14 +833,14 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const bool pushing = push && rank > 0;
     // the first CTA's partial slots and barrier, as addresses of the cluster
     const uint32_t lead_slots = pushing ? smem_addr_in_cta(sbase + Cfg::kPartOff, 0u) : 0u;
-    const int my_first = seg_block_start(rank, ns, parts);  // this CTA's first segment
+    const int my_first = seg_block_start(rank, ns, C);  // this CTA's first segment
     if (pushing) cluster_wait();                       // the first CTA's barriers are initialised
 
     auto finish_segment = [&](const RowState& sg, const uint32_t (&o0)[32], const uint32_t (&o1)[32]) {
       if (ws_mode) {
         if (row_used) {
           float* dst = args.part + ((((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) *
-                                     args.n_seg + (ws_block ? my_first + nfin : seg_ws)) * kPartFloats);
+                                     args.n_seg + seg_ws) * kPartFloats);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             *reinterpret_cast<float2*>(dst + 8 * q + 2 * u) =
@@ -1269,9 +1240,7 @@ cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     if (a.lean) return launch_packed_t<false, 1, true>(tk, tv, a, n_sub, s);
     return launch_packed_t<false, 3, true>(tk, tv, a, n_sub, s);
   }
-  if (a.k_exp != nullptr)
-    return a.L <= 2 ? launch_packed_t<false, 3, false, true>(tk, tv, a, n_sub, s)
-                    : launch_packed_t<true, 2, false, true>(tk, tv, a, n_sub, s);
+  if (a.k_exp != nullptr) return launch_packed_t<true, 2, false, true>(tk, tv, a, n_sub, s);
   if (a.L <= 2) return launch_packed_t<false, 3>(tk, tv, a, n_sub, s);
   if (a.part != nullptr) return launch_packed_t<true, 3>(tk, tv, a, n_sub, s);
   return launch_packed_t<true, 2>(tk, tv, a, n_sub, s);

@@ -409,12 +409,12 @@ kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64
 // alone would leave SMs idle.  Narrow rows only; the other CTAs of a cluster
 // keep their segments' partials in shared memory, so a CTA may own at most
 // as many segments as it has partial slots.
-int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max, bool bytes) {
+int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max) {
   if (L > 2) return 1;
   const long long units = static_cast<long long>(n_sub) * B * Hkv;
   if (2 * units > sm_count) return 1;
   const int ns = (n_kv_max + kSegTiles - 1) / kSegTiles;
-  const long long slots = packed_partial_slots(kGroup * L, false, bytes);
+  const long long slots = packed_partial_slots(kGroup * L);
   for (int i = 3, c = 8; i >= 1; --i, c /= 2) {
     if (c > ns || units > cluster_fit[i]) continue;
     if ((ns + c - 1) / c > slots) continue;

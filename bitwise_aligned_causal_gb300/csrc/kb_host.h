@@ -39,8 +39,7 @@ kb_status host_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64
 // (row 32 * head + r) in two swizzled slabs.
 kb_status host_group_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t groups);
 // CTAs per (sub-chunk, batch, KV head) of the packed kernel's fold mode.
-int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max,
-                        bool bytes = false);
+int host_choose_cluster(int sm_count, const int* cluster_fit, int L, int n_sub, int B, int Hkv, int n_kv_max);
 kb_status host_check_heads(int B, int Hq, int Hkv);
 // A page table: pages_per_seq * page_size positions per sequence, page_size a
 // multiple of 128.

@@ -69,22 +69,19 @@ long long partial_bytes(int B, int Hkv, int L, long long rows) {
 }
 
 // CTAs that share a (batch, KV head)'s segments: the number for which the
-// waves of CTAs take the least time, a segment counted as 9 us, a CTA's start
-// as 3 and the fold of the partials as 5 (fitted to timings at 16K and 64K);
-// 1 where a cluster of `cluster` CTAs, which needs no fold, does as well.
-int choose_split(int sm_count, long long units, long long segments, int cluster) {
+// waves of CTAs take the least time.  A segment counts as 7.8 us (tokens) or 10.5
+// (chunks), a CTA's start and end as 6 and the fold of the partials as 8 (fitted
+// to timings of 1 to 19 CTAs at 16K, 32K and 64K).
+int choose_split(int sm_count, long long units, long long segments, bool token) {
+  const double seg_us = token ? 7.8 : 10.5;
   auto cost = [&](long long split) {
     const long long waves = (units * split + sm_count - 1) / sm_count;
-    return waves * (static_cast<double>((segments + split - 1) / split) * 9.0 + 3.0);
+    return waves * (static_cast<double>((segments + split - 1) / split) * seg_us + 6.0) + (split > 1 ? 8.0 : 0.0);
   };
-  double best = (units * cluster + sm_count - 1) / sm_count * (static_cast<double>((segments + cluster - 1) / cluster) * 9.0 + 3.0);
-  int split = 1;
+  int best = 1;
   for (int n = 2; n <= segments && n <= sm_count; ++n)
-    if (cost(n) + 5.0 < best) {
-      best = cost(n) + 5.0;
-      split = n;
-    }
-  return split;
+    if (cost(n) < cost(best)) best = n;
+  return best;
 }
 
 // At most 32 rows: the packed kernel reads the bytes.
@@ -111,7 +108,7 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* work
   a.n_sub = n_sub;
   const long long keys = ragged || c.ctx_lens != nullptr ? cap : static_cast<long long>(c.start) + c.L;
   a.fold_seg = kb::kSegTiles;
-  a.cluster = kb::host_choose_cluster(dev.sm_count, dev.cluster_fit, c.L, n_sub, c.B, c.Hkv, static_cast<int>(blocks_of(keys)), true);
+  a.cluster = 1;
   a.k_exp = c.k_exp;
   a.v_exp = c.v_exp;
   a.plane_rows = c.block_table != nullptr ? c.page_size : c.kv_cap;
@@ -130,14 +127,15 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* work
   if (workspace != nullptr) {
     if (!host_aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(part)) return KB_ERR_INVALID_ARG;
     if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
-    if (part > 0) share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv, segments_of(keys), a.cluster);
+    if (part > 0) share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv, segments_of(keys), c.L <= kb::kMaxRows8);
   }
-  if (share == 1) return host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
+  const auto launch = c.L <= kb::kMaxRows8 ? kb::launch_decode8 : kb::launch_packed;
+  if (share == 1) return host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
   a.cluster = 1;
   a.part = static_cast<float*>(workspace);
   a.n_seg = static_cast<int>(segments_of(keys));
   a.split = share;
-  if ((s = host_done(kb::launch_packed(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)))) != KB_OK) return s;
+  if ((s = host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)))) != KB_OK) return s;
   kb::RowsFoldArgs f{};
   f.part = a.part;
   f.o = c.o;

@@ -88,9 +88,12 @@ cudaError_t launch_prefill_s2(const CUtensorMap& tq, const CUtensorMap& tk, cons
 // n_sub: 1, or 2 when the chunk crosses a 128-position tile boundary.
 cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub,
                           cudaStream_t s);
+// The same for at most kMaxRows8 query rows over a cache held in 8 bits (kb_decode8.cu; a.cluster unused).
+constexpr int kMaxRows8 = 2;
+cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub, cudaStream_t s);
 // Partials a CTA of the narrow packed kernel can keep in shared memory for
 // the cluster's first CTA, with n_rows packed rows.
-uint32_t packed_partial_slots(int n_rows, bool sparse = false, bool bytes = false);
+uint32_t packed_partial_slots(int n_rows, bool sparse = false);
 // Clusters of 2, 4 and 8 CTAs (entries 1, 2, 3) of the narrow packed kernel
 // the current device runs at once; entry 0 is unused.
 void packed_cluster_capacity(int (&active)[4]);

@@ -53,8 +53,11 @@ cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, i
 }
 
 // One CTA per output row, thread t owns column t: the loads of the next eight
-// segments are in flight while eight are folded, left to right.
+// segments are in flight while eight are folded, left to right.  Launched ahead
+// of the partials' kernel's end (it waits for it here), so that its own launch
+// costs no time.
 __global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldArgs args) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (*reinterpret_cast<const volatile uint32_t*>(args.err) != 0) return;    // the partials are not there
   const int row = static_cast<int>(blockIdx.x);
   const int r = row % args.L, b = row / args.L / args.Hq;
@@ -74,8 +77,8 @@ __global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldAr
   float4 st[kAhead];
   auto load = [&](int sg, int i) {
     const int at = min(sg, ns - 1);
-    o[i] = __ldg(p + static_cast<size_t>(at) * kPartFloats + t);
-    st[i] = __ldg(reinterpret_cast<const float4*>(p + static_cast<size_t>(at) * kPartFloats + kHeadDim));
+    o[i] = __ldcg(p + static_cast<size_t>(at) * kPartFloats + t);
+    st[i] = __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(at) * kPartFloats + kHeadDim));
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(i, i);
@@ -102,8 +105,16 @@ __global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldAr
 }
 
 cudaError_t launch_rows_fold(const RowsFoldArgs& a, cudaStream_t s) {
-  kb_rows_fold_kernel<<<static_cast<unsigned>(static_cast<long long>(a.B) * a.Hq * a.L), kHeadDim, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hq * a.L), 1, 1);
+  cfg.blockDim = dim3(kHeadDim, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kb_rows_fold_kernel, a);
 }
 
 }  // namespace kb
