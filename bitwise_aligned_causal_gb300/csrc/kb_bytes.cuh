@@ -23,6 +23,8 @@ __device__ __forceinline__ void drain_bytes(uint32_t bar, uint32_t parity) {
     if (global_timer_ns() - t0 > 50000000ull) break;
 }
 
+static __device__ __noinline__ void drain_far(uint32_t bar, uint32_t parity) { drain_bytes(bar, parity); }
+
 // Rows 128 j .. of sequence b, KV head g: the row of the byte map and its
 // plane, and the place of the block's exponent.  False for a page index out of
 // range (reported; the map reads zeros there).
@@ -78,6 +80,9 @@ __device__ __forceinline__ void produce_bytes(const CUtensorMap& tmap_k, const C
     return p;
   };
   Place cur{}, next = look_up(lane);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return kFar ? wait_near(bar, parity, abort_flag, args.err, kDevTimeoutSlot) : mbar_wait(bar, parity, abort_flag, args.err, kDevTimeoutSlot);
+  };
   int k_issued = 0, v_issued = 0;
   bool ok = true;
   for (int jj = 0; jj < nt && ok; ++jj) {
@@ -89,28 +94,29 @@ __device__ __forceinline__ void produce_bytes(const CUtensorMap& tmap_k, const C
     const int row = __shfl_sync(0xffffffffu, cur.row, from), plane = __shfl_sync(0xffffffffu, cur.plane, from);
     const int ke = __shfl_sync(0xffffffffu, cur.ke, from), ve = __shfl_sync(0xffffffffu, cur.ve, from);
     if (lane == 0) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t at = static_cast<uint32_t>(v * kStages + st);
-        if (ok && jj >= kStages)
-          ok = kFar ? wait_near(read0 + 8u * at, (jj / kStages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot)
-                    : mbar_wait(read0 + 8u * at, (jj / kStages - 1) & 1, abort_flag, args.err, kDevTimeoutSlot);
-        if (ok) {
-          held[at] = v ? ve : ke;
-          mbar_arrive_expect_tx(full0 + 8u * at, kBytes);
-          tma_load_3d_hint((v ? v_staged : k_staged) + st * kBytes, v ? &tmap_v : &tmap_k, 0, row, plane, full0 + 8u * at, stream_once);
-          (v ? v_issued : k_issued) = jj + 1;
-        }
+      if (jj >= kStages) ok = wait(read0 + 8u * st, (jj / kStages - 1) & 1);
+      if (ok) {
+        held[st] = ke;
+        mbar_arrive_expect_tx(full0 + 8u * st, kBytes);
+        tma_load_3d_hint(k_staged + st * kBytes, &tmap_k, 0, row, plane, full0 + 8u * st, stream_once);
+        k_issued = jj + 1;
+        if (jj >= kStages) ok = wait(read0 + 8u * (kStages + st), (jj / kStages - 1) & 1);
+      }
+      if (ok) {
+        held[kStages + st] = ve;
+        mbar_arrive_expect_tx(full0 + 8u * (kStages + st), kBytes);
+        tma_load_3d_hint(v_staged + st * kBytes, &tmap_v, 0, row, plane, full0 + 8u * (kStages + st), stream_once);
+        v_issued = jj + 1;
       }
     }
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   }
   // no copy is in flight when the CTA leaves, whoever gave up
-  if (lane == 0)
-    for (int v = 0; v < 2; ++v) {
-      const int issued = v ? v_issued : k_issued;
-      for (int x = max(0, issued - kStages); x < issued; ++x) drain_bytes(full0 + 8u * (v * kStages + x % kStages), (x / kStages) & 1);
-    }
+  auto drain = [](uint32_t bar, uint32_t parity) { kFar ? drain_far(bar, parity) : drain_bytes(bar, parity); };
+  if (lane == 0) {
+    for (int x = max(0, k_issued - kStages); x < k_issued; ++x) drain(full0 + 8u * (x % kStages), (x / kStages) & 1);
+    for (int x = max(0, v_issued - kStages); x < v_issued; ++x) drain(full0 + 8u * (kStages + x % kStages), (x / kStages) & 1);
+  }
 }
 
 }  // namespace kb

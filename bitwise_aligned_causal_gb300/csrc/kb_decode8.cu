@@ -29,14 +29,16 @@
 // A CTA runs a contiguous block of the row's segments: all of them, folded
 // here, or (args.split CTAs) its share, whose partials go to the workspace.
 //
-// Measured (B = 32, contexts of 16K): 266 us, 4.0 TB/s of bytes, against 332 in
-// the packed kernel's shape; a pair of tiles takes a CTA 1.0 us whatever HBM
-// does, where its share of HBM would allow 0.74.  What bounds it is the four
-// schedulers: 1200 instructions each per pair of tiles, half of them the
-// conversion's, on an ALU pipe that takes one every other cycle.  Eight warps
-// for K and for V, unrolled loops and the shift on the FMA pipe (where the
-// compiler puts it anyway) changed nothing; loops that did not fit the
-// instruction caches cost up to twice.
+// Measured (B = 32, contexts of 16K): 258 us, 4.2 TB/s of bytes, against 332 in
+// the packed kernel's shape (one conversation of 64K: 55 us with its segments
+// over all CTAs).  What bounds it is the four schedulers: 1200 instructions
+// each per pair of tiles, half of them the conversion's, on an ALU pipe that
+// takes one every other cycle; HBM would allow 172 us.  Next come the
+// instruction caches that sixteen warps of seven roles share: what is rare is
+// out of line (timeouts, drains, odd tiles: 284 to 258 us), and the conversion
+// loops hold two chunks (one: 297 us; four: 261; eight: 309).  Eight warps for
+// K and for V, one loop for both (279 us) and the shift on the FMA pipe were no
+// better.
 #include "kb_bytes.cuh"
 #include "kb_cache8.cuh"
 #include "kb_contract.cuh"
@@ -99,6 +101,36 @@ struct Decode8Cfg {
   static constexpr uint32_t kSmemBytes = kSmemUsed + 1024;
   static_assert(kSmemBytes <= 227u * 1024u, "shared memory budget");
 };
+
+constexpr int kPasses = 8;                                // 16-byte chunks of a tile's bytes per conversion thread
+constexpr int kVStep = 16 * kHeadDim;                     // V, from a thread's row to its next: bytes staged, and of a slab
+
+// A tile that ends the sequence (n of its rows lie in it; values past them are
+// zero, whatever the block's mark) or whose values reach beyond 448 * 2^7, out
+// of the way of the loops for whole ones.
+__device__ __forceinline__ void odd16(const uint4& w, const Scale8& sc, bool live, uint4& lo, uint4& hi) {
+  values8x16(w, sc.first, lo, hi);
+  lo = scaled_again(lo, sc.second);
+  hi = scaled_again(hi, sc.second);
+  if (!live) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __noinline__ void odd_values(const uint8_t* src, uint8_t* dst, int next_chunk, int row0, int n, Scale8 sc) {
+#pragma unroll 1
+  for (int i = 0; i < kPasses; ++i) {
+    uint4 lo, hi;
+    odd16(*reinterpret_cast<const uint4*>(src + i * kVStep), sc, row0 + kVStep / kHeadDim * i < n, lo, hi);
+    *reinterpret_cast<uint4*>(dst + i * kVStep) = lo;
+    *reinterpret_cast<uint4*>(dst + i * kVStep + next_chunk) = hi;
+  }
+}
+__device__ __noinline__ void odd_keys(const uint8_t* src, uint32_t dst, int row, int n, Scale8 sc) {
+#pragma unroll 1
+  for (int i = 0; i < kPasses; ++i) {
+    uint4 lo, hi;
+    odd16(*reinterpret_cast<const uint4*>(src + ((i ^ (row & 7)) << 4)), sc, row < n, lo, hi);
+    tmem_st8(dst + i * 8u, lo, hi);
+  }
+}
 
 }  // namespace
 
@@ -244,37 +276,37 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const bool due = mbar_test_wait(bar(Cfg::kBarStFull + (G & 1)), (G >> 1) & 1) &&
                          mbar_test_wait(bar(Cfg::kBarPvDone + t_last % Cfg::kPvBufs), (t_last / Cfg::kPvBufs) & 1);
         if (__all_sync(0xffffffffu, due)) {
-                    tc_fence_after();
-                    uint32_t o[Cfg::kN];
-                    tmem_ld16_wait(o_tmem, o);
-                    tc_fence_before();
-                    mbar_arrive(bar(Cfg::kBarORead));
-                    const float2 sv = lane < kRows ? reinterpret_cast<const float2*>(smem + Cfg::kStatsOff)[(G & 1) * kRows + lane]
-                                                   : make_float2(-INFINITY, 0.0f);
-                    mbar_arrive(bar(Cfg::kBarStEmpty + (G & 1)));
-                    const RowState sg{sv.x, __fmul_rn(sv.x, c_log2), sv.y};
-                    if (args.part != nullptr) {
-                      // the segment's partial, for the fold of all CTAs' segments
+          tc_fence_after();
+          uint32_t o[Cfg::kN];
+          tmem_ld16_wait(o_tmem, o);
+          tc_fence_before();
+          mbar_arrive(bar(Cfg::kBarORead));
+          const float2 sv = lane < kRows ? reinterpret_cast<const float2*>(smem + Cfg::kStatsOff)[(G & 1) * kRows + lane]
+                                         : make_float2(-INFINITY, 0.0f);
+          mbar_arrive(bar(Cfg::kBarStEmpty + (G & 1)));
+          const RowState sg{sv.x, __fmul_rn(sv.x, c_log2), sv.y};
+          if (args.part != nullptr) {
+            // the segment's partial, for the fold of all CTAs' segments
 #pragma unroll
-                      for (int i = 0; i < kRows; ++i)
-                        if (i < n_rows)
-                          args.part[(((static_cast<size_t>(b) * args.Hq + g * kGroup + i / Lc) * args.L + r0 + i % Lc) * args.n_seg + g0 + G) *
-                                        kPartFloats + me] = __uint_as_float(o[i]);
-                      if (warp == 0 && lane < n_rows)
-                        *reinterpret_cast<float4*>(
-                            args.part + (((static_cast<size_t>(b) * args.Hq + g * kGroup + lane / Lc) * args.L + r0 + lane % Lc) * args.n_seg +
-                                         g0 + G) * kPartFloats + kHeadDim) = make_float4(sg.m, sg.mc, sg.l, 0.0f);
-                    } else if (G == 0) {
-                      acc = sg;
+            for (int i = 0; i < kRows; ++i)
+              if (i < n_rows)
+                args.part[(((static_cast<size_t>(b) * args.Hq + g * kGroup + i / Lc) * args.L + r0 + i % Lc) * args.n_seg + g0 + G) *
+                              kPartFloats + me] = __uint_as_float(o[i]);
+            if (warp == 0 && lane < n_rows)
+              *reinterpret_cast<float4*>(
+                  args.part + (((static_cast<size_t>(b) * args.Hq + g * kGroup + lane / Lc) * args.L + r0 + lane % Lc) * args.n_seg +
+                               g0 + G) * kPartFloats + kHeadDim) = make_float4(sg.m, sg.mc, sg.l, 0.0f);
+          } else if (G == 0) {
+            acc = sg;
 #pragma unroll
-                      for (int i = 0; i < kRows; ++i) acc_o[i] = __uint_as_float(o[i]);
-                    } else {
-                      const FoldScale f = fold_state(acc, sg);
+            for (int i = 0; i < kRows; ++i) acc_o[i] = __uint_as_float(o[i]);
+          } else {
+            const FoldScale f = fold_state(acc, sg);
 #pragma unroll
-                      for (int i = 0; i < kRows; ++i)
-                        acc_o[i] = fold_o(acc_o[i], __uint_as_float(o[i]),
-                                          FoldScale{__shfl_sync(0xffffffffu, f.a, i), __shfl_sync(0xffffffffu, f.b, i)});
-                    }
+            for (int i = 0; i < kRows; ++i)
+              acc_o[i] = fold_o(acc_o[i], __uint_as_float(o[i]),
+                                FoldScale{__shfl_sync(0xffffffffu, f.a, i), __shfl_sync(0xffffffffu, f.b, i)});
+          }
           ++G;
           moved = true;
         }
@@ -336,7 +368,6 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const int* held = reinterpret_cast<const int*>(smem + Cfg::kExpOff) + (is_v ? kStages : 0);
       // V: a thread's column of eight rows, as in the packed kernel's rings; K:
       // the thread's own row
-      constexpr int kPasses = 8;                          // 16-byte chunks per thread
       const int col = (t & 3) | ((t >> 1) & 4), low = is_v ? ((t >> 4) & 3) ^ ((t & 4) ? 5 : 0) : (t & 7);
       const int row0 = is_v ? low + 8 * (t >> 6) : t;
       const int next_chunk = (low & 1) ? -16 : 16;
@@ -356,19 +387,14 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         const int n = seq_kv - (j0 + jj) * kTileKeys;     // rows of the sequence in the tile
         const bool whole = n >= kTileKeys && !sc.two;     // else: the sequence's last tile, or values beyond 448 * 2^7
         const uint8_t* src = staged + st * Cfg::kByteTile + row0 * 128;
-        // values past the sequence are zero (a marked block's factor is NaN)
-        auto mend = [&](uint4& lo, uint4& hi, int row) {
-          lo = scaled_again(lo, sc.second);
-          hi = scaled_again(hi, sc.second);
-          if (row >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-        };
         // (small loops stay in the schedulers' instruction caches, which the kernel's many roles share)
         if (is_v) {
-          constexpr int kStep = 16 * kHeadDim;             // from a thread's row to its next: bytes staged, and of a slab
+          constexpr int kStep = kVStep;                    // from a thread's row to its next: bytes staged, and of a slab
           uint8_t* dst = dst0 + buf * kTileBytes;
           src += (col ^ low) << 4;
+          if (!whole) odd_values(src, dst, next_chunk, row0, n, sc);
 #pragma unroll 1
-          for (int i = 0; i < kPasses; i += 2) {
+          for (int i = 0; i < kPasses && whole; i += 2) {
             uint4 w[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) w[q] = *reinterpret_cast<const uint4*>(src + (i + q) * kStep);
@@ -376,7 +402,6 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             for (int q = 0; q < 2; ++q) {
               uint4 lo, hi;
               values8x16(w[q], sc.first, lo, hi);
-              if (!whole) mend(lo, hi, row0 + kStep / kHeadDim * (i + q));
               *reinterpret_cast<uint4*>(dst + (i + q) * kStep) = lo;
               *reinterpret_cast<uint4*>(dst + (i + q) * kStep + next_chunk) = hi;
             }
@@ -385,8 +410,9 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           mbar_arrive(full0 + 8u * buf);
         } else {
           tc_fence_after();
+          if (!whole) odd_keys(src, k_tmem + buf * 64u, row0, n, sc);
 #pragma unroll 1
-          for (int i = 0; i < kPasses; i += 2) {
+          for (int i = 0; i < kPasses && whole; i += 2) {
             uint4 w[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) w[q] = *reinterpret_cast<const uint4*>(src + (((i + q) ^ low) << 4));
@@ -394,7 +420,6 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             for (int q = 0; q < 2; ++q) {
               uint4 lo, hi;
               values8x16(w[q], sc.first, lo, hi);
-              if (!whole) mend(lo, hi, row0);
               tmem_st8(k_tmem + buf * 64u + (i + q) * 8u, lo, hi);
             }
           }
@@ -428,7 +453,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       }
       if (!ok) {
         tc_commit(bar(Cfg::kBarDrain));
-        drain_bytes(bar(Cfg::kBarDrain), 0);
+        drain_far(bar(Cfg::kBarDrain), 0);
       }
     }
   } else if (warp == Cfg::kPvWarp) {
@@ -454,7 +479,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       }
       if (!ok) {
         tc_commit(bar(Cfg::kBarDrain + 1));
-        drain_bytes(bar(Cfg::kBarDrain + 1), 0);
+        drain_far(bar(Cfg::kBarDrain + 1), 0);
       }
     }
   } else if (warp == Cfg::kProdWarp) {
