@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libkb_attn.so")
 SOURCES = ["kb_host.cu", "kb_prefill2.cu", "kb_decode.cu", "kb_backward.cu", "kb_segment.cu",
            "kb_host_sparse.cu", "kb_append.cu", "kb_select.cu", "kb_sparse_plan.cu", "kb_sparse.cu",
            "kb_sparse_bwd.cu", "kb_host_cache.cu", "kb_cache8.cu",
-           "kb_weights.cu", "kb_evict.cu", "kb_decode8.cu"]
+           "kb_weights.cu", "kb_weights_rows.cu", "kb_evict.cu", "kb_decode8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -119,11 +119,12 @@ kb_status check_device_pointer(const void* p) {
 // {64, 128, 2} moves a whole 128-row tile into the two 128-byte-swizzled
 // slabs the MMA descriptors expect.  `rows` rows are in bounds in each of
 // `planes` planes `plane_stride` bytes apart; reads beyond `rows` are
-// zero-filled by the TMA unit.
-kb_status encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {
+// zero-filled by the TMA unit.  halves = 1: boxes of one column half.
+kb_status encode_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride,
+                          cuuint32_t halves = 2u) {
   cuuint64_t dims[4] = {64u, rows, 2u, planes};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(kb::kHeadDim) * 2u, 128u, plane_stride};
-  cuuint32_t box[4] = {64u, 128u, 2u, 1u};
+  cuuint32_t box[4] = {64u, 128u, halves, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -379,6 +380,10 @@ kb_status host_device_pointer(const void* p) { return check_device_pointer(p); }
 
 kb_status host_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {
   return encode_rows_map(m, base, rows, planes, plane_stride);
+}
+
+kb_status host_halves_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {
+  return encode_rows_map(m, base, rows, planes, plane_stride, 1u);
 }
 
 kb_status host_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride) {

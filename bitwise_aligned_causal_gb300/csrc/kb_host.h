@@ -30,6 +30,8 @@ kb_status host_device_pointer(const void* p);
 // Tensor map of whole 128-row tiles: box {64 columns, 128 rows, 2 halves} of
 // a [planes, rows, 128] bf16 tensor (kb_host.cu).
 kb_status host_rows_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride);
+// The same with boxes of one column half (tma_load_half).
+kb_status host_halves_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride);
 // Tensor map of whole 128-row tiles of a cache held in 8 bits: box {128 bytes,
 // 128 rows} of a [planes, rows, 128] byte tensor, 128-byte swizzle.
 kb_status host_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t planes, uint64_t plane_stride);

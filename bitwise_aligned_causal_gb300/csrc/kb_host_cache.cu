@@ -359,11 +359,14 @@ kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, fl
   const bool paged = block_table != nullptr;
   const uint64_t stride_rows = static_cast<uint64_t>(paged ? page_size : kv_cap);
   const uint64_t rows = paged || starts != nullptr ? stride_rows : static_cast<uint64_t>(start) + L;
+  const bool few = L <= kb::kMaxPackedRows;
   CUtensorMap tq, tk;
-  if ((s = kb::host_rows_map(&tq, q, static_cast<uint64_t>(L), static_cast<uint64_t>(B) * Hq, static_cast<uint64_t>(L) * row_bytes)) != KB_OK)
+  if ((s = (few ? kb::host_rows_map : kb::host_halves_map)(&tk, k, rows, static_cast<uint64_t>(paged ? num_pages : B) * Hkv,
+                                                          stride_rows * row_bytes)) != KB_OK)
     return s;
-  if ((s = kb::host_rows_map(&tk, k, rows, static_cast<uint64_t>(paged ? num_pages : B) * Hkv, stride_rows * row_bytes)) != KB_OK)
-    return s;
+  // (a group's four heads are one run of rows)
+  const uint64_t group_rows = static_cast<uint64_t>(kb::kGroup) * L;
+  if (!few && (s = kb::host_rows_map(&tq, q, group_rows, static_cast<uint64_t>(B) * Hkv, group_rows * row_bytes)) != KB_OK) return s;
   kb::WeightsArgs a{};
   a.q = q;
   a.lse = lse;
@@ -380,7 +383,10 @@ kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, fl
   a.page_size = page_size;
   a.num_pages = num_pages;
   a.err = dev.err;
-  return host_done(kb::launch_weights(tq, tk, a, starts != nullptr ? cap : start + L, dev.sm_count, static_cast<cudaStream_t>(stream)));
+  const int max_keys = starts != nullptr ? cap : start + L;
+  const auto st = static_cast<cudaStream_t>(stream);
+  return host_done(few ? kb::launch_weights(tk, a, max_keys, dev.sm_count, st)
+                       : kb::launch_weights_rows(tq, tk, a, max_keys, dev.sm_count, st));
 }
 
 kb_status kb_attn_evict(void* k, void* v, const float* weights, float* weights_out, int* kept, int B, int Hkv, const int* lens,

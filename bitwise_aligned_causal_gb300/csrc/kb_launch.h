@@ -229,12 +229,15 @@ struct WeightsArgs {
   int kv_cap;                  // positions per sequence the cache can hold
   const int* block_table;
   int pages_per_seq, page_size, num_pages;
-  int splits;                  // CTAs per (batch, KV head)
+  int splits;                  // shares of a (batch, KV head)'s key tiles
+  int ctas;                    // many rows: CTAs of the cluster that shares a pair of key tiles
   uint32_t* err;
 };
-// tq, tk: host_rows_map of q and of the cache; max_keys: keys of the longest sequence the call can have.
-cudaError_t launch_weights(const CUtensorMap& tq, const CUtensorMap& tk, WeightsArgs a, int max_keys, int sm_count,
-                           cudaStream_t s);
+// max_keys: keys of the longest sequence the call can have.  At most kMaxPackedRows rows; tk: host_rows_map of the cache.
+cudaError_t launch_weights(const CUtensorMap& tk, WeightsArgs a, int max_keys, int sm_count, cudaStream_t s);
+// More rows; tq: host_rows_map of q's [B * Hkv] planes of 4 L rows, tk: host_halves_map of the cache.
+cudaError_t launch_weights_rows(const CUtensorMap& tq, const CUtensorMap& tk, WeightsArgs a, int max_keys, int sm_count,
+                                cudaStream_t s);
 
 // Eviction of a cache's lightest keys (kb_evict.cu).
 struct EvictArgs {

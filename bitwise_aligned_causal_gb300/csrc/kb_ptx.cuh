@@ -214,6 +214,15 @@ __device__ __forceinline__ void tma_load_tile_hint(uint32_t dst, const void* tma
       : "memory");
 }
 
+// One column half (64 columns) of a tile, from a map whose boxes are halves.
+__device__ __forceinline__ void tma_load_half(uint32_t dst, const void* tmap, int row, int half, int plane, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(0), "r"(row), "r"(half), "r"(plane), "r"(bar)
+      : "memory");
+}
+
 // Prefetch one whole 128-row tile (addressed as tma_load_tile) into L2 only.
 __device__ __forceinline__ void tma_prefetch_tile_l2(const void* tmap, int row, int plane) {
   asm volatile(
@@ -232,15 +241,6 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
-}
-
-// Sixteen bytes that are read once, past L1.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(reinterpret_cast<uint64_t>(p)));
-  return v;
 }
 
 // ------------------------------------------------------------------- tcgen05
