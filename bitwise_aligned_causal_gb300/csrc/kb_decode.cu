@@ -343,11 +343,13 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     Lb = 1;
   }
   const int seq_kv = pos0 + Lb;
-  const int split = min(Lb, (pos0 / kTileKeys + 1) * kTileKeys - pos0);   // rows before the first tile boundary
-  const int r0 = (sub == 0) ? 0 : split;
-  const int r1 = (sub == 0) ? split : Lb;
+  // sub-chunks: the rows of a tile's positions, or of 32 positions of a longer chunk
+  const int cell = k8 && args.L > kMaxPackedRows ? kMaxPackedRows : kTileKeys;
+  const int cell0 = (pos0 / cell + sub) * cell - pos0;
+  const int r0 = max(cell0, 0);
+  const int r1 = min(cell0 + cell, Lb);
   const int Lc = max(r1 - r0, 1);
-  if (r1 - r0 <= 0) active = false;                     // the chunk does not reach a second tile
+  if (r1 - r0 <= 0) active = false;                     // the chunk does not reach this one
   const int n_rows = kGroup * Lc;                       // packed rows in use
   const int n_kv = (pos0 + r1 - 1) / kTileKeys + 1;     // C1: KV tiles 0..floor(last position / 128)
   int* walk = reinterpret_cast<int*>(smem + Cfg::kWalkOff);

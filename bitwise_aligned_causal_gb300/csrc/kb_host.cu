@@ -309,10 +309,12 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
     // from S=1.5K to 16K) under the previous unit, against a unit of (n+1)/2
     // key tiles at about 1550 cycles each; its static split leaves a tail of
     // (ceil(p) - p) / p with p pairs per CTA, where the one-CTA-per-tile
-    // launch ends on the shortest tiles.
+    // launch ends on the shortest tiles.  Where every tile finds an SM of its own
+    // and sees many keys, none shares one (256 rows at 32K: 401 us in pairs, 204 so).
     const long long pairs = static_cast<long long>((a.n_tiles + 1) / 2) * kb::kGroup * B * Hkv;
-    bool persistent = pairs <= a.max_ctas;
-    if (!persistent) {
+    const bool roomy = static_cast<long long>(a.n_tiles) * B * Hq <= a.max_ctas && (ragged ? kv_cap - L : start) >= L;
+    bool persistent = pairs <= a.max_ctas && !roomy;
+    if (!persistent && !roomy) {
       const double p = static_cast<double>(pairs) / a.max_ctas;
       const double tail = (std::ceil(p) - p) / p;
       const double saved = 5000.0 / (0.5 * (a.n_tiles + 1) * 1550.0 + 5000.0);
@@ -325,7 +327,7 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
     const long long kv_bytes = 2LL * B * Hkv * (start + L) * kb::kHeadDim * 2;
     if (force_snake) {
       a.persistent = kb::kSchedSnake;
-    } else if (!force_persistent && !ragged && 4 * kv_bytes <= 3 * dst->l2_bytes &&
+    } else if (!force_persistent && !roomy && !ragged && 4 * kv_bytes <= 3 * dst->l2_bytes &&
                pairs < 32LL * a.max_ctas) {
       const long long n = a.n_tiles, G = a.max_ctas;
       const long long units = n * B * Hq;

@@ -58,7 +58,7 @@ kb_status check_call(const Call8& c, int* cap, kb::HostDevice* dev) {
 // Segments of 1024 keys of the longest sequence a call over `rows` positions can have.
 long long segments_of(long long rows) { return (blocks_of(rows) + kb::kSegTiles - 1) / kb::kSegTiles; }
 
-// Bytes of the segments' partials of a call of at most 32 rows, where CTAs
+// Bytes of the segments' partials of a call that reads the bytes, where CTAs
 // can share a KV head's segments: 0 for batches that fill the SMs without, and
 // where the partials would pass 1 GB.
 constexpr long long kMaxSplitUnits = 304;
@@ -68,27 +68,48 @@ long long partial_bytes(int B, int Hkv, int L, long long rows) {
   return n <= (1LL << 30) ? align256(n) : 0;
 }
 
-// CTAs that share a (batch, KV head)'s segments: the number for which the
-// waves of CTAs take the least time.  A segment counts as 7.8 us (tokens) or 10.5
-// (chunks), a CTA's start and end as 6 and the fold of the partials as 8 (fitted
-// to timings of 1 to 19 CTAs at 16K, 32K and 64K).
-int choose_split(int sm_count, long long units, long long segments, bool token) {
+// Sub-chunks of a call: the rows of one tile's positions each, of 32 positions in a chunk of more than 32 rows.
+int sub_chunks(int L, int start, bool ragged) {
+  const int cell = L > kb::kMaxPackedRows ? kb::kMaxPackedRows : kb::kTileKeys;
+  if (L == 1) return 1;                                               // (one row never crosses a tile boundary)
+  return ragged ? (L - 2) / cell + 2 : (start + L - 1) / cell - start / cell + 1;
+}
+
+// CTAs that share the segments of a unit (a sub-chunk of a batch entry and KV
+// head): the number for which the waves of CTAs take the least time, and that
+// time in us.  A segment counts as 7.8 us (tokens) or 10.5 (chunks), a CTA's
+// start and end as 6, the fold of the partials as 8 and their bytes, written and
+// read, as 1.4 MB a us (fitted to timings of 1 to 19 CTAs at 16K, 32K and 64K,
+// and of 64 to 256 rows at 28K and 32K).
+struct Split {
+  int ctas;
+  double us;
+};
+Split choose_split(int sm_count, long long units, long long segments, bool token, long long part) {
   const double seg_us = token ? 7.8 : 10.5;
   auto cost = [&](long long split) {
     const long long waves = (units * split + sm_count - 1) / sm_count;
-    return waves * (static_cast<double>((segments + split - 1) / split) * seg_us + 6.0) + (split > 1 ? 8.0 : 0.0);
+    return waves * (static_cast<double>((segments + split - 1) / split) * seg_us + 6.0) +
+           (split > 1 ? 8.0 + static_cast<double>(part) / 1.4e6 : 0.0);
   };
-  int best = 1;
-  for (int n = 2; n <= segments && n <= sm_count; ++n)
-    if (cost(n) < cost(best)) best = n;
+  Split best{1, cost(1)};
+  for (int n = 2; part > 0 && n <= segments && n <= sm_count; ++n)
+    if (cost(n) < best.us) best = {n, cost(n)};
   return best;
 }
 
-// At most 32 rows: the packed kernel reads the bytes.
+// The time in us of a chunk's other way: its keys and values into bf16 in the
+// workspace (3 bytes moved for each, at 5.5 TB/s), then the bf16 chunk, 0.8 us a
+// tile of a head's rows and a tile of keys on one SM (64 to 1000 rows at 32K).
+double gathered_us(int sm_count, int B, int Hkv, int L, long long rows) {
+  const long long tiles = static_cast<long long>(B) * Hkv * kb::kGroup * blocks_of(L);
+  return 2.0 + static_cast<double>(B) * Hkv * rows * kb::kHeadDim * 6 / 5.5e6 + (tiles + sm_count - 1) / sm_count * (blocks_of(rows) * 0.8 + 2.0);
+}
+
+// The packed kernels read the bytes.
 kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* workspace, size_t workspace_bytes, void* stream) {
   const bool ragged = c.starts != nullptr;
-  const int split = std::min(c.L, kb::kTileKeys - c.start % kb::kTileKeys);
-  const int n_sub = c.L > 1 && (ragged || split < c.L) ? 2 : 1;       // (one row never crosses a tile boundary)
+  const int n_sub = sub_chunks(c.L, c.start, ragged);
   kb::PackedArgs a{};
   a.q = c.q;
   a.o = c.o;
@@ -127,7 +148,9 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* work
   if (workspace != nullptr) {
     if (!host_aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(part)) return KB_ERR_INVALID_ARG;
     if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
-    if (part > 0) share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv, segments_of(keys), c.L <= kb::kMaxRows8);
+    if (part > 0)
+      share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv * (c.L > kb::kMaxPackedRows ? n_sub : 1),
+                           segments_of(keys), c.L <= kb::kMaxRows8, part).ctas;
   }
   const auto launch = c.L <= kb::kMaxRows8 ? kb::launch_decode8 : kb::launch_packed;
   if (share == 1) return host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
@@ -278,7 +301,7 @@ kb_status kb_attn_cache_values(const void* cache, const signed char* exps, void*
 size_t kb_attn_chunk_8bit_workspace_bytes(int B, int Hkv, int L, int rows) {
   if (B < 1 || Hkv < 1 || L < 1 || rows < L || rows > kMaxRows) return 0;
   if (L <= kb::kMaxPackedRows) return static_cast<size_t>(partial_bytes(B, Hkv, L, rows));
-  return static_cast<size_t>(2 * gathered_bytes(B, Hkv, rows));
+  return static_cast<size_t>(std::max(2 * gathered_bytes(B, Hkv, rows), partial_bytes(B, Hkv, L, rows)));
 }
 
 kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const signed char* k_exp, const signed char* v_exp,
@@ -297,6 +320,10 @@ kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const 
   if (workspace == nullptr || !host_aligned(workspace, 256) || workspace_bytes < need) return KB_ERR_INVALID_ARG;
   if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
   if (static_cast<long long>(B) * Hkv * blocks_of(rows) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  const long long units = static_cast<long long>(B) * Hkv * sub_chunks(L, c.start, starts != nullptr);
+  if (units <= 8LL * dev.sm_count && choose_split(dev.sm_count, units, segments_of(rows), false, partial_bytes(B, Hkv, L, rows)).us <
+                                         gathered_us(dev.sm_count, B, Hkv, L, rows))
+    return packed8(c, cap, dev, workspace, workspace_bytes, stream);
   kb::Gather8Args a{};
   a.k = k;
   a.v = v;

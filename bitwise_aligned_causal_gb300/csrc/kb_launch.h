@@ -43,7 +43,7 @@ struct PackedArgs {
   int pages_per_seq, page_size, num_pages;
   const int* starts;       // optional device [B]: per-sequence start and row count (ragged
   const int* lens;         //   batch); L is then the row stride of q and o
-  int n_sub;               // sub-chunks per (b, kv head) in the grid (1 or 2)
+  int n_sub;               // sub-chunks per (b, kv head) in the grid (1 or 2; more over a cache in 8 bits)
   // fold mode (part == nullptr): C5 segments of fold_seg key tiles, cut into
   // contiguous blocks over a cluster of `cluster` CTAs per (sub, b, g); the
   // cluster's first CTA folds them all and writes o
@@ -85,7 +85,8 @@ constexpr int kSchedPairs = 1;       // persistent, balanced pairs of query tile
 constexpr int kSchedSnake = 2;       // persistent, single units longest first, dealt back and forth
 cudaError_t launch_prefill_s2(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PrefillArgs& a, cudaStream_t s);
-// n_sub: 1, or 2 when the chunk crosses a 128-position tile boundary.
+// n_sub: 1, or 2 when the chunk crosses a 128-position tile boundary.  Over a
+// cache held in 8 bits L may be larger: sub-chunks of 32 positions then.
 cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub,
                           cudaStream_t s);
 // The same for at most kMaxRows8 query rows over a cache held in 8 bits (kb_decode8.cu; a.cluster unused).

@@ -1198,8 +1198,8 @@ def _chunk_8bit(q, k, v, k_exp, v_exp, start, starts, lens, block_table, out, wo
 
 def chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, start, out=None, workspace=None, stream=None, check=False):
     """chunk over a cache held in 8 bits (append_8bit): q [B,Hq,L,128] at positions start.. .  The bits are chunk's on the
-    bf16 caches that cache_values gives.  Up to 32 rows read the bytes; a longer chunk turns the visible keys and
-    values into bf16 in the workspace (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
+    bf16 caches that cache_values gives.  Few rows read the bytes; where a longer chunk gains by it, the visible keys
+    and values are turned into bf16 in the workspace first (kb_attn_chunk_8bit_workspace_bytes; a new one by default)."""
     return _chunk_8bit(q, k_cache, v_cache, k_exp, v_exp, int(start), None, None, None, out, workspace, stream, check)
 
 

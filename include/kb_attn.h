@@ -501,8 +501,9 @@ kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, 
  * starts or ctx_lens is given; calls that can overlap on the GPU need one each.
  * L <= 32 reads the bytes; with a workspace several CTAs share the keys of a KV
  * head where the batch leaves SMs idle, and with NULL it runs without, slower
- * there, with the same bits.  A longer chunk is computed from the visible
- * values in bf16, in the workspace, which it needs.
+ * there, with the same bits.  A longer chunk needs its workspace: it reads the
+ * bytes as well where few rows see many keys, else it is computed from the
+ * visible values in bf16, in the workspace; the bits are the same.
  */
 kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
                               void* k_cache, void* v_cache, signed char* k_exp, signed char* v_exp,

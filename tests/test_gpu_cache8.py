@@ -280,6 +280,33 @@ def test_ragged_chunks(kb, page, L, starts, lens):
         assert bool((out[b, :, lens[b]:] == 7.0).all())
 
 
+@pytest.mark.parametrize("page", [0, 128])
+@pytest.mark.parametrize("B,L,start", [(1, 33, 9000), (1, 64, 20448), (2, 100, 12001), (1, 200, 24577), (3, 65, 8100), (1, 300, 9000)])
+def test_longer_chunks_late_in_a_context(kb, page, B, L, start):
+    """Few query rows for many keys: the ways that fill the SMs, against the packed kernel's rows over bf16."""
+    import torch
+
+    cap = -(-(start + L + 5) // (page or 1)) * (page or 1)
+    cache, pages, seq = filled(kb, B, cap, page, n=start + L)
+    q = randn(83, B, 32, L, 128)
+    k, v = (t[:, :, :start + L].contiguous() for t in bf16_of(kb, cache, pages, seq, B))
+    want = torch.cat([kb.chunk(q[:, :, i:i + 32].contiguous(), k, v, start + i, check=True) for i in range(0, L, 32)], 2)
+    assert bool(torch.isfinite(want).all())
+    assert torch.equal(bits(kb.chunk(q, k, v, start, check=True)), bits(want))
+    if page == 0:
+        assert torch.equal(bits(kb.chunk_8bit(q, *cache, start, check=True)), bits(want))
+    # sequences of their own: the last one row short, the one before empty
+    lens = [L] * B
+    lens[-1] = L - 1
+    if B > 1:
+        lens[-2] = 0
+    st, ln = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([start] * B, lens))
+    out = torch.full_like(q, 7.0)
+    kb.chunk_8bit_varlen(q, *cache, st, ln, block_table=pages, out=out, check=True)
+    for b in range(B):
+        assert torch.equal(bits(out[b, :, :lens[b]]), bits(want[b, :, :lens[b]])) and bool((out[b, :, lens[b]:] == 7.0).all())
+
+
 @pytest.mark.parametrize("B,L,start", [(1, 1, 9000), (2, 1, 70000), (1, 20, 9000)])
 def test_without_a_workspace_and_with_one_of_its_own(kb, B, L, start):
     """Long contexts of small batches: CTAs that share a KV head's keys through the workspace, and the way without."""
