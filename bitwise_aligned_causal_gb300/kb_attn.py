@@ -997,16 +997,28 @@ def _check_type(t, name, dtype, what, ndim):
     _on_current_device(t, name)
 
 
-def _need_8bit(t, name, device):
-    if not _plain(t, _torch().float8_e4m3fn, device) or t.dim() != 4:
-        _check_type(t, name, _torch().float8_e4m3fn, "float8_e4m3fn", 4)
+def _all_plain(device, dtype, *tensors):
+    """_plain for several tensors at once."""
+    try:
+        for t in tensors:
+            if not (t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
+                return False
+    except AttributeError:
+        return False
+    return True
 
 
-def _need_exp(t, name, device):
-    if not _plain(t, _torch().int8, device) or t.dim() != 3:
-        _check_type(t, name, _torch().int8, "int8", 3)
+def _need_8bit(device, caches, exps, names=("k_cache", "v_cache", "k_exp", "v_exp")):
+    torch = _torch()
+    if not _all_plain(device, torch.float8_e4m3fn, *caches) or not _all_plain(device, torch.int8, *exps):
+        for t, name in zip(caches, names):
+            _check_type(t, name, torch.float8_e4m3fn, "float8_e4m3fn", 4)
+        for t, name in zip(exps, names[len(caches):]):
+            _check_type(t, name, torch.int8, "int8", 3)
 
 
+_strides_of = functools.lru_cache(maxsize=1024)(lambda *strides: (ctypes.c_longlong * (3 * len(strides)))(
+    *(x for s in strides for x in s[:3])))
 _shapes_append_8bit = functools.lru_cache(maxsize=1024)(shapes.append_8bit)
 _shapes_cache_values = functools.lru_cache(maxsize=1024)(shapes.cache_values)
 _shapes_attend_8bit = functools.lru_cache(maxsize=1024)(shapes.attend_8bit)
@@ -1065,10 +1077,7 @@ def _append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, start, starts, 
         _check_view(q, "q", device)
     _check_view(k, "k", device)
     _check_view(v, "v", device)
-    _need_8bit(k_cache, "k_cache", device)
-    _need_8bit(v_cache, "v_cache", device)
-    _need_exp(k_exp, "k_exp", device)
-    _need_exp(v_exp, "v_exp", device)
+    _need_8bit(device, (k_cache, v_cache), (k_exp, v_exp))
     _need_f32(table, "table", device)
     _need_i32(block_table, "block_table", device)
     if out is not None:
@@ -1084,8 +1093,8 @@ def _append_8bit(q, k, v, k_cache, v_cache, k_exp, v_exp, table, start, starts, 
     if q is not None and out is None:
         out = _empty((B, Hq, L, 128), q.dtype, q.device, stream)
     _finish(kb_attn_append_8bit(_ptr(q), k.data_ptr(), v.data_ptr(),
-                                _stride_array(*_stride3(q), *_stride3(k), *_stride3(v)), _ptr(out), k_cache.data_ptr(),
-                                v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _ptr(table), n_pos, rot_dim,
+                                _strides_of((0, 0, 0, 0) if q is None else q.stride(), k.stride(), v.stride()), _ptr(out),
+                                k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _ptr(table), n_pos, rot_dim,
                                 bool(interleaved), B, Hq, Hkv, L, start, _ptr(starts), _ptr(lens), cap,
                                 _ptr(block_table), pps, page, num_pages, _handle(stream, device)),
             "kb_attn_append_8bit", check, stream)
@@ -1115,8 +1124,7 @@ def cache_values(cache, exps, out=None, stream=None, check=False):
     """What an 8-bit cache or pool [n,Hkv,rows,128] with exponents [n,Hkv,ceil(rows/128)] stands for, in bfloat16
     (exactly).  A block with exponent 127 reads as NaN."""
     device = _device()
-    _need_8bit(cache, "cache", device)
-    _need_exp(exps, "exps", device)
+    _need_8bit(device, (cache,), (exps,), ("cache", "exps"))
     if out is not None:
         _need_bf16(out, "out", device)
     n, Hkv, rows = _shapes_cache_values(cache.shape, exps.shape, _shape(out))
@@ -1128,10 +1136,7 @@ def cache_values(cache, exps, out=None, stream=None, check=False):
 
 def _attend_8bit(q, k, v, k_exp, v_exp, block_table, out, stream, device):
     _need_bf16(q, "q", device)
-    _need_8bit(k, "k_cache", device)
-    _need_8bit(v, "v_cache", device)
-    _need_exp(k_exp, "k_exp", device)
-    _need_exp(v_exp, "v_exp", device)
+    _need_8bit(device, (k, v), (k_exp, v_exp))
     _need_i32(block_table, "block_table", device)
     if out is not None:
         _need_bf16(out, "out", device)
