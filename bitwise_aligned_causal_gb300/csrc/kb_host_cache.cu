@@ -100,9 +100,11 @@ Split choose_split(int sm_count, long long units, long long segments, bool token
 
 // The time in us of a chunk's other way: its keys and values into bf16 in the
 // workspace (3 bytes moved for each, at 5.5 TB/s), then the bf16 chunk, 0.8 us a
-// tile of a head's rows and a tile of keys on one SM (64 to 1000 rows at 32K).
-double gathered_us(int sm_count, int B, int Hkv, int L, long long rows) {
-  const long long tiles = static_cast<long long>(B) * Hkv * kb::kGroup * blocks_of(L);
+// tile of a head's rows and a tile of keys on one SM (64 to 1000 rows at 32K;
+// a ragged batch's grid has the tiles that its rows can touch).
+double gathered_us(int sm_count, int B, int Hkv, int L, int start, bool ragged, long long rows) {
+  const long long per_head = ragged ? (L + kb::kTileRows - 2) / kb::kTileRows + 1 : (start + L - 1) / kb::kTileRows - start / kb::kTileRows + 1;
+  const long long tiles = static_cast<long long>(B) * Hkv * kb::kGroup * per_head;
   return 2.0 + static_cast<double>(B) * Hkv * rows * kb::kHeadDim * 6 / 5.5e6 + (tiles + sm_count - 1) / sm_count * (blocks_of(rows) * 0.8 + 2.0);
 }
 
@@ -322,7 +324,7 @@ kb_status kb_attn_chunk_8bit(const void* q, const void* k, const void* v, const 
   if (static_cast<long long>(B) * Hkv * blocks_of(rows) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   const long long units = static_cast<long long>(B) * Hkv * sub_chunks(L, c.start, starts != nullptr);
   if (units <= 8LL * dev.sm_count && choose_split(dev.sm_count, units, segments_of(rows), false, partial_bytes(B, Hkv, L, rows)).us <
-                                         gathered_us(dev.sm_count, B, Hkv, L, rows))
+                                         gathered_us(dev.sm_count, B, Hkv, L, c.start, starts != nullptr, rows))
     return packed8(c, cap, dev, workspace, workspace_bytes, stream);
   kb::Gather8Args a{};
   a.k = k;

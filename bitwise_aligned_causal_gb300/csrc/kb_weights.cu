@@ -227,7 +227,8 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_k, const WeightsArgs 
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
-        const bool masked = pos0 < j * kTileKeys + kTileKeys - 1;    // some row does not see some key of the tile
+        // some row does not see some key of the tile, or a column has no row (its zeros times an infinite key are NaN)
+        const bool masked = pos0 < j * kTileKeys + kTileKeys - 1 || n_cols > kGroup * rows;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const int pkey = j * kTileKeys + key;
         const uint32_t d = d_tmem + db * d_cols + 64u * half;

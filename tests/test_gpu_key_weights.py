@@ -204,3 +204,22 @@ def test_far_rows(kb):
     for g in (0, 7):
         want, tol = plain.key_weights(f64(q)[0, 4 * g:4 * g + 4], f64(k[0, g, -100:]), l64[0, 4 * g:4 * g + 4], np.arange(100 - L, 100))
         assert np.all(np.abs(w[0, g, -100:].cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("L", [1, 3, 20, 33, 130])
+def test_infinite_keys_that_weigh_nothing(kb, L):
+    """A key of -inf scores adds exactly nothing, and the others' weights keep their bits, however many rows there are."""
+    import torch
+
+    S, j = 700, 301
+    q, k = randn(90, 1, 32, L, 128), randn(91, 1, 8, S, 128)
+    q[..., 5] = -q[..., 5].abs() - 1
+    lse = torch.full((1, 32, L), 5.0, device="cuda")
+    want = torch.rand(1, 8, S, device="cuda")
+    got, before = want.clone(), want.clone()
+    kb.key_weights(q, k, lse, want, S - L, check=True)
+    k[:, :, j, 5] = float("inf")
+    kb.key_weights(q, k, lse, got, S - L, check=True)
+    assert torch.equal(got[:, :, j], before[:, :, j])
+    got[:, :, j] = want[:, :, j]
+    assert torch.equal(got, want)
