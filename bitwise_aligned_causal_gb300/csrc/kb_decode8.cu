@@ -30,7 +30,7 @@
 // here, or (args.split CTAs) its share, whose partials go to the workspace.
 //
 // Measured (B = 32, contexts of 16K): 258 us, 4.2 TB/s of bytes, against 332 in
-// the packed kernel's shape (one conversation of 64K: 55 us with its segments
+// the packed kernel's shape (one conversation of 64K: 43 us with its segments
 // over all CTAs).  What bounds it is the four schedulers: 1200 instructions
 // each per pair of tiles, half of them the conversion's, on an ALU pipe that
 // takes one every other cycle; HBM would allow 172 us.  Next come the

@@ -78,8 +78,8 @@ int sub_chunks(int L, int start, bool ragged) {
 // CTAs that share the segments of a unit (a sub-chunk of a batch entry and KV
 // head): the number for which the waves of CTAs take the least time, and that
 // time in us.  A segment counts as 7.8 us (tokens) or 10.5 (chunks), a CTA's
-// start and end as 6, the fold of the partials as 8 and their bytes, written and
-// read, as 1.4 MB a us (fitted to timings of 1 to 19 CTAs at 16K, 32K and 64K,
+// start and end as 6, the fold of the partials as 5 and their bytes, written and
+// read, as 2 MB a us (fitted to timings of 1 to 19 CTAs at 16K, 32K and 64K,
 // and of 64 to 256 rows at 28K and 32K).
 struct Split {
   int ctas;
@@ -90,7 +90,7 @@ Split choose_split(int sm_count, long long units, long long segments, bool token
   auto cost = [&](long long split) {
     const long long waves = (units * split + sm_count - 1) / sm_count;
     return waves * (static_cast<double>((segments + split - 1) / split) * seg_us + 6.0) +
-           (split > 1 ? 8.0 + static_cast<double>(part) / 1.4e6 : 0.0);
+           (split > 1 ? 5.0 + static_cast<double>(part) / 2e6 : 0.0);
   };
   Split best{1, cost(1)};
   for (int n = 2; part > 0 && n <= segments && n <= sm_count; ++n)

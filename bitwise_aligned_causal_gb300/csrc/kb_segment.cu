@@ -52,10 +52,13 @@ cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, i
   return cudaGetLastError();
 }
 
-// One CTA per output row, thread t owns column t: the loads of the next eight
-// segments are in flight while eight are folded, left to right.  Launched ahead
-// of the partials' kernel's end (it waits for it here), so that its own launch
-// costs no time.
+// One CTA per output row, thread t owns column t.  The row's partials come to
+// shared memory together, 64 segments at a time, and are folded left to right:
+// a row of 64 segments waits for memory once (eight at a time, in registers, a
+// token at 64K took 55 us, so 43).  Launched ahead of the partials' kernel's end (it waits for it here), so
+// that its own launch costs no time.
+constexpr int kFoldChunk = 64;
+
 __global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldArgs args) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (*reinterpret_cast<const volatile uint32_t*>(args.err) != 0) return;    // the partials are not there
@@ -72,25 +75,22 @@ __global__ void __launch_bounds__(kHeadDim) kb_rows_fold_kernel(const RowsFoldAr
   const int ns = min((n_kv + kSegTiles - 1) / kSegTiles, args.n_seg);
   const int t = static_cast<int>(threadIdx.x);
   const float* p = args.part + static_cast<size_t>(row) * args.n_seg * kPartFloats;
-  constexpr int kAhead = 8;
-  float o[kAhead];
-  float4 st[kAhead];
-  auto load = [&](int sg, int i) {
-    const int at = min(sg, ns - 1);
-    o[i] = __ldcg(p + static_cast<size_t>(at) * kPartFloats + t);
-    st[i] = __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(at) * kPartFloats + kHeadDim));
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i, i);
+  __shared__ __align__(16) float held[kFoldChunk][kPartFloats];
   RowState acc = row_state_init();
   float acc_o = 0.0f;
-  for (int s0 = 0; s0 < ns; s0 += kAhead) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float os = o[i];
-      const RowState seg{st[i].x, st[i].y, st[i].z};
-      if (s0 + kAhead < ns) load(s0 + kAhead + i, i);
-      if (s0 + i >= ns) continue;
+  for (int s0 = 0; s0 < ns; s0 += kFoldChunk) {
+    const int n = min(kFoldChunk, ns - s0);
+    const float4* from = reinterpret_cast<const float4*>(p + static_cast<size_t>(s0) * kPartFloats);
+    __syncthreads();                                              // (the chunk before has been folded)
+    for (int x = t; x < n * (kPartFloats / 4); x += kHeadDim)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&held[0][4 * x])), "l"(from + x) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&held[i][kHeadDim]);
+      const float os = held[i][t];
+      const RowState seg{v.x, v.y, v.z};
       if (s0 + i == 0) {                                          // segment 0 as it is
         acc = seg;
         acc_o = os;
