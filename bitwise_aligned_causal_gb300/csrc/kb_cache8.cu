@@ -98,13 +98,16 @@ __device__ __forceinline__ void regrid(uint8_t* base, int n16, int d, int E) {
 
 // ------------------------------------------------------------------ append
 
-// One CTA per (batch, KV head, key block that the call's rows touch), as
-// kb_append_kernel.  A block's exponent needs all of the block's new keys
-// before the first byte is written, so a thread keeps its rows (at most two)
-// in registers, turns its keys once for the largest magnitude and once more
-// for the bytes; the queries pass two heads at a time.  That keeps to 64
-// registers, so that two CTAs of 16 warps share an SM.  Where the exponent has grown, the block's earlier keys are
-// brought to it: a CTA has the block to itself.
+// Two CTAs per (batch, KV head, key block that the call's rows touch): one for
+// the block's keys and values, one for its queries, which wait for nothing
+// (in one CTA, L2 flushed: 4 ragged prompts 58.5 us, so 54.4; 16 tokens 11.4, so
+// 9.3; 4 x 40 rows 15.5, so 11.4).  A block's
+// exponent needs all of the block's new keys before the first byte is written,
+// so a thread keeps its rows (at most two) in registers, turns its keys once for
+// the largest magnitude and once more for the bytes.  That keeps to 64
+// registers, so that two CTAs of 16 warps share an SM.  Where the exponent has
+// grown, the block's earlier keys are brought to it: a CTA has the block to
+// itself.
 __global__ void __launch_bounds__(512, 2) kb_append8_kernel(const Append8Args args) {
   __shared__ uint32_t amax[2][16];
   // one decision for the CTA: the word may change while its threads read it
@@ -112,8 +115,10 @@ __global__ void __launch_bounds__(512, 2) kb_append8_kernel(const Append8Args ar
   const AppendArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   const int u = lane & 7, r4 = lane >> 3;
-  const int c = static_cast<int>(blockIdx.x) / (a.B * a.Hkv);          // which touched block
-  const int bg = static_cast<int>(blockIdx.x) % (a.B * a.Hkv);
+  const int units = static_cast<int>(gridDim.x) / (a.q != nullptr ? 2 : 1);
+  const bool q_part = static_cast<int>(blockIdx.x) >= units;           // the block's queries; else its keys and values
+  const int c = static_cast<int>(blockIdx.x) % units / (a.B * a.Hkv);  // which touched block
+  const int bg = static_cast<int>(blockIdx.x) % units % (a.B * a.Hkv);
   const int b = bg / a.Hkv, g = bg % a.Hkv;
 
   int start = a.start, len = a.L;
@@ -155,23 +160,15 @@ __global__ void __launch_bounds__(512, 2) kb_append8_kernel(const Append8Args ar
   const bool turns = a.table != nullptr && lc.turns;
   const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k) + b * a.ks[0] + g * a.ks[1];
   const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + b * a.vs[0] + g * a.vs[1];
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qs[0] + (g * kGroup) * a.qs[1];
-  uint4 kx[kPasses], ky[kPasses], vx[kPasses], vy[kPasses];
-  uint32_t k_max = 0, v_max = 0;
+  if (q_part) {
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + b * a.qs[0] + (g * kGroup) * a.qs[1];
 #pragma unroll
-  for (int it = 0; it < kPasses; ++it) {
-    const int p = p0 + (it * n_warps + warp) * kRowsPerWarp + r4;
-    if (p >= p1) continue;
-    const long long i = p - start;                                     // row of the call's tensors
-    const uint4* ksrc = reinterpret_cast<const uint4*>(kp + i * a.ks[2]);
-    const uint4* vsrc = reinterpret_cast<const uint4*>(vp + i * a.vs[2]);
-    kx[it] = ksrc[lc.c0];
-    ky[it] = ksrc[lc.c1];
-    vx[it] = vsrc[u];
-    vy[it] = vsrc[u + 8];
-    Turn t;
-    if (turns) load_turn(t, a.table, p, a.rot_dim, u, false);
-    if (a.q != nullptr) {
+    for (int it = 0; it < kPasses; ++it) {
+      const int p = p0 + (it * n_warps + warp) * kRowsPerWarp + r4;
+      if (p >= p1) continue;
+      const long long i = p - start;
+      Turn t;
+      if (turns) load_turn(t, a.table, p, a.rot_dim, u, false);
 #pragma unroll
       for (int h0 = 0; h0 < kGroup; h0 += 2) {
         uint4 qx[2], qy[2];
@@ -192,6 +189,23 @@ __global__ void __launch_bounds__(512, 2) kb_append8_kernel(const Append8Args ar
         }
       }
     }
+    return;
+  }
+  uint4 kx[kPasses], ky[kPasses], vx[kPasses], vy[kPasses];
+  uint32_t k_max = 0, v_max = 0;
+#pragma unroll
+  for (int it = 0; it < kPasses; ++it) {
+    const int p = p0 + (it * n_warps + warp) * kRowsPerWarp + r4;
+    if (p >= p1) continue;
+    const long long i = p - start;                                     // row of the call's tensors
+    const uint4* ksrc = reinterpret_cast<const uint4*>(kp + i * a.ks[2]);
+    const uint4* vsrc = reinterpret_cast<const uint4*>(vp + i * a.vs[2]);
+    kx[it] = ksrc[lc.c0];
+    ky[it] = ksrc[lc.c1];
+    vx[it] = vsrc[u];
+    vy[it] = vsrc[u + 8];
+    Turn t;
+    if (turns) load_turn(t, a.table, p, a.rot_dim, u, false);
     float fx[8], fy[8];
     turned_values(kx[it], ky[it], t, turns, a.interleaved, fx, fy);
 #pragma unroll
@@ -241,7 +255,7 @@ cudaError_t launch_append8(const Append8Args& args, cudaStream_t s) {
   // known to sit on a block's first key)
   const bool aligned = a.starts == nullptr && a.start % kTileKeys == 0;
   const long long touched = aligned ? (a.L + kTileKeys - 1) / kTileKeys : (a.L + kTileKeys - 2) / kTileKeys + 1;
-  const long long grid = touched * a.B * a.Hkv;
+  const long long grid = touched * a.B * a.Hkv * (a.q != nullptr ? 2 : 1);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int rows = a.L < kTileKeys ? a.L : kTileKeys;
   const int warps = std::min((rows + kRowsPerWarp - 1) / kRowsPerWarp, 16);

@@ -241,7 +241,7 @@ kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const
   if ((s = host_cache_rows(&cap, kv_cap, block_table, pages_per_seq, page_size, num_pages, Hkv)) != KB_OK) return s;
   if (L < 1 || L > cap) return KB_ERR_INVALID_ARG;
   if (starts == nullptr && (start < 0 || start > cap - L || (table != nullptr && start > n_pos - L))) return KB_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * Hkv * (blocks_of(L) + 1) > 0x7FFFFFFFLL) return KB_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hkv * (blocks_of(L) + 1) > 0x3FFFFFFFLL) return KB_ERR_UNSUPPORTED;
   kb::HostDevice dev;
   if ((s = kb::host_device(&dev)) != KB_OK) return s;
   const void* p[] = {q, k, v, q_out, k_cache, v_cache, k_exp, v_exp, table, starts, lens, block_table};
