@@ -421,7 +421,7 @@ kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, fl
 kb_status kb_attn_evict(void* k, void* v, const float* weights, float* weights_out, int* kept, int B, int Hkv, const int* lens,
                         int keep, int keep_first, int keep_last, int kv_cap, const int* block_table, int pages_per_seq,
                         int page_size, int num_pages, void* stream) {
-  if (!k || !v || !weights || !weights_out || !kept || !lens || !host_aligned(k, 16) || !host_aligned(v, 16))
+  if (!k || !v || k == v || !weights || !weights_out || !kept || !lens || !host_aligned(k, 16) || !host_aligned(v, 16))
     return KB_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(weights_out), static_cast<const void*>(kept),
                         static_cast<const void*>(lens)})

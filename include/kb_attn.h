@@ -567,7 +567,7 @@ kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, fl
  * min(n, keep)-1 in their old order, in place; rows behind are left as they
  * were.  A sequence of at most `keep` keys stays as it is.
  *   k, v        : bf16 contiguous caches [B, Hkv, kv_cap, 128] or pools, in
- *                 which no two sequences share a page
+ *                 which no two sequences share a page; not the same buffer
  *   weights     : [B, Hkv, kv_cap] fp32 (positions per sequence of a paged
  *                 cache) as kb_attn_key_weights adds them
  *   weights_out : the same shape: the kept keys' weights, zero behind; may be

@@ -307,6 +307,49 @@ def test_longer_chunks_late_in_a_context(kb, page, B, L, start):
         assert torch.equal(bits(out[b, :, :lens[b]]), bits(want[b, :, :lens[b]])) and bool((out[b, :, lens[b]:] == 7.0).all())
 
 
+@pytest.mark.parametrize("kind", ["grows", "falls", "jumps"])
+@pytest.mark.parametrize("L", [1, 2, 6, 40])
+def test_rows_whose_maximum_moves(kb, kind, L):
+    """Keys along the queries, louder or quieter tile by tile: rows that are scaled again and again, and never."""
+    import torch
+
+    S = 3000
+    at = torch.arange(S, device="cuda")
+    scale = {"grows": 0.2 + at / S * 6, "falls": 6.2 - at / S * 6, "jumps": 0.3 + 5.0 * ((at // 128) % 3)}[kind]
+    q = randn(84, 1, 32, L, 128)
+    k = (randn(85, 1, 8, S, 128) + q.view(1, 8, 4 * L, 128).mean(2, keepdim=True)) * scale[None, None, :, None].bfloat16()
+    v = randn(87, 1, 8, S, 128)
+    k8, v8, ke, ve = empty8(1, S)[:4]
+    kb.append_8bit(None, k, v, k8, v8, ke, ve, None, 0, check=True)
+    kk, vv = kb.cache_values(k8, ke), kb.cache_values(v8, ve)
+    want = kb.chunk(q, kk, vv, S - L, check=True)
+    assert torch.equal(bits(kb.chunk_8bit(q, k8, v8, ke, ve, S - L, check=True)), bits(want))
+
+
+def test_longer_chunks_captured_and_on_two_streams(kb):
+    import torch
+
+    L, start = 70, 12000
+    cache, _, _ = filled(kb, 1, start + L)
+    q = randn(88, 1, 32, L, 128)
+    want = kb.chunk_8bit(q, *cache, start, check=True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [kb.chunk_8bit(q, *cache, start, stream=st) for st in streams for _ in range(3)]
+    torch.cuda.synchronize()
+    g, o = torch.cuda.CUDAGraph(), torch.zeros_like(q)
+    with torch.cuda.graph(g):
+        kb.chunk_8bit(q, *cache, start, out=o)
+    for _ in range(2):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(o), bits(want))
+    kb.check_device_status()
+    assert all(torch.equal(bits(x), bits(want)) for x in got)
+
+
 @pytest.mark.parametrize("B,L,start", [(1, 1, 9000), (2, 1, 70000), (1, 20, 9000)])
 def test_without_a_workspace_and_with_one_of_its_own(kb, B, L, start):
     """Long contexts of small batches: CTAs that share a KV head's keys through the workspace, and the way without."""

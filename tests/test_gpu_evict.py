@@ -78,6 +78,36 @@ def test_sizes(kb, B, cap, keep):
     run_and_check(kb, k, v, weights_of("spread", B, cap), [cap - b for b in range(B)], keep, 4, min(64, keep // 2), pages, seq)
 
 
+@pytest.mark.parametrize("page", [0, 128])
+@pytest.mark.parametrize("B", [1, 2, 3, 4, 5, 6, 8, 13, 40])
+def test_any_number_of_planes(kb, page, B):
+    """As many CTAs share a plane's rows as find a place: keeps that end inside and on the ends of their tiles."""
+    cap = 1536
+    for keep in (127, 1024, 1300):
+        k, v, _, pages, seq = caches(B, cap, page, seed=50)
+        run_and_check(kb, k, v, weights_of("ties", B, cap, seed=keep), [cap - 7 * (b % 20) for b in range(B)], keep, 4, 64, pages, seq)
+
+
+def test_two_streams_at_once(kb):
+    import torch
+
+    cap, keep = 5000, 1700
+    k, v, _, _, _ = caches(2, cap, seed=55)
+    w = weights_of("spread", 2, cap)
+    n = i32(cap, cap - 11)
+    want = [t.clone() for t in (k, v, w)]
+    kept = kb.evict(*want, n, keep, check=True)
+    sets = [[t.clone() for t in (k, v, w)] for _ in range(6)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [kb.evict(*x, n, keep, stream=streams[i % 3]) for i, x in enumerate(sets)]
+    torch.cuda.synchronize()
+    kb.check_device_status()
+    for x, r in zip(sets, got):
+        assert torch.equal(r, kept) and all(torch.equal(a, b) for a, b in zip(x, want))
+
+
 def test_the_whole_cache_may_stay(kb):
     k, v, _, pages, seq = caches(2, 200, seed=40)
     run_and_check(kb, k, v, weights_of("odd", 2, 200), (200, 77), 200, 0, 200, pages, seq)
@@ -112,6 +142,8 @@ def test_refusals(kb):
     for args in ((k.float(), v, w, n, 50), (k, v, w.double(), n, 50), (k, v, w, n.long(), 50), (k, v, w, n.cpu(), 50)):
         with pytest.raises(TypeError):
             kb.evict(*args)
+    with pytest.raises(kb.KBError):                               # one plane cannot be moved as two
+        kb.evict(k, k, w, n, 90)
     for args in ((k, v, w, n, 0), (k, v, w, n, 101), (k, v, w, n, 50, 30, 30), (k, v[:, :, :99].contiguous(), w, n, 50)):
         with pytest.raises(ValueError):
             kb.evict(*args)
