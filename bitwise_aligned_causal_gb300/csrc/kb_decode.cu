@@ -255,23 +255,24 @@ __device__ __forceinline__ void fill_ring8(bool is_v, uint8_t* ring, const uint8
     uint8_t* dst = dst0 + slot * kTileBytes;
     const int n = seq_kv - (j0 + jj) * kTileKeys;          // rows of the sequence in the tile
     const bool whole = n >= kTileKeys && !sc.two;          // else: the sequence's last tile, or values beyond 448 * 2^7
-#pragma unroll 1
-    for (int i0 = 0; i0 < 8; i0 += 4) {
-      uint4 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 2048);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 lo, hi;
-        values8x16(w[i], sc.first, lo, hi);
-        if (!whole) {
-          lo = scaled_again(lo, sc.second);
-          hi = scaled_again(hi, sc.second);
-          if (row0 + 16 * (i0 + i) >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);    // (a marked block's factor is NaN)
-        }
-        *reinterpret_cast<uint4*>(dst + (i0 + i) * 2048) = lo;
-        *reinterpret_cast<uint4*>(dst + (i0 + i) * 2048 + next_chunk) = hi;
+    // small loops: the instruction caches are shared with the row math (four chunks at a time: 128 rows at 28K 5 % slower)
+    auto convert = [&](int i, bool odd) {
+      uint4 lo, hi;
+      values8x16(*reinterpret_cast<const uint4*>(src + i * 2048), sc.first, lo, hi);
+      if (odd) {
+        lo = scaled_again(lo, sc.second);
+        hi = scaled_again(hi, sc.second);
+        if (row0 + 16 * i >= n) lo = hi = make_uint4(0u, 0u, 0u, 0u);    // (a marked block's factor is NaN)
       }
+      *reinterpret_cast<uint4*>(dst + i * 2048) = lo;
+      *reinterpret_cast<uint4*>(dst + i * 2048 + next_chunk) = hi;
+    };
+    if (whole) {
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) convert(i, false);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) convert(i, true);
     }
     fence_proxy_async_smem();
     mbar_arrive(full0 + 8u * slot);
@@ -351,6 +352,10 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   const int Lc = max(r1 - r0, 1);
   if (r1 - r0 <= 0) active = false;                     // the chunk does not reach this one
   const int n_rows = kGroup * Lc;                       // packed rows in use
+  // over bytes, up to 32 packed rows go eight to a softmax warp, four threads
+  // a row, instead of all to the first: packed row m is the MMA's row 32 (m / 8)
+  // + m % 8 then (7 rows of 2 sequences at 32K: 54 us in one warp, 50 so)
+  const bool spread = k8 && n_rows <= 32;
   const int n_kv = (pos0 + r1 - 1) / kTileKeys + 1;     // C1: KV tiles 0..floor(last position / 128)
   int* walk = reinterpret_cast<int*>(smem + Cfg::kWalkOff);
   int* seg_first = reinterpret_cast<int*>(smem + Cfg::kSegFirstOff);
@@ -457,9 +462,10 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       const int m = idx >> 4;
       const int c = idx & 15;
       uint4 val = make_uint4(0u, 0u, 0u, 0u);
-      if (active && m < n_rows) {
-        const int i = m / Lc;
-        const int r = r0 + m % Lc;
+      const int row = !spread ? m : (m & 31) < 8 ? 8 * (m >> 5) + (m & 7) : n_rows;    // packed row
+      if (active && row < n_rows) {
+        const int i = row / Lc;
+        const int r = r0 + row % Lc;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(args.q) +
             ((static_cast<size_t>(b) * args.Hq + g * kGroup + i) * args.L + r) * kHeadDim);
@@ -649,7 +655,8 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   } else if constexpr (kWide) {
     // ------------------------------------------------- softmax, row per thread
     if constexpr (k8) regs_increase<Cfg::kSoftmaxRegs>();
-    const int m = warp * 32 + lane;                    // packed row = TMEM lane
+    const int m = spread ? 8 * warp + (lane & 7) : warp * 32 + lane;   // packed row of this TMEM lane
+    const bool row_live = m < n_rows && (!spread || lane < 8);
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_tmem = tmem_base + Cfg::kOCol + lane_off;
     const uint32_t oacc_tmem = tmem_base + Cfg::kOAccCol + lane_off;   // kFoldTmem only
@@ -660,7 +667,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     int nfin = 0;                                      // segments finished (and folded into O_acc)
     // C5: a finished segment's partial (O unnormalised, m, mc, l) for the fold
     auto store_partial = [&](const RowState& sg, int seg) {
-      const bool store = m < n_rows;
+      const bool store = row_live;
       float* dst = args.part + ((((static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r) * args.n_seg + seg) *
                                 kPartFloats);
 #pragma unroll 1
@@ -677,6 +684,12 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
       if (store) reinterpret_cast<float4*>(dst + 128)[0] = make_float4(sg.m, sg.mc, sg.l, 0.0f);
     };
+    // spread: the state of this lane's row, from the four threads that share it
+    auto lane_state = [&](const RowState& x) {
+      if (!spread) return x;
+      const int from = 4 * (lane & 7);
+      return RowState{__shfl_sync(0xffffffffu, x.m, from), __shfl_sync(0xffffffffu, x.mc, from), __shfl_sync(0xffffffffu, x.l, from)};
+    };
     int js = 0;                                        // tile index within its segment (j0 starts one)
     bool ok = run && no_error(args.err, abort_flag);
     for (int j = 0; j < nt && ok; ++j) {               // j: tile j0 + j
@@ -686,18 +699,42 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (!ok) break;
       tc_fence_after();
       const uint32_t s_tmem = tmem_base + (j % Cfg::kSBufs) * 128u + lane_off;
-      uint32_t s[128];
-      tmem_ld128_wait(s_tmem, s);
-      uint32_t p[64];
       const int jt = j0 + j;
       const bool seg_start = (js == 0);
       if (++js == seg_len) js = 0;
       if (seg_start) {
-        prev = st;
+        prev = lane_state(st);
         st = row_state_init();
       }
-      const float alpha = (jt == n_kv - 1) ? row_softmax_tile<true>(s, pos - jt * kTileKeys + 1, st, p)
-                                           : row_softmax_tile<false>(s, kTileKeys, st, p);
+      uint32_t p[64];                                  // spread: 16 of them, of the row that four threads share
+      float alpha;
+      if (spread) {
+        const int u = lane & 3, mq = 8 * warp + (lane >> 2);
+        float x[32];
+        {
+          uint32_t v0[32], v1[32];
+          tmem_ld_16x256b_x8_pair_wait(s_tmem, s_tmem + 64u, v0, v1);   // keys 0..63, 64..127
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            x[2 * q] = __uint_as_float(v0[4 * q]);
+            x[2 * q + 1] = __uint_as_float(v0[4 * q + 1]);
+            x[16 + 2 * q] = __uint_as_float(v1[4 * q]);
+            x[16 + 2 * q + 1] = __uint_as_float(v1[4 * q + 1]);
+          }
+        }
+        uint32_t pq[16];
+        const int posq = pos0 + r0 + (mq < n_rows ? mq % Lc : 0);       // unused rows take the sub-chunk's first position
+        alpha = (jt == n_kv - 1) ? row_softmax_tile_quad<true>(x, u, posq - jt * kTileKeys + 1, st, pq)
+                                 : row_softmax_tile_quad<false>(x, u, kTileKeys, st, pq);
+        alpha = __shfl_sync(0xffffffffu, alpha, 4 * (lane & 7));
+#pragma unroll
+        for (int q = 0; q < 16; ++q) p[q] = pq[q];
+      } else {
+        uint32_t s[128];
+        tmem_ld128_wait(s_tmem, s);
+        alpha = (jt == n_kv - 1) ? row_softmax_tile<true>(s, pos - jt * kTileKeys + 1, st, p)
+                                 : row_softmax_tile<false>(s, kTileKeys, st, p);
+      }
       // O is rescaled only when some row's reference max moved, and only then
       // must the previous tile's P V have finished (its barrier is that tile's
       // S buffer's; the MMA issuer's wait before reusing an S buffer keeps it
@@ -717,7 +754,12 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           tmem_st32(o_tmem + c * 32u, o);
         }
       }
-      {
+      if (spread) {
+        uint32_t pv[32];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) { pv[2 * q] = p[q]; pv[2 * q + 1] = p[q]; }   // lanes m and m + 8 (unused)
+        tmem_st_16x128b_x16(s_tmem, pv);
+      } else {
         uint32_t p0[32], p1[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) { p0[i] = p[i]; p1[i] = p[32 + i]; }
@@ -769,6 +811,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       ok = mbar_wait(bar(Cfg::kBarOFull + (nt - 1) % Cfg::kSBufs), ((nt - 1) / Cfg::kSBufs) & 1, abort_flag,
                      args.err, kDevTimeoutMma);
     ok = __all_sync(0xffffffffu, ok) && nt > 0;
+    st = lane_state(st);
     if (ok && ws_mode) {
       tc_fence_after();
       store_partial(st, ws_block ? seg_block_start(rank, ns, parts) + nfin : seg_ws);
@@ -779,7 +822,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       if (nfin == 0) acc = st;
       else f = fold_state(acc, st);
       const float inv_l = row_inv_l(acc);
-      const bool store = m < n_rows;
+      const bool store = row_live;
       if (store && args.lse != nullptr)
         args.lse[(static_cast<size_t>(b) * args.Hq + g * kGroup + head) * args.L + r] = row_lse(acc);
       uint4* dst = reinterpret_cast<uint4*>(
