@@ -27,15 +27,17 @@
 // Tensor memory: three K tiles of 64 columns, four S^T and O^T of 16.
 //
 // A CTA runs a contiguous block of the row's segments: all of them, folded
-// here, or (args.split CTAs) its share, whose partials go to the workspace.
+// here, or (args.split CTAs) its share, whose partials go to the workspace; or
+// (flat) a run of all KV heads' segments, piece by piece, so that every SM has
+// as many as the others.
 //
-// Measured (B = 32, contexts of 16K): 258 us, 4.2 TB/s of bytes, against 332 in
-// the packed kernel's shape (one conversation of 64K: 43 us with its segments
-// over all CTAs).  What bounds it is the four schedulers: 1200 instructions
+// Measured (B = 32, contexts of 16K): 244 us, 4.4 TB/s of bytes, against 332 in
+// the packed kernel's shape and 258 with a CTA per KV head (256 of them); one
+// conversation of 64K: 43 us with its segments over 128 CTAs.  What bounds it is the four schedulers: 1200 instructions
 // each per pair of tiles, half of them the conversion's, on an ALU pipe that
 // takes one every other cycle; HBM would allow 172 us.  Next come the
 // instruction caches that sixteen warps of seven roles share: what is rare is
-// out of line (timeouts, drains, odd tiles: 284 to 258 us), and the conversion
+// out of line (timeouts, drains, odd tiles: 284 to 258 us with a CTA per head), and the conversion
 // loops hold two chunks (one: 297 us; four: 261; eight: 309).  Eight warps for
 // K and for V, one loop for both (279 us) and the shift on the FMA pipe were no
 // better.
@@ -134,6 +136,8 @@ __device__ __noinline__ void odd_keys(const uint8_t* src, uint32_t dst, int row,
 
 }  // namespace
 
+// kFlat: the CTAs share all segments of the call.
+template <bool kFlat>
 __global__ void __launch_bounds__(Decode8Cfg::kThreads, 1)
 kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const PackedArgs args) {
   using Cfg = Decode8Cfg;
@@ -148,40 +152,94 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = args.B * args.Hkv;
-  const int split = args.part != nullptr ? args.split : 1;
-  const int rank = static_cast<int>(blockIdx.x) / bh % split;
-  const int sub = static_cast<int>(blockIdx.x) / (bh * split);       // sub-chunk 0 first
-  const int b = static_cast<int>(blockIdx.x) % bh / args.Hkv, g = static_cast<int>(blockIdx.x) % args.Hkv;
+  const int split = args.part != nullptr && !kFlat ? args.split : 1;
 
-  // position of query row 0, the sub-chunk's rows [r0, r1), as in the packed kernel
-  int pos0 = args.start, rows = args.L;
-  if (args.ctx_lens != nullptr) {
-    const int ctx = args.ctx_lens[b];
-    if (ctx < args.L || ctx > args.max_ctx) {
-      if (threadIdx.x == 0) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
-      return;
+  // Sequence b: the position of its query row 0 and its rows; false (reported
+  // by the CTAs that it concerns) for a length out of range.
+  auto rows_of = [&](int b, int& pos0, int& rows) {
+    pos0 = args.start;
+    rows = args.L;
+    bool ok = true;
+    if (args.ctx_lens != nullptr) {
+      const int ctx = __ldg(args.ctx_lens + b);
+      ok = ctx >= args.L && ctx <= args.max_ctx;
+      pos0 = ctx - args.L;
     }
-    pos0 = ctx - args.L;
+    if (args.starts != nullptr) {
+      pos0 = __ldg(args.starts + b);
+      rows = __ldg(args.lens + b);
+      ok = pos0 >= 0 && rows >= 0 && rows <= args.L && pos0 <= args.max_ctx - rows;
+    }
+    if (!ok) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
+    return ok;
+  };
+  // flat (one row a sequence): all segments of all KV heads in a row, cut into
+  // as many runs as there are CTAs
+  auto segments = [&](int b) {
+    int pos0, rows;
+    return b < args.B && rows_of(b, pos0, rows) && rows > 0 ? (pos0 / kTileKeys + kSegTiles) / kSegTiles : 0;
+  };
+  int f = 0, f_end = 1;                                   // this CTA's run (else: one piece)
+  if constexpr (kFlat) {
+    int total = 0;
+    for (int b0 = 0; b0 < args.B; b0 += 32) total += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(segments(b0 + lane))));
+    const long long all = static_cast<long long>(total) * args.Hkv;
+    f = static_cast<int>(all * blockIdx.x / gridDim.x);
+    f_end = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
   }
-  if (args.starts != nullptr) {
-    pos0 = args.starts[b];
-    rows = args.lens[b];
-    if (pos0 < 0 || rows < 0 || rows > args.L || pos0 > args.max_ctx - rows) {
-      if (threadIdx.x == 0) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
-      return;
+  bool begun = false;                                     // barriers and TMEM are there
+  do {
+    if (f >= f_end) break;
+  int rank = 0, sub = 0, b = 0, g = 0, g0 = 0, g1 = 0;
+  int pos0, rows;
+  if constexpr (kFlat) {
+    int before = 0;                                       // segments of a KV head in the sequences before
+    for (int b0 = 0; b0 < args.B; b0 += 32) {
+      const int ns = segments(b0 + lane);
+      int incl = ns;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, (before + incl) * args.Hkv > f);
+      if (past != 0) {
+        const int at = __ffs(static_cast<int>(past)) - 1;
+        const int ns_b = __shfl_sync(0xffffffffu, ns, at);
+        const int rest = f - (before + __shfl_sync(0xffffffffu, incl, at) - ns_b) * args.Hkv;
+        b = b0 + at;
+        g = rest / ns_b;
+        g0 = rest % ns_b;
+        g1 = min(ns_b, g0 + f_end - f);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
     }
+    rows_of(b, pos0, rows);
+    f += g1 - g0;
+  } else {
+    rank = static_cast<int>(blockIdx.x) / bh % split;
+    sub = static_cast<int>(blockIdx.x) / (bh * split);    // sub-chunk 0 first
+    b = static_cast<int>(blockIdx.x) % bh / args.Hkv;
+    g = static_cast<int>(blockIdx.x) % args.Hkv;
+    f = f_end;
+    if (!rows_of(b, pos0, rows)) return;
   }
   const int seq_kv = pos0 + rows;
+  // the sub-chunk's rows [r0, r1), as in the packed kernel
   const int cut = min(rows, (pos0 / kTileKeys + 1) * kTileKeys - pos0);   // rows before the first tile boundary
   const int r0 = sub == 0 ? 0 : cut, r1 = sub == 0 ? cut : rows;
   const int Lc = r1 - r0;
   if (Lc <= 0) return;                                    // no rows, or the chunk does not reach a second tile
   const int n_rows = kGroup * Lc;
   const int n_kv = (pos0 + r1 - 1) / kTileKeys + 1;       // C1
-  const int ns = (n_kv + kSegTiles - 1) / kSegTiles;
-  // this CTA's segments (ceil(rank ns / split) ..) and tiles
-  const int g0 = (rank * ns + split - 1) / split, g1 = ((rank + 1) * ns + split - 1) / split;
-  if (g0 >= g1) return;
+  if constexpr (!kFlat) {
+    // this CTA's segments (ceil(rank ns / split) ..)
+    const int ns = (n_kv + kSegTiles - 1) / kSegTiles;
+    g0 = (rank * ns + split - 1) / split;
+    g1 = ((rank + 1) * ns + split - 1) / split;
+    if (g0 >= g1) return;
+  }
   const int j0 = g0 * kSegTiles, nt = min(n_kv, g1 * kSegTiles) - j0;
 
   if (threadIdx.x == 0) {
@@ -194,19 +252,21 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       if ((i >= Cfg::kBarXEmpty && i < Cfg::kBarVFull) || (i >= Cfg::kBarPFull && i < Cfg::kBarPvDone) ||
           (i >= Cfg::kBarStFull && i < Cfg::kBarStEmpty))
         count = 32u;
+      if (begun) mbar_inval(bar(i));
       mbar_init(bar(i), count);
     }
-    misc[1] = (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) ? 1u : 0u;
+    if (!begun) misc[1] = (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) ? 1u : 0u;
     reinterpret_cast<volatile int2*>(smem + Cfg::kAskOff)->x = 0;
     fence_mbar_init();
   }
-  if (warp == Cfg::kQkWarp) {
+  if (warp == Cfg::kQkWarp && !begun) {
     tmem_alloc(sbase + Cfg::kMiscOff, Cfg::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  begun = true;
   const uint32_t tmem_base = misc[0];
   const bool skip = *abort_flag != 0;
 
@@ -451,7 +511,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         tc_commit(bar(Cfg::kBarSFull + sb));
         tc_commit(bar(Cfg::kBarKEmpty + kb));
       }
-      if (!ok) {
+      if (!ok || kFlat) {                                  // (flat: no arrival comes late for the next piece's barriers)
         tc_commit(bar(Cfg::kBarDrain));
         drain_far(bar(Cfg::kBarDrain), 0);
       }
@@ -477,7 +537,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                  desc_kmajor(sbase + Cfg::kPOff + pb * 2 * Cfg::kQSlab, kk, 1024u, Cfg::kQSlab), idesc, (first && kk == 0) ? 0u : 1u);
         tc_commit(bar(Cfg::kBarPvDone + pb));
       }
-      if (!ok) {
+      if (!ok || kFlat) {
         tc_commit(bar(Cfg::kBarDrain + 1));
         drain_far(bar(Cfg::kBarDrain + 1), 0);
       }
@@ -603,27 +663,34 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
   tc_fence_before();
   __syncthreads();
-  if (warp == Cfg::kQkWarp) {
+  tc_fence_after();
+  if (*abort_flag != 0) break;
+  } while (kFlat);                                        // pieces
+  if (begun && warp == Cfg::kQkWarp) {
     __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem_base, Cfg::kTmemCols);
+    tmem_dealloc(misc[0], Cfg::kTmemCols);
   }
 }
 
-cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub, cudaStream_t s) {
+template <bool kFlat>
+static cudaError_t launch_decode8_t(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, long long grid, cudaStream_t s) {
   using Cfg = Decode8Cfg;
   static int configured_device = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(kb_decode8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Cfg::kSmemBytes));
+    e = cudaFuncSetAttribute(kb_decode8_kernel<kFlat>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Cfg::kSmemBytes));
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  const unsigned grid = static_cast<unsigned>((a.part != nullptr ? a.split : 1) * n_sub * a.B * a.Hkv);
-  kb_decode8_kernel<<<grid, Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
+  kb_decode8_kernel<kFlat><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub, cudaStream_t s) {
+  if (a.part != nullptr && a.split == 0) return launch_decode8_t<true>(tk, tv, a, a.ctas, s);
+  return launch_decode8_t<false>(tk, tv, a, static_cast<long long>(a.part != nullptr ? a.split : 1) * n_sub * a.B * a.Hkv, s);
 }
 
 }  // namespace kb

@@ -98,6 +98,13 @@ Split choose_split(int sm_count, long long units, long long segments, bool token
   return best;
 }
 
+// Tokens: the time in us of runs of all segments, one per SM, cut where the
+// SMs' shares end; a piece of a KV head begins and ends in 4 us.
+double flat_us(int sm_count, long long units, long long segments, long long part) {
+  const long long run = (units * segments + sm_count - 1) / sm_count;
+  return run * 7.8 + (static_cast<double>(run) / segments + 1.0) * 4.0 + 9.0 + static_cast<double>(part) / 2e6;
+}
+
 // The time in us of a chunk's other way: its keys and values into bf16 in the
 // workspace (3 bytes moved for each, at 5.5 TB/s), then the bf16 chunk, 0.8 us a
 // tile of a head's rows and a tile of keys on one SM (64 to 1000 rows at 32K;
@@ -146,20 +153,24 @@ kb_status packed8(const Call8& c, int cap, const kb::HostDevice& dev, void* work
   if (s != KB_OK) return s;
   if ((s = kb::host_bytes_map(&tv, c.v, rows, planes, stride)) != KB_OK) return s;
   const long long part = partial_bytes(c.B, c.Hkv, c.L, keys);
-  int share = 1;
+  int share = 1, flat = 0;
   if (workspace != nullptr) {
     if (!host_aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(part)) return KB_ERR_INVALID_ARG;
     if ((s = kb::host_device_pointer(workspace)) != KB_OK) return s;
-    if (part > 0)
-      share = choose_split(dev.sm_count, static_cast<long long>(c.B) * c.Hkv * (c.L > kb::kMaxPackedRows ? n_sub : 1),
-                           segments_of(keys), c.L <= kb::kMaxRows8, part).ctas;
+    if (part > 0) {
+      const long long units = static_cast<long long>(c.B) * c.Hkv * (c.L > kb::kMaxPackedRows ? n_sub : 1);
+      const Split best = choose_split(dev.sm_count, units, segments_of(keys), c.L <= kb::kMaxRows8, part);
+      share = best.ctas;
+      if (c.L == 1 && flat_us(dev.sm_count, units, segments_of(keys), part) < best.us) flat = dev.sm_count;
+    }
   }
   const auto launch = c.L <= kb::kMaxRows8 ? kb::launch_decode8 : kb::launch_packed;
-  if (share == 1) return host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
+  if (share == 1 && flat == 0) return host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)));
   a.cluster = 1;
   a.part = static_cast<float*>(workspace);
   a.n_seg = static_cast<int>(segments_of(keys));
-  a.split = share;
+  a.split = flat > 0 ? 0 : share;
+  a.ctas = flat;
   if ((s = host_done(launch(tk, tv, a, n_sub, static_cast<cudaStream_t>(stream)))) != KB_OK) return s;
   kb::RowsFoldArgs f{};
   f.part = a.part;

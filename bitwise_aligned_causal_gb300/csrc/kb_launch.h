@@ -62,7 +62,9 @@ struct PackedArgs {
   // blocks of a plane] (null: a bf16 cache)
   const int8_t *k_exp, *v_exp;
   int plane_rows;          // rows of a plane: the cache's capacity or the page size
-  int split;               // with part: CTAs that share the segments of a (sub-chunk, batch, KV head)
+  int split;               // with part: CTAs that share the segments of a (sub-chunk, batch, KV head);
+                           // 0 (tokens over bytes): `ctas` CTAs share all segments of the call
+  int ctas;
   float* lse;              // optional [B, Hq, L] fp32 (fold mode): natural-log log-sum-exp of each row's scaled scores
   uint32_t* err;
 };

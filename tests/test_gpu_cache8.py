@@ -240,6 +240,36 @@ def test_decode_has_the_bits_of_the_bf16_cache(kb, page, B, ctx):
     assert torch.equal(bits(again), bits(want))
 
 
+@pytest.mark.parametrize("page", [0, 128])
+@pytest.mark.parametrize("lens", [(9000,) * 20, (1, 9000, 1024, 1025, 127, 128, 5000, 129, 8999, 3, 7168, 2049, 6000, 6001, 800, 9000, 2048, 4097, 1, 8193),
+                                  tuple(200 * i + 1 for i in range(37))])
+def test_tokens_of_many_contexts(kb, page, lens):
+    """Batches that fill the SMs unevenly: runs of segments cut across sequences and heads."""
+    import torch
+
+    B, cap = len(lens), -(-max(lens) // 128) * 128
+    cache, pages, seq = filled(kb, B, cap, page, seed=7)
+    k, v = bf16_of(kb, cache, pages, seq, B)
+    q = randn(89, B, 32, 1, 128)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = torch.cat([kb.decode(q[b:b + 1], k[b:b + 1], v[b:b + 1], lens[b]) for b in range(B)])
+    got = kb.decode_8bit_paged(q, *cache, pages, n, check=True) if page else kb.chunk_8bit_varlen(q, *cache, n - 1, torch.ones_like(n), check=True)
+    assert torch.equal(bits(got), bits(want))
+    if not page and len(set(lens)) == 1:
+        assert torch.equal(bits(kb.decode_8bit(q, *cache, lens[0], check=True)), bits(want))
+    # some of them without a row
+    on = torch.arange(B, device="cuda") % 3 != 1
+    out = torch.full_like(q, 7.0)
+    kb.chunk_8bit_varlen(q, *cache, n - 1, on.int(), block_table=pages, out=out, check=True)
+    assert torch.equal(bits(out[on]), bits(want[on])) and bool((out[~on] == 7.0).all())
+    # a length out of range is reported, and the next call is as ever
+    n[5] = cap + 1
+    with pytest.raises(kb.KBError):
+        kb.chunk_8bit_varlen(q, *cache, n - 1, torch.ones_like(n), block_table=pages, check=True)
+    n[5] = lens[5]
+    assert torch.equal(bits(kb.chunk_8bit_varlen(q, *cache, n - 1, torch.ones_like(n), block_table=pages, check=True)), bits(want))
+
+
 @pytest.mark.parametrize("page", [0, 256])
 @pytest.mark.parametrize("B,L,start", [(1, 2, 126), (2, 2, 127), (1, 3, 0), (2, 7, 1500), (1, 32, 1000), (3, 32, 112), (1, 33, 500),
                                        (2, 130, 60), (1, 700, 0), (1, 257, 2047), (1, 5, 9000), (2, 32, 4090), (1, 2, 20479)])
