@@ -1027,9 +1027,7 @@ _shapes_key_weights = functools.lru_cache(maxsize=1024)(shapes.key_weights)
 _shapes_evict = functools.lru_cache(maxsize=1024)(shapes.evict)
 
 
-@functools.lru_cache(maxsize=1024)
-def _shapes_rope_axes(x, table, positions, planes, out):
-    return (*shapes.rope_axes(x, table, positions, planes, out), bytes(planes))
+_shapes_rope_axes = functools.lru_cache(maxsize=1024)(shapes.rope_axes)
 
 
 def _need_rows(start, L, cap, n_pos=None):
@@ -1043,9 +1041,10 @@ def _ragged(B, starts, lens, device, both=True):
     if starts is None or (both and lens is None):
         raise TypeError("starts and lens must be contiguous int32 CUDA tensors" if both else
                         "starts must be a contiguous int32 CUDA tensor")
-    for t, name in ((starts, "starts"), (lens, "lens")):
-        _need_i32(t, name, device)
-        _per_sequence(B, t, name)
+    if lens is None or not _all_plain(device, _torch().int32, starts, lens) or not starts.shape == lens.shape == (B,):
+        for t, name in ((starts, "starts"), (lens, "lens")):
+            _need_i32(t, name, device)
+            _per_sequence(B, t, name)
 
 
 def rope_axes(x, table, positions, planes, inverse=False, interleaved=False, out=None, stream=None, check=False):
@@ -1061,11 +1060,11 @@ def rope_axes(x, table, positions, planes, inverse=False, interleaved=False, out
         _check_i32(positions, "positions")
     if out is not None:
         _need_bf16(out, "out", device)
-    B, H, L, n_pos, rot_dim, axes, plane_axes = _shapes_rope_axes(x.shape, table.shape, positions.shape, tuple(planes),
-                                                                  _shape(out))
+    planes = bytes(planes if type(planes) in (list, tuple, bytes) else [int(a) for a in planes])
+    B, H, L, n_pos, rot_dim, axes = _shapes_rope_axes(x.shape, table.shape, positions.shape, planes, _shape(out))
     o = _empty((B, H, L, 128), x.dtype, x.device, stream) if out is None else out
     _finish(kb_attn_rope_axes(x.data_ptr(), _stride_array(*x.stride()[:3]), o.data_ptr(), table.data_ptr(), n_pos,
-                              rot_dim, bool(interleaved), bool(inverse), positions.data_ptr(), axes, plane_axes, B, H, L,
+                              rot_dim, bool(interleaved), bool(inverse), positions.data_ptr(), axes, planes, B, H, L,
                               _handle(stream, device)), "kb_attn_rope_axes", check, stream)
     return o
 
@@ -1250,12 +1249,15 @@ def chunk_lse_varlen(q, k, v, starts, lens, block_table=None, out=None, lse=None
 
 
 def _key_weights(q, k, lse, weights, start, starts, lens, block_table, stream, check):
+    torch = _torch()
     device = _device()
-    _need_bf16(q, "q", device)
-    _need_bf16(k, "k", device)
-    for t, n in ((lse, "lse"), (weights, "weights")):
-        if not _plain(t, _torch().float32, device):
-            _check_f32(t, n)
+    if not _all_plain(device, torch.bfloat16, q, k):
+        _need_bf16(q, "q", device)
+        _need_bf16(k, "k", device)
+    if not _all_plain(device, torch.float32, lse, weights):
+        for t, n in ((lse, "lse"), (weights, "weights")):
+            if not _plain(t, torch.float32, device):
+                _check_f32(t, n)
     _need_i32(block_table, "block_table", device)
     B, Hq, Hkv, L, cap, num_pages, page, pps = _shapes_key_weights(q.shape, k.shape, lse.shape, weights.shape,
                                                                    _shape(block_table))
