@@ -27,7 +27,9 @@
 // Tensor memory: three K tiles of 64 columns, four S^T and O^T of 16.
 //
 // A CTA runs a contiguous block of the row's segments: all of them, folded
-// here, or (args.split CTAs) its share, whose partials go to the workspace; or
+// here; or (args.cluster CTAs, a segment each) one, folded through the first
+// CTA's shared memory; or (args.split CTAs) its share, whose partials go to the
+// workspace; or
 // (flat) a run of all KV heads' segments, piece by piece, so that every SM has
 // as many as the others.
 //
@@ -136,8 +138,9 @@ __device__ __noinline__ void odd_keys(const uint8_t* src, uint32_t dst, int row,
 
 }  // namespace
 
-// kFlat: the CTAs share all segments of the call.
-template <bool kFlat>
+// kFlat: the CTAs share all segments of the call; kCluster: a cluster shares a
+// KV head's.  (Kernels of their own: either's code in the others' costs them 1 us.)
+template <bool kFlat, bool kCluster>
 __global__ void __launch_bounds__(Decode8Cfg::kThreads, 1)
 kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const PackedArgs args) {
   using Cfg = Decode8Cfg;
@@ -152,7 +155,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = args.B * args.Hkv;
-  const int split = args.part != nullptr && !kFlat ? args.split : 1;
+  const int split = kCluster ? args.cluster : args.part != nullptr && !kFlat ? args.split : 1;
 
   // Sequence b: the position of its query row 0 and its rows; false (reported
   // by the CTAs that it concerns) for a length out of range.
@@ -220,10 +223,12 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       rows_of(b, pos0, rows);
       f += g1 - g0;
     } else {
-      rank = static_cast<int>(blockIdx.x) / bh % split;
-      sub = static_cast<int>(blockIdx.x) / (bh * split);    // sub-chunk 0 first
-      b = static_cast<int>(blockIdx.x) % bh / args.Hkv;
-      g = static_cast<int>(blockIdx.x) % args.Hkv;
+      // (sub-chunk 0 first; a cluster's CTAs are neighbours)
+      const int cta = static_cast<int>(blockIdx.x) / (kCluster ? split : 1);
+      rank = kCluster ? static_cast<int>(blockIdx.x) % split : cta / bh % split;
+      sub = kCluster ? 0 : cta / (bh * split);
+      b = cta % bh / args.Hkv;
+      g = cta % args.Hkv;
       f = f_end;
       if (!rows_of(b, pos0, rows)) return;
     }
@@ -240,9 +245,9 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const int ns = (n_kv + kSegTiles - 1) / kSegTiles;
       g0 = (rank * ns + split - 1) / split;
       g1 = ((rank + 1) * ns + split - 1) / split;
-      if (g0 >= g1) return;
+      if (g0 >= g1 && !kCluster) return;                    // (a cluster's CTA stays for its barriers)
     }
-    const int j0 = g0 * kSegTiles, nt = min(n_kv, g1 * kSegTiles) - j0;
+    const int j0 = g0 * kSegTiles, nt = max(min(n_kv, g1 * kSegTiles) - j0, 0);
 
     if (threadIdx.x == 0) {
       for (int i = 0; i < Cfg::kNumBars; ++i) {
@@ -406,6 +411,32 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             *abort_flag = 1;
             ok = false;
           }
+        }
+      }
+      if constexpr (kCluster) {
+        // A segment a CTA (one row a sequence): once every CTA is done with its
+        // rings, the partials go to the first CTA's, which folds them in order.
+        // (A CTA that gave up has set the error word; then nothing is written.)
+        constexpr uint32_t kSlot = 128 * 16 + 64;           // four rows of each channel, then the rows' states
+        cluster_sync();
+        if (ok && rank > 0 && nt > 0) {
+          const uint32_t slot = smem_addr_in_cta(sbase + Cfg::kVOff + (g0 - 1) * kSlot, 0u);
+          st_cluster_f32x4(slot + me * 16u, make_float4(acc_o[0], acc_o[1], acc_o[2], acc_o[3]));
+          if (warp == 0 && lane < kGroup) st_cluster_f32x4(slot + 2048u + lane * 16u, make_float4(acc.m, acc.mc, acc.l, 0.0f));
+        }
+        cluster_sync();
+        ok = ok && rank == 0 && *reinterpret_cast<volatile uint32_t*>(args.err) == 0;
+        const int ns = (n_kv + kSegTiles - 1) / kSegTiles;
+#pragma unroll 1
+        for (int sg = 1; sg < ns && rank == 0; ++sg) {
+          const uint8_t* slot = smem + Cfg::kVOff + (sg - 1) * kSlot;
+          const float4 v = reinterpret_cast<const float4*>(slot)[me];
+          const float4 x = lane < kGroup ? reinterpret_cast<const float4*>(slot + 2048)[lane] : make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+          const FoldScale f = fold_state(acc, RowState{x.x, x.y, x.z});
+          const float o[kGroup] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+            acc_o[i] = fold_o(acc_o[i], o[i], FoldScale{__shfl_sync(0xffffffffu, f.a, i), __shfl_sync(0xffffffffu, f.b, i)});
         }
       }
       if (ok && args.part == nullptr) {
@@ -663,6 +694,11 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       }
     }
 
+    if (kCluster && warp >= 4) {                              // the other warps' part in the cluster's barriers
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -674,7 +710,7 @@ kb_decode8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   }
 }
 
-template <bool kFlat>
+template <bool kFlat, bool kCluster>
 static cudaError_t launch_decode8_t(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, long long grid, cudaStream_t s) {
   using Cfg = Decode8Cfg;
   static int configured_device = -1;
@@ -682,17 +718,34 @@ static cudaError_t launch_decode8_t(const CUtensorMap& tk, const CUtensorMap& tv
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(kb_decode8_kernel<kFlat>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Cfg::kSmemBytes));
+    e = cudaFuncSetAttribute(kb_decode8_kernel<kFlat, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(Cfg::kSmemBytes));
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  kb_decode8_kernel<kFlat><<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmemBytes, s>>>(tk, tv, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(kCluster ? a.cluster : 1);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kb_decode8_kernel<kFlat, kCluster>, tk, tv, a);
 }
 
 cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub, cudaStream_t s) {
-  if (a.part != nullptr && a.split == 0) return launch_decode8_t<true>(tk, tv, a, a.ctas, s);
-  return launch_decode8_t<false>(tk, tv, a, static_cast<long long>(a.part != nullptr ? a.split : 1) * n_sub * a.B * a.Hkv, s);
+  const long long units = static_cast<long long>(n_sub) * a.B * a.Hkv;
+  if (a.part != nullptr) {
+    if (a.split == 0) return launch_decode8_t<true, false>(tk, tv, a, a.ctas, s);
+    return launch_decode8_t<false, false>(tk, tv, a, a.split * units, s);
+  }
+  if (a.cluster > 1) return launch_decode8_t<false, true>(tk, tv, a, a.cluster * units, s);
+  return launch_decode8_t<false, false>(tk, tv, a, units, s);
 }
 
 }  // namespace kb

@@ -499,9 +499,9 @@ kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, 
  * kb_attn_chunk_8bit_workspace_bytes(B, Hkv, L, rows) bytes (L = 1 for a
  * decode), rows being start + L, or the cache's positions per sequence when
  * starts or ctx_lens is given; calls that can overlap on the GPU need one each.
- * L <= 32 reads the bytes; with a workspace several CTAs share the keys of a KV
- * head where the batch leaves SMs idle, and with NULL it runs without, slower
- * there, with the same bits.  A longer chunk needs its workspace: it reads the
+ * L <= 32 reads the bytes; several CTAs share the keys of a KV head where the
+ * batch leaves SMs idle: through a workspace where its size is not 0 (with NULL
+ * it runs without, slower, with the same bits), else through shared memory.  A longer chunk needs its workspace: it reads the
  * bytes as well where few rows see many keys, else it is computed from the
  * visible values in bf16, in the workspace; the bits are the same.
  */
