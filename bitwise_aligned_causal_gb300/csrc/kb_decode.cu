@@ -333,7 +333,7 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   if (args.starts != nullptr) {
     pos0 = args.starts[b];
     Lb = args.lens[b];
-    if (pos0 < 0 || Lb < 0 || Lb > args.L || pos0 + Lb > args.max_ctx) {
+    if (pos0 < 0 || Lb < 0 || Lb > args.L || pos0 > args.max_ctx - Lb) {   // (a sum could wrap)
       if (threadIdx.x == 0) atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
       active = false;
     }

@@ -145,7 +145,7 @@ __device__ __forceinline__ bool unit_of(int p, int second, const PrefillArgs& ar
   if (args.starts != nullptr) {
     w.start = args.starts[w.b];
     w.L = args.lens[w.b];
-    if (w.start < 0 || w.L < 0 || w.L > args.L || w.start + w.L > args.kv_cap) {
+    if (w.start < 0 || w.L < 0 || w.L > args.L || w.start > args.kv_cap - w.L) {   // (a sum could wrap)
       if (threadIdx.x == 0 && tile_rank == 0 && (w.h % kGroup) == 0)
         atomicCAS(args.err, 0u, static_cast<uint32_t>(kDevBadInput));
       return false;
