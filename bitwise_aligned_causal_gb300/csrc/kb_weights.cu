@@ -190,6 +190,7 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_k, const WeightsArgs 
   } else if (warp >= Cfg::kSumWarp0) {
     // ------------------------------------------------------------ weights
     const int st = static_cast<int>(threadIdx.x) - 32 * Cfg::kSumWarp0;
+    bool some_off;                                        // some column's row gives nothing
     {
       // Q, zero behind its columns, in the swizzled layout; the columns' offsets and positions
       for (int idx = st; idx < n_cols * 16; idx += Cfg::kSumThreads) {
@@ -201,16 +202,20 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_k, const WeightsArgs 
         *reinterpret_cast<uint4*>(smem + Cfg::kQOff + (c >> 3) * q_slab + (m >> 3) * 1024 + (m & 7) * 128 + (((c & 7) ^ (m & 7)) << 4)) = val;
       }
       constexpr float kLog2e = 1.44269504088896341f;
+      bool off_row = false;
       if (st < 128) {
         const bool used = st < kGroup * rows;
         const float l = used ? __ldg(args.lse + (static_cast<size_t>(bg) * kGroup + st / rows) * args.L + st % rows) : INFINITY;
-        // (a row that saw nothing, -inf, has no weights to give)
-        reinterpret_cast<float*>(smem + Cfg::kColOff)[st] = l == -INFINITY ? -INFINITY : __fmul_rn(-l, kLog2e);
-        reinterpret_cast<int*>(smem + Cfg::kColOff + 512)[st] = used ? pos0 + st % rows : -1;
+        // A row of an infinite log-sum-exp has no weights to give, whatever stands
+        // in q: it sees no key (its scores times the scale, minus infinity, could
+        // be NaN).
+        off_row = used && isinf(l);
+        reinterpret_cast<float*>(smem + Cfg::kColOff)[st] = isinf(l) ? -INFINITY : __fmul_rn(-l, kLog2e);
+        reinterpret_cast<int*>(smem + Cfg::kColOff + 512)[st] = used && !off_row ? pos0 + st % rows : -1;
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(Cfg::kBarQFull));
-      named_bar_sync(1, Cfg::kSumThreads);
+      some_off = named_bar_or(1, Cfg::kSumThreads, off_row);
     }
     const int half = (warp - Cfg::kSumWarp0) >> 2;
     const int key = 32 * (warp & 3) + lane;               // TMEM lane = key of the tile
@@ -228,7 +233,7 @@ kb_weights_kernel(const __grid_constant__ CUtensorMap tmap_k, const WeightsArgs 
       if (ok) {
         tc_fence_after();
         // some row does not see some key of the tile, or a column has no row (its zeros times an infinite key are NaN)
-        const bool masked = pos0 < j * kTileKeys + kTileKeys - 1 || n_cols > kGroup * rows;
+        const bool masked = pos0 < j * kTileKeys + kTileKeys - 1 || n_cols > kGroup * rows || some_off;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const int pkey = j * kTileKeys + key;
         const uint32_t d = d_tmem + db * d_cols + 64u * half;

@@ -333,7 +333,9 @@ kb_weights_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_
         const uint32_t d = d_tmem + db * 256u;
         const int2 head = reinterpret_cast<const int2*>(smem + Cfg::kHeadOff)[db];
         const float off = row_off[db * kTileRows];
-        if (head.y & Cfg::kMasked) {
+        // (some row of these 32 does not see some key, or gives nothing; told by the
+        // offsets' warp, the latter cost the 8K prompt 11 us)
+        if ((head.y & Cfg::kMasked) || __any_sync(0xffffffffu, off == -INFINITY)) {
           int r = head.x + me;
           while (r >= args.L) r -= args.L;
           // a row that gives nothing (whatever stands in q) sees no key
