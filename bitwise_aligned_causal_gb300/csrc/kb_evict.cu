@@ -99,7 +99,7 @@ __device__ __forceinline__ int2 find_bin(const uint32_t* hist, int m, int2* foun
 // held: weights of a CTA's run that fit in its dynamic shared memory.
 __global__ void __launch_bounds__(kChoiceThreads) kb_evict_choose_kernel(const EvictArgs args, int held) {
   extern __shared__ float own[];
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(16) uint32_t hist[kBins];         // (read in pairs of bins)
   __shared__ int warp_sum[kChoiceWarps], warp_eq[kChoiceWarps];
   __shared__ int totals[2], skip_word;                    // this CTA's keys above and at the threshold; nothing to do
   __shared__ int2 found;
