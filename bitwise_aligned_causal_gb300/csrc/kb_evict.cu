@@ -15,15 +15,17 @@
 // copied in ascending order in place: a tile's rows are in registers before the
 // first is stored, and later tiles' sources lie behind every store made before
 // them, so the loads of the next tile are in flight meanwhile.  A tile is shared
-// by a cluster of CTAs, as many (1 to 8) as find SMs.  A warp looks up the old
-// new places of its 16 rows in its lanes and hands them round, so a 16-byte
+// by a cluster of CTAs, as many (1 to 8) as find SMs; its mbarriers put all loads
+// of a tile before its stores.  A warp looks up the old
+// and new places of its 16 rows in its lanes and hands them round, so a 16-byte
 // piece costs four shuffles and no address arithmetic.
 //
-// Measured: 16 paged sequences of 4.5K cut to 2000: choice 13 us, move 38 (in
-// slices of rows, with a look-up per piece, 65), the move at a plain copy's rate;
-// a paged 28K cache of 18K kept keys 52 us in all; 64K cut to 8K 40, of which the
-// choice takes 25: three digits' rounds of the cluster, a few us each.  A third
-// tile in registers cost 15 us in the second case.
+// Measured, in a replayed graph: 16 paged sequences of 4.5K cut to 2000, a CTA a
+// plane, 52 us, of which the choice takes 13 (in slices of rows, with a look-up
+// per piece, the move took 65, not 38), the move at a plain copy's rate; a paged
+// 28K cache of 18K kept keys, clusters of eight, 62; 64K cut to 8K 41, of which
+// the choice takes 25: three digits' rounds of the cluster, a few us each.  A
+// third tile in registers cost 15 us in the second case.
 #include <algorithm>
 
 #include "kb_contract.cuh"
@@ -257,24 +259,23 @@ __global__ void __launch_bounds__(kChoiceThreads) kb_evict_choose_kernel(const E
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = kMoveThreads / 2;               // of a CTA's part of a tile: 16 a warp
 
-// page_magic: 2^32 / page_size, rounded down.
-// A barrier of the cluster that orders a load whose value has been used before
-// another CTA's store, and nothing else: cluster_sync waits for every load on
-// its way (three caches of 32K: move 101 us instead of 73).  bar: this CTA's mbarrier, of which each CTA's thread 0 .. ctas - 1
-// arrives on one.  Bounded as mbar_wait; false: gave up, after which no thread of
-// the CTA waits any more (all go on through their tiles, so no barrier of the CTA
-// is missed; a vote on it in __syncthreads_and cost a quarter of the time).
-__device__ __forceinline__ bool meet(uint32_t bar, int ctas, uint32_t parity, volatile int* gave_up, uint32_t* err) {
-  __syncthreads();
-  if (ctas == 1) return true;
-  if (static_cast<int>(threadIdx.x) < ctas)
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(smem_addr_in_cta(bar, threadIdx.x)) : "memory");
+// All CTAs of the cluster have read their part of a tile: tell_read, after the
+// CTA's threads have met, arrives on every CTA's mbarrier (bar: this CTA's) with
+// release, and wait_read waits for this CTA's with acquire.  That puts every load
+// of the tile before any store of it.
+__device__ __forceinline__ void tell_read(uint32_t bar, int ctas) {
+  if (static_cast<int>(threadIdx.x) < ctas) mbar_arrive_cluster(smem_addr_in_cta(bar, threadIdx.x));
+}
+// Bounded as mbar_wait; false: gave up, after which no thread of the CTA waits
+// any more (all go on through their tiles, so no barrier of the CTA is missed; a
+// vote on it in __syncthreads_and cost a quarter of the time).
+__device__ __forceinline__ bool wait_read(uint32_t bar, uint32_t parity, volatile int* gave_up, uint32_t* err) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -289,6 +290,8 @@ __device__ __forceinline__ bool meet(uint32_t bar, int ctas, uint32_t parity, vo
   }
 }
 
+// kShared: a plane's CTAs are a cluster.  page_magic: 2^32 / page_size, rounded down.
+template <bool kShared>
 __global__ void __launch_bounds__(kMoveThreads, 2) kb_evict_move_kernel(const EvictArgs args, int ctas, uint32_t page_magic) {
   asm volatile("griddepcontrol.wait;" ::: "memory");      // (the choice is made)
   const int rank = static_cast<int>(blockIdx.x) % ctas;
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) kb_evict_move_kernel(const Ev
   __shared__ uint64_t met;
   __shared__ int gave_up;
   const uint32_t bar = smem_addr(&met);
-  if (ctas > 1) {
+  if (kShared) {
     if (threadIdx.x == 0) {
       gave_up = 0;
       mbar_init(bar, static_cast<uint32_t>(ctas));
@@ -368,13 +371,24 @@ __global__ void __launch_bounds__(kMoveThreads, 2) kb_evict_move_kernel(const Ev
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       const int i = i0 + a * tile;                        // (past the last row nothing is read or written)
-      load(set[a ^ 1], i + tile + mine, ahead);
-      ahead = old_row(i + 2 * tile + mine);
-      wait_loaded(set[a]);                                // the tile is loaded, here and in every thread
-      if (meet(bar, ctas, static_cast<uint32_t>(a), &gave_up, args.err)) store(set[a]);
+      // A release waits for all loads on their way, so a cluster's next tile leaves
+      // behind it (three caches of 32K 104 us; before it 120); a CTA alone has none
+      // and gains by an earlier start (16 caches of 4.5K 52 us; behind it 55).
+      auto load_next = [&]() {
+        load(set[a ^ 1], i + tile + mine, ahead);
+        ahead = old_row(i + 2 * tile + mine);
+      };
+      if (!kShared) load_next();
+      wait_loaded(set[a]);                                // the tile is loaded, here ...
+      __syncthreads();                                    // ... in the CTA ...
+      if (kShared) {
+        tell_read(bar, ctas);
+        load_next();
+      }
+      if (!kShared || wait_read(bar, static_cast<uint32_t>(a), &gave_up, args.err)) store(set[a]);    // ... and in the cluster
     }
   }
-  if (ctas > 1) cluster_sync();                           // (no CTA leaves while another may arrive on its barrier)
+  if (kShared) cluster_sync();                            // (no CTA leaves while another may arrive on its barrier)
 }
 
 cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s) {
@@ -424,7 +438,7 @@ cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s) {
   mv.attrs = mattr;
   mv.numAttrs = movers > 1 ? 2 : 1;
   const uint32_t magic = a.block_table != nullptr ? static_cast<uint32_t>((1ull << 32) / static_cast<uint32_t>(a.page_size)) : 0u;
-  return cudaLaunchKernelEx(&mv, kb_evict_move_kernel, a, movers, magic);
+  return cudaLaunchKernelEx(&mv, movers > 1 ? kb_evict_move_kernel<true> : kb_evict_move_kernel<false>, a, movers, magic);
 }
 
 }  // namespace kb
