@@ -255,7 +255,7 @@ kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const
   kb_status s = kb::host_check_heads(B, Hq, Hkv);
   if (s != KB_OK) return s;
   if (table != nullptr && (s = host_check_table(table, n_pos, rot_dim)) != KB_OK) return s;
-  for (int i = 0; i < 3; ++i)
+  for (int i = q == nullptr ? 1 : 0; i < 3; ++i)
     if ((s = host_check_strides(strides + 3 * i)) != KB_OK) return s;
   if ((s = host_check_ragged(starts, lens)) != KB_OK) return s;
   int cap = 0;
