@@ -344,11 +344,18 @@ kb_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     Lb = 1;
   }
   const int seq_kv = pos0 + Lb;
-  // sub-chunks: the rows of a tile's positions, or of 32 positions of a longer chunk
-  const int cell = k8 && args.L > kMaxPackedRows ? kMaxPackedRows : kTileKeys;
-  const int cell0 = (pos0 / cell + sub) * cell - pos0;
-  const int r0 = max(cell0, 0);
-  const int r1 = min(cell0 + cell, Lb);
+  // the sub-chunk's rows: those before the first tile boundary and those behind
+  // it, or (longer chunks over bytes) of 32 positions each
+  int r0, r1;
+  if (k8 && args.L > kMaxPackedRows) {
+    const int cell0 = (pos0 / kMaxPackedRows + sub) * kMaxPackedRows - pos0;
+    r0 = max(cell0, 0);
+    r1 = min(cell0 + kMaxPackedRows, Lb);
+  } else {
+    const int split = min(Lb, (pos0 / kTileKeys + 1) * kTileKeys - pos0);
+    r0 = sub == 0 ? 0 : split;
+    r1 = sub == 0 ? split : Lb;
+  }
   const int Lc = max(r1 - r0, 1);
   if (r1 - r0 <= 0) active = false;                     // the chunk does not reach this one
   const int n_rows = kGroup * Lc;                       // packed rows in use
