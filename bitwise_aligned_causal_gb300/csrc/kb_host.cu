@@ -310,9 +310,12 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
     // key tiles at about 1550 cycles each; its static split leaves a tail of
     // (ceil(p) - p) / p with p pairs per CTA, where the one-CTA-per-tile
     // launch ends on the shortest tiles.  Where every tile finds an SM of its own
-    // and sees many keys, none shares one (256 rows at 32K: 401 us in pairs, 204 so).
+    // and sees many keys, none shares one (256 rows at 32K: 401 us in pairs, 204
+    // so; ragged, 300 rows at 300: 13.3 and 10.9), but for the snake's calls below.
     const long long pairs = static_cast<long long>((a.n_tiles + 1) / 2) * kb::kGroup * B * Hkv;
-    const bool roomy = static_cast<long long>(a.n_tiles) * B * Hq <= a.max_ctas && (ragged ? kv_cap - L : start) >= L;
+    const long long kv_bytes = 2LL * B * Hkv * (start + L) * kb::kHeadDim * 2;
+    const bool in_l2 = !ragged && 4 * kv_bytes <= 3 * dst->l2_bytes;
+    const bool roomy = static_cast<long long>(a.n_tiles) * B * Hq <= a.max_ctas && (ragged ? kv_cap - L : start) >= L && !in_l2;
     bool persistent = pairs <= a.max_ctas && !roomy;
     if (!persistent && !roomy) {
       const double p = static_cast<double>(pairs) / a.max_ctas;
@@ -324,11 +327,9 @@ kb_status chunk_impl(const void* q, const void* k, const void* v, void* o, int B
     // The snake, when it balances better than the pairs (few pairs per CTA)
     // and all of K and V fit in three quarters of L2: it runs every group at
     // once.
-    const long long kv_bytes = 2LL * B * Hkv * (start + L) * kb::kHeadDim * 2;
     if (force_snake) {
       a.persistent = kb::kSchedSnake;
-    } else if (!force_persistent && !roomy && !ragged && 4 * kv_bytes <= 3 * dst->l2_bytes &&
-               pairs < 32LL * a.max_ctas) {
+    } else if (!force_persistent && in_l2 && pairs < 32LL * a.max_ctas) {
       const long long n = a.n_tiles, G = a.max_ctas;
       const long long units = n * B * Hq;
       const long long per_cta_pairs = (pairs + G - 1) / G;
