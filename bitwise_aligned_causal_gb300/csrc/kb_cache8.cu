@@ -305,7 +305,8 @@ cudaError_t launch_cache_values(const Values8Args& a, cudaStream_t s) {
 
 // A CTA per (batch, KV head, key block) of a call's visible keys, K or V:
 // what the block stands for, as rows of a contiguous bf16 cache of `rows`
-// positions per sequence (zeros behind the sequence's last key).
+// positions per sequence (rows behind the sequence's last key are left as they
+// are: the tile kernel masks their scores and clears their values).
 __global__ void __launch_bounds__(256) kb_cache_gather_kernel(const Gather8Args args) {
   if (*reinterpret_cast<volatile uint32_t*>(args.err) != 0) return;
   const bool is_v = blockIdx.y != 0;

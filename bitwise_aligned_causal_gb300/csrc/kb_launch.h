@@ -91,7 +91,8 @@ cudaError_t launch_prefill_s2(const CUtensorMap& tq, const CUtensorMap& tk, cons
 // cache held in 8 bits L may be larger: sub-chunks of 32 positions then.
 cudaError_t launch_packed(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub,
                           cudaStream_t s);
-// The same for at most kMaxRows8 query rows over a cache held in 8 bits (kb_decode8.cu; a.cluster unused).
+// The same for at most kMaxRows8 query rows over a cache held in 8 bits (kb_decode8.cu; a.cluster > 1: that many CTAs
+// share a KV head, a segment each).
 constexpr int kMaxRows8 = 2;
 cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const PackedArgs& a, int n_sub, cudaStream_t s);
 // Partials a CTA of the narrow packed kernel can keep in shared memory for
@@ -122,6 +123,8 @@ cudaError_t launch_backward(const CUtensorMap& tq, const CUtensorMap& tk, const 
 cudaError_t launch_bwd_delta(const void* o, const void* dout, float* delta, long long rows, cudaStream_t s);
 // C5 fold of the packed kernel's per-segment partials, one warp per row
 // (rows = B*Hq*L, row r of a (b, h) at position start + r), then C4 into o.
+cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
+                            cudaStream_t s);
 // The same for the partials of 8-bit calls, whose rows' positions may be given per sequence: one CTA per row.
 struct RowsFoldArgs {
   const float* part;       // [B, Hq, L, n_seg][132]
@@ -129,12 +132,9 @@ struct RowsFoldArgs {
   int B, Hq, L, n_seg;
   int start;
   const int *starts, *lens, *ctx_lens;   // as PackedArgs
-  int max_ctx;
   const uint32_t* err;
 };
 cudaError_t launch_rows_fold(const RowsFoldArgs& a, cudaStream_t s);
-cudaError_t launch_seg_fold(const float* part, void* o, long long rows, int L, int start, int seg_tiles, int n_seg,
-                            cudaStream_t s);
 
 constexpr int kMaxAxes = 4;          // positions a row can have in rope_axes
 constexpr int kPlanesPerLane = 8;    // planes of a row that one lane turns
