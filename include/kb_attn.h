@@ -501,9 +501,13 @@ kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, 
  * starts or ctx_lens is given; calls that can overlap on the GPU need one each.
  * L <= 32 reads the bytes; several CTAs share the keys of a KV head where the
  * batch leaves SMs idle: through a workspace where its size is not 0 (with NULL
- * it runs without, slower, with the same bits), else through shared memory.  A longer chunk needs its workspace: it reads the
- * bytes as well where few rows see many keys, else it is computed from the
- * visible values in bf16, in the workspace; the bits are the same.
+ * it runs without, slower, with the same bits), else through shared memory.
+ * From 304 (batch, KV head) pairs on the size is 0 and a CTA has a KV head's
+ * keys to itself.  A longer chunk needs its workspace: it reads the bytes as
+ * well where few rows see many keys, else it is computed from the visible
+ * values in bf16, in the workspace; the bits are the same.  Its size is at least
+ * that of two bf16 caches of `rows` positions (512 bytes each for B * Hkv *
+ * rows of them, twice what the 8-bit caches take), whichever way is taken.
  */
 kb_status kb_attn_append_8bit(const void* q, const void* k, const void* v, const long long* strides, void* q_out,
                               void* k_cache, void* v_cache, signed char* k_exp, signed char* v_exp,
@@ -579,6 +583,8 @@ kb_status kb_attn_key_weights(const void* q, const void* k, const float* lse, fl
  * the cache's blocks must be made anew (kb_attn_block_boxes).  An out-of-range
  * lens or page index is found on the device (nothing of that sequence moves)
  * and reported by the next kb_attn_check_device_status as KB_ERR_INVALID_ARG.
+ * After KB_ERR_TIMEOUT (a wait between the move's CTAs gave up) some rows have
+ * moved and others have not: the caches' contents are undefined.
  */
 kb_status kb_attn_evict(void* k, void* v, const float* weights, float* weights_out, int* kept, int B, int Hkv,
                         const int* lens, int keep, int keep_first, int keep_last, int kv_cap,
