@@ -502,8 +502,8 @@ kb_status kb_attn_rope_axes(const void* x, const long long* strides, void* out, 
  * L <= 32 reads the bytes; several CTAs share the keys of a KV head where the
  * batch leaves SMs idle: through a workspace where its size is not 0 (with NULL
  * it runs without, slower, with the same bits), else through shared memory.
- * From 304 (batch, KV head) pairs on the size is 0 and a CTA has a KV head's
- * keys to itself.  A longer chunk needs its workspace: it reads the bytes as
+ * From 304 (batch, KV head) pairs on, and where it would pass 1 GB, the size is
+ * 0 and a CTA has a KV head's keys to itself.  A longer chunk needs its workspace: it reads the bytes as
  * well where few rows see many keys, else it is computed from the visible
  * values in bf16, in the workspace; the bits are the same.  Its size is at least
  * that of two bf16 caches of `rows` positions (512 bytes each for B * Hkv *
